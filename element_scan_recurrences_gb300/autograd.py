@@ -23,12 +23,13 @@ differentiated again.
 from __future__ import annotations
 
 import threading
-from typing import Sequence
+from typing import Optional, Sequence
 
 import torch
 from torch.autograd.function import once_differentiable
 
 from . import binding as es
+from . import sequence
 
 _programs = {}
 _programs_lock = threading.Lock()
@@ -145,3 +146,60 @@ def linear_scan(a: torch.Tensor, b: torch.Tensor, axis: int = 0, reverse: bool =
     """The states of a linear-scan, differentiable with respect to a and b."""
     a, b = _one_shape(a, b, a.shape, b.shape)
     return _MatrixScan.apply(True, int(axis), bool(reverse), False, False, a, b)
+
+
+class _LinearAttention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, log_decay, initial_state, lengths, scale, final_state):
+        out, fin = sequence.linear_attention(q, k, v, log_decay, initial_state=initial_state, lengths=lengths, scale=scale,
+                                             final_state=final_state)
+        ctx.save_for_backward(q, k, v, log_decay, initial_state, lengths)
+        ctx.scale = scale
+        return out, fin
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_out, grad_fin):
+        q, k, v, log_decay, initial_state, lengths = ctx.saved_tensors
+        gq, gk, gv, gg, gi = sequence.linear_attention_backward(
+            q, k, v, log_decay, grad_out if grad_out.stride(-1) == 1 else grad_out.contiguous(),
+            initial_state=initial_state,
+            grad_final_state=None if grad_fin is None else grad_fin.contiguous(), lengths=lengths, scale=ctx.scale,
+            decay_grad=ctx.needs_input_grad[3])
+        return gq, gk, gv, gg, gi, None, None, None
+
+
+def linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: Optional[torch.Tensor] = None,
+                     initial_state: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None,
+                     scale: Optional[float] = None, final_state: bool = False):
+    """``sequence.linear_attention``, differentiable with respect to q, k, v,
+    the log decays and the initial state: (out, the last state or None).  The
+    backward needs nothing of the forward but its inputs."""
+    return _LinearAttention.apply(q, k, v, log_decay, initial_state, lengths, scale, bool(final_state))
+
+
+class _QkNormRotate(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, cos, sin, positions, eps, neighbours):
+        ctx.save_for_backward(q, k, q_weight, k_weight, cos, sin, positions)
+        ctx.eps, ctx.neighbours = eps, neighbours
+        return sequence.qk_norm_rotate(q, k, q_weight, k_weight, cos, sin, positions=positions, eps=eps,
+                                       neighbours=neighbours)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, gq, gk):
+        q, k, q_weight, k_weight, cos, sin, positions = ctx.saved_tensors
+        gq, gk = (g if g is None or g.stride(-1) == 1 else g.contiguous() for g in (gq, gk))
+        grads = sequence.qk_norm_rotate_backward(q, k, q_weight, k_weight, cos, sin, gq, gk, positions=positions,
+                                                 eps=ctx.eps, neighbours=ctx.neighbours)
+        return grads + (None, None, None, None, None)
+
+
+def qk_norm_rotate(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: Optional[torch.Tensor] = None,
+                   k_weight: Optional[torch.Tensor] = None, cos: Optional[torch.Tensor] = None,
+                   sin: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                   neighbours: bool = False):
+    """``sequence.qk_norm_rotate``, differentiable with respect to q, k and
+    the weights; the tables take no gradient."""
+    return _QkNormRotate.apply(q, k, q_weight, k_weight, cos, sin, positions, float(eps), bool(neighbours))

@@ -24,7 +24,7 @@ STATUS = {0: "ES_OK", 1: "ES_E_DIM_001", 2: "ES_E_DIM_002", 3: "ES_E_ARG", 4: "E
           5: "ES_E_CUDA", 6: "ES_E_TIMEOUT", 7: "ES_E_BODY"}
 MAX_SEQS = 8
 PATHS = {0: "auto", 1: "empty", 2: "generic", 3: "lane_tma", 4: "time_tma", 5: "vec_tma", 6: "mat_tma",
-         7: "mat_chunked", 8: "mat_chunked_tma"}
+         7: "mat_chunked", 8: "mat_chunked_tma", 9: "tensor"}
 PATH_IDS = {v: k for k, v in PATHS.items()}
 
 # every function include/es.h declares
@@ -39,7 +39,9 @@ EXPORTS = ("es_scan_f32", "es_plan_f32", "es_scan_backward_f32", "es_plan_backwa
            "es_body_source_backward", "es_body_prepare_backward", "es_matrix_scan_backward_f32",
            "es_plan_matrix_scan_backward_f32", "es_linear_scan_backward_f32", "es_plan_linear_scan_backward_f32",
            "es_scan_host_f32", "es_scan_body_host_f32", "es_matrix_scan_backward_ws_f32",
-           "es_plan_matrix_scan_backward_ws_f32")
+           "es_plan_matrix_scan_backward_ws_f32", "es_linear_attention", "es_linear_attention_backward",
+           "es_linear_attention_workspace", "es_plan_linear_attention", "es_linear_attention_step", "es_qk_norm_rotate",
+           "es_qk_norm_rotate_backward", "es_qk_norm_rotate_workspace", "es_plan_qk_norm_rotate")
 
 
 class LibraryMissing(ImportError):
@@ -170,6 +172,15 @@ def lib():
         L.es_table_scan_i32.restype = ctypes.c_int
         L.es_plan_table_scan_i32.argtypes = tsig + [P, ctypes.POINTER(PlanInfo)]
         L.es_plan_table_scan_i32.restype = ctypes.c_int
+        # the sequence-layer operators (sequence.py): structs packed as bytes, then (workspace, plan) a result or a stream
+        C, szp = ctypes.c_char_p, ctypes.POINTER(ctypes.c_size_t)
+        for op in ("linear_attention", "qk_norm_rotate"):
+            for name, args in (("es_%s" % op, [C, P]), ("es_%s_backward" % op, [C, C, P]),
+                               ("es_%s_workspace" % op, [C, C, szp]), ("es_plan_%s" % op, [C, C, ctypes.POINTER(PlanInfo)])):
+                getattr(L, name).argtypes = args
+                getattr(L, name).restype = ctypes.c_int
+        L.es_linear_attention_step.argtypes = [C, P]
+        L.es_linear_attention_step.restype = ctypes.c_int
         _lib = L
         return L
 

@@ -1,0 +1,170 @@
+// es_attn.h -- launch descriptions of linear attention and of the query/key
+// norm with rotation, shared by the entry points (es_attn_api.cu) and the
+// kernels (k_attn_*.cu, k_rotate.cu).  Not part of the ABI.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "es_internal.h"
+
+namespace es {
+
+// [B, T, heads, dim] operand, innermost stride 1 (strides in elements); head h
+// of the call reads operand head h / div.
+struct AttnOperand {
+    const void* p;
+    int64_t sb, st, sh;
+    int div;
+};
+
+// One run of the recurrence over the sequences of a call:
+//
+//     state[t] = e^{g[t]} state[t-1] + y[t] z[t]^T,   out[t] = out_scale * x[t] state[t]
+//
+// or, reversed, from the last token to the first,
+//
+//     state[t] = e^{g[t+1]} state[t+1] + y[t] z[t]^T, out[t] = out_scale * x[t] state[t]
+//
+// with a state of dx x dz values.  The forward pass is one run (x, y, z) =
+// (q, k, v); the gradients are three more over the same data:
+//     grad_q  forward  (grad_out, v, k),  the state transposed
+//     grad_v  reversed (k, q, grad_out)
+//     grad_k  reversed (v, grad_out, q),  the state transposed
+struct AttnRun {
+    AttnOperand x, y, z;
+    void* out;                   // [B, T, H, dz] by strides, bf16 or f32
+    int64_t ob, ot, oh;
+    int out_f32;                 // out is f32 whatever the operands' type
+    const float* init;           // value (a, c) of the state of (b, h) at [(b*H + h)*dx*dz + a*sa + c*sc], or null (zero)
+    float* fin;                  // state after the last trip, the same layout, or null
+    int64_t sa, sc;
+    float init_scale, fin_scale, out_scale;
+    int reverse;
+    // For the decays' gradient: out[t] (unrounded) . w[t], per slice of dz
+    // columns, [slices, B*H, T]; null: not wanted.
+    AttnOperand w;
+    float* dots;
+    // A forward run writes its state after every `anchor_every` chunks (and
+    // after the last one) to anchors[(bh*n + m)*dx*dz + a*dz + c]; a reversed
+    // run instead writes out_scale * <its state there, the anchor> per slice
+    // to anchor_dots [slices, B*H, n].
+    float* anchors;
+    float* anchor_dots;
+    int dx, dz;
+};
+
+struct AttnLaunch {
+    AttnRun run[3];
+    int runs;
+    int bf16;
+    int64_t B, T;
+    int H;
+    const float* g;              // log decays, strides in elements; null: none
+    int64_t gb, gt, gh;
+    const int* lengths;          // [B] or null
+    int64_t anchor_every;        // in chunks
+    int64_t n_anchors;           // per (b, h)
+    // segments of tokens (tensor-core path): see k_attn_tc.cu
+    int64_t seg_chunks;          // chunks a segment; 0: one segment
+    int n_segs;
+    float* seg_states;
+    float* seg_decays;
+    unsigned int* status;
+    uint64_t wait_ns;
+    int64_t drop_tile;
+    cudaStream_t stream;
+    int num_sms;
+    EncodeTiledFn encode;
+};
+
+// chunk of tokens and slice of value columns of the direct kernel
+constexpr int kAttnChunk = 32;
+constexpr int kAttnSlice = 32;
+constexpr int kAttnMaxDim = 256;
+
+cudaError_t launch_attn_direct(const AttnLaunch& L);
+
+// The decays' gradient from the two runs' dots: for each token t of anchor
+// block m, sum over s >= t of the block of (dq[s] - dk[s]) + e[m].
+struct AttnDecayGrad {
+    const float* dots_q;         // [slices_q, B*H, T]
+    const float* dots_k;
+    const float* ends;           // [slices_k, B*H, n]
+    int slices_q, slices_k;
+    int64_t B, T;
+    int H;
+    const int* lengths;
+    int64_t block;               // tokens of an anchor block
+    int64_t n;                   // anchor blocks per (b, h)
+    float* grad;                 // [B, T, H], or null
+    float* partial;              // per head: [H, B*n] block sums, then summed to `grad_h`
+    float* grad_h;               // [H], or null
+    cudaStream_t stream;
+};
+cudaError_t launch_attn_decay_grad(const AttnDecayGrad& G, int* kernels);
+
+// grads of operand heads read by several heads: out[b,t,j,:] = sum of part[b,t,j*div+r,:] over r
+struct AttnFold {
+    const float* part;           // [B, T, H, d] dense
+    void* out;
+    int64_t ob, ot, oh;
+    int bf16;
+    int64_t B, T;
+    int heads, div, d;
+    cudaStream_t stream;
+};
+cudaError_t launch_attn_fold(const AttnFold& F);
+
+struct AttnStep {
+    AttnOperand q, k, v;         // st unused
+    void* out;                   // [B, H, dv] by strides
+    int64_t ob, oh;
+    int bf16;
+    const float* g;
+    int64_t gb, gh;
+    const float* state;          // [B, H, dk, dv] dense
+    float* state_out;
+    float scale;
+    int64_t B;
+    int H, dk, dv;
+    cudaStream_t stream;
+    int num_sms;
+};
+cudaError_t launch_attn_step(const AttnStep& S);
+
+// ---------------------------------------------------------------------------
+// norm of queries and keys with the position rotation
+
+struct RotateSide {
+    const void* x;               // [B, T, heads, d]
+    int64_t xb, xt, xh;
+    const void* g;               // gradient of the output (backward)
+    int64_t gb, gt, gh;
+    void* out;                   // forward: the output; backward: the gradient of x
+    int64_t ob, ot, oh;
+    const void* w;               // [d] or null
+    void* gw;                    // backward: gradient of w, or null
+    int heads;
+};
+
+struct RotateLaunch {
+    RotateSide side[2];          // queries, keys
+    int bf16, w_bf16;
+    int64_t B, T;
+    int d, turned, neighbours;
+    float eps;
+    const float* cos;
+    const float* sin;            // [rows, turned / 2]
+    int64_t rows;
+    const void* positions;       // [B, T] by strides, or null (0, 1, ...)
+    int pos64;
+    int64_t pb, pt;
+    float* partial;              // backward: [blocks, d] partial sums of both weights' gradients
+    int backward;
+    cudaStream_t stream;
+    int num_sms;
+};
+int rotate_blocks(const RotateLaunch& L, int side);
+cudaError_t launch_rotate(const RotateLaunch& L, int* kernels);
+
+}  // namespace es

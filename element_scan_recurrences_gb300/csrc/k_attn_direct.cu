@@ -1,0 +1,421 @@
+// k_attn_direct.cu -- linear attention in chunks on the FMA units: any head
+// widths up to 256, any strides and alignment, f32 or bf16 operands, every sum
+// in f32.  Also the kernels that finish the gradients: the decays' gradient
+// from the row products and the sum over heads that share an operand.
+//
+// One CTA runs one (batch row, head) and a slice of 32 value columns through
+// the tokens, 32 at a time.  With G the inclusive sum of the chunk's log
+// decays,
+//
+//     out_i  = sum_{j<=i} e^{G_i-G_j} (x_i.y_j) z_j + e^{G_i} x_i state
+//     state' = e^{G_C} state + sum_j e^{G_C-G_j} y_j z_j^T
+//
+// (reversed: j >= i, e^{G_j-G_i}, and the two chunk coefficients swapped).  A
+// log decay below -104 makes e^g zero in f32: such a token starts a new group
+// and contributes nothing to G, so the sums of later tokens keep their
+// precision and a decay of -inf needs no other care.
+#include "es_attn.h"
+#include "es_device.cuh"
+
+namespace es {
+namespace {
+
+constexpr int C = kAttnChunk;
+constexpr int ZS = kAttnSlice;
+constexpr int kThreads = 256;
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T v) {
+    return static_cast<float>(v);
+}
+
+struct DirectArgs {
+    AttnRun run[3];
+    int64_t T;
+    int H;
+    const float* g;
+    int64_t gb, gt, gh;
+    const int* lengths;
+    int64_t anchor_every, n_anchors;
+    int64_t BH;
+};
+
+// Bounded on GB300 by shared-memory reads and FMA issue, not by HBM: for one
+// chunk and slice, dx = 128, 426 K FMAs (the 32 x 32 products of x and y are
+// formed again in every slice).  It serves the calls the tensor-core kernel
+// cannot take.
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_constant__ DirectArgs A) {
+    extern __shared__ __align__(16) float sm[];
+    const AttnRun& R = A.run[blockIdx.z];
+    const int slice = blockIdx.y;
+    const int z0 = slice * ZS;
+    if (z0 >= R.dz) return;
+    const int64_t bh = blockIdx.x;
+    const int64_t b = bh / A.H;
+    const int h = static_cast<int>(bh % A.H);
+    const int tid = threadIdx.x;
+    const int dx = R.dx, dxp = (dx + 3) & ~3, ld = dxp + 4;
+    const int nz = min(ZS, R.dz - z0);
+
+    float* sX = sm;                       // [C][ld]
+    float* sY = sX + C * ld;              // [C][ld]
+    float* sS = sY + C * ld;              // state slice [dxp][ZS]
+    float* sZ = sS + dxp * ZS;            // [C][ZS]
+    float* sU = sZ + C * ZS;              // z scaled by its chunk coefficient
+    float* sP = sU + C * ZS;              // [C][C + 1]
+    float* sG = sP + C * (C + 1);         // G, and per token: coefficient of the read, of the update
+    float* sRead = sG + C;
+    float* sUpd = sRead + C;
+    int* sLo = reinterpret_cast<int*>(sUpd + C);    // first token of the group of token i
+    float* sDecay = reinterpret_cast<float*>(sLo + C);
+
+    int64_t len = A.T;
+    if (A.lengths != nullptr) {
+        const int64_t l = A.lengths[b];
+        len = l < 0 ? 0 : l < A.T ? l : A.T;
+    }
+    const T* X = static_cast<const T*>(R.x.p) + b * R.x.sb + (h / R.x.div) * R.x.sh;
+    const T* Y = static_cast<const T*>(R.y.p) + b * R.y.sb + (h / R.y.div) * R.y.sh;
+    const T* Z = static_cast<const T*>(R.z.p) + b * R.z.sb + (h / R.z.div) * R.z.sh + z0;
+    const T* Wd = R.dots != nullptr ? static_cast<const T*>(R.w.p) + b * R.w.sb + (h / R.w.div) * R.w.sh + z0 : nullptr;
+    const float* G = A.g != nullptr ? A.g + b * A.gb + h * A.gh : nullptr;
+    float* dots = R.dots != nullptr ? R.dots + (slice * A.BH + bh) * A.T : nullptr;
+    const int64_t out_at = b * R.ob + static_cast<int64_t>(h) * R.oh + z0;
+    const bool store_f32 = R.out_f32 != 0;
+
+    // the first state
+    const int64_t sbase = bh * R.dx * static_cast<int64_t>(R.dz);
+    for (int e = tid; e < dxp * ZS; e += kThreads) {
+        const int a = e / ZS, c = e % ZS;
+        float v = 0.0f;
+        if (R.init != nullptr && a < dx && c < nz) v = R.init[sbase + a * R.sa + (z0 + c) * R.sc] * R.init_scale;
+        sS[e] = v;
+    }
+    // rows past the length: zero
+    for (int64_t e = len * nz + tid; e < A.T * nz; e += kThreads) {
+        const int64_t t = e / nz, at = out_at + t * R.ot + e % nz;
+        if (store_f32) static_cast<float*>(R.out)[at] = 0.0f;
+        else static_cast<T*>(R.out)[at] = static_cast<T>(0.0f);
+    }
+    const int64_t n_chunks = (len + C - 1) / C;
+    const int ty = tid / 16, tx = tid % 16;
+
+    for (int64_t k = 0; k < n_chunks; ++k) {
+        const int64_t ci = R.reverse ? n_chunks - 1 - k : k;
+        const int64_t t0 = ci * C;
+        const int n = static_cast<int>(len - t0 < C ? len - t0 : C);
+        __syncthreads();
+        // the gradient of the decays: the state at the end of an anchor block
+        const bool at_anchor = (ci + 1) % A.anchor_every == 0 || ci == n_chunks - 1;
+        if (R.anchor_dots != nullptr && at_anchor) {
+            const int64_t m = ci / A.anchor_every;
+            const float* an = R.anchors + (bh * A.n_anchors + m) * R.dx * static_cast<int64_t>(R.dz);
+            float s = 0.0f;
+            for (int e = tid; e < dx * ZS; e += kThreads) {
+                const int a = e / ZS, c = e % ZS;
+                if (c < nz) s += sS[e] * an[static_cast<int64_t>(a) * R.dz + z0 + c];
+            }
+            for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            if (tid % 32 == 0) sP[tid / 32] = s;
+            __syncthreads();
+            if (tid == 0) {
+                float all = 0.0f;
+                for (int w = 0; w < kThreads / 32; ++w) all += sP[w];
+                R.anchor_dots[(slice * A.BH + bh) * A.n_anchors + m] = all * R.out_scale;
+            }
+            __syncthreads();
+        }
+        for (int e = tid; e < C * dxp; e += kThreads) {
+            const int t = e / dxp, a = e % dxp;
+            const bool in = t < n && a < dx;
+            sX[t * ld + a] = in ? to_f32(X[(t0 + t) * R.x.st + a]) : 0.0f;
+            sY[t * ld + a] = in ? to_f32(Y[(t0 + t) * R.y.st + a]) : 0.0f;
+        }
+        for (int e = tid; e < C * ZS; e += kThreads) {
+            const int t = e / ZS, c = e % ZS;
+            sZ[e] = (t < n && c < nz) ? to_f32(Z[(t0 + t) * R.z.st + c]) : 0.0f;
+        }
+        if (tid < 32) {
+            // one token a lane: G, the sum after it, and its group
+            float g = 0.0f;
+            if (G != nullptr && tid < n) g = G[(t0 + tid) * A.gt];
+            const bool cut = g < -104.0f;
+            if (cut) g = 0.0f;
+            float pre = g, nxt = __shfl_down_sync(0xffffffffu, g, 1);
+            float suf = tid == 31 ? 0.0f : nxt;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float p = __shfl_up_sync(0xffffffffu, pre, o);
+                const float q = __shfl_down_sync(0xffffffffu, suf, o);
+                if (tid >= o) pre += p;
+                if (tid + o < 32) suf += q;
+            }
+            const unsigned cuts = __ballot_sync(0xffffffffu, cut);
+            const unsigned upto = cuts & (0xffffffffu >> (31 - tid));
+            const unsigned after = tid == 31 ? 0u : cuts >> (tid + 1);
+            sG[tid] = pre;
+            sLo[tid] = upto ? 31 - __clz(upto) : 0;
+            const float er = upto ? 0.0f : expf(pre), eu = after ? 0.0f : expf(suf);
+            sRead[tid] = R.reverse ? eu : er;
+            sUpd[tid] = R.reverse ? er : eu;
+            if (tid == 31) *sDecay = cuts ? 0.0f : expf(pre);
+        }
+        __syncthreads();
+        // x_i . y_j with its decay: thread (ty, tx) rows ty, ty+16, columns tx, tx+16
+        {
+            float s[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+            for (int a = 0; a < dxp; a += 4) {
+                float4 xv[2], yv[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    xv[r] = *reinterpret_cast<const float4*>(sX + (ty + 16 * r) * ld + a);
+                    yv[r] = *reinterpret_cast<const float4*>(sY + (tx + 16 * r) * ld + a);
+                }
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        s[r][c] += xv[r].x * yv[c].x + xv[r].y * yv[c].y + xv[r].z * yv[c].z + xv[r].w * yv[c].w;
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int i = ty + 16 * r, j = tx + 16 * c;
+                    const int late = R.reverse ? j : i, early = R.reverse ? i : j;
+                    const bool in = early <= late && early >= sLo[late];
+                    sP[i * (C + 1) + j] = in ? s[r][c] * expf(sG[late] - sG[early]) : 0.0f;
+                }
+        }
+        for (int e = tid; e < C * ZS; e += kThreads) sU[e] = sZ[e] * sUpd[e / ZS];
+        __syncthreads();
+        // out: thread (ty, tx) rows ty, ty+16, columns 2tx, 2tx+1
+        {
+            float o[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}}, q[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+            for (int a = 0; a < dxp; a += 4) {
+                const float4 x0 = *reinterpret_cast<const float4*>(sX + ty * ld + a);
+                const float4 x1 = *reinterpret_cast<const float4*>(sX + (ty + 16) * ld + a);
+                const float xs[2][4] = {{x0.x, x0.y, x0.z, x0.w}, {x1.x, x1.y, x1.z, x1.w}};
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const float2 st = *reinterpret_cast<const float2*>(sS + (a + u) * ZS + 2 * tx);
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        q[r][0] += xs[r][u] * st.x;
+                        q[r][1] += xs[r][u] * st.y;
+                    }
+                }
+            }
+#pragma unroll 4
+            for (int j = 0; j < C; ++j) {
+                const float2 zv = *reinterpret_cast<const float2*>(sZ + j * ZS + 2 * tx);
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float p = sP[(ty + 16 * r) * (C + 1) + j];
+                    o[r][0] += p * zv.x;
+                    o[r][1] += p * zv.y;
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int i = ty + 16 * r;
+                float dot = 0.0f;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float v = (o[r][c] + sRead[i] * q[r][c]) * R.out_scale;
+                    const int zc = 2 * tx + c;
+                    if (i < n && zc < nz) {
+                        const int64_t at = out_at + (t0 + i) * R.ot + zc;
+                        if (store_f32) static_cast<float*>(R.out)[at] = v;
+                        else static_cast<T*>(R.out)[at] = static_cast<T>(v);
+                        if (Wd != nullptr) dot += v * to_f32(Wd[(t0 + i) * R.w.st + zc]);
+                    }
+                }
+                if (dots != nullptr) {
+#pragma unroll
+                    for (int s = 8; s; s >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, s);
+                    if (tx == 0 && i < n) dots[t0 + i] = dot;
+                }
+            }
+        }
+        __syncthreads();
+        // the state: 4 x 4 tiles
+        const float decay = *sDecay;
+        for (int tile = tid; tile < (dxp / 4) * (ZS / 4); tile += kThreads) {
+            const int a = (tile / (ZS / 4)) * 4, c = (tile % (ZS / 4)) * 4;
+            float acc[4][4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float4 v = *reinterpret_cast<const float4*>(sS + (a + r) * ZS + c);
+                acc[r][0] = decay * v.x;
+                acc[r][1] = decay * v.y;
+                acc[r][2] = decay * v.z;
+                acc[r][3] = decay * v.w;
+            }
+#pragma unroll 4
+            for (int j = 0; j < C; ++j) {
+                const float4 yv = *reinterpret_cast<const float4*>(sY + j * ld + a);
+                const float4 uv = *reinterpret_cast<const float4*>(sU + j * ZS + c);
+                const float ya[4] = {yv.x, yv.y, yv.z, yv.w};
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    acc[r][0] += ya[r] * uv.x;
+                    acc[r][1] += ya[r] * uv.y;
+                    acc[r][2] += ya[r] * uv.z;
+                    acc[r][3] += ya[r] * uv.w;
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                *reinterpret_cast<float4*>(sS + (a + r) * ZS + c) = make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
+        }
+        if (R.anchors != nullptr && R.anchor_dots == nullptr && at_anchor) {
+            __syncthreads();
+            float* an = R.anchors + (bh * A.n_anchors + ci / A.anchor_every) * R.dx * static_cast<int64_t>(R.dz);
+            for (int e = tid; e < dx * ZS; e += kThreads) {
+                const int a = e / ZS, c = e % ZS;
+                if (c < nz) an[static_cast<int64_t>(a) * R.dz + z0 + c] = sS[e];
+            }
+        }
+    }
+    __syncthreads();
+    if (R.fin != nullptr)
+        for (int e = tid; e < dx * ZS; e += kThreads) {
+            const int a = e / ZS, c = e % ZS;
+            if (c < nz) R.fin[sbase + a * R.sa + (z0 + c) * R.sc] = sS[e] * R.fin_scale;
+        }
+}
+
+// One warp an anchor block: the block's tokens from its end in groups of 32,
+// each group summed from its end by shuffles and carried in f32.  Reads the
+// rows' dots once (4 bytes a token and slice), so it is a small fraction of
+// the runs before it.
+__global__ void __launch_bounds__(256) k_attn_decay_grad(const AttnDecayGrad G) {
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32;
+    const int lane = threadIdx.x % 32;
+    const int64_t BH = G.B * G.H;
+    if (unit >= BH * G.n) return;
+    const int64_t bh = unit / G.n, m = unit % G.n, b = bh / G.H;
+    const int h = static_cast<int>(bh % G.H);
+    int64_t len = G.T;
+    if (G.lengths != nullptr) {
+        const int64_t l = G.lengths[b];
+        len = l < 0 ? 0 : l < G.T ? l : G.T;
+    }
+    const int64_t lo = m * G.block, full = lo + G.block < G.T ? lo + G.block : G.T, hi = full < len ? full : len;
+    float carry = 0.0f, sum = 0.0f;
+    if (lo < hi)
+        for (int s = 0; s < G.slices_k; ++s) carry += G.ends[(s * BH + bh) * G.n + m];
+    for (int64_t top = hi; top > lo; top -= 32) {
+        const int64_t t = top - 32 + lane;
+        float v = 0.0f;
+        if (t >= lo) {
+            for (int s = 0; s < G.slices_q; ++s) v += G.dots_q[(s * BH + bh) * G.T + t];
+            for (int s = 0; s < G.slices_k; ++s) v -= G.dots_k[(s * BH + bh) * G.T + t];
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float q = __shfl_down_sync(0xffffffffu, v, o);
+            if (lane + o < 32) v += q;
+        }
+        v += carry;
+        if (t >= lo) {
+            if (G.grad != nullptr) G.grad[(b * G.T + t) * G.H + h] = v;
+            sum += v;
+        }
+        carry = __shfl_sync(0xffffffffu, v, 0);
+    }
+    if (G.grad != nullptr)
+        for (int64_t t = (hi > lo ? hi : lo) + lane; t < full; t += 32) G.grad[(b * G.T + t) * G.H + h] = 0.0f;
+    if (G.partial != nullptr) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) G.partial[h * (G.B * G.n) + b * G.n + m] = sum;
+    }
+}
+
+// [H, n] -> [H] in a fixed order (64-bit sums: a head's gradient adds every token of every row)
+__global__ void __launch_bounds__(256) k_attn_sum_rows(const float* __restrict__ part, int64_t n, float* __restrict__ out) {
+    __shared__ double s[8];
+    double v = 0.0;
+    for (int64_t i = threadIdx.x; i < n; i += 256) v += part[blockIdx.x * n + i];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (threadIdx.x % 32 == 0) s[threadIdx.x / 32] = v;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double all = 0.0;
+        for (int w = 0; w < 8; ++w) all += s[w];
+        out[blockIdx.x] = static_cast<float>(all);
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) k_attn_fold(const AttnFold F) {
+    const int64_t n = F.B * F.T * F.heads * static_cast<int64_t>(F.d);
+    for (int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; e < n; e += static_cast<int64_t>(gridDim.x) * 256) {
+        const int c = static_cast<int>(e % F.d);
+        const int j = static_cast<int>(e / F.d % F.heads);
+        const int64_t bt = e / F.d / F.heads;
+        const float* p = F.part + (bt * F.heads + j) * F.div * static_cast<int64_t>(F.d) + c;
+        float s = 0.0f;
+        for (int r = 0; r < F.div; ++r) s += p[static_cast<int64_t>(r) * F.d];
+        static_cast<T*>(F.out)[bt / F.T * F.ob + bt % F.T * F.ot + j * F.oh + c] = static_cast<T>(s);
+    }
+}
+
+size_t direct_smem(int dx) {
+    const size_t dxp = (dx + 3) & ~3;
+    return sizeof(float) * (2 * C * (dxp + 4) + dxp * ZS + 2 * C * ZS + C * (C + 1) + 4 * C + 4);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_direct(const AttnLaunch& L) {
+    DirectArgs A{};
+    int dx = 0, dz = 0;
+    for (int r = 0; r < L.runs; ++r) {
+        A.run[r] = L.run[r];
+        dx = L.run[r].dx > dx ? L.run[r].dx : dx;
+        dz = L.run[r].dz > dz ? L.run[r].dz : dz;
+    }
+    A.T = L.T;
+    A.H = L.H;
+    A.g = L.g;
+    A.gb = L.gb;
+    A.gt = L.gt;
+    A.gh = L.gh;
+    A.lengths = L.lengths;
+    A.anchor_every = L.anchor_every;
+    A.n_anchors = L.n_anchors;
+    A.BH = L.B * L.H;
+    const auto kernel = L.bf16 ? k_attn_direct<__nv_bfloat16> : k_attn_direct<float>;
+    const size_t smem = direct_smem(dx);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    const dim3 grid(static_cast<unsigned>(A.BH), (dz + ZS - 1) / ZS, L.runs);
+    kernel<<<grid, kThreads, smem, L.stream>>>(A);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_attn_decay_grad(const AttnDecayGrad& G, int* kernels) {
+    const int64_t units = G.B * G.H * G.n;
+    *kernels = 1;
+    k_attn_decay_grad<<<static_cast<unsigned>((units + 7) / 8), 256, 0, G.stream>>>(G);
+    if (G.grad_h != nullptr) {
+        k_attn_sum_rows<<<G.H, 256, 0, G.stream>>>(G.partial, G.B * G.n, G.grad_h);
+        ++*kernels;
+    }
+    return cudaGetLastError();
+}
+
+cudaError_t launch_attn_fold(const AttnFold& F) {
+    const int64_t n = F.B * F.T * F.heads * static_cast<int64_t>(F.d);
+    const unsigned blocks = static_cast<unsigned>((n + 255) / 256 < 152 * 16 ? (n + 255) / 256 : 152 * 16);
+    if (F.bf16) k_attn_fold<__nv_bfloat16><<<blocks, 256, 0, F.stream>>>(F);
+    else k_attn_fold<float><<<blocks, 256, 0, F.stream>>>(F);
+    return cudaGetLastError();
+}
+
+}  // namespace es

@@ -12,8 +12,9 @@
  *                axis; a sequence whose last width is 1 is a per-trip value
  *                broadcast over the whole state ("Arguments and body").
  *   precision    the recurrence computes in f32 ("Precision and gradients").
- * Layout: every array is dense, C-contiguous, row-major f32 ("lucid.tensor"
- * page, contiguity paragraph).
+ * Layout: every array of a scan is dense, C-contiguous, row-major f32
+ * ("lucid.tensor" page, contiguity paragraph).  The sequence-layer operators
+ * further down take strided views in f32 or bf16.
  *
  * All pointers passed to es_scan_f32 except `seqs`, `shape` and `seq_widths`
  * are DEVICE pointers owned by the caller; the library never frees or keeps
@@ -55,7 +56,7 @@ typedef enum es_body {
 typedef enum es_status {
     ES_OK = 0,
     ES_E_DIM_001 = 1,     /* shapes do not fit: axis, widths, T = 0, rank    */
-    ES_E_DIM_002 = 2,     /* dtype (reserved: only f32 entry points exist)   */
+    ES_E_DIM_002 = 2,     /* dtype: none the entry point takes               */
     ES_E_ARG = 3,         /* null / misaligned / overlapping pointer, bad id */
     ES_E_UNSUPPORTED = 4, /* valid on the pages but not in this library      */
     ES_E_CUDA = 5,        /* a CUDA runtime or driver call failed            */
@@ -79,7 +80,8 @@ typedef enum es_path {
     ES_PATH_VEC_TMA = 5,   /* vector state: TMA pipeline + xor shuffles        */
     ES_PATH_MAT_TMA = 6,   /* matrix-scan, dense operands: TMA pipeline        */
     ES_PATH_MAT_CHUNKED = 7, /* matrix-scan, few long lanes: chunked scan (3 kernels) */
-    ES_PATH_MAT_CHUNKED_TMA = 8 /* the same chunked scan, its scan passes on the TMA pipeline */
+    ES_PATH_MAT_CHUNKED_TMA = 8, /* the same chunked scan, its scan passes on the TMA pipeline */
+    ES_PATH_TENSOR = 9     /* linear attention on the tensor cores (tcgen05, TMA)  */
 } es_path;
 
 /*
@@ -619,6 +621,174 @@ es_status es_table_scan_i32(const int32_t *table, int64_t n_states, int64_t n_sy
 es_status es_plan_table_scan_i32(const int32_t *table, int64_t n_states, int64_t n_syms,
                                  const int32_t *symbols, const int64_t *shape, int rank, int axis,
                                  int32_t start, const int32_t *out, es_plan_info *info);
+
+/* ---------------------------------------------------------------------------
+ * Sequence-layer operators: linear attention with a decay for each head, and
+ * the norm of queries and keys with the position rotation.
+ *
+ * Their operands are views [B, T, heads, dim] with an innermost stride of 1
+ * and any other strides (in elements, not negative; an output's are not zero
+ * where its extent is above one), in f32 or bf16 (ES_F32, ES_BF16; every sum
+ * is f32).  Pointers are device pointers aligned to their elements; addresses
+ * and strides that keep to 16 bytes take the faster kernels.  All fields are
+ * 64 bits wide.  As everywhere here, calls are asynchronous on the caller's
+ * stream, allocate nothing, and refuse what does not fit with a status and a
+ * message. */
+typedef enum es_dtype {
+    ES_F32 = 0,
+    ES_BF16 = 1
+} es_dtype;
+
+typedef struct es_heads {
+    void *data;
+    int64_t stride_b, stride_t, stride_h;
+    int64_t heads;
+} es_heads;
+
+/*
+ * es_linear_attention -- for each batch row and head, with a state h of
+ * key_dim x value_dim values:
+ *
+ *     h[t] = exp(g[t]) * h[t-1] + k[t] v[t]^T        from h[-1] = initial
+ *     out[t] = scale * q[t] h[t]
+ *
+ *   dtype             of q, k, v, out (ES_F32 or ES_BF16; else ES_E_DIM_002).
+ *   batch, length     B, T >= 0; heads H: the heads of g, out and the states.
+ *   key_dim, value_dim   1..256.
+ *   q, k, v           [B, T, Hq, key_dim], [B, T, Hk, key_dim], [B, T, Hv,
+ *                     value_dim]; each number of heads divides H, and head h
+ *                     reads operand head h / (H / Hx).
+ *   log_decay         device f32 g: [B, T, H] by element strides, or [H] with
+ *                     decay_per_head = 1 (decay_b and decay_t unused); null:
+ *                     no decay.  Meant to be <= 0.  Below -104 (where e^g is
+ *                     zero in f32; -inf included) the token starts afresh.
+ *   lengths           device i32 [B], or null: tokens at and past a row's
+ *                     length (clamped to 0..T) are not read, their `out` is 0.
+ *   scale             finite, not zero.
+ *   initial_state     device f32 [B, H, key_dim, value_dim] dense, or null
+ *                     (zero); final_state the same, or null (not wanted); the
+ *                     state after each row's last token.  It may be
+ *                     initial_state itself.
+ *   out               [B, T, H, value_dim]; may not overlap an input.
+ *   workspace         es_linear_attention_workspace bytes, 16-byte aligned
+ *                     (may be null where that is 0).
+ * bf16 with widths of at most 128 that are multiples of 8, 16-byte addresses
+ * and strides: ES_PATH_TENSOR, chunks of tokens as products on the tensor
+ * cores; anything else ES_PATH_GENERIC, the same chunk form on the FMA units.
+ * In both the states, sums and decays are f32.
+ */
+typedef struct es_linear_attention_args {
+    int64_t dtype, batch, length, heads, key_dim, value_dim;
+    double scale;
+    es_heads q, k, v, out;
+    const float *log_decay;
+    int64_t decay_b, decay_t, decay_h, decay_per_head;
+    const int32_t *lengths;
+    const float *initial_state;
+    float *final_state;
+    void *workspace;
+    int64_t workspace_bytes;
+} es_linear_attention_args;
+
+es_status es_linear_attention(const es_linear_attention_args *args, es_stream_t stream);
+
+/*
+ * es_linear_attention_backward -- gradients of es_linear_attention: from
+ * grad_out [B, T, H, value_dim] and, where not null, grad_final_state
+ *     grad_q, grad_k, grad_v    of the operands' shapes (an operand head that
+ *                               several heads read gets their sum)
+ *     grad_log_decay            f32 [B, T, H] dense, or [H] with
+ *                               decay_per_head (summed over B and T); null:
+ *                               not wanted
+ *     grad_initial_state        or null
+ * args->out and args->final_state are not used.  Nothing of the forward call
+ * but its inputs is needed.  Gradients may overlap nothing else.  Padded tokens
+ * (lengths) get zeros.  Not differentiable again.
+ */
+typedef struct es_linear_attention_grads {
+    es_heads grad_out, grad_q, grad_k, grad_v;
+    const float *grad_final_state;
+    float *grad_log_decay;
+    float *grad_initial_state;
+} es_linear_attention_grads;
+
+es_status es_linear_attention_backward(const es_linear_attention_args *args,
+                                       const es_linear_attention_grads *grads, es_stream_t stream);
+
+/* Workspace bytes of a forward call (grads null) or a backward call. */
+es_status es_linear_attention_workspace(const es_linear_attention_args *args,
+                                        const es_linear_attention_grads *grads, size_t *bytes);
+
+/* Validate and plan a forward (grads null) or backward call without a GPU:
+ * O, T, J = B, T, H; W = key_dim * value_dim; elements of `out`. */
+es_status es_plan_linear_attention(const es_linear_attention_args *args,
+                                   const es_linear_attention_grads *grads, es_plan_info *info);
+
+/*
+ * es_linear_attention_step -- one token of each batch row (serving): the
+ * recurrence above for T = 1 with q, k, v [B, heads, dim] (stride_t unused),
+ * g [B, H] by (decay_b, decay_h) or [H].  initial_state is required;
+ * final_state receives the new state and may be initial_state itself.  length
+ * must be 1, lengths null; no workspace.
+ */
+es_status es_linear_attention_step(const es_linear_attention_args *args, es_stream_t stream);
+
+/*
+ * es_qk_norm_rotate -- for each head's row x of q and k:
+ *
+ *     n = x / sqrt(mean(x^2) + eps) * w
+ *     pairs (a, b) of n's first `turned` values become
+ *     (a cos - b sin, b cos + a sin), the angles those of the token's position
+ *
+ *   dtype             of q, k and the outputs; dim 1..256; turned even, 0..dim.
+ *   neighbours        0: value i < turned/2 pairs with value i + turned/2;
+ *                     1: values 2i and 2i+1 pair.
+ *   q, k              [B, T, heads, dim]; k.heads may be 0 (queries alone).
+ *   q_weight, k_weight  [dim] of weight_dtype, or null (ones).
+ *   cos, sin          device f32 [table_rows, turned/2], dense.
+ *   positions         [B, T] by element strides, i32 or (positions_64) i64, or
+ *                     null: token t is at position t.  Positions are clamped
+ *                     to the tables' rows.
+ *   q_out, k_out      of q's and k's shapes; each may be its own input (the
+ *                     same view), and may otherwise overlap no input.
+ *   eps               >= 0.
+ */
+typedef struct es_qk_norm_rotate_args {
+    int64_t dtype, weight_dtype, batch, length, dim, turned, neighbours;
+    double eps;
+    es_heads q, k, q_out, k_out;
+    const void *q_weight, *k_weight;
+    const float *cos, *sin;
+    int64_t table_rows;
+    const void *positions;
+    int64_t positions_64, position_b, position_t;
+    void *workspace;
+    int64_t workspace_bytes;
+} es_qk_norm_rotate_args;
+
+es_status es_qk_norm_rotate(const es_qk_norm_rotate_args *args, es_stream_t stream);
+
+/*
+ * es_qk_norm_rotate_backward -- gradients with respect to q, k and the
+ * weights (grad_q_weight, grad_k_weight: [dim] of weight_dtype, or null) from
+ * those of the outputs.  args->q_out and k_out receive the gradients of q and
+ * k (they may be grad_q_out / grad_k_out themselves).  The weights' sums are
+ * taken in a fixed order (the same bits each time) through the workspace.
+ */
+typedef struct es_qk_norm_rotate_grads {
+    es_heads grad_q_out, grad_k_out;
+    void *grad_q_weight, *grad_k_weight;
+} es_qk_norm_rotate_grads;
+
+es_status es_qk_norm_rotate_backward(const es_qk_norm_rotate_args *args,
+                                     const es_qk_norm_rotate_grads *grads, es_stream_t stream);
+
+es_status es_qk_norm_rotate_workspace(const es_qk_norm_rotate_args *args,
+                                      const es_qk_norm_rotate_grads *grads, size_t *bytes);
+
+/* Validate a forward (grads null) or backward call without a GPU. */
+es_status es_plan_qk_norm_rotate(const es_qk_norm_rotate_args *args,
+                                 const es_qk_norm_rotate_grads *grads, es_plan_info *info);
 
 /* Synchronise `stream`, then read and clear this device's status word.
  * Returns ES_E_TIMEOUT if a kernel since the last check gave up a bounded
