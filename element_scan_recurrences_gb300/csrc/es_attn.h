@@ -65,7 +65,7 @@ struct AttnLaunch {
     int64_t anchor_every;        // in chunks
     int64_t n_anchors;           // per (b, h)
     // segments of tokens (tensor-core path): see k_attn_tc.cu
-    int64_t seg_chunks;          // chunks a segment; 0: one segment
+    int64_t seg_chunks;          // chunks a segment
     int n_segs;
     float* seg_states;
     float* seg_decays;
@@ -83,6 +83,11 @@ constexpr int kAttnSlice = 32;
 constexpr int kAttnMaxDim = 256;
 
 cudaError_t launch_attn_direct(const AttnLaunch& L);
+
+// the tensor-core kernel: chunk of tokens, and whether it can load an operand
+constexpr int kAttnTcChunk = 64;
+bool attn_tc_operand_ok(const AttnOperand& o, int heads, int d, int64_t T, int64_t B);
+cudaError_t launch_attn_tc(const AttnLaunch& L, int* kernels, const char** err);
 
 // The decays' gradient from the two runs' dots: for each token t of anchor
 // block m, sum over s >= t of the block of (dq[s] - dk[s]) + e[m].

@@ -91,9 +91,27 @@ struct AttnPlan {
     int path;
     bool empty;
     // backward: byte offsets into the workspace
-    size_t dots_q, dots_k, anchors, ends, partial, fold_q, fold_k, fold_v, bytes;
+    size_t seg_states, seg_decays, dots_q, dots_k, anchors, ends, partial, fold_q, fold_k, fold_v, bytes;
     int slices_k, slices_v;      // slices of the runs that produce key- and value-wide outputs
 };
+
+// Tokens between the states the decays' gradient starts from: its sums of
+// differences run within such a block (see k_attn_decay_grad).
+constexpr int64_t kAnchorTokens = 256;
+
+// Segments a sequence is cut into (tensor-core path).  One CTA runs one (batch
+// row, head, run), one CTA an SM; with few of them the chunks are shared out
+// among more CTAs, which costs a pass over the keys and values for the states
+// between segments (about 0.6 of a main pass a chunk) and two launches (about 6
+// chunks' time).
+int segments(int64_t ctas, int64_t chunks, int64_t* seg_chunks) {
+    const int64_t most = 152 / ctas;
+    if (most < 2) return 1;
+    const int64_t each = (chunks + most - 1) / most;
+    if (16 * each + 60 >= 10 * chunks) return 1;
+    *seg_chunks = each;
+    return static_cast<int>((chunks + each - 1) / each);
+}
 
 size_t take(size_t* at, int64_t bytes) {
     const size_t here = *at;
@@ -246,18 +264,33 @@ es_status plan_attn(const char* fn, const es_linear_attention_args* a, const es_
         rv.fin = g->grad_initial_state;
         rv.fin_scale = scale;
     }
-    L.anchor_every = 16;
-    P->path = ES_PATH_GENERIC;
+    // the path: every run's operands have to suit the tensor-core kernel's loads
+    bool tensor = L.bf16 && T > 0 && !step;
+    for (int r = 0; r < L.runs && tensor; ++r) {
+        const AttnRun& u = L.run[r];
+        tensor = attn_tc_operand_ok(u.x, L.H / u.x.div, u.dx, T, B) && attn_tc_operand_ok(u.y, L.H / u.y.div, u.dx, T, B) &&
+                 attn_tc_operand_ok(u.z, L.H / u.z.div, u.dz, T, B);
+    }
     const int forced = api_path_override();
-    if (forced != ES_PATH_AUTO && forced != ES_PATH_GENERIC)
+    if (forced != ES_PATH_AUTO && forced != ES_PATH_GENERIC && !(forced == ES_PATH_TENSOR && tensor))
         return api_fail(ES_E_UNSUPPORTED, "%s: the forced kernel path %d cannot serve this call", fn, forced);
+    P->path = tensor && forced != ES_PATH_GENERIC ? ES_PATH_TENSOR : ES_PATH_GENERIC;
 
     // workspace
-    const int64_t chunk = kAttnChunk;
-    L.n_anchors = (T + L.anchor_every * chunk - 1) / (L.anchor_every * chunk);
+    const int64_t chunk = P->path == ES_PATH_TENSOR ? kAttnTcChunk : kAttnChunk;
+    L.anchor_every = kAnchorTokens / chunk;
+    L.n_anchors = (T + kAnchorTokens - 1) / kAnchorTokens;
+    L.n_segs = 1;
+    const int64_t chunks = (T + chunk - 1) / chunk;
+    L.seg_chunks = chunks > 0 ? chunks : 1;
+    if (P->path == ES_PATH_TENSOR) L.n_segs = segments(bh * L.runs, chunks, &L.seg_chunks);
     P->slices_k = static_cast<int>((dk + kAttnSlice - 1) / kAttnSlice);
     P->slices_v = static_cast<int>((dv + kAttnSlice - 1) / kAttnSlice);
     size_t at = 0;
+    if (L.n_segs > 1) {
+        P->seg_states = take(&at, 4 * L.runs * bh * L.n_segs * dk * dv);
+        P->seg_decays = take(&at, 4 * bh * L.n_segs);
+    }
     if (backward && T > 0) {
         if (g->grad_log_decay != nullptr) {
             P->dots_q = take(&at, 4 * P->slices_k * bh * T);
@@ -310,6 +343,28 @@ void fill_info(es_plan_info* info, int64_t O, int64_t T, int64_t J, int64_t W, i
     info->path = path;
 }
 
+// one launch of P's path over `runs` of L
+es_status launch_runs(const char* fn, const AttnPlan& P, AttnLaunch L, void* workspace) {
+    cudaError_t e;
+    if (P.path == ES_PATH_TENSOR) {
+        es_status st = api_encoder(&L.encode);
+        if (st != ES_OK) return st;
+        if (L.n_segs > 1) {
+            L.seg_states = reinterpret_cast<float*>(static_cast<char*>(workspace) + P.seg_states);
+            L.seg_decays = reinterpret_cast<float*>(static_cast<char*>(workspace) + P.seg_decays);
+        }
+        int n = 0;
+        const char* msg = nullptr;
+        e = launch_attn_tc(L, &n, &msg);
+        if (msg != nullptr) return api_fail(ES_E_CUDA, "%s: %s", fn, msg);
+        count_launch(n);
+    } else {
+        e = launch_attn_direct(L);
+        count_launch();
+    }
+    return e == cudaSuccess ? ES_OK : cuda_fail(fn, e);
+}
+
 es_status run_backward(const char* fn, const es_linear_attention_args* a, const es_linear_attention_grads* g, AttnPlan& P) {
     AttnLaunch& L = P.L;
     char* ws = static_cast<char*>(a->workspace);
@@ -347,11 +402,11 @@ es_status run_backward(const char* fn, const es_linear_attention_args* a, const 
         // the keys' run reads the states that the queries' run leaves
         AttnLaunch first = L;
         first.runs = 2;
-        if ((e = launch_attn_direct(first)) != cudaSuccess) return cuda_fail(fn, e);
+        es_status st = launch_runs(fn, P, first, a->workspace);
+        if (st != ES_OK) return st;
         first.run[0] = rk;
         first.runs = 1;
-        if ((e = launch_attn_direct(first)) != cudaSuccess) return cuda_fail(fn, e);
-        count_launch(2);
+        if ((st = launch_runs(fn, P, first, a->workspace)) != ES_OK) return st;
         AttnDecayGrad D{};
         D.dots_q = rq.dots;
         D.dots_k = rk.dots;
@@ -361,7 +416,7 @@ es_status run_backward(const char* fn, const es_linear_attention_args* a, const 
         D.T = L.T;
         D.H = L.H;
         D.lengths = L.lengths;
-        D.block = L.anchor_every * kAttnChunk;
+        D.block = kAnchorTokens;
         D.n = L.n_anchors;
         D.stream = L.stream;
         if (a->decay_per_head) {
@@ -374,8 +429,8 @@ es_status run_backward(const char* fn, const es_linear_attention_args* a, const 
         if ((e = launch_attn_decay_grad(D, &n)) != cudaSuccess) return cuda_fail(fn, e);
         count_launch(n);
     } else {
-        if ((e = launch_attn_direct(L)) != cudaSuccess) return cuda_fail(fn, e);
-        count_launch();
+        const es_status st = launch_runs(fn, P, L, a->workspace);
+        if (st != ES_OK) return st;
         if (g->grad_log_decay != nullptr && a->decay_per_head &&
             (e = cudaMemsetAsync(g->grad_log_decay, 0, H * 4, L.stream)) != cudaSuccess)
             return cuda_fail(fn, e);      // no tokens: a sum of nothing
@@ -562,10 +617,7 @@ es_status es_linear_attention(const es_linear_attention_args* args, es_stream_t 
     if (st != ES_OK || P.empty) return st;
     if ((st = es::check_workspace(fn, args->workspace, args->workspace_bytes, P.bytes)) != ES_OK) return st;
     if ((st = es::device_of(fn, &P.L, stream)) != ES_OK) return st;
-    const cudaError_t e = es::launch_attn_direct(P.L);
-    if (e != cudaSuccess) return es::cuda_fail(fn, e);
-    es::count_launch();
-    return ES_OK;
+    return es::launch_runs(fn, P, P.L, args->workspace);
 }
 
 es_status es_linear_attention_backward(const es_linear_attention_args* args, const es_linear_attention_grads* grads,

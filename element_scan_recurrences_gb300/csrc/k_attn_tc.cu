@@ -1,0 +1,870 @@
+// k_attn_tc.cu -- linear attention in chunks of 64 tokens on the tensor cores.
+//
+// One CTA takes one (batch row, head), or a segment of its tokens, through the
+// chunks in order; its 20 warps are a pipeline of roles linked by mbarriers:
+//
+//     warp 2       TMA loads of the operands' tiles (X, Y, Z, and W for the
+//                  decays' gradient), 128-byte swizzled panels of 64 values
+//     warp 7       hands a loaded stage on; in a row's last, ragged chunk it
+//                  first clears the rows of Y and Z past the length
+//     warp 6       the chunk's decays: G, the coefficients of read and update
+//     warp 3       issues every product (tcgen05.mma, one thread)
+//     warps 0,1,4,5  scores -> P: mask and decay, split into bf16 terms, to
+//                  shared memory
+//     warps 8-11   Z scaled by its update coefficients and transposed into
+//                  tensor memory, three bf16 terms
+//     warps 12-15  the state: f32 in tensor memory, decayed once a chunk, and
+//                  its two bf16 terms for the read
+//     warps 16-19  the outputs: read, joined, rounded once, stored
+//
+// The state lies transposed, a value column a lane and a key column a column,
+// so that everything made from it or for it is the A operand, read from tensor
+// memory, and X, Y and Z are used where TMA put them:
+//
+//     S[i, j]    = X Y^T              both K innermost; 128 rows asked of which
+//                                     the chunk's 64 are used
+//     H^T[c, a] += Z'^T Y             A = the scaled Z (tensor memory), B = Y
+//                                     rows innermost
+//     O2^T[c, i] = H^T X^T            A = the state's terms, B = X
+//     O1^T[c, i] = Z^T P^T            A = Z rows innermost, B = P
+//     out_i      = scale (O1_i + read_i O2_i)
+//
+// Precision: bf16 operands go in as they are.  Every f32 factor is split into
+// bf16 terms that are multiplied in turn and summed in f32: P and the state as
+// read in two (2^-16 of each factor, below the result's own rounding; the
+// decays' gradient takes differences of these results, which one term would
+// spoil), Z' in three (2^-24: the state is an f32 result).
+//
+// Every wait is bounded: a role that gives up sets the status word and the
+// abort flag, all roles leave their loops, copies and products in flight are
+// waited for (bounded too), and tensor memory is freed.
+#include "es_attn.h"
+#include "es_device.cuh"
+#include "es_tcgen05.cuh"
+
+namespace es {
+namespace {
+
+constexpr int C = kAttnTcChunk;               // 64 tokens
+constexpr int kThreads = 640;
+constexpr int kCoefs = 4;                     // slots of chunk coefficients
+constexpr int kMaxStages = 4;
+constexpr uint32_t kPanel = C * 128;          // bytes of a panel: 64 rows of 64 bf16
+constexpr uint32_t kTmemCols = 512;
+
+struct alignas(16) Coef {
+    float g2[C];                              // inclusive sums of the log decays, base 2
+    float read[C], upd[C];
+    int bound[C];                             // forward: the first token row i sees; reversed: the last
+    float decay;
+    float pad[3];
+};
+
+struct TcRun {
+    CUtensorMap x, y, z, w;
+    void* out;
+    int64_t ob, ot, oh;
+    const float* init;
+    float* fin;
+    int64_t sa, sc;
+    float init_scale, fin_scale, out_scale;
+    float* dots;
+    float* anchors;
+    float* anchor_dots;
+    int xdiv, ydiv, zdiv, wdiv;
+    int xb, yb, zb, wb;                       // 1; 0: one batch row for all
+    int dx, dz;                               // real widths
+    int reverse, out_f32;
+};
+
+struct TcArgs {
+    TcRun run[3];
+    int64_t T, BH;
+    int H;
+    int n_segs, seg_chunks;
+    const float* g;
+    int64_t gb, gt, gh;
+    const int* lengths;
+    int64_t anchor_every, n_anchors;
+    float* seg_states;                        // [runs][BH][n_segs][dx * dz] states entering each segment's successor
+    float* seg_decays;                        // [BH][n_segs]
+    int64_t seg_stride;                       // floats of one run's seg_states
+    unsigned int* status;
+    uint64_t wait_ns;
+    int64_t drop_tile;
+    int stages;
+    uint32_t stage_bytes;
+};
+
+struct Shared {
+    uint64_t full[kMaxStages], ready[kMaxStages], empty[kMaxStages];
+    uint64_t coef_full[kCoefs], coef_empty[kCoefs];
+    uint64_t s_done, p_ready, zt_ready, h_ready, kv_done, o_done, o_read, drained;
+    uint32_t tmem;
+    int abort_flag;
+    Coef coef[kCoefs];
+};
+
+struct Wait {
+    uint64_t ns;
+    volatile int* flag;
+    unsigned int* status;
+    // the whole warp waits; false: leave the loop
+    __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
+        const bool ok = mbar_wait_bounded(bar, parity & 1, ns, flag);
+        if (__all_sync(0xffffffffu, ok)) return true;
+        if (!ok && !*flag) report_timeout(status, flag);
+        return false;
+    }
+};
+
+__device__ __forceinline__ void arrive_warp(uint64_t* bar, int lane) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+}
+
+// two bf16 terms of pairs of values
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+    hi = tc::pack_bf16(a, b);
+    lo = tc::pack_bf16(a - tc::low_bf16(hi), b - tc::high_bf16(hi));
+}
+
+__device__ __forceinline__ void split3(float a, float b, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+    hi = tc::pack_bf16(a, b);
+    const float ra = a - tc::low_bf16(hi), rb = b - tc::high_bf16(hi);
+    mid = tc::pack_bf16(ra, rb);
+    lo = tc::pack_bf16(ra - tc::low_bf16(mid), rb - tc::high_bf16(mid));
+}
+
+// kStateOnly: a segment's own state and decay, from zero (the first segment's
+// from the call's initial state): only Y and Z are read.
+template <bool kStateOnly>
+__global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__ TcArgs A) {
+    extern __shared__ __align__(1024) unsigned char raw[];
+    __shared__ Shared sh;
+    unsigned char* tiles = raw + smem_align_pad(raw);
+    const TcRun& R = A.run[blockIdx.y];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int64_t bh = blockIdx.x / A.n_segs;
+    const int seg = static_cast<int>(blockIdx.x % A.n_segs);
+    const int b = static_cast<int>(bh / A.H), h = static_cast<int>(bh % A.H);
+    int64_t len = A.T;
+    if (A.lengths != nullptr) {
+        const int64_t l = A.lengths[b];
+        len = l < 0 ? 0 : l < A.T ? l : A.T;
+    }
+    // the segment's chunks [c0, c1) and whether they begin or end the run
+    const int chunks = static_cast<int>((len + C - 1) / C);
+    const int c0 = seg * A.seg_chunks;
+    const int c1 = min(chunks, c0 + A.seg_chunks);
+    const int last_seg = chunks > 0 ? (chunks - 1) / A.seg_chunks : 0;
+    const int n = max(0, c1 - c0);
+    const bool begins = R.reverse ? seg == last_seg : seg == 0;
+    const bool ends = R.reverse ? seg == 0 : seg == last_seg;
+    if constexpr (kStateOnly) {
+        if (seg > last_seg) return;
+        if (ends) {
+            // No successor: its place keeps the initial state, which the main pass may find overwritten
+            // (the last state may take its place) before its first segment reads it.
+            if (R.init != nullptr) {
+                const int64_t size = static_cast<int64_t>(R.dx) * R.dz;
+                float* to = A.seg_states + blockIdx.y * A.seg_stride + (bh * A.n_segs + seg) * size;
+                for (int64_t e = threadIdx.x; e < size; e += kThreads)
+                    to[e] = R.init[bh * size + e / R.dz * R.sa + e % R.dz * R.sc] * R.init_scale;
+            }
+            return;
+        }
+    }
+    const int dxp = (R.dx + 63) & ~63, dzp = (R.dz + 63) & ~63;
+    const int px = dxp / 64, pz = dzp / 64;
+    const bool dots = !kStateOnly && R.dots != nullptr;
+
+    // a stage: X, Y, Z, W
+    const uint32_t off_y = kStateOnly ? 0 : px * kPanel, off_z = off_y + px * kPanel, off_w = off_z + pz * kPanel;
+    unsigned char* p_hi = tiles + A.stages * A.stage_bytes;
+    unsigned char* p_lo = p_hi + kPanel;
+
+    if (warp == 2) tc::alloc(&sh.tmem, kTmemCols);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < A.stages; ++s) {
+            mbar_init(&sh.full[s], 1);
+            mbar_init(&sh.ready[s], 1);
+            mbar_init(&sh.empty[s], 1 + 4 + (dots ? 4 : 0));
+        }
+        for (int s = 0; s < kCoefs; ++s) {
+            mbar_init(&sh.coef_full[s], 1);
+            mbar_init(&sh.coef_empty[s], kStateOnly ? 8 : 16);
+        }
+        mbar_init(&sh.s_done, 1);
+        mbar_init(&sh.p_ready, 4);
+        mbar_init(&sh.zt_ready, 4);
+        mbar_init(&sh.h_ready, 4);
+        mbar_init(&sh.kv_done, 1);
+        mbar_init(&sh.o_done, 1);
+        mbar_init(&sh.o_read, 4);
+        mbar_init(&sh.drained, 1);
+        sh.abort_flag = 0;
+        mbar_fence_init();
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = *static_cast<volatile uint32_t*>(&sh.tmem);
+    const uint32_t t_h = tmem, t_hb = t_h + dxp, t_zt = t_hb + dxp, t_s = t_zt + 96, t_o2 = t_s + C;
+    const Wait wait{A.wait_ns, &sh.abort_flag, A.status};
+    auto chunk_of = [&](int k) { return R.reverse ? c1 - 1 - k : c0 + k; };
+
+    if (warp == 2) {
+        // ---- loads
+        if (lane == 0) {
+            const uint64_t pol = l2_policy_stream();
+            int issued = 0;
+            for (int k = 0; k < n; ++k) {
+                const int s = k % A.stages, round = k / A.stages;
+                if (round > 0 && !mbar_wait_bounded(&sh.empty[s], (round - 1) & 1, A.wait_ns, &sh.abort_flag)) {
+                    report_timeout(A.status, &sh.abort_flag);
+                    break;
+                }
+                issued = k + 1;
+                if (k == A.drop_tile) continue;      // testing hook: this tile never arrives
+                unsigned char* st = tiles + s * A.stage_bytes;
+                const int t0 = chunk_of(k) * C;
+                mbar_arrive_expect_tx(&sh.full[s], (kStateOnly ? 0 : px * kPanel) + (px + pz + (dots ? pz : 0)) * kPanel);
+                for (int p = 0; p < px; ++p) {
+                    if constexpr (!kStateOnly) tma_load_4d(st + p * kPanel, &R.x, p * 64, h / R.xdiv, t0, b * R.xb, &sh.full[s], pol);
+                    tma_load_4d(st + off_y + p * kPanel, &R.y, p * 64, h / R.ydiv, t0, b * R.yb, &sh.full[s], pol);
+                }
+                for (int p = 0; p < pz; ++p) {
+                    tma_load_4d(st + off_z + p * kPanel, &R.z, p * 64, h / R.zdiv, t0, b * R.zb, &sh.full[s], pol);
+                    if (dots) tma_load_4d(st + off_w + p * kPanel, &R.w, p * 64, h / R.wdiv, t0, b * R.wb, &sh.full[s], pol);
+                }
+            }
+            for (int k = max(0, issued - A.stages); k < issued; ++k) {
+                if (k == A.drop_tile) continue;
+                if (!mbar_wait_bounded(&sh.full[k % A.stages], (k / A.stages) & 1, A.wait_ns, nullptr))
+                    atomicOr(A.status, ES_DEVICE_TIMEOUT);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 7) {
+        // ---- hand the stages on
+        for (int k = 0; k < n; ++k) {
+            const int s = k % A.stages;
+            if (!wait(&sh.full[s], k / A.stages)) break;
+            const int left = static_cast<int>(min(static_cast<int64_t>(C), len - static_cast<int64_t>(chunk_of(k)) * C));
+            if (left < C) {
+                // rows past the length may hold anything (a NaN times a zero of P is a NaN): cleared
+                unsigned char* st = tiles + s * A.stage_bytes;
+                const int rows = C - left;
+                for (int p = 0; p < px + pz; ++p) {
+                    uint4* panel = reinterpret_cast<uint4*>(st + off_y + p * kPanel + left * 128);
+                    for (int e = lane; e < rows * 8; e += 32) panel[e] = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+            }
+            arrive_warp(&sh.ready[s], lane);
+        }
+    } else if (warp == 6) {
+        // ---- the chunks' decays, tokens lane and lane + 32
+        const float* G = A.g != nullptr ? A.g + b * A.gb + h * A.gh : nullptr;
+        auto load = [&](int k, float (&g)[2]) {
+            g[0] = g[1] = 0.0f;
+            if (G == nullptr || k >= n) return;
+            const int64_t t0 = static_cast<int64_t>(chunk_of(k)) * C;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                if (t0 + lane + 32 * u < len) g[u] = __ldg(G + (t0 + lane + 32 * u) * A.gt);
+        };
+        float g[2], next[2];
+        float all = 1.0f;
+        load(0, g);
+        for (int k = 0; k < n; ++k) {
+            load(k + 1, next);
+            const bool cut0 = g[0] < -104.0f, cut1 = g[1] < -104.0f;
+            const uint64_t cuts = static_cast<uint64_t>(__ballot_sync(0xffffffffu, cut0)) |
+                                  (static_cast<uint64_t>(__ballot_sync(0xffffffffu, cut1)) << 32);
+            float pre[2], suf[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const float v = (u ? cut1 : cut0) ? 0.0f : g[u] * 1.4426950408889634f;
+                pre[u] = v;
+                suf[u] = __shfl_down_sync(0xffffffffu, v, 1);
+                if (lane == 31) suf[u] = 0.0f;
+                if (u == 1) {
+                    // token 32 follows token 31
+                    const float first = __shfl_sync(0xffffffffu, v, 0);
+                    if (lane == 31) suf[0] = first;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const float p = __shfl_up_sync(0xffffffffu, pre[u], o);
+                    const float q = __shfl_down_sync(0xffffffffu, suf[u], o);
+                    if (lane >= o) pre[u] += p;
+                    if (lane + o < 32) suf[u] += q;
+                }
+            pre[1] += __shfl_sync(0xffffffffu, pre[0], 31);
+            suf[0] += __shfl_sync(0xffffffffu, suf[1], 0);
+            const int s = k % kCoefs;
+            if (k >= kCoefs && !wait(&sh.coef_empty[s], k / kCoefs - 1)) break;
+            Coef& c = sh.coef[s];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int t = lane + 32 * u;
+                const uint64_t upto = cuts & (~0ull >> (63 - t));
+                const uint64_t after = t == 63 ? 0ull : cuts >> (t + 1);
+                const float er = upto ? 0.0f : exp2f(pre[u]), eu = after ? 0.0f : exp2f(suf[u]);
+                c.g2[t] = pre[u];
+                c.read[t] = R.reverse ? eu : er;
+                c.upd[t] = R.reverse ? er : eu;
+                c.bound[t] = R.reverse ? (after ? t + __ffsll(static_cast<long long>(after)) - 1 : 63)
+                                       : (upto ? 63 - __clzll(static_cast<long long>(upto)) : 0);
+            }
+            const float whole = cuts ? 0.0f : exp2f(__shfl_sync(0xffffffffu, pre[1], 31));
+            if (lane == 0) c.decay = whole;
+            all *= whole;
+            arrive_warp(&sh.coef_full[s], lane);
+            g[0] = next[0];
+            g[1] = next[1];
+        }
+        if constexpr (kStateOnly) {
+            if (lane == 0 && blockIdx.y == 0) A.seg_decays[bh * A.n_segs + seg] = all;
+        }
+    } else if (warp == 3) {
+        // ---- products
+        const uint32_t i_s = tc::instr_bf16(C, false, false), i_o1 = tc::instr_bf16(C, true, false);
+        const uint32_t i_kv = tc::instr_bf16(static_cast<uint32_t>(dxp), false, true);
+        const uint32_t base = smem_u32(tiles);
+        bool ok = true;
+        for (int k = 0; k < n && ok; ++k) {
+            const int s = k % A.stages;
+            const uint32_t sx = base + s * A.stage_bytes, sy = sx + off_y, sz = sx + off_z;
+            ok = wait(&sh.ready[s], k / A.stages);
+            if constexpr (!kStateOnly) {
+                // the region of the scores holds the last chunk's O1 until it is read
+                if (ok && k > 0) ok = wait(&sh.o_read, k - 1);
+                if (!ok) break;
+                tc::fence_after();
+                if (lane == 0) {
+                    for (int q = 0; q < dxp / 16; ++q) {
+                        const uint32_t at = (q / 4) * kPanel + (q % 4) * 32;
+                        tc::mma_ss(t_s, tc::smem_desc(sx + at, 16, 1024), tc::smem_desc(sy + at, 16, 1024), i_s, q > 0);
+                    }
+                    tc::commit(&sh.s_done);
+                }
+                __syncwarp();
+            }
+            if (!ok || !(ok = wait(&sh.h_ready, k))) break;
+            if constexpr (!kStateOnly) {
+                tc::fence_after();
+                if (lane == 0)
+                    for (int m = 0; m < 2; ++m)
+                        for (int q = 0; q < dxp / 16; ++q)
+                            tc::mma_ts(t_o2, t_hb + m * (dxp / 2) + q * 8,
+                                       tc::smem_desc(sx + (q / 4) * kPanel + (q % 4) * 32, 16, 1024), i_s, m + q > 0);
+                __syncwarp();
+            }
+            if (!(ok = wait(&sh.zt_ready, k))) break;
+            tc::fence_after();
+            if (lane == 0) {
+                for (int m = 0; m < 3; ++m)
+                    for (int q = 0; q < C / 16; ++q)
+                        tc::mma_ts(t_h, t_zt + m * (C / 2) + q * 8, tc::smem_desc(sy + q * 2048, kPanel, 1024), i_kv, true);
+                tc::commit(&sh.kv_done);
+            }
+            __syncwarp();
+            if constexpr (!kStateOnly) {
+                if (!(ok = wait(&sh.p_ready, k))) break;
+                tc::fence_after();
+                if (lane == 0) {
+                    for (int m = 0; m < 2; ++m)
+                        for (int q = 0; q < C / 16; ++q)
+                            tc::mma_ss(t_s, tc::smem_desc(sz + q * 2048, kPanel, 1024),
+                                       tc::smem_desc(smem_u32(m ? p_lo : p_hi) + q * 32, 16, 1024), i_o1, m + q > 0);
+                    tc::commit(&sh.o_done);
+                }
+            }
+            if (lane == 0) tc::commit(&sh.empty[s]);
+            __syncwarp();
+        }
+        // nothing of this CTA's may still run when its tensor memory goes
+        if (lane == 0) tc::commit(&sh.drained);
+        __syncwarp();
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&sh.drained, 0, A.wait_ns, nullptr)) && lane == 0)
+            atomicOr(A.status, ES_DEVICE_TIMEOUT);
+    } else if (warp < 8) {
+        // ---- P: row i, 32 columns
+        if constexpr (!kStateOnly) {
+            const int i = lane + 32 * (warp & 1), half = warp >> 2;
+            const uint32_t from = t_s + (static_cast<uint32_t>(32 * (warp & 1)) << 16) + 32 * half;
+            // rows of one half never see the columns of the other: forward rows 0-31 the late columns
+            const bool none = R.reverse ? (warp & 1) > half : (warp & 1) < half;
+            for (int k = 0; k < n; ++k) {
+                const int cs = k % kCoefs;
+                if (!wait(&sh.coef_full[cs], k / kCoefs) || !wait(&sh.s_done, k)) break;
+                const Coef& c = sh.coef[cs];
+                uint4 hi[4], lo[4];
+                if (none) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) hi[q] = lo[q] = make_uint4(0, 0, 0, 0);
+                } else {
+                    tc::fence_after();
+                    uint32_t r[32];
+                    tc::ld32(from, r);
+                    const float gi = c.g2[i];
+                    const int bound = c.bound[i];
+                    const int first = R.reverse ? i : bound, last = R.reverse ? bound : i;
+                    const float sign = R.reverse ? -1.0f : 1.0f;
+                    tc::wait_ld();
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t ph[4], pl[4];
+#pragma unroll
+                        for (int u = 0; u < 4; u += 2) {
+                            const float4 gj = *reinterpret_cast<const float4*>(&c.g2[32 * half + 8 * q + 2 * u]);
+                            const float gv[4] = {gj.x, gj.y, gj.z, gj.w};
+                            float v[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int j = 32 * half + 8 * q + 2 * u + e;
+                                const float d = tc::exp2_approx(sign * (gi - gv[e]));
+                                v[e] = (j >= first && j <= last) ? __uint_as_float(r[8 * q + 2 * u + e]) * d : 0.0f;
+                            }
+                            split2(v[0], v[1], ph[u], pl[u]);
+                            split2(v[2], v[3], ph[u + 1], pl[u + 1]);
+                        }
+                        hi[q] = make_uint4(ph[0], ph[1], ph[2], ph[3]);
+                        lo[q] = make_uint4(pl[0], pl[1], pl[2], pl[3]);
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t at = i * 128 + (((4 * half + q) ^ (i & 7)) << 4);
+                    *reinterpret_cast<uint4*>(p_hi + at) = hi[q];
+                    *reinterpret_cast<uint4*>(p_lo + at) = lo[q];
+                }
+                fence_proxy_async_smem();
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&sh.p_ready);
+                    mbar_arrive(&sh.coef_empty[cs]);
+                }
+            }
+        }
+    } else if (warp < 12) {
+        // ---- Z scaled and transposed: lane = value column, token pairs along the columns
+        const int c = (warp - 8) * 32 + lane;
+        const uint32_t to = t_zt + (static_cast<uint32_t>((warp - 8) * 32) << 16);
+        const bool on = (warp - 8) * 32 < R.dz;
+        uint32_t off[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) off[u] = (c / 64) * kPanel + ((((c % 64) >> 3) ^ u) << 4) + (c & 7) * 2 + u * 128;
+        for (int k = 0; k < n; ++k) {
+            const int s = k % A.stages, cs = k % kCoefs;
+            if (!wait(&sh.coef_full[cs], k / kCoefs) || !wait(&sh.ready[s], k / A.stages)) break;
+            if (k > 0 && !wait(&sh.kv_done, k - 1)) break;
+            tc::fence_after();
+            if (on) {
+                const unsigned char* z = tiles + s * A.stage_bytes + off_z;
+                const Coef& cf = sh.coef[cs];
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t t0[16], t1[16], t2[16];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const float4 w = *reinterpret_cast<const float4*>(&cf.upd[32 * half + 4 * q]);
+                        const float wv[4] = {w.x, w.y, w.z, w.w};
+                        float v[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int j = 32 * half + 4 * q + e;
+                            const uint32_t raw16 = *reinterpret_cast<const unsigned short*>(z + (j / 8) * 1024 + off[j % 8]);
+                            v[e] = __uint_as_float(raw16 << 16) * wv[e];
+                        }
+                        split3(v[0], v[1], t0[2 * q], t1[2 * q], t2[2 * q]);
+                        split3(v[2], v[3], t0[2 * q + 1], t1[2 * q + 1], t2[2 * q + 1]);
+                    }
+                    tc::st16(to + 16 * half, t0);
+                    tc::st16(to + 32 + 16 * half, t1);
+                    tc::st16(to + 64 + 16 * half, t2);
+                }
+                tc::wait_st();
+            }
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&sh.zt_ready);
+                mbar_arrive(&sh.empty[s]);
+                mbar_arrive(&sh.coef_empty[cs]);
+            }
+        }
+    } else if (warp < 16) {
+        // ---- the state: lane = value column c, key columns along
+        const int c = (warp - 12) * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>((warp - 12) * 32) << 16;
+        const bool on = (warp - 12) * 32 < R.dz, real = c < R.dz;
+        const int64_t size = static_cast<int64_t>(R.dx) * R.dz;
+        // where the run's first state comes from
+        const float* from = nullptr;
+        int64_t fa = 0;
+        float fs = 1.0f;
+        if (real) {
+            if (begins && !kStateOnly && A.n_segs > 1) {
+                if (R.init != nullptr)
+                    from = A.seg_states + blockIdx.y * A.seg_stride + (bh * A.n_segs + (R.reverse ? 0 : last_seg)) * size + c;
+                fa = R.dz;
+            } else if (begins) {
+                if (R.init != nullptr) from = R.init + bh * size + c * R.sc;
+                fa = R.sa;
+                fs = R.init_scale;
+            } else if (!kStateOnly) {
+                const int prev = R.reverse ? seg + 1 : seg - 1;
+                from = A.seg_states + blockIdx.y * A.seg_stride + (bh * A.n_segs + prev) * size + c;
+                fa = R.dz;
+            }
+        }
+        const int slice = warp - 12;
+        bool ok = true;
+        // n + 1 visits: the last one only takes the final state out
+        for (int k = 0; k <= n && ok; ++k) {
+            const int cs = k % kCoefs;
+            if (k > 0) {
+                ok = wait(&sh.kv_done, k - 1);
+                if (!ok) break;
+                tc::fence_after();
+            }
+            float decay = 0.0f;
+            if (k < n) {
+                if (!(ok = wait(&sh.coef_full[cs], k / kCoefs))) break;
+                decay = sh.coef[cs].decay;
+            }
+            // the state between trip k - 1 and trip k is an anchor's
+            const int done = k > 0 ? chunk_of(k - 1) : 0, next = k < n ? chunk_of(k) : 0;
+            float* dump = nullptr;
+            const float* anchor = nullptr;
+            float* anchor_to = nullptr;
+            if (!kStateOnly && on && R.anchors != nullptr) {
+                if (R.anchor_dots == nullptr) {
+                    if (k > 0 && ((done + 1) % A.anchor_every == 0 || done == chunks - 1))
+                        dump = R.anchors + (bh * A.n_anchors + done / A.anchor_every) * size + c;
+                } else if (k < n && ((next + 1) % A.anchor_every == 0 || next == chunks - 1)) {
+                    anchor = R.anchors + (bh * A.n_anchors + next / A.anchor_every) * size + c;
+                    anchor_to = R.anchor_dots + (slice * A.BH + bh) * A.n_anchors + next / A.anchor_every;
+                }
+            }
+            float* out = nullptr;
+            int64_t oa = 0;
+            float os = 1.0f;
+            if (k == n && real) {
+                if (kStateOnly) {
+                    out = A.seg_states + blockIdx.y * A.seg_stride + (bh * A.n_segs + seg) * size + c;
+                    oa = R.dz;
+                } else if (ends && R.fin != nullptr) {
+                    out = R.fin + bh * size + c * R.sc;
+                    oa = R.sa;
+                    os = R.fin_scale;
+                }
+            }
+            float dot = 0.0f;
+            const bool leaves = __any_sync(0xffffffffu, out != nullptr || dump != nullptr);
+            if (on && (k < n || leaves))
+                for (int a0 = 0; a0 < dxp; a0 += 32) {
+                    uint32_t r[32];
+                    if (k == 0) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            r[e] = __float_as_uint(from != nullptr && a0 + e < R.dx ? from[(a0 + e) * fa] * fs : 0.0f);
+                    } else {
+                        tc::ld32(t_h + lanes + a0, r);
+                        tc::wait_ld();
+                    }
+                    if (dump != nullptr && real) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (a0 + e < R.dx) dump[static_cast<int64_t>(a0 + e) * R.dz] = __uint_as_float(r[e]);
+                    }
+                    if (anchor != nullptr && real) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (a0 + e < R.dx) dot += anchor[static_cast<int64_t>(a0 + e) * R.dz] * __uint_as_float(r[e]);
+                    }
+                    if (out != nullptr) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (a0 + e < R.dx) out[(a0 + e) * oa] = __uint_as_float(r[e]) * os;
+                    }
+                    if (k < n) {
+                        if constexpr (!kStateOnly) {
+                            uint32_t hi[16], lo[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                split2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]), hi[e], lo[e]);
+                            tc::st16(t_hb + lanes + a0 / 2, hi);
+                            tc::st16(t_hb + lanes + dxp / 2 + a0 / 2, lo);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * decay);
+                        tc::st32(t_h + lanes + a0, r);
+                    }
+                }
+            if (anchor_to != nullptr) {
+#pragma unroll
+                for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+                if (lane == 0) *anchor_to = dot * R.out_scale;
+            }
+            if (k < n) {
+                tc::wait_st();
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&sh.h_ready);
+                    mbar_arrive(&sh.coef_empty[cs]);
+                }
+            }
+        }
+    } else {
+        // ---- outputs: lane = value column c, tokens along the columns
+        if constexpr (!kStateOnly) {
+            const int c = (warp - 16) * 32 + lane;
+            const uint32_t lanes = static_cast<uint32_t>((warp - 16) * 32) << 16;
+            const bool on = (warp - 16) * 32 < R.dz, real = c < R.dz;
+            const int64_t out0 = b * R.ob + static_cast<int64_t>(h) * R.oh + c;
+            __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(R.out) + out0;
+            float* of = static_cast<float*>(R.out) + out0;
+            // this segment's rows past the length are zero
+            const int64_t hi = seg == A.n_segs - 1 ? A.T : min(A.T, static_cast<int64_t>(c0 + A.seg_chunks) * C);
+            if (real)
+                for (int64_t t = max(len, static_cast<int64_t>(c0) * C); t < hi; ++t) {
+                    if (R.out_f32) of[t * R.ot] = 0.0f;
+                    else ob[t * R.ot] = __float2bfloat16_rn(0.0f);
+                }
+            uint32_t off[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) off[u] = (c / 64) * kPanel + ((((c % 64) >> 3) ^ u) << 4) + (c & 7) * 2 + u * 128;
+            for (int k = 0; k < n; ++k) {
+                const int s = k % A.stages, cs = k % kCoefs;
+                if (!wait(&sh.coef_full[cs], k / kCoefs) || !wait(&sh.o_done, k)) break;
+                if (dots && !wait(&sh.ready[s], k / A.stages)) break;
+                tc::fence_after();
+                const int64_t t0 = static_cast<int64_t>(chunk_of(k)) * C;
+                const int left = static_cast<int>(min(static_cast<int64_t>(C), len - t0));
+                const Coef& cf = sh.coef[cs];
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t r1[32], r2[32];
+                    if (on) {
+                        tc::ld32(t_s + lanes + 32 * half, r1);
+                        tc::ld32(t_o2 + lanes + 32 * half, r2);
+                        tc::wait_ld();
+                    }
+                    if (half == 1) {
+                        // the products of the next chunk may overwrite what was read
+                        tc::fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh.o_read);
+                    }
+                    if (!on) continue;
+                    float v[32];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const float4 rd = *reinterpret_cast<const float4*>(&cf.read[32 * half + 4 * q]);
+                        const float rv[4] = {rd.x, rd.y, rd.z, rd.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            v[4 * q + e] = R.out_scale * (__uint_as_float(r1[4 * q + e]) + rv[e] * __uint_as_float(r2[4 * q + e]));
+                    }
+                    if (real) {
+                        const int64_t at = (t0 + 32 * half) * R.ot;
+                        const int rows = min(32, left - 32 * half);
+                        if (R.out_f32) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (e < rows) of[at + e * R.ot] = v[e];
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (e < rows) ob[at + e * R.ot] = __float2bfloat16_rn(v[e]);
+                        }
+                    }
+                    if (dots) {
+                        // out . w over the warp's columns: products, then halves of the tokens
+                        // are exchanged until lane l holds token l's sum
+                        const unsigned char* w = tiles + s * A.stage_bytes + off_w;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const int j = 32 * half + e;
+                            const uint32_t raw16 = *reinterpret_cast<const unsigned short*>(w + (j / 8) * 1024 + off[j % 8]);
+                            // padded columns hold zeros; rows past the length are not stored
+                            v[e] = v[e] * __uint_as_float(raw16 << 16);
+                        }
+#pragma unroll
+                        for (int o = 16; o; o >>= 1) {
+                            const bool up = lane & o;
+#pragma unroll
+                            for (int e = 0; e < o; ++e) {
+                                const float give = up ? v[e] : v[e + o], keep = up ? v[e + o] : v[e];
+                                v[e] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                            }
+                        }
+                        const int64_t t = t0 + 32 * half + lane;
+                        if (32 * half + lane < left) R.dots[((warp - 16) * A.BH + bh) * A.T + t] = v[0];
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&sh.coef_empty[cs]);
+                    if (dots) mbar_arrive(&sh.empty[s]);
+                }
+            }
+        }
+    }
+    tc::fence_before();
+    __syncthreads();
+    if (warp == 2) {
+        tc::fence_after();
+        tc::dealloc(tmem, kTmemCols);
+    }
+}
+
+// State entering each segment from the one before: in order along the run,
+// segment s's own state plus its decay times what came into it.
+__global__ void __launch_bounds__(256) k_attn_tc_join(const __grid_constant__ TcArgs A) {
+    const TcRun& R = A.run[blockIdx.y];
+    const int64_t size = static_cast<int64_t>(R.dx) * R.dz;
+    const int64_t bh = blockIdx.z;
+    const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (e >= size) return;
+    const int b = static_cast<int>(bh / A.H);
+    int64_t len = A.T;
+    if (A.lengths != nullptr) {
+        const int64_t l = A.lengths[b];
+        len = l < 0 ? 0 : l < A.T ? l : A.T;
+    }
+    const int chunks = static_cast<int>((len + C - 1) / C);
+    const int last_seg = chunks > 0 ? (chunks - 1) / A.seg_chunks : 0;
+    float* st = A.seg_states + blockIdx.y * A.seg_stride + bh * A.n_segs * size + e;
+    const float* d = A.seg_decays + bh * A.n_segs;
+    float v = 0.0f;
+    for (int s = 0; s < last_seg; ++s) {
+        const int at = R.reverse ? last_seg - s : s;
+        v = s == 0 ? st[at * size] : fmaf(d[at], v, st[at * size]);
+        st[at * size] = v;
+    }
+}
+
+bool encode(EncodeTiledFn fn, CUtensorMap* m, const AttnOperand& o, int heads, int d, int64_t T, int64_t B) {
+    // a broadcast axis (stride 0) has an extent of one; extents of one take a stride that keeps the map valid
+    if (o.sb == 0) B = 1;
+    if (o.sh == 0) heads = 1;
+    const int64_t row = (static_cast<int64_t>(d) * 2 + 15) & ~int64_t(15);
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(T),
+                                static_cast<cuuint64_t>(B)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(heads > 1 ? o.sh * 2 : row), static_cast<cuuint64_t>(T > 1 ? o.st * 2 : row),
+                                   static_cast<cuuint64_t>(B > 1 ? o.sb * 2 : row)};
+    const cuuint32_t box[4] = {64, 1, C, 1}, one[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(o.p), dims, strides, box, one,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+bool attn_tc_operand_ok(const AttnOperand& o, int heads, int d, int64_t T, int64_t B) {
+    if (d > 128 || d % 8 != 0) return false;
+    if (reinterpret_cast<uintptr_t>(o.p) % 16 != 0) return false;
+    auto fits = [](int64_t n, int64_t s) { return n <= 1 || (s % 8 == 0 && s < (int64_t(1) << 38)); };
+    return fits(heads, o.sh) && fits(T, o.st) && fits(B, o.sb) && (T <= 1 || o.st > 0);
+}
+
+cudaError_t launch_attn_tc(const AttnLaunch& L, int* kernels, const char** err) {
+    TcArgs A{};
+    uint32_t stage = 0;
+    for (int r = 0; r < L.runs; ++r) {
+        const AttnRun& f = L.run[r];
+        TcRun& t = A.run[r];
+        const bool maps = encode(L.encode, &t.x, f.x, L.H / f.x.div, f.dx, L.T, L.B) &&
+                          encode(L.encode, &t.y, f.y, L.H / f.y.div, f.dx, L.T, L.B) &&
+                          encode(L.encode, &t.z, f.z, L.H / f.z.div, f.dz, L.T, L.B) &&
+                          (f.dots == nullptr || encode(L.encode, &t.w, f.w, L.H / f.w.div, f.dz, L.T, L.B));
+        if (!maps) {
+            *err = "cuTensorMapEncodeTiled failed";
+            return cudaErrorInvalidValue;
+        }
+        t.out = f.out;
+        t.ob = f.ob;
+        t.ot = f.ot;
+        t.oh = f.oh;
+        t.init = f.init;
+        t.fin = f.fin;
+        t.sa = f.sa;
+        t.sc = f.sc;
+        t.init_scale = f.init_scale;
+        t.fin_scale = f.fin_scale;
+        t.out_scale = f.out_scale;
+        t.dots = f.dots;
+        t.anchors = f.anchors;
+        t.anchor_dots = f.anchor_dots;
+        t.xdiv = f.x.sh > 0 ? f.x.div : L.H;
+        t.xb = f.x.sb > 0;
+        t.ydiv = f.y.sh > 0 ? f.y.div : L.H;
+        t.yb = f.y.sb > 0;
+        t.zdiv = f.z.sh > 0 ? f.z.div : L.H;
+        t.zb = f.z.sb > 0;
+        t.wdiv = f.w.sh > 0 ? f.w.div : L.H;
+        t.wb = f.w.sb > 0;
+        t.dx = f.dx;
+        t.dz = f.dz;
+        t.reverse = f.reverse;
+        t.out_f32 = f.out_f32;
+        const uint32_t px = (f.dx + 63) / 64, pz = (f.dz + 63) / 64;
+        const uint32_t bytes = (2 * px + pz + (f.dots != nullptr ? pz : 0)) * kPanel;
+        stage = bytes > stage ? bytes : stage;
+        const int64_t size = static_cast<int64_t>(f.dx) * f.dz;
+        A.seg_stride = L.B * L.H * L.n_segs * size;
+    }
+    A.T = L.T;
+    A.BH = L.B * L.H;
+    A.H = L.H;
+    A.n_segs = L.n_segs;
+    A.seg_chunks = static_cast<int>(L.seg_chunks);
+    A.g = L.g;
+    A.gb = L.gb;
+    A.gt = L.gt;
+    A.gh = L.gh;
+    A.lengths = L.lengths;
+    A.anchor_every = L.anchor_every;
+    A.n_anchors = L.n_anchors;
+    A.seg_states = L.seg_states;
+    A.seg_decays = L.seg_decays;
+    A.status = L.status;
+    A.wait_ns = L.wait_ns;
+    A.drop_tile = L.drop_tile;
+    A.stage_bytes = stage;
+    // tiles, P's two terms, alignment; the rest of the 227 KB is the static struct
+    const uint32_t room = 227 * 1024 - static_cast<uint32_t>(sizeof(Shared)) - 1024 - 1024;
+    const uint32_t fit = (room - 2 * kPanel) / stage;
+    A.stages = static_cast<int>(fit < kMaxStages ? fit : kMaxStages);
+    const size_t smem = A.stages * stage + 2 * kPanel + 1024;
+    *kernels = 0;
+    cudaError_t e;
+    const unsigned blocks = static_cast<unsigned>(A.BH * A.n_segs);
+    if (A.n_segs > 1) {
+        e = cudaFuncSetAttribute(k_attn_tc<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
+        k_attn_tc<true><<<dim3(blocks, L.runs), kThreads, smem, L.stream>>>(A);
+        int most = 0;
+        for (int r = 0; r < L.runs; ++r) most = L.run[r].dx * L.run[r].dz > most ? L.run[r].dx * L.run[r].dz : most;
+        k_attn_tc_join<<<dim3((most + 255) / 256, L.runs, static_cast<unsigned>(A.BH)), 256, 0, L.stream>>>(A);
+        *kernels += 2;
+    }
+    e = cudaFuncSetAttribute(k_attn_tc<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    k_attn_tc<false><<<dim3(blocks, L.runs), kThreads, smem, L.stream>>>(A);
+    ++*kernels;
+    return cudaGetLastError();
+}
+
+}  // namespace es
