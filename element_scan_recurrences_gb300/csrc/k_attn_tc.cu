@@ -75,6 +75,7 @@ struct TcRun {
     int xb, yb, zb, wb;                       // 1; 0: one batch row for all
     int dx, dz;                               // real widths
     int reverse, out_f32;
+    int wide;                                 // the result's addresses and strides keep to 16 bytes
 };
 
 struct TcArgs {
@@ -105,13 +106,46 @@ struct Shared {
     Coef coef[kCoefs];
 };
 
+// A bounded wait that lets the hardware hold the thread, up to 50 us a try.
+// Without the hint a try comes back after some tens of cycles, and the waiting
+// warps' tries (20 warps, most of them waiting) crowd the stores and
+// shared-memory reads of the working ones out of the queue they share.
+__device__ __noinline__ bool wait_more(uint64_t* bar, uint32_t parity, uint64_t limit_ns, volatile int* abort_flag) {
+    const uint32_t at = smem_u32(bar);
+    auto tried = [&]() {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(at), "r"(parity), "r"(50000u)
+            : "memory");
+        return done != 0;
+    };
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (uint32_t i = 0;; ++i) {
+        if (tried()) return true;
+        if (i < 8) continue;
+        if (abort_flag != nullptr && *abort_flag) return false;
+        const uint64_t now = global_timer_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > limit_ns) return false;
+    }
+}
+
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, uint64_t limit_ns, volatile int* abort_flag) {
+    return mbar_try_wait(bar, parity) || wait_more(bar, parity, limit_ns, abort_flag);
+}
+
 struct Wait {
     uint64_t ns;
     volatile int* flag;
     unsigned int* status;
     // the whole warp waits; false: leave the loop
     __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
-        const bool ok = mbar_wait_bounded(bar, parity & 1, ns, flag);
+        const bool ok = wait_bounded(bar, parity & 1, ns, flag);
         if (__all_sync(0xffffffffu, ok)) return true;
         if (!ok && !*flag) report_timeout(status, flag);
         return false;
@@ -121,19 +155,6 @@ struct Wait {
 __device__ __forceinline__ void arrive_warp(uint64_t* bar, int lane) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
-}
-
-// two bf16 terms of pairs of values
-__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-    hi = tc::pack_bf16(a, b);
-    lo = tc::pack_bf16(a - tc::low_bf16(hi), b - tc::high_bf16(hi));
-}
-
-__device__ __forceinline__ void split3(float a, float b, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
-    hi = tc::pack_bf16(a, b);
-    const float ra = a - tc::low_bf16(hi), rb = b - tc::high_bf16(hi);
-    mid = tc::pack_bf16(ra, rb);
-    lo = tc::pack_bf16(ra - tc::low_bf16(mid), rb - tc::high_bf16(mid));
 }
 
 // kStateOnly: a segment's own state and decay, from zero (the first segment's
@@ -179,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
     const int px = dxp / 64, pz = dzp / 64;
     const bool dots = !kStateOnly && R.dots != nullptr;
 
-    // a stage: X, Y, Z, W
+    // a stage: X, Y, Z, and W's place, which is then the output tile's
     const uint32_t off_y = kStateOnly ? 0 : px * kPanel, off_z = off_y + px * kPanel, off_w = off_z + pz * kPanel;
     unsigned char* p_hi = tiles + A.stages * A.stage_bytes;
     unsigned char* p_lo = p_hi + kPanel;
@@ -189,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         for (int s = 0; s < A.stages; ++s) {
             mbar_init(&sh.full[s], 1);
             mbar_init(&sh.ready[s], 1);
-            mbar_init(&sh.empty[s], 1 + 4 + (dots ? 4 : 0));
+            mbar_init(&sh.empty[s], 1 + 4 + (kStateOnly ? 0 : 4));
         }
         for (int s = 0; s < kCoefs; ++s) {
             mbar_init(&sh.coef_full[s], 1);
@@ -221,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             int issued = 0;
             for (int k = 0; k < n; ++k) {
                 const int s = k % A.stages, round = k / A.stages;
-                if (round > 0 && !mbar_wait_bounded(&sh.empty[s], (round - 1) & 1, A.wait_ns, &sh.abort_flag)) {
+                if (round > 0 && !wait_bounded(&sh.empty[s], (round - 1) & 1, A.wait_ns, &sh.abort_flag)) {
                     report_timeout(A.status, &sh.abort_flag);
                     break;
                 }
@@ -241,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             }
             for (int k = max(0, issued - A.stages); k < issued; ++k) {
                 if (k == A.drop_tile) continue;
-                if (!mbar_wait_bounded(&sh.full[k % A.stages], (k / A.stages) & 1, A.wait_ns, nullptr))
+                if (!wait_bounded(&sh.full[k % A.stages], (k / A.stages) & 1, A.wait_ns, nullptr))
                     atomicOr(A.status, ES_DEVICE_TIMEOUT);
             }
         }
@@ -337,41 +358,45 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         const uint32_t i_s = tc::instr_bf16(C, false, false), i_o1 = tc::instr_bf16(C, true, false);
         const uint32_t i_kv = tc::instr_bf16(static_cast<uint32_t>(dxp), false, true);
         const uint32_t base = smem_u32(tiles);
+        const uint64_t d_phi = tc::smem_desc(smem_u32(p_hi), 16, 1024);
         bool ok = true;
-        for (int k = 0; k < n && ok; ++k) {
+        for (int k = 0; k < n; ++k) {
             const int s = k % A.stages;
-            const uint32_t sx = base + s * A.stage_bytes, sy = sx + off_y, sz = sx + off_z;
-            ok = wait(&sh.ready[s], k / A.stages);
+            const uint32_t sx = base + s * A.stage_bytes;
+            const uint64_t d_x = tc::smem_desc(sx, 16, 1024), d_y = tc::smem_desc(sx + off_y, 16, 1024);
+            const uint64_t d_yt = tc::smem_desc(sx + off_y, kPanel, 1024), d_zt = tc::smem_desc(sx + off_z, kPanel, 1024);
+            if (!(ok = wait(&sh.ready[s], k / A.stages))) break;
             if constexpr (!kStateOnly) {
                 // the region of the scores holds the last chunk's O1 until it is read
-                if (ok && k > 0) ok = wait(&sh.o_read, k - 1);
-                if (!ok) break;
+                if (k > 0 && !(ok = wait(&sh.o_read, k - 1))) break;
                 tc::fence_after();
                 if (lane == 0) {
-                    for (int q = 0; q < dxp / 16; ++q) {
-                        const uint32_t at = (q / 4) * kPanel + (q % 4) * 32;
-                        tc::mma_ss(t_s, tc::smem_desc(sx + at, 16, 1024), tc::smem_desc(sy + at, 16, 1024), i_s, q > 0);
-                    }
+                    for (int p = 0; p < px; ++p)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            tc::mma_ss(t_s, d_x + p * (kPanel >> 4) + q * 2, d_y + p * (kPanel >> 4) + q * 2, i_s, p + q > 0);
                     tc::commit(&sh.s_done);
                 }
                 __syncwarp();
             }
-            if (!ok || !(ok = wait(&sh.h_ready, k))) break;
+            if (!(ok = wait(&sh.h_ready, k))) break;
             if constexpr (!kStateOnly) {
                 tc::fence_after();
                 if (lane == 0)
-                    for (int m = 0; m < 2; ++m)
-                        for (int q = 0; q < dxp / 16; ++q)
-                            tc::mma_ts(t_o2, t_hb + m * (dxp / 2) + q * 8,
-                                       tc::smem_desc(sx + (q / 4) * kPanel + (q % 4) * 32, 16, 1024), i_s, m + q > 0);
+                    for (int p = 0; p < 2 * px; ++p) {
+                        const uint64_t d = d_x + (p < px ? p : p - px) * (kPanel >> 4);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) tc::mma_ts(t_o2, t_hb + 32 * p + 8 * q, d + q * 2, i_s, p + q > 0);
+                    }
                 __syncwarp();
             }
             if (!(ok = wait(&sh.zt_ready, k))) break;
             tc::fence_after();
             if (lane == 0) {
+#pragma unroll 1
                 for (int m = 0; m < 3; ++m)
-                    for (int q = 0; q < C / 16; ++q)
-                        tc::mma_ts(t_h, t_zt + m * (C / 2) + q * 8, tc::smem_desc(sy + q * 2048, kPanel, 1024), i_kv, true);
+#pragma unroll
+                    for (int q = 0; q < C / 16; ++q) tc::mma_ts(t_h, t_zt + m * (C / 2) + q * 8, d_yt + q * 128, i_kv, true);
                 tc::commit(&sh.kv_done);
             }
             __syncwarp();
@@ -379,10 +404,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 if (!(ok = wait(&sh.p_ready, k))) break;
                 tc::fence_after();
                 if (lane == 0) {
+#pragma unroll 1
                     for (int m = 0; m < 2; ++m)
+#pragma unroll
                         for (int q = 0; q < C / 16; ++q)
-                            tc::mma_ss(t_s, tc::smem_desc(sz + q * 2048, kPanel, 1024),
-                                       tc::smem_desc(smem_u32(m ? p_lo : p_hi) + q * 32, 16, 1024), i_o1, m + q > 0);
+                            tc::mma_ss(t_s, d_zt + q * 128, d_phi + m * (kPanel >> 4) + q * 2, i_o1, m + q > 0);
                     tc::commit(&sh.o_done);
                 }
             }
@@ -392,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         // nothing of this CTA's may still run when its tensor memory goes
         if (lane == 0) tc::commit(&sh.drained);
         __syncwarp();
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&sh.drained, 0, A.wait_ns, nullptr)) && lane == 0)
+        if (!__all_sync(0xffffffffu, wait_bounded(&sh.drained, 0, A.wait_ns, nullptr)) && lane == 0)
             atomicOr(A.status, ES_DEVICE_TIMEOUT);
     } else if (warp < 8) {
         // ---- P: row i, 32 columns
@@ -400,50 +426,52 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             const int i = lane + 32 * (warp & 1), half = warp >> 2;
             const uint32_t from = t_s + (static_cast<uint32_t>(32 * (warp & 1)) << 16) + 32 * half;
             // rows of one half never see the columns of the other: forward rows 0-31 the late columns
+            const float sign = R.reverse ? -1.0f : 1.0f;
             const bool none = R.reverse ? (warp & 1) > half : (warp & 1) < half;
             for (int k = 0; k < n; ++k) {
                 const int cs = k % kCoefs;
                 if (!wait(&sh.coef_full[cs], k / kCoefs) || !wait(&sh.s_done, k)) break;
                 const Coef& c = sh.coef[cs];
-                uint4 hi[4], lo[4];
+                const uint32_t swz = i & 7;
                 if (none) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) hi[q] = lo[q] = make_uint4(0, 0, 0, 0);
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t at = i * 128 + (((4 * half + q) ^ swz) << 4);
+                        *reinterpret_cast<uint4*>(p_hi + at) = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4*>(p_lo + at) = make_uint4(0, 0, 0, 0);
+                    }
                 } else {
                     tc::fence_after();
-                    uint32_t r[32];
-                    tc::ld32(from, r);
                     const float gi = c.g2[i];
                     const int bound = c.bound[i];
-                    const int first = R.reverse ? i : bound, last = R.reverse ? bound : i;
-                    const float sign = R.reverse ? -1.0f : 1.0f;
-                    tc::wait_ld();
+                    // the half's columns that row i sees, as bits
+                    const int first = max(0, (R.reverse ? i : bound) - 32 * half), last = min(31, (R.reverse ? bound : i) - 32 * half);
+                    const uint32_t seen = first <= last ? (0xffffffffu >> (31 - (last - first))) << first : 0u;
+#pragma unroll 1
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t r[16];
+                        tc::ld(from + 16 * q, r);
+                        const uint32_t mask = seen >> (16 * q);
+                        tc::wait_ld();
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t ph[4], pl[4];
-#pragma unroll
-                        for (int u = 0; u < 4; u += 2) {
-                            const float4 gj = *reinterpret_cast<const float4*>(&c.g2[32 * half + 8 * q + 2 * u]);
-                            const float gv[4] = {gj.x, gj.y, gj.z, gj.w};
-                            float v[4];
+                        for (int u = 0; u < 2; ++u) {
+                            uint32_t hi[4], lo[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                const int j = 32 * half + 8 * q + 2 * u + e;
-                                const float d = tc::exp2_approx(sign * (gi - gv[e]));
-                                v[e] = (j >= first && j <= last) ? __uint_as_float(r[8 * q + 2 * u + e]) * d : 0.0f;
+                                const int j = 8 * u + 2 * e;
+                                const float2 gj = *reinterpret_cast<const float2*>(&c.g2[32 * half + 16 * q + j]);
+                                const float2 d = tc::fma2(gj, make_float2(-sign, -sign), make_float2(gi * sign, gi * sign));
+                                float2 v = tc::mul2(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])),
+                                                    make_float2(tc::exp2_approx(d.x), tc::exp2_approx(d.y)));
+                                if (!(mask & (1u << j))) v.x = 0.0f;
+                                if (!(mask & (2u << j))) v.y = 0.0f;
+                                tc::split2(v, hi[e], lo[e]);
                             }
-                            split2(v[0], v[1], ph[u], pl[u]);
-                            split2(v[2], v[3], ph[u + 1], pl[u + 1]);
+                            const uint32_t at = i * 128 + (((4 * half + 2 * q + u) ^ swz) << 4);
+                            *reinterpret_cast<uint4*>(p_hi + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                            *reinterpret_cast<uint4*>(p_lo + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                         }
-                        hi[q] = make_uint4(ph[0], ph[1], ph[2], ph[3]);
-                        lo[q] = make_uint4(pl[0], pl[1], pl[2], pl[3]);
                     }
-                }
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint32_t at = i * 128 + (((4 * half + q) ^ (i & 7)) << 4);
-                    *reinterpret_cast<uint4*>(p_hi + at) = hi[q];
-                    *reinterpret_cast<uint4*>(p_lo + at) = lo[q];
                 }
                 fence_proxy_async_smem();
                 tc::fence_before();
@@ -470,26 +498,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             if (on) {
                 const unsigned char* z = tiles + s * A.stage_bytes + off_z;
                 const Coef& cf = sh.coef[cs];
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t t0[8], t1[8], t2[8];
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t t0[16], t1[16], t2[16];
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const float4 w = *reinterpret_cast<const float4*>(&cf.upd[32 * half + 4 * q]);
-                        const float wv[4] = {w.x, w.y, w.z, w.w};
-                        float v[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int j = 32 * half + 4 * q + e;
-                            const uint32_t raw16 = *reinterpret_cast<const unsigned short*>(z + (j / 8) * 1024 + off[j % 8]);
-                            v[e] = __uint_as_float(raw16 << 16) * wv[e];
-                        }
-                        split3(v[0], v[1], t0[2 * q], t1[2 * q], t2[2 * q]);
-                        split3(v[2], v[3], t0[2 * q + 1], t1[2 * q + 1], t2[2 * q + 1]);
+                    for (int e = 0; e < 8; ++e) {
+                        const float2 w = *reinterpret_cast<const float2*>(&cf.upd[16 * q + 2 * e]);
+                        const unsigned char* at = z + q * 2048 + (e / 4) * 1024;
+                        const uint32_t z0 = *reinterpret_cast<const unsigned short*>(at + off[2 * e % 8]);
+                        const uint32_t z1 = *reinterpret_cast<const unsigned short*>(at + off[(2 * e + 1) % 8]);
+                        tc::split3(tc::mul2(make_float2(__uint_as_float(z0 << 16), __uint_as_float(z1 << 16)), w), t0[e], t1[e], t2[e]);
                     }
-                    tc::st16(to + 16 * half, t0);
-                    tc::st16(to + 32 + 16 * half, t1);
-                    tc::st16(to + 64 + 16 * half, t2);
+                    tc::st(to + 8 * q, t0);
+                    tc::st(to + 32 + 8 * q, t1);
+                    tc::st(to + 64 + 8 * q, t2);
                 }
                 tc::wait_st();
             }
@@ -568,47 +590,54 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                     os = R.fin_scale;
                 }
             }
+            if (k == 0 && on) {
+                for (int a0 = 0; a0 < dxp; a0 += 8) {
+                    uint32_t r[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        r[e] = __float_as_uint(from != nullptr && a0 + e < R.dx ? from[(a0 + e) * fa] * fs : 0.0f);
+                    tc::st(t_h + lanes + a0, r);
+                }
+                tc::wait_st();
+            }
+            // now and then the state leaves, or meets an anchor
             float dot = 0.0f;
-            const bool leaves = __any_sync(0xffffffffu, out != nullptr || dump != nullptr);
-            if (on && (k < n || leaves))
+            const bool leaves = __any_sync(0xffffffffu, out != nullptr || dump != nullptr || anchor != nullptr);
+            if (leaves && on)
+#pragma unroll 1
+                for (int a0 = 0; a0 < R.dx; a0 += 8) {
+                    uint32_t r[8];
+                    tc::ld(t_h + lanes + a0, r);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float v = __uint_as_float(r[e]);
+                        const int64_t row = static_cast<int64_t>(a0 + e) * R.dz;
+                        if (!real) continue;
+                        if (dump != nullptr) dump[row] = v;
+                        if (anchor != nullptr) dot += anchor[row] * v;
+                        if (out != nullptr) out[(a0 + e) * oa] = v * os;
+                    }
+                }
+            if (on && k < n)
+#pragma unroll 1
                 for (int a0 = 0; a0 < dxp; a0 += 32) {
-                    uint32_t r[32];
-                    if (k == 0) {
+                    uint32_t r[32], hi[16], lo[16];
+                    tc::ld(t_h + lanes + a0, r);
+                    tc::wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            r[e] = __float_as_uint(from != nullptr && a0 + e < R.dx ? from[(a0 + e) * fa] * fs : 0.0f);
-                    } else {
-                        tc::ld32(t_h + lanes + a0, r);
-                        tc::wait_ld();
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 v = make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
+                        if constexpr (!kStateOnly) tc::split2(v, hi[e], lo[e]);
+                        const float2 d = tc::mul2(v, make_float2(decay, decay));
+                        r[2 * e] = __float_as_uint(d.x);
+                        r[2 * e + 1] = __float_as_uint(d.y);
                     }
-                    if (dump != nullptr && real) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (a0 + e < R.dx) dump[static_cast<int64_t>(a0 + e) * R.dz] = __uint_as_float(r[e]);
+                    if constexpr (!kStateOnly) {
+                        tc::st(t_hb + lanes + a0 / 2, hi);
+                        tc::st(t_hb + lanes + dxp / 2 + a0 / 2, lo);
                     }
-                    if (anchor != nullptr && real) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (a0 + e < R.dx) dot += anchor[static_cast<int64_t>(a0 + e) * R.dz] * __uint_as_float(r[e]);
-                    }
-                    if (out != nullptr) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (a0 + e < R.dx) out[(a0 + e) * oa] = __uint_as_float(r[e]) * os;
-                    }
-                    if (k < n) {
-                        if constexpr (!kStateOnly) {
-                            uint32_t hi[16], lo[16];
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                split2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]), hi[e], lo[e]);
-                            tc::st16(t_hb + lanes + a0 / 2, hi);
-                            tc::st16(t_hb + lanes + dxp / 2 + a0 / 2, lo);
-                        }
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * decay);
-                        tc::st32(t_h + lanes + a0, r);
-                    }
+                    tc::st(t_h + lanes + a0, r);
                 }
             if (anchor_to != nullptr) {
 #pragma unroll
@@ -644,80 +673,106 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             uint32_t off[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u) off[u] = (c / 64) * kPanel + ((((c % 64) >> 3) ^ u) << 4) + (c & 7) * 2 + u * 128;
+            const int wt = threadIdx.x - 512;
+            // pieces of 16 bytes a row, and the rows of a pass over the tile
+            const int cols = dzp / 8, rows = 128 / cols;
+            const bool wide = !R.out_f32 && R.wide;
             for (int k = 0; k < n; ++k) {
                 const int s = k % A.stages, cs = k % kCoefs;
-                if (!wait(&sh.coef_full[cs], k / kCoefs) || !wait(&sh.o_done, k)) break;
-                if (dots && !wait(&sh.ready[s], k / A.stages)) break;
+                // (ready: the W tile is there, and its place is the output tile's from here on)
+                const bool go = wait(&sh.coef_full[cs], k / kCoefs) && wait(&sh.o_done, k) && wait(&sh.ready[s], k / A.stages);
+                // the four warps leave together: they meet at a barrier below
+                if (consumer_vote_any_failed(!go, 128)) break;
                 tc::fence_after();
                 const int64_t t0 = static_cast<int64_t>(chunk_of(k)) * C;
                 const int left = static_cast<int>(min(static_cast<int64_t>(C), len - t0));
                 const Coef& cf = sh.coef[cs];
+                unsigned char* w = tiles + s * A.stage_bytes + off_w;
+                if (on) {
+                    const float2 scale = make_float2(R.out_scale, R.out_scale);
 #pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t r1[32], r2[32];
-                    if (on) {
-                        tc::ld32(t_s + lanes + 32 * half, r1);
-                        tc::ld32(t_o2 + lanes + 32 * half, r2);
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t r1[16], r2[16];
+                        tc::ld(t_s + lanes + 16 * q, r1);
+                        tc::ld(t_o2 + lanes + 16 * q, r2);
                         tc::wait_ld();
-                    }
-                    if (half == 1) {
-                        // the products of the next chunk may overwrite what was read
-                        tc::fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sh.o_read);
-                    }
-                    if (!on) continue;
-                    float v[32];
+                        float v[16];
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const float4 rd = *reinterpret_cast<const float4*>(&cf.read[32 * half + 4 * q]);
-                        const float rv[4] = {rd.x, rd.y, rd.z, rd.w};
+                        for (int e = 0; e < 16; e += 2) {
+                            const float2 rd = *reinterpret_cast<const float2*>(&cf.read[16 * q + e]);
+                            const float2 o = tc::mul2(tc::fma2(make_float2(__uint_as_float(r2[e]), __uint_as_float(r2[e + 1])), rd,
+                                                               make_float2(__uint_as_float(r1[e]), __uint_as_float(r1[e + 1]))), scale);
+                            v[e] = o.x;
+                            v[e + 1] = o.y;
+                        }
+                        unsigned char* at = w + q * 2048;
+                        if (dots) {
+                            // out . w over the warp's columns: products, then halves of the tokens are
+                            // exchanged until lane l holds token l / 2's sum (padded columns hold zeros)
+                            float m[16];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            v[4 * q + e] = R.out_scale * (__uint_as_float(r1[4 * q + e]) + rv[e] * __uint_as_float(r2[4 * q + e]));
-                    }
-                    if (real) {
-                        const int64_t at = (t0 + 32 * half) * R.ot;
-                        const int rows = min(32, left - 32 * half);
+                            for (int e = 0; e < 16; ++e) {
+                                const uint32_t raw16 = *reinterpret_cast<const unsigned short*>(at + (e / 8) * 1024 + off[e % 8]);
+                                m[e] = v[e] * __uint_as_float(raw16 << 16);
+                            }
+#pragma unroll
+                            for (int o = 16; o >= 2; o >>= 1) {
+                                const bool up = lane & o;
+#pragma unroll
+                                for (int e = 0; e < o / 2; ++e) {
+                                    const float give = up ? m[e] : m[e + o / 2], keep = up ? m[e + o / 2] : m[e];
+                                    m[e] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                                }
+                            }
+                            m[0] += __shfl_xor_sync(0xffffffffu, m[0], 1);
+                            const int row = 16 * q + lane / 2;
+                            if (row < left && !(lane & 1)) R.dots[((warp - 16) * A.BH + bh) * A.T + t0 + row] = m[0];
+                        }
                         if (R.out_f32) {
+                            if (real) {
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (e < rows) of[at + e * R.ot] = v[e];
+                                for (int e = 0; e < 16; ++e)
+                                    if (16 * q + e < left) of[(t0 + 16 * q + e) * R.ot] = v[e];
+                            }
                         } else {
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (e < rows) ob[at + e * R.ot] = __float2bfloat16_rn(v[e]);
-                        }
-                    }
-                    if (dots) {
-                        // out . w over the warp's columns: products, then halves of the tokens
-                        // are exchanged until lane l holds token l's sum
-                        const unsigned char* w = tiles + s * A.stage_bytes + off_w;
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const int j = 32 * half + e;
-                            const uint32_t raw16 = *reinterpret_cast<const unsigned short*>(w + (j / 8) * 1024 + off[j % 8]);
-                            // padded columns hold zeros; rows past the length are not stored
-                            v[e] = v[e] * __uint_as_float(raw16 << 16);
-                        }
-#pragma unroll
-                        for (int o = 16; o; o >>= 1) {
-                            const bool up = lane & o;
-#pragma unroll
-                            for (int e = 0; e < o; ++e) {
-                                const float give = up ? v[e] : v[e + o], keep = up ? v[e + o] : v[e];
-                                v[e] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                            for (int e = 0; e < 16; e += 2) {
+                                const uint32_t two = tc::pack_bf16(v[e], v[e + 1]);
+                                *reinterpret_cast<unsigned short*>(at + (e / 8) * 1024 + off[e % 8]) = static_cast<unsigned short>(two);
+                                *reinterpret_cast<unsigned short*>(at + (e / 8) * 1024 + off[(e + 1) % 8]) =
+                                    static_cast<unsigned short>(two >> 16);
                             }
                         }
-                        const int64_t t = t0 + 32 * half + lane;
-                        if (32 * half + lane < left) R.dots[((warp - 16) * A.BH + bh) * A.T + t] = v[0];
                     }
                 }
+                // the products of the next chunk may overwrite what was read
+                tc::fence_before();
                 __syncwarp();
                 if (lane == 0) {
+                    mbar_arrive(&sh.o_read);
                     mbar_arrive(&sh.coef_empty[cs]);
-                    if (dots) mbar_arrive(&sh.empty[s]);
                 }
+                if (!R.out_f32) {
+                    named_barrier_sync(2, 128);
+                    // rows out, 16 bytes a thread where the result's addresses allow it
+                    const int piece = wt % cols;
+                    for (int row = wt / cols; row < left; row += rows) {
+                        const uint4 u = *reinterpret_cast<const uint4*>(w + (piece / 8) * kPanel + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
+                        __nv_bfloat16* to = static_cast<__nv_bfloat16*>(R.out) + b * R.ob + static_cast<int64_t>(h) * R.oh + (t0 + row) * R.ot + piece * 8;
+                        if (wide) {
+                            if (piece * 8 < R.dz) *reinterpret_cast<uint4*>(to) = u;
+                        } else {
+                            const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                if (piece * 8 + e < R.dz)
+                                    *reinterpret_cast<unsigned short*>(to + e) = static_cast<unsigned short>(e % 2 ? x[e / 2] >> 16 : x[e / 2]);
+                        }
+                    }
+                }
+                // the next load of this place comes through the async proxy
+                fence_proxy_async_smem();
+                arrive_warp(&sh.empty[s], lane);
             }
         }
     }
@@ -819,8 +874,9 @@ cudaError_t launch_attn_tc(const AttnLaunch& L, int* kernels, const char** err) 
         t.dz = f.dz;
         t.reverse = f.reverse;
         t.out_f32 = f.out_f32;
+        t.wide = reinterpret_cast<uintptr_t>(f.out) % 16 == 0 && f.ob % 8 == 0 && f.ot % 8 == 0 && f.oh % 8 == 0;
         const uint32_t px = (f.dx + 63) / 64, pz = (f.dz + 63) / 64;
-        const uint32_t bytes = (2 * px + pz + (f.dots != nullptr ? pz : 0)) * kPanel;
+        const uint32_t bytes = (2 * px + 2 * pz) * kPanel;
         stage = bytes > stage ? bytes : stage;
         const int64_t size = static_cast<int64_t>(f.dx) * f.dz;
         A.seg_stride = L.B * L.H * L.n_segs * size;
