@@ -47,7 +47,7 @@ struct AttnRun {
     // A forward run writes its state after every `anchor_every` chunks (and
     // after the last one) to anchors[(bh*n + m)*dx*dz + a*dz + c]; a reversed
     // run instead writes out_scale * <its state there, the anchor> per slice
-    // to anchor_dots [slices, B*H, n].
+    // to anchor_dots [slices, B*H, n] (the tensor-core kernel has two parts a slice).
     float* anchors;
     float* anchor_dots;
     int dx, dz;
@@ -84,6 +84,10 @@ constexpr int kAttnMaxDim = 256;
 
 cudaError_t launch_attn_direct(const AttnLaunch& L);
 
+// Tokens between the states the decays' gradient starts from: its sums of
+// differences run within such a block (see k_attn_decay_grad).
+constexpr int kAttnAnchorTokens = 256;
+
 // the tensor-core kernel: chunk of tokens, and whether it can load an operand
 constexpr int kAttnTcChunk = 64;
 bool attn_tc_operand_ok(const AttnOperand& o, int heads, int d, int64_t T, int64_t B);
@@ -94,8 +98,8 @@ cudaError_t launch_attn_tc(const AttnLaunch& L, int* kernels, const char** err);
 struct AttnDecayGrad {
     const float* dots_q;         // [slices_q, B*H, T]
     const float* dots_k;
-    const float* ends;           // [slices_k, B*H, n]
-    int slices_q, slices_k;
+    const float* ends;           // [slices_e, B*H, n]
+    int slices_q, slices_k, slices_e;
     int64_t B, T;
     int H;
     const int* lengths;

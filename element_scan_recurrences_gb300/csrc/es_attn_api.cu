@@ -95,10 +95,6 @@ struct AttnPlan {
     int slices_k, slices_v;      // slices of the runs that produce key- and value-wide outputs
 };
 
-// Tokens between the states the decays' gradient starts from: its sums of
-// differences run within such a block (see k_attn_decay_grad).
-constexpr int64_t kAnchorTokens = 256;
-
 // Segments a sequence is cut into (tensor-core path).  One CTA runs one (batch
 // row, head, run), one CTA an SM; with few of them the chunks are shared out
 // among more CTAs, which costs a pass over the keys and values for the states
@@ -112,6 +108,9 @@ int segments(int64_t ctas, int64_t chunks, int64_t* seg_chunks) {
     *seg_chunks = each;
     return static_cast<int>((chunks + each - 1) / each);
 }
+
+// parts of a slice's product of a state and an anchor
+int ends_parts(const AttnPlan& P) { return P.path == ES_PATH_TENSOR ? 2 : 1; }
 
 size_t take(size_t* at, int64_t bytes) {
     const size_t here = *at;
@@ -278,8 +277,8 @@ es_status plan_attn(const char* fn, const es_linear_attention_args* a, const es_
 
     // workspace
     const int64_t chunk = P->path == ES_PATH_TENSOR ? kAttnTcChunk : kAttnChunk;
-    L.anchor_every = kAnchorTokens / chunk;
-    L.n_anchors = (T + kAnchorTokens - 1) / kAnchorTokens;
+    L.anchor_every = kAttnAnchorTokens / chunk;
+    L.n_anchors = (T + kAttnAnchorTokens - 1) / kAttnAnchorTokens;
     L.n_segs = 1;
     const int64_t chunks = (T + chunk - 1) / chunk;
     L.seg_chunks = chunks > 0 ? chunks : 1;
@@ -296,7 +295,7 @@ es_status plan_attn(const char* fn, const es_linear_attention_args* a, const es_
             P->dots_q = take(&at, 4 * P->slices_k * bh * T);
             P->dots_k = take(&at, 4 * P->slices_k * bh * T);
             P->anchors = take(&at, 4 * bh * L.n_anchors * dk * dv);
-            P->ends = take(&at, 4 * P->slices_k * bh * L.n_anchors);
+            P->ends = take(&at, 4 * ends_parts(*P) * P->slices_k * bh * L.n_anchors);
             P->partial = take(&at, 4 * bh * L.n_anchors);
         }
         if (a->q.heads < H) P->fold_q = take(&at, 4 * bh * T * dk);
@@ -412,11 +411,12 @@ es_status run_backward(const char* fn, const es_linear_attention_args* a, const 
         D.dots_k = rk.dots;
         D.ends = rk.anchor_dots;
         D.slices_q = D.slices_k = P.slices_k;
+        D.slices_e = ends_parts(P) * P.slices_k;
         D.B = L.B;
         D.T = L.T;
         D.H = L.H;
         D.lengths = L.lengths;
-        D.block = kAnchorTokens;
+        D.block = kAttnAnchorTokens;
         D.n = L.n_anchors;
         D.stream = L.stream;
         if (a->decay_per_head) {

@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(256) k_attn_decay_grad(const AttnDecayGrad G) 
     const int64_t lo = m * G.block, full = lo + G.block < G.T ? lo + G.block : G.T, hi = full < len ? full : len;
     float carry = 0.0f, sum = 0.0f;
     if (lo < hi)
-        for (int s = 0; s < G.slices_k; ++s) carry += G.ends[(s * BH + bh) * G.n + m];
+        for (int s = 0; s < G.slices_e; ++s) carry += G.ends[(s * BH + bh) * G.n + m];
     for (int64_t top = hi; top > lo; top -= 32) {
         const int64_t t = top - 32 + lane;
         float v = 0.0f;

@@ -1,7 +1,7 @@
 // k_attn_tc.cu -- linear attention in chunks of 64 tokens on the tensor cores.
 //
 // One CTA takes one (batch row, head), or a segment of its tokens, through the
-// chunks in order; its 20 warps are a pipeline of roles linked by mbarriers:
+// chunks in order; its 28 warps are a pipeline of roles linked by mbarriers:
 //
 //     warp 2       TMA loads of the operands' tiles (X, Y, Z, and W for the
 //                  decays' gradient), 128-byte swizzled panels of 64 values
@@ -13,9 +13,9 @@
 //                  shared memory
 //     warps 8-11   Z scaled by its update coefficients and transposed into
 //                  tensor memory, three bf16 terms
-//     warps 12-15  the state: f32 in tensor memory, decayed once a chunk, and
+//     warps 12-19  the state: f32 in tensor memory, decayed once a chunk, and
 //                  its two bf16 terms for the read
-//     warps 16-19  the outputs: read, joined, rounded once, stored
+//     warps 20-27  the outputs: read, joined, rounded once, stored
 //
 // The state lies transposed, a value column a lane and a key column a column,
 // so that everything made from it or for it is the A operand, read from tensor
@@ -46,8 +46,9 @@ namespace es {
 namespace {
 
 constexpr int C = kAttnTcChunk;               // 64 tokens
-constexpr int kThreads = 640;
-constexpr int kCoefs = 4;                     // slots of chunk coefficients
+constexpr int kThreads = 896;
+constexpr int kCoefs = 4;                     // slots of chunk coefficients (a power of two)
+constexpr int kAnchorChunks = kAttnAnchorTokens / C;
 constexpr int kMaxStages = 4;
 constexpr uint32_t kPanel = C * 128;          // bytes of a panel: 64 rows of 64 bf16
 constexpr uint32_t kTmemCols = 512;
@@ -86,7 +87,7 @@ struct TcArgs {
     const float* g;
     int64_t gb, gt, gh;
     const int* lengths;
-    int64_t anchor_every, n_anchors;
+    int64_t n_anchors;
     float* seg_states;                        // [runs][BH][n_segs][dx * dz] states entering each segment's successor
     float* seg_decays;                        // [BH][n_segs]
     int64_t seg_stride;                       // floats of one run's seg_states
@@ -106,28 +107,32 @@ struct Shared {
     Coef coef[kCoefs];
 };
 
-// A bounded wait that lets the hardware hold the thread, up to 50 us a try.
-// Without the hint a try comes back after some tens of cycles, and the waiting
-// warps' tries (20 warps, most of them waiting) crowd the stores and
-// shared-memory reads of the working ones out of the queue they share.
-__device__ __noinline__ bool wait_more(uint64_t* bar, uint32_t parity, uint64_t limit_ns, volatile int* abort_flag) {
+// A bounded wait that lets the hardware hold the thread, up to 20 us a try: a
+// try without that hint comes back after some tens of cycles.  The clock and
+// the abort flag are looked at after every 64 tries; what runs in between is
+// kept short, for the roles' loops together have to stay in the instruction
+// caches.
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, uint64_t limit_ns, volatile int* abort_flag) {
     const uint32_t at = smem_u32(bar);
-    auto tried = [&]() {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(at), "r"(parity), "r"(50000u)
-            : "memory");
-        return done != 0;
-    };
     uint64_t t0 = 0;
 #pragma unroll 1
-    for (uint32_t i = 0;; ++i) {
-        if (tried()) return true;
-        if (i < 8) continue;
+    while (true) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .u32 n;\n\tmov.u32 n, 64;\n"
+            "TRY:\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "@p bra DONE;\n\t"
+            "sub.u32 n, n, 1;\n\t"
+            "setp.ne.u32 p, n, 0;\n\t"
+            "@p bra TRY;\n\t"
+            "setp.ne.u32 p, n, 0;\n"
+            "DONE:\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(at), "r"(parity), "r"(20000u)
+            : "memory");
+        if (done) return true;
         if (abort_flag != nullptr && *abort_flag) return false;
         const uint64_t now = global_timer_ns();
         if (t0 == 0) t0 = now;
@@ -135,9 +140,17 @@ __device__ __noinline__ bool wait_more(uint64_t* bar, uint32_t parity, uint64_t 
     }
 }
 
-__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, uint64_t limit_ns, volatile int* abort_flag) {
-    return mbar_try_wait(bar, parity) || wait_more(bar, parity, limit_ns, abort_flag);
-}
+// A place in a ring of stages and the parity of its current round.
+struct Ring {
+    int s = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void next(int n) {
+        if (++s == n) {
+            s = 0;
+            parity ^= 1;
+        }
+    }
+};
 
 struct Wait {
     uint64_t ns;
@@ -151,6 +164,20 @@ struct Wait {
         return false;
     }
 };
+
+// named barrier of 128 threads with an OR vote
+__device__ __forceinline__ bool any_of(uint32_t id, bool failed) {
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 q, %2, 0;\n\t"
+        "bar.red.or.pred p, %1, 128, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(any)
+        : "r"(id), "r"(static_cast<uint32_t>(failed))
+        : "memory");
+    return any != 0;
+}
 
 __device__ __forceinline__ void arrive_warp(uint64_t* bar, int lane) {
     __syncwarp();
@@ -210,19 +237,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         for (int s = 0; s < A.stages; ++s) {
             mbar_init(&sh.full[s], 1);
             mbar_init(&sh.ready[s], 1);
-            mbar_init(&sh.empty[s], 1 + 4 + (kStateOnly ? 0 : 4));
+            mbar_init(&sh.empty[s], 1 + 4 + (kStateOnly ? 0 : 8));
         }
         for (int s = 0; s < kCoefs; ++s) {
             mbar_init(&sh.coef_full[s], 1);
-            mbar_init(&sh.coef_empty[s], kStateOnly ? 8 : 16);
+            mbar_init(&sh.coef_empty[s], kStateOnly ? 12 : 24);
         }
         mbar_init(&sh.s_done, 1);
         mbar_init(&sh.p_ready, 4);
         mbar_init(&sh.zt_ready, 4);
-        mbar_init(&sh.h_ready, 4);
+        mbar_init(&sh.h_ready, 8);
         mbar_init(&sh.kv_done, 1);
         mbar_init(&sh.o_done, 1);
-        mbar_init(&sh.o_read, 4);
+        mbar_init(&sh.o_read, 8);
         mbar_init(&sh.drained, 1);
         sh.abort_flag = 0;
         mbar_fence_init();
@@ -230,7 +257,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    const uint32_t tmem = *static_cast<volatile uint32_t*>(&sh.tmem);
+    // all of the SM's tensor memory is this CTA's, so its address is 0
+    constexpr uint32_t tmem = 0;
     const uint32_t t_h = tmem, t_hb = t_h + dxp, t_zt = t_hb + dxp, t_s = t_zt + 96, t_o2 = t_s + C;
     const Wait wait{A.wait_ns, &sh.abort_flag, A.status};
     auto chunk_of = [&](int k) { return R.reverse ? c1 - 1 - k : c0 + k; };
@@ -239,27 +267,35 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         // ---- loads
         if (lane == 0) {
             const uint64_t pol = l2_policy_stream();
+            const int hx = h / R.xdiv, hy = h / R.ydiv, hz = h / R.zdiv, hw = h / R.wdiv;
+            const int bx = b * R.xb, by = b * R.yb, bz = b * R.zb, bw = b * R.wb;
+            const uint32_t bytes = ((kStateOnly ? px : 2 * px) + (dots ? 2 * pz : pz)) * kPanel;
             int issued = 0;
-            for (int k = 0; k < n; ++k) {
-                const int s = k % A.stages, round = k / A.stages;
-                if (round > 0 && !wait_bounded(&sh.empty[s], (round - 1) & 1, A.wait_ns, &sh.abort_flag)) {
+            Ring ring;
+#pragma unroll 1
+            for (int k = 0; k < n; ++k, ring.next(A.stages)) {
+                uint64_t* full = &sh.full[ring.s];
+                if (k >= A.stages && !wait_bounded(&sh.empty[ring.s], ring.parity ^ 1, A.wait_ns, &sh.abort_flag)) {
                     report_timeout(A.status, &sh.abort_flag);
                     break;
                 }
                 issued = k + 1;
                 if (k == A.drop_tile) continue;      // testing hook: this tile never arrives
-                unsigned char* st = tiles + s * A.stage_bytes;
+                unsigned char* st = tiles + ring.s * A.stage_bytes;
                 const int t0 = chunk_of(k) * C;
-                mbar_arrive_expect_tx(&sh.full[s], (kStateOnly ? 0 : px * kPanel) + (px + pz + (dots ? pz : 0)) * kPanel);
+                mbar_arrive_expect_tx(full, bytes);
+#pragma unroll 1
                 for (int p = 0; p < px; ++p) {
-                    if constexpr (!kStateOnly) tma_load_4d(st + p * kPanel, &R.x, p * 64, h / R.xdiv, t0, b * R.xb, &sh.full[s], pol);
-                    tma_load_4d(st + off_y + p * kPanel, &R.y, p * 64, h / R.ydiv, t0, b * R.yb, &sh.full[s], pol);
+                    if constexpr (!kStateOnly) tma_load_4d(st + p * kPanel, &R.x, p * 64, hx, t0, bx, full, pol);
+                    tma_load_4d(st + off_y + p * kPanel, &R.y, p * 64, hy, t0, by, full, pol);
                 }
+#pragma unroll 1
                 for (int p = 0; p < pz; ++p) {
-                    tma_load_4d(st + off_z + p * kPanel, &R.z, p * 64, h / R.zdiv, t0, b * R.zb, &sh.full[s], pol);
-                    if (dots) tma_load_4d(st + off_w + p * kPanel, &R.w, p * 64, h / R.wdiv, t0, b * R.wb, &sh.full[s], pol);
+                    tma_load_4d(st + off_z + p * kPanel, &R.z, p * 64, hz, t0, bz, full, pol);
+                    if (dots) tma_load_4d(st + off_w + p * kPanel, &R.w, p * 64, hw, t0, bw, full, pol);
                 }
             }
+#pragma unroll 1
             for (int k = max(0, issued - A.stages); k < issued; ++k) {
                 if (k == A.drop_tile) continue;
                 if (!wait_bounded(&sh.full[k % A.stages], (k / A.stages) & 1, A.wait_ns, nullptr))
@@ -269,16 +305,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         __syncwarp();
     } else if (warp == 7) {
         // ---- hand the stages on
-        for (int k = 0; k < n; ++k) {
-            const int s = k % A.stages;
-            if (!wait(&sh.full[s], k / A.stages)) break;
+        Ring ring;
+#pragma unroll 1
+        for (int k = 0; k < n; ++k, ring.next(A.stages)) {
+            const int s = ring.s;
+            if (!wait(&sh.full[s], ring.parity)) break;
             const int left = static_cast<int>(min(static_cast<int64_t>(C), len - static_cast<int64_t>(chunk_of(k)) * C));
             if (left < C) {
                 // rows past the length may hold anything (a NaN times a zero of P is a NaN): cleared
                 unsigned char* st = tiles + s * A.stage_bytes;
                 const int rows = C - left;
+#pragma unroll 1
                 for (int p = 0; p < px + pz; ++p) {
                     uint4* panel = reinterpret_cast<uint4*>(st + off_y + p * kPanel + left * 128);
+#pragma unroll 1
                     for (int e = lane; e < rows * 8; e += 32) panel[e] = make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
@@ -299,6 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         float g[2], next[2];
         float all = 1.0f;
         load(0, g);
+#pragma unroll 1
         for (int k = 0; k < n; ++k) {
             load(k + 1, next);
             const bool cut0 = g[0] < -104.0f, cut1 = g[1] < -104.0f;
@@ -336,14 +377,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 const int t = lane + 32 * u;
                 const uint64_t upto = cuts & (~0ull >> (63 - t));
                 const uint64_t after = t == 63 ? 0ull : cuts >> (t + 1);
-                const float er = upto ? 0.0f : exp2f(pre[u]), eu = after ? 0.0f : exp2f(suf[u]);
+                const float er = upto ? 0.0f : tc::exp2_approx(pre[u]), eu = after ? 0.0f : tc::exp2_approx(suf[u]);
                 c.g2[t] = pre[u];
                 c.read[t] = R.reverse ? eu : er;
                 c.upd[t] = R.reverse ? er : eu;
                 c.bound[t] = R.reverse ? (after ? t + __ffsll(static_cast<long long>(after)) - 1 : 63)
                                        : (upto ? 63 - __clzll(static_cast<long long>(upto)) : 0);
             }
-            const float whole = cuts ? 0.0f : exp2f(__shfl_sync(0xffffffffu, pre[1], 31));
+            const float whole = cuts ? 0.0f : tc::exp2_approx(__shfl_sync(0xffffffffu, pre[1], 31));
             if (lane == 0) c.decay = whole;
             all *= whole;
             arrive_warp(&sh.coef_full[s], lane);
@@ -360,19 +401,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         const uint32_t base = smem_u32(tiles);
         const uint64_t d_phi = tc::smem_desc(smem_u32(p_hi), 16, 1024);
         bool ok = true;
-        for (int k = 0; k < n; ++k) {
-            const int s = k % A.stages;
+        Ring ring;
+#pragma unroll 1
+        for (int k = 0; k < n; ++k, ring.next(A.stages)) {
+            const int s = ring.s;
             const uint32_t sx = base + s * A.stage_bytes;
             const uint64_t d_x = tc::smem_desc(sx, 16, 1024), d_y = tc::smem_desc(sx + off_y, 16, 1024);
             const uint64_t d_yt = tc::smem_desc(sx + off_y, kPanel, 1024), d_zt = tc::smem_desc(sx + off_z, kPanel, 1024);
-            if (!(ok = wait(&sh.ready[s], k / A.stages))) break;
+            if (!(ok = wait(&sh.ready[s], ring.parity))) break;
             if constexpr (!kStateOnly) {
                 // the region of the scores holds the last chunk's O1 until it is read
                 if (k > 0 && !(ok = wait(&sh.o_read, k - 1))) break;
                 tc::fence_after();
-                if (lane == 0) {
+                if (tc::elect()) {
+#pragma unroll 1
                     for (int p = 0; p < px; ++p)
-#pragma unroll
+#pragma unroll 1
                         for (int q = 0; q < 4; ++q)
                             tc::mma_ss(t_s, d_x + p * (kPanel >> 4) + q * 2, d_y + p * (kPanel >> 4) + q * 2, i_s, p + q > 0);
                     tc::commit(&sh.s_done);
@@ -382,20 +426,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             if (!(ok = wait(&sh.h_ready, k))) break;
             if constexpr (!kStateOnly) {
                 tc::fence_after();
-                if (lane == 0)
+                if (tc::elect())
+#pragma unroll 1
                     for (int p = 0; p < 2 * px; ++p) {
                         const uint64_t d = d_x + (p < px ? p : p - px) * (kPanel >> 4);
-#pragma unroll
+#pragma unroll 1
                         for (int q = 0; q < 4; ++q) tc::mma_ts(t_o2, t_hb + 32 * p + 8 * q, d + q * 2, i_s, p + q > 0);
                     }
                 __syncwarp();
             }
             if (!(ok = wait(&sh.zt_ready, k))) break;
             tc::fence_after();
-            if (lane == 0) {
+            if (tc::elect()) {
 #pragma unroll 1
                 for (int m = 0; m < 3; ++m)
-#pragma unroll
+#pragma unroll 1
                     for (int q = 0; q < C / 16; ++q) tc::mma_ts(t_h, t_zt + m * (C / 2) + q * 8, d_yt + q * 128, i_kv, true);
                 tc::commit(&sh.kv_done);
             }
@@ -403,16 +448,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             if constexpr (!kStateOnly) {
                 if (!(ok = wait(&sh.p_ready, k))) break;
                 tc::fence_after();
-                if (lane == 0) {
+                if (tc::elect()) {
 #pragma unroll 1
                     for (int m = 0; m < 2; ++m)
-#pragma unroll
+#pragma unroll 1
                         for (int q = 0; q < C / 16; ++q)
                             tc::mma_ss(t_s, d_zt + q * 128, d_phi + m * (kPanel >> 4) + q * 2, i_o1, m + q > 0);
                     tc::commit(&sh.o_done);
                 }
             }
-            if (lane == 0) tc::commit(&sh.empty[s]);
+            if (tc::elect()) tc::commit(&sh.empty[s]);
             __syncwarp();
         }
         // nothing of this CTA's may still run when its tensor memory goes
@@ -428,6 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             // rows of one half never see the columns of the other: forward rows 0-31 the late columns
             const float sign = R.reverse ? -1.0f : 1.0f;
             const bool none = R.reverse ? (warp & 1) > half : (warp & 1) < half;
+#pragma unroll 1
             for (int k = 0; k < n; ++k) {
                 const int cs = k % kCoefs;
                 if (!wait(&sh.coef_full[cs], k / kCoefs) || !wait(&sh.s_done, k)) break;
@@ -448,29 +494,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                     const int first = max(0, (R.reverse ? i : bound) - 32 * half), last = min(31, (R.reverse ? bound : i) - 32 * half);
                     const uint32_t seen = first <= last ? (0xffffffffu >> (31 - (last - first))) << first : 0u;
 #pragma unroll 1
-                    for (int q = 0; q < 2; ++q) {
-                        uint32_t r[16];
-                        tc::ld(from + 16 * q, r);
-                        const uint32_t mask = seen >> (16 * q);
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t r[8], hi[4], lo[4];
+                        tc::ld(from + 8 * q, r);
+                        const uint32_t mask = seen >> (8 * q);
                         tc::wait_ld();
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            uint32_t hi[4], lo[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int j = 8 * u + 2 * e;
-                                const float2 gj = *reinterpret_cast<const float2*>(&c.g2[32 * half + 16 * q + j]);
-                                const float2 d = tc::fma2(gj, make_float2(-sign, -sign), make_float2(gi * sign, gi * sign));
-                                float2 v = tc::mul2(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])),
-                                                    make_float2(tc::exp2_approx(d.x), tc::exp2_approx(d.y)));
-                                if (!(mask & (1u << j))) v.x = 0.0f;
-                                if (!(mask & (2u << j))) v.y = 0.0f;
-                                tc::split2(v, hi[e], lo[e]);
-                            }
-                            const uint32_t at = i * 128 + (((4 * half + 2 * q + u) ^ swz) << 4);
-                            *reinterpret_cast<uint4*>(p_hi + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                            *reinterpret_cast<uint4*>(p_lo + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        for (int e = 0; e < 4; ++e) {
+                            const int j = 2 * e;
+                            const float2 gj = *reinterpret_cast<const float2*>(&c.g2[32 * half + 8 * q + j]);
+                            const float2 d = tc::fma2(gj, make_float2(-sign, -sign), make_float2(gi * sign, gi * sign));
+                            float2 v = tc::mul2(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])),
+                                                make_float2(tc::exp2_approx(d.x), tc::exp2_approx(d.y)));
+                            if (!(mask & (1u << j))) v.x = 0.0f;
+                            if (!(mask & (2u << j))) v.y = 0.0f;
+                            tc::split2(v, hi[e], lo[e]);
                         }
+                        const uint32_t at = i * 128 + (((4 * half + q) ^ swz) << 4);
+                        *reinterpret_cast<uint4*>(p_hi + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4*>(p_lo + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
                 }
                 fence_proxy_async_smem();
@@ -490,28 +532,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         uint32_t off[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u) off[u] = (c / 64) * kPanel + ((((c % 64) >> 3) ^ u) << 4) + (c & 7) * 2 + u * 128;
-        for (int k = 0; k < n; ++k) {
-            const int s = k % A.stages, cs = k % kCoefs;
-            if (!wait(&sh.coef_full[cs], k / kCoefs) || !wait(&sh.ready[s], k / A.stages)) break;
+        Ring ring;
+#pragma unroll 1
+        for (int k = 0; k < n; ++k, ring.next(A.stages)) {
+            const int s = ring.s, cs = k % kCoefs;
+            if (!wait(&sh.coef_full[cs], k / kCoefs) || !wait(&sh.ready[s], ring.parity)) break;
             if (k > 0 && !wait(&sh.kv_done, k - 1)) break;
             tc::fence_after();
             if (on) {
                 const unsigned char* z = tiles + s * A.stage_bytes + off_z;
                 const Coef& cf = sh.coef[cs];
 #pragma unroll 1
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t t0[8], t1[8], t2[8];
+                for (int q = 0; q < 8; ++q) {
+                    uint32_t t0[4], t1[4], t2[4];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float2 w = *reinterpret_cast<const float2*>(&cf.upd[16 * q + 2 * e]);
-                        const unsigned char* at = z + q * 2048 + (e / 4) * 1024;
-                        const uint32_t z0 = *reinterpret_cast<const unsigned short*>(at + off[2 * e % 8]);
-                        const uint32_t z1 = *reinterpret_cast<const unsigned short*>(at + off[(2 * e + 1) % 8]);
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 w = *reinterpret_cast<const float2*>(&cf.upd[8 * q + 2 * e]);
+                        const uint32_t z0 = *reinterpret_cast<const unsigned short*>(z + q * 1024 + off[2 * e]);
+                        const uint32_t z1 = *reinterpret_cast<const unsigned short*>(z + q * 1024 + off[2 * e + 1]);
                         tc::split3(tc::mul2(make_float2(__uint_as_float(z0 << 16), __uint_as_float(z1 << 16)), w), t0[e], t1[e], t2[e]);
                     }
-                    tc::st(to + 8 * q, t0);
-                    tc::st(to + 32 + 8 * q, t1);
-                    tc::st(to + 64 + 8 * q, t2);
+                    tc::st(to + 4 * q, t0);
+                    tc::st(to + 32 + 4 * q, t1);
+                    tc::st(to + 64 + 4 * q, t2);
                 }
                 tc::wait_st();
             }
@@ -523,11 +566,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 mbar_arrive(&sh.coef_empty[cs]);
             }
         }
-    } else if (warp < 16) {
-        // ---- the state: lane = value column c, key columns along
-        const int c = (warp - 12) * 32 + lane;
-        const uint32_t lanes = static_cast<uint32_t>((warp - 12) * 32) << 16;
-        const bool on = (warp - 12) * 32 < R.dz, real = c < R.dz;
+    } else if (warp < 20) {
+        // ---- the state: lane = value column c, half of the key columns along
+        const int slice = warp & 3, side = (warp - 12) / 4, a_lo = side * (dxp / 2), a_hi = a_lo + dxp / 2;
+        const int c = slice * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>(slice * 32) << 16;
+        const bool on = slice * 32 < R.dz, real = c < R.dz;
         const int64_t size = static_cast<int64_t>(R.dx) * R.dz;
         // where the run's first state comes from
         const float* from = nullptr;
@@ -548,9 +592,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 fa = R.dz;
             }
         }
-        const int slice = warp - 12;
+        const int slices = (R.dz + 31) / 32;
         bool ok = true;
         // n + 1 visits: the last one only takes the final state out
+#pragma unroll 1
         for (int k = 0; k <= n && ok; ++k) {
             const int cs = k % kCoefs;
             if (k > 0) {
@@ -570,11 +615,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             float* anchor_to = nullptr;
             if (!kStateOnly && on && R.anchors != nullptr) {
                 if (R.anchor_dots == nullptr) {
-                    if (k > 0 && ((done + 1) % A.anchor_every == 0 || done == chunks - 1))
-                        dump = R.anchors + (bh * A.n_anchors + done / A.anchor_every) * size + c;
-                } else if (k < n && ((next + 1) % A.anchor_every == 0 || next == chunks - 1)) {
-                    anchor = R.anchors + (bh * A.n_anchors + next / A.anchor_every) * size + c;
-                    anchor_to = R.anchor_dots + (slice * A.BH + bh) * A.n_anchors + next / A.anchor_every;
+                    if (k > 0 && ((done + 1) % kAnchorChunks == 0 || done == chunks - 1))
+                        dump = R.anchors + (bh * A.n_anchors + done / kAnchorChunks) * size + c;
+                } else if (k < n && ((next + 1) % kAnchorChunks == 0 || next == chunks - 1)) {
+                    anchor = R.anchors + (bh * A.n_anchors + next / kAnchorChunks) * size + c;
+                    anchor_to = R.anchor_dots + ((side * slices + slice) * A.BH + bh) * A.n_anchors + next / kAnchorChunks;
                 }
             }
             float* out = nullptr;
@@ -591,7 +636,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 }
             }
             if (k == 0 && on) {
-                for (int a0 = 0; a0 < dxp; a0 += 8) {
+#pragma unroll 1
+                for (int a0 = a_lo; a0 < a_hi; a0 += 8) {
                     uint32_t r[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
@@ -605,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             const bool leaves = __any_sync(0xffffffffu, out != nullptr || dump != nullptr || anchor != nullptr);
             if (leaves && on)
 #pragma unroll 1
-                for (int a0 = 0; a0 < R.dx; a0 += 8) {
+                for (int a0 = a_lo; a0 < min(a_hi, R.dx); a0 += 8) {
                     uint32_t r[8];
                     tc::ld(t_h + lanes + a0, r);
                     tc::wait_ld();
@@ -621,12 +667,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 }
             if (on && k < n)
 #pragma unroll 1
-                for (int a0 = 0; a0 < dxp; a0 += 32) {
-                    uint32_t r[32], hi[16], lo[16];
+                for (int a0 = a_lo; a0 < a_hi; a0 += 16) {
+                    uint32_t r[16], hi[8], lo[8];
                     tc::ld(t_h + lanes + a0, r);
                     tc::wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
+                    for (int e = 0; e < 8; ++e) {
                         const float2 v = make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
                         if constexpr (!kStateOnly) tc::split2(v, hi[e], lo[e]);
                         const float2 d = tc::mul2(v, make_float2(decay, decay));
@@ -657,32 +703,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
     } else {
         // ---- outputs: lane = value column c, tokens along the columns
         if constexpr (!kStateOnly) {
-            const int c = (warp - 16) * 32 + lane;
-            const uint32_t lanes = static_cast<uint32_t>((warp - 16) * 32) << 16;
-            const bool on = (warp - 16) * 32 < R.dz, real = c < R.dz;
-            const int64_t out0 = b * R.ob + static_cast<int64_t>(h) * R.oh + c;
-            __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(R.out) + out0;
-            float* of = static_cast<float*>(R.out) + out0;
-            // this segment's rows past the length are zero
-            const int64_t hi = seg == A.n_segs - 1 ? A.T : min(A.T, static_cast<int64_t>(c0 + A.seg_chunks) * C);
-            if (real)
-                for (int64_t t = max(len, static_cast<int64_t>(c0) * C); t < hi; ++t) {
-                    if (R.out_f32) of[t * R.ot] = 0.0f;
-                    else ob[t * R.ot] = __float2bfloat16_rn(0.0f);
-                }
+            const int slice = warp & 3, side = (warp - 20) / 4;       // 32 value columns, 32 of the tokens
+            const int c = slice * 32 + lane;
+            const uint32_t lanes = static_cast<uint32_t>(slice * 32) << 16;
+            const bool on = slice * 32 < R.dz, real = c < R.dz;
+            float* of = static_cast<float*>(R.out) + b * R.ob + static_cast<int64_t>(h) * R.oh + c;
             uint32_t off[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u) off[u] = (c / 64) * kPanel + ((((c % 64) >> 3) ^ u) << 4) + (c & 7) * 2 + u * 128;
-            const int wt = threadIdx.x - 512;
+            const int wt = (threadIdx.x - 640) & 127;
             // pieces of 16 bytes a row, and the rows of a pass over the tile
             const int cols = dzp / 8, rows = 128 / cols;
             const bool wide = !R.out_f32 && R.wide;
-            for (int k = 0; k < n; ++k) {
-                const int s = k % A.stages, cs = k % kCoefs;
+            Ring ring;
+#pragma unroll 1
+            for (int k = 0; k < n; ++k, ring.next(A.stages)) {
+                const int s = ring.s, cs = k % kCoefs;
                 // (ready: the W tile is there, and its place is the output tile's from here on)
-                const bool go = wait(&sh.coef_full[cs], k / kCoefs) && wait(&sh.o_done, k) && wait(&sh.ready[s], k / A.stages);
-                // the four warps leave together: they meet at a barrier below
-                if (consumer_vote_any_failed(!go, 128)) break;
+                const bool go = wait(&sh.coef_full[cs], k / kCoefs) && wait(&sh.o_done, k) && wait(&sh.ready[s], ring.parity);
+                // a side's four warps leave together: they meet at a barrier below
+                if (any_of(side + 1, !go)) break;
                 tc::fence_after();
                 const int64_t t0 = static_cast<int64_t>(chunk_of(k)) * C;
                 const int left = static_cast<int>(min(static_cast<int64_t>(C), len - t0));
@@ -691,11 +731,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 if (on) {
                     const float2 scale = make_float2(R.out_scale, R.out_scale);
 #pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {
+                    for (int q = 2 * side; q < 2 * side + 2; ++q) {
                         uint32_t r1[16], r2[16];
                         tc::ld(t_s + lanes + 16 * q, r1);
                         tc::ld(t_o2 + lanes + 16 * q, r2);
                         tc::wait_ld();
+                        if (q == 2 * side + 1) {
+                            // the products of the next chunk may overwrite what was read
+                            tc::fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&sh.o_read);
+                        }
                         float v[16];
 #pragma unroll
                         for (int e = 0; e < 16; e += 2) {
@@ -726,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                             }
                             m[0] += __shfl_xor_sync(0xffffffffu, m[0], 1);
                             const int row = 16 * q + lane / 2;
-                            if (row < left && !(lane & 1)) R.dots[((warp - 16) * A.BH + bh) * A.T + t0 + row] = m[0];
+                            if (row < left && !(lane & 1)) R.dots[(slice * A.BH + bh) * A.T + t0 + row] = m[0];
                         }
                         if (R.out_f32) {
                             if (real) {
@@ -744,21 +790,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                             }
                         }
                     }
-                }
-                // the products of the next chunk may overwrite what was read
-                tc::fence_before();
-                __syncwarp();
-                if (lane == 0) {
+                } else if (lane == 0) {
                     mbar_arrive(&sh.o_read);
-                    mbar_arrive(&sh.coef_empty[cs]);
                 }
+                arrive_warp(&sh.coef_empty[cs], lane);
                 if (!R.out_f32) {
-                    named_barrier_sync(2, 128);
+                    named_barrier_sync(side + 1, 128);
                     // rows out, 16 bytes a thread where the result's addresses allow it
-                    const int piece = wt % cols;
-                    for (int row = wt / cols; row < left; row += rows) {
+                    const int piece = wt & (cols - 1);
+                    unsigned short* base = static_cast<unsigned short*>(R.out) + b * R.ob + static_cast<int64_t>(h) * R.oh + t0 * R.ot + piece * 8;
+#pragma unroll 2
+                    for (int row = 32 * side + (wt >> (cols == 16 ? 4 : 3)); row < min(left, 32 * side + 32); row += rows) {
                         const uint4 u = *reinterpret_cast<const uint4*>(w + (piece / 8) * kPanel + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
-                        __nv_bfloat16* to = static_cast<__nv_bfloat16*>(R.out) + b * R.ob + static_cast<int64_t>(h) * R.oh + (t0 + row) * R.ot + piece * 8;
+                        unsigned short* to = base + row * R.ot;
                         if (wide) {
                             if (piece * 8 < R.dz) *reinterpret_cast<uint4*>(to) = u;
                         } else {
@@ -766,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
                                 if (piece * 8 + e < R.dz)
-                                    *reinterpret_cast<unsigned short*>(to + e) = static_cast<unsigned short>(e % 2 ? x[e / 2] >> 16 : x[e / 2]);
+                                    to[e] = static_cast<unsigned short>(e % 2 ? x[e / 2] >> 16 : x[e / 2]);
                         }
                     }
                 }
@@ -774,13 +818,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 fence_proxy_async_smem();
                 arrive_warp(&sh.empty[s], lane);
             }
+            // this segment's rows past the length are zero
+            const int64_t lo = max(len, static_cast<int64_t>(c0) * C);
+            const int64_t hi = seg == A.n_segs - 1 ? A.T : min(A.T, static_cast<int64_t>(c0 + A.seg_chunks) * C);
+            if (wide) {
+                unsigned short* to = static_cast<unsigned short*>(R.out) + b * R.ob + static_cast<int64_t>(h) * R.oh + (wt & (cols - 1)) * 8;
+                if ((wt & (cols - 1)) * 8 < R.dz)
+#pragma unroll 4
+                    for (int64_t t = lo + side * rows + wt / cols; t < hi; t += 2 * rows) *reinterpret_cast<uint4*>(to + t * R.ot) = make_uint4(0, 0, 0, 0);
+            } else if (real) {
+#pragma unroll 1
+                for (int64_t t = lo + side; t < hi; t += 2) {
+                    if (R.out_f32) of[t * R.ot] = 0.0f;
+                    else static_cast<unsigned short*>(R.out)[b * R.ob + static_cast<int64_t>(h) * R.oh + t * R.ot + c] = 0;
+                }
+            }
         }
     }
     tc::fence_before();
     __syncthreads();
     if (warp == 2) {
         tc::fence_after();
-        tc::dealloc(tmem, kTmemCols);
+        tc::dealloc(sh.tmem, kTmemCols);
     }
 }
 
@@ -891,7 +950,6 @@ cudaError_t launch_attn_tc(const AttnLaunch& L, int* kernels, const char** err) 
     A.gt = L.gt;
     A.gh = L.gh;
     A.lengths = L.lengths;
-    A.anchor_every = L.anchor_every;
     A.n_anchors = L.n_anchors;
     A.seg_states = L.seg_states;
     A.seg_decays = L.seg_decays;
