@@ -68,6 +68,8 @@ _lib = None
 def lib():
     """Load libes.so (built in-tree); raise LibraryMissing if it is absent."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
