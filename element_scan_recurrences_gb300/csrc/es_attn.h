@@ -174,6 +174,7 @@ struct RotateLaunch {
     int num_sms;
 };
 int rotate_blocks(const RotateLaunch& L, int side);
+int64_t rotate_units(const RotateLaunch& L, int side);     // below 2^31 - 2^20: the kernel counts them in 32 bits
 cudaError_t launch_rotate(const RotateLaunch& L, int* kernels);
 
 }  // namespace es

@@ -578,6 +578,8 @@ es_status plan_rotate(const char* fn, const es_qk_norm_rotate_args* a, const es_
     L.pt = a->position_t;
     L.backward = backward ? 1 : 0;
     P->empty = rows == 0 || a->q.heads + a->k.heads == 0;
+    if (rows >= 0x7ff00000 || rotate_units(L, 0) >= 0x7ff00000 || rotate_units(L, 1) >= 0x7ff00000)
+        return api_fail(ES_E_UNSUPPORTED, "%s: %lld tokens are too many", fn, static_cast<long long>(rows));
     if (!P->empty && (gw[0] != nullptr || gw[1] != nullptr))
         P->bytes = static_cast<size_t>(rotate_blocks(L, 0) + rotate_blocks(L, 1)) * d * 4;
     return ES_OK;

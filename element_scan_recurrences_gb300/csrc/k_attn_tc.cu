@@ -503,8 +503,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                         for (int e = 0; e < 4; ++e) {
                             const int j = 2 * e;
                             const float2 gj = *reinterpret_cast<const float2*>(&c.g2[32 * half + 8 * q + j]);
-                            const float2 d = tc::fma2(gj, make_float2(-sign, -sign), make_float2(gi * sign, gi * sign));
-                            float2 v = tc::mul2(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])),
+                            const float2 d = pair_fma(gj, make_float2(-sign, -sign), make_float2(gi * sign, gi * sign));
+                            float2 v = pair_mul(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])),
                                                 make_float2(tc::exp2_approx(d.x), tc::exp2_approx(d.y)));
                             if (!(mask & (1u << j))) v.x = 0.0f;
                             if (!(mask & (2u << j))) v.y = 0.0f;
@@ -550,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                         const float2 w = *reinterpret_cast<const float2*>(&cf.upd[8 * q + 2 * e]);
                         const uint32_t z0 = *reinterpret_cast<const unsigned short*>(z + q * 1024 + off[2 * e]);
                         const uint32_t z1 = *reinterpret_cast<const unsigned short*>(z + q * 1024 + off[2 * e + 1]);
-                        tc::split3(tc::mul2(make_float2(__uint_as_float(z0 << 16), __uint_as_float(z1 << 16)), w), t0[e], t1[e], t2[e]);
+                        tc::split3(pair_mul(make_float2(__uint_as_float(z0 << 16), __uint_as_float(z1 << 16)), w), t0[e], t1[e], t2[e]);
                     }
                     tc::st(to + 4 * q, t0);
                     tc::st(to + 32 + 4 * q, t1);
@@ -675,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                     for (int e = 0; e < 8; ++e) {
                         const float2 v = make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
                         if constexpr (!kStateOnly) tc::split2(v, hi[e], lo[e]);
-                        const float2 d = tc::mul2(v, make_float2(decay, decay));
+                        const float2 d = pair_mul(v, make_float2(decay, decay));
                         r[2 * e] = __float_as_uint(d.x);
                         r[2 * e + 1] = __float_as_uint(d.y);
                     }
@@ -746,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
 #pragma unroll
                         for (int e = 0; e < 16; e += 2) {
                             const float2 rd = *reinterpret_cast<const float2*>(&cf.read[16 * q + e]);
-                            const float2 o = tc::mul2(tc::fma2(make_float2(__uint_as_float(r2[e]), __uint_as_float(r2[e + 1])), rd,
+                            const float2 o = pair_mul(pair_fma(make_float2(__uint_as_float(r2[e]), __uint_as_float(r2[e + 1])), rd,
                                                                make_float2(__uint_as_float(r1[e]), __uint_as_float(r1[e + 1]))), scale);
                             v[e] = o.x;
                             v[e + 1] = o.y;
