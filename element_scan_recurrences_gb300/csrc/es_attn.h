@@ -40,6 +40,7 @@ struct AttnRun {
     int64_t sa, sc;
     float init_scale, fin_scale, out_scale;
     int reverse;
+    int state_result;            // the run's last state can be asked for (its results do not depend on whether it is)
     // For the decays' gradient: out[t] (unrounded) . w[t], per slice of dz
     // columns, [slices, B*H, T]; null: not wanted.
     AttnOperand w;

@@ -231,6 +231,7 @@ es_status plan_attn(const char* fn, const es_linear_attention_args* a, const es_
         f.sc = 1;
         f.init_scale = f.fin_scale = 1.0f;
         f.out_scale = scale;
+        f.state_result = 1;
         f.dx = static_cast<int>(dk);
         f.dz = static_cast<int>(dv);
     } else {
@@ -261,6 +262,7 @@ es_status plan_attn(const char* fn, const es_linear_attention_args* a, const es_
         rv.init = rk.init = g->grad_final_state;
         rv.init_scale = rk.init_scale = 1.0f / scale;
         rv.fin = g->grad_initial_state;
+        rv.state_result = 1;
         rv.fin_scale = scale;
     }
     // the path: every run's operands have to suit the tensor-core kernel's loads

@@ -28,6 +28,12 @@ __device__ __forceinline__ void dealloc(uint32_t addr, uint32_t cols) {
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// keeps the uses of loaded values behind the wait before it
+template <int N>
+__device__ __forceinline__ void loaded(uint32_t (&r)[N]) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) asm volatile("" : "+r"(r[e]));
+}
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // N columns of the warp's 32 lanes: lane l of the warp holds its lane's N values

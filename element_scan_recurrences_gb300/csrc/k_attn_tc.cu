@@ -47,7 +47,6 @@ namespace {
 
 constexpr int C = kAttnTcChunk;               // 64 tokens
 constexpr int kThreads = 896;
-constexpr int kCoefs = 4;                     // slots of chunk coefficients (a power of two)
 constexpr int kAnchorChunks = kAttnAnchorTokens / C;
 constexpr int kMaxStages = 4;
 constexpr uint32_t kPanel = C * 128;          // bytes of a panel: 64 rows of 64 bf16
@@ -76,6 +75,7 @@ struct TcRun {
     int xb, yb, zb, wb;                       // 1; 0: one batch row for all
     int dx, dz;                               // real widths
     int reverse, out_f32;
+    int terms;                                // bf16 terms of the scaled Z: 3 where the state can be a result, else 2
     int wide;                                 // the result's addresses and strides keep to 16 bytes
 };
 
@@ -100,11 +100,10 @@ struct TcArgs {
 
 struct Shared {
     uint64_t full[kMaxStages], ready[kMaxStages], empty[kMaxStages];
-    uint64_t coef_full[kCoefs], coef_empty[kCoefs];
-    uint64_t s_done, p_ready, zt_ready, h_ready, kv_done, o_done, o_read, drained;
+    uint64_t s_done, p_ready, zh_ready, kv_done, o_done, o_read, drained;
     uint32_t tmem;
     int abort_flag;
-    Coef coef[kCoefs];
+    Coef coef[kMaxStages];
 };
 
 // A bounded wait that lets the hardware hold the thread, up to 20 us a try: a
@@ -236,17 +235,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
     if (threadIdx.x == 0) {
         for (int s = 0; s < A.stages; ++s) {
             mbar_init(&sh.full[s], 1);
-            mbar_init(&sh.ready[s], 1);
-            mbar_init(&sh.empty[s], 1 + 4 + (kStateOnly ? 0 : 8));
-        }
-        for (int s = 0; s < kCoefs; ++s) {
-            mbar_init(&sh.coef_full[s], 1);
-            mbar_init(&sh.coef_empty[s], kStateOnly ? 12 : 24);
+            mbar_init(&sh.ready[s], 2);                              // the tiles, the coefficients
+            mbar_init(&sh.empty[s], 1 + 4 + 8 + (kStateOnly ? 0 : 4 + 8));   // products, Z, state, P, outputs
         }
         mbar_init(&sh.s_done, 1);
         mbar_init(&sh.p_ready, 4);
-        mbar_init(&sh.zt_ready, 4);
-        mbar_init(&sh.h_ready, 8);
+        mbar_init(&sh.zh_ready, 4 + 8);
         mbar_init(&sh.kv_done, 1);
         mbar_init(&sh.o_done, 1);
         mbar_init(&sh.o_read, 8);
@@ -259,7 +253,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
     tc::fence_after();
     // all of the SM's tensor memory is this CTA's, so its address is 0
     constexpr uint32_t tmem = 0;
-    const uint32_t t_h = tmem, t_hb = t_h + dxp, t_zt = t_hb + dxp, t_s = t_zt + 96, t_o2 = t_s + C;
+    const uint32_t t_h = tmem, t_hb = t_h + dxp, t_zt = t_hb + dxp, t_s = t_zt + R.terms * (C / 2), t_o2 = t_s + C;
+    const uint32_t t_o1 = R.terms == 2 ? t_o2 + C : t_s;
     const Wait wait{A.wait_ns, &sh.abort_flag, A.status};
     auto chunk_of = [&](int k) { return R.reverse ? c1 - 1 - k : c0 + k; };
 
@@ -339,8 +334,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         float g[2], next[2];
         float all = 1.0f;
         load(0, g);
+        Ring ring;
 #pragma unroll 1
-        for (int k = 0; k < n; ++k) {
+        for (int k = 0; k < n; ++k, ring.next(A.stages)) {
             load(k + 1, next);
             const bool cut0 = g[0] < -104.0f, cut1 = g[1] < -104.0f;
             const uint64_t cuts = static_cast<uint64_t>(__ballot_sync(0xffffffffu, cut0)) |
@@ -369,9 +365,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 }
             pre[1] += __shfl_sync(0xffffffffu, pre[0], 31);
             suf[0] += __shfl_sync(0xffffffffu, suf[1], 0);
-            const int s = k % kCoefs;
-            if (k >= kCoefs && !wait(&sh.coef_empty[s], k / kCoefs - 1)) break;
-            Coef& c = sh.coef[s];
+            if (k >= A.stages && !wait(&sh.empty[ring.s], ring.parity ^ 1)) break;
+            Coef& c = sh.coef[ring.s];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int t = lane + 32 * u;
@@ -387,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             const float whole = cuts ? 0.0f : tc::exp2_approx(__shfl_sync(0xffffffffu, pre[1], 31));
             if (lane == 0) c.decay = whole;
             all *= whole;
-            arrive_warp(&sh.coef_full[s], lane);
+            arrive_warp(&sh.ready[ring.s], lane);
             g[0] = next[0];
             g[1] = next[1];
         }
@@ -410,8 +405,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             const uint64_t d_yt = tc::smem_desc(sx + off_y, kPanel, 1024), d_zt = tc::smem_desc(sx + off_z, kPanel, 1024);
             if (!(ok = wait(&sh.ready[s], ring.parity))) break;
             if constexpr (!kStateOnly) {
-                // the region of the scores holds the last chunk's O1 until it is read
-                if (k > 0 && !(ok = wait(&sh.o_read, k - 1))) break;
+                // with three terms of Z the scores' region holds the last chunk's O1 until it is read
+                if (R.terms == 3 && k > 0 && !(ok = wait(&sh.o_read, k - 1))) break;
                 tc::fence_after();
                 if (tc::elect()) {
 #pragma unroll 1
@@ -422,24 +417,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                     tc::commit(&sh.s_done);
                 }
                 __syncwarp();
+                if (R.terms == 2 && k > 0 && !(ok = wait(&sh.o_read, k - 1))) break;
             }
-            if (!(ok = wait(&sh.h_ready, k))) break;
-            if constexpr (!kStateOnly) {
-                tc::fence_after();
-                if (tc::elect())
+            if (!(ok = wait(&sh.zh_ready, k))) break;
+            tc::fence_after();
+            if (tc::elect()) {
+                if constexpr (!kStateOnly) {
 #pragma unroll 1
                     for (int p = 0; p < 2 * px; ++p) {
                         const uint64_t d = d_x + (p < px ? p : p - px) * (kPanel >> 4);
 #pragma unroll 1
                         for (int q = 0; q < 4; ++q) tc::mma_ts(t_o2, t_hb + 32 * p + 8 * q, d + q * 2, i_s, p + q > 0);
                     }
-                __syncwarp();
-            }
-            if (!(ok = wait(&sh.zt_ready, k))) break;
-            tc::fence_after();
-            if (tc::elect()) {
+                }
 #pragma unroll 1
-                for (int m = 0; m < 3; ++m)
+                for (int m = 0; m < R.terms; ++m)
 #pragma unroll 1
                     for (int q = 0; q < C / 16; ++q) tc::mma_ts(t_h, t_zt + m * (C / 2) + q * 8, d_yt + q * 128, i_kv, true);
                 tc::commit(&sh.kv_done);
@@ -453,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                     for (int m = 0; m < 2; ++m)
 #pragma unroll 1
                         for (int q = 0; q < C / 16; ++q)
-                            tc::mma_ss(t_s, d_zt + q * 128, d_phi + m * (kPanel >> 4) + q * 2, i_o1, m + q > 0);
+                            tc::mma_ss(t_o1, d_zt + q * 128, d_phi + m * (kPanel >> 4) + q * 2, i_o1, m + q > 0);
                     tc::commit(&sh.o_done);
                 }
             }
@@ -473,11 +465,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             // rows of one half never see the columns of the other: forward rows 0-31 the late columns
             const float sign = R.reverse ? -1.0f : 1.0f;
             const bool none = R.reverse ? (warp & 1) > half : (warp & 1) < half;
+            Ring ring;
 #pragma unroll 1
-            for (int k = 0; k < n; ++k) {
-                const int cs = k % kCoefs;
-                if (!wait(&sh.coef_full[cs], k / kCoefs) || !wait(&sh.s_done, k)) break;
-                const Coef& c = sh.coef[cs];
+            for (int k = 0; k < n; ++k, ring.next(A.stages)) {
+                if (!wait(&sh.ready[ring.s], ring.parity) || !wait(&sh.s_done, k)) break;
+                const Coef& c = sh.coef[ring.s];
                 const uint32_t swz = i & 7;
                 if (none) {
 #pragma unroll
@@ -499,6 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                         tc::ld(from + 8 * q, r);
                         const uint32_t mask = seen >> (8 * q);
                         tc::wait_ld();
+                        tc::loaded(r);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int j = 2 * e;
@@ -520,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(&sh.p_ready);
-                    mbar_arrive(&sh.coef_empty[cs]);
+                    mbar_arrive(&sh.empty[ring.s]);
                 }
             }
         }
@@ -535,35 +528,42 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         Ring ring;
 #pragma unroll 1
         for (int k = 0; k < n; ++k, ring.next(A.stages)) {
-            const int s = ring.s, cs = k % kCoefs;
-            if (!wait(&sh.coef_full[cs], k / kCoefs) || !wait(&sh.ready[s], ring.parity)) break;
+            const int s = ring.s;
+            if (!wait(&sh.ready[s], ring.parity)) break;
             if (k > 0 && !wait(&sh.kv_done, k - 1)) break;
             tc::fence_after();
             if (on) {
                 const unsigned char* z = tiles + s * A.stage_bytes + off_z;
-                const Coef& cf = sh.coef[cs];
+                const Coef& cf = sh.coef[s];
 #pragma unroll 1
                 for (int q = 0; q < 8; ++q) {
                     uint32_t t0[4], t1[4], t2[4];
+                    float2 v[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float2 w = *reinterpret_cast<const float2*>(&cf.upd[8 * q + 2 * e]);
                         const uint32_t z0 = *reinterpret_cast<const unsigned short*>(z + q * 1024 + off[2 * e]);
                         const uint32_t z1 = *reinterpret_cast<const unsigned short*>(z + q * 1024 + off[2 * e + 1]);
-                        tc::split3(pair_mul(make_float2(__uint_as_float(z0 << 16), __uint_as_float(z1 << 16)), w), t0[e], t1[e], t2[e]);
+                        v[e] = pair_mul(make_float2(__uint_as_float(z0 << 16), __uint_as_float(z1 << 16)), w);
+                    }
+                    if (R.terms == 2) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) tc::split2(v[e], t0[e], t1[e]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) tc::split3(v[e], t0[e], t1[e], t2[e]);
+                        tc::st(to + 64 + 4 * q, t2);
                     }
                     tc::st(to + 4 * q, t0);
                     tc::st(to + 32 + 4 * q, t1);
-                    tc::st(to + 64 + 4 * q, t2);
                 }
                 tc::wait_st();
             }
             tc::fence_before();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&sh.zt_ready);
+                mbar_arrive(&sh.zh_ready);
                 mbar_arrive(&sh.empty[s]);
-                mbar_arrive(&sh.coef_empty[cs]);
             }
         }
     } else if (warp < 20) {
@@ -594,10 +594,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         }
         const int slices = (R.dz + 31) / 32;
         bool ok = true;
+        Ring ring;
         // n + 1 visits: the last one only takes the final state out
 #pragma unroll 1
-        for (int k = 0; k <= n && ok; ++k) {
-            const int cs = k % kCoefs;
+        for (int k = 0; k <= n && ok; ++k, ring.next(A.stages)) {
             if (k > 0) {
                 ok = wait(&sh.kv_done, k - 1);
                 if (!ok) break;
@@ -605,8 +605,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             }
             float decay = 0.0f;
             if (k < n) {
-                if (!(ok = wait(&sh.coef_full[cs], k / kCoefs))) break;
-                decay = sh.coef[cs].decay;
+                if (!(ok = wait(&sh.ready[ring.s], ring.parity))) break;
+                decay = sh.coef[ring.s].decay;
             }
             // the state between trip k - 1 and trip k is an anchor's
             const int done = k > 0 ? chunk_of(k - 1) : 0, next = k < n ? chunk_of(k) : 0;
@@ -655,6 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                     uint32_t r[8];
                     tc::ld(t_h + lanes + a0, r);
                     tc::wait_ld();
+                    tc::loaded(r);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const float v = __uint_as_float(r[e]);
@@ -665,12 +666,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                         if (out != nullptr) out[(a0 + e) * oa] = v * os;
                     }
                 }
-            if (on && k < n)
-#pragma unroll 1
-                for (int a0 = a_lo; a0 < a_hi; a0 += 16) {
-                    uint32_t r[16], hi[8], lo[8];
-                    tc::ld(t_h + lanes + a0, r);
-                    tc::wait_ld();
+            if (on && k < n) {
+                // pieces of 16 columns, an even number: one on its way while the other is split
+                auto piece = [&](int a0, uint32_t (&r)[16]) {
+                    uint32_t hi[8], lo[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const float2 v = make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
@@ -684,7 +683,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                         tc::st(t_hb + lanes + dxp / 2 + a0 / 2, lo);
                     }
                     tc::st(t_h + lanes + a0, r);
+                };
+                uint32_t r0[16], r1[16];
+                tc::ld(t_h + lanes + a_lo, r0);
+#pragma unroll 1
+                for (int a0 = a_lo; a0 < a_hi; a0 += 32) {
+                    tc::wait_ld();
+                    tc::loaded(r0);
+                    tc::ld(t_h + lanes + a0 + 16, r1);
+                    piece(a0, r0);
+                    tc::wait_ld();
+                    tc::loaded(r1);
+                    if (a0 + 32 < a_hi) tc::ld(t_h + lanes + a0 + 32, r0);
+                    piece(a0 + 16, r1);
                 }
+            }
             if (anchor_to != nullptr) {
 #pragma unroll
                 for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
@@ -695,8 +708,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 tc::fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&sh.h_ready);
-                    mbar_arrive(&sh.coef_empty[cs]);
+                    mbar_arrive(&sh.zh_ready);
+                    mbar_arrive(&sh.empty[ring.s]);
                 }
             }
         }
@@ -718,24 +731,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             Ring ring;
 #pragma unroll 1
             for (int k = 0; k < n; ++k, ring.next(A.stages)) {
-                const int s = ring.s, cs = k % kCoefs;
+                const int s = ring.s;
                 // (ready: the W tile is there, and its place is the output tile's from here on)
-                const bool go = wait(&sh.coef_full[cs], k / kCoefs) && wait(&sh.o_done, k) && wait(&sh.ready[s], ring.parity);
+                const bool go = wait(&sh.ready[s], ring.parity) && wait(&sh.o_done, k);
                 // a side's four warps leave together: they meet at a barrier below
                 if (any_of(side + 1, !go)) break;
                 tc::fence_after();
                 const int64_t t0 = static_cast<int64_t>(chunk_of(k)) * C;
                 const int left = static_cast<int>(min(static_cast<int64_t>(C), len - t0));
-                const Coef& cf = sh.coef[cs];
+                const Coef& cf = sh.coef[s];
                 unsigned char* w = tiles + s * A.stage_bytes + off_w;
                 if (on) {
                     const float2 scale = make_float2(R.out_scale, R.out_scale);
 #pragma unroll 1
                     for (int q = 2 * side; q < 2 * side + 2; ++q) {
                         uint32_t r1[16], r2[16];
-                        tc::ld(t_s + lanes + 16 * q, r1);
+                        tc::ld(t_o1 + lanes + 16 * q, r1);
                         tc::ld(t_o2 + lanes + 16 * q, r2);
                         tc::wait_ld();
+                        tc::loaded(r1);
+                        tc::loaded(r2);
                         if (q == 2 * side + 1) {
                             // the products of the next chunk may overwrite what was read
                             tc::fence_before();
@@ -793,7 +808,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 } else if (lane == 0) {
                     mbar_arrive(&sh.o_read);
                 }
-                arrive_warp(&sh.coef_empty[cs], lane);
+                // the next load of this place comes through the async proxy
+                fence_proxy_async_smem();
                 if (!R.out_f32) {
                     named_barrier_sync(side + 1, 128);
                     // rows out, 16 bytes a thread where the result's addresses allow it
@@ -814,8 +830,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                         }
                     }
                 }
-                // the next load of this place comes through the async proxy
-                fence_proxy_async_smem();
                 arrive_warp(&sh.empty[s], lane);
             }
             // this segment's rows past the length are zero
@@ -933,6 +947,7 @@ cudaError_t launch_attn_tc(const AttnLaunch& L, int* kernels, const char** err) 
         t.dz = f.dz;
         t.reverse = f.reverse;
         t.out_f32 = f.out_f32;
+        t.terms = f.state_result ? 3 : 2;
         t.wide = reinterpret_cast<uintptr_t>(f.out) % 16 == 0 && f.ob % 8 == 0 && f.ot % 8 == 0 && f.oh % 8 == 0;
         const uint32_t px = (f.dx + 63) / 64, pz = (f.dz + 63) / 64;
         const uint32_t bytes = (2 * px + 2 * pz) * kPanel;
