@@ -94,6 +94,36 @@ __device__ __forceinline__ void st(uint32_t addr, const uint32_t (&r)[32]) {
                  : "memory");
 }
 
+// Fragments: of 16 lanes (the address names the first), thread t holds lanes
+// t / 4 and t / 4 + 8.  ld_pairs: per 8 columns two neighbouring values of each,
+// columns 2 (t % 4) and the next; st_words: per 4 columns one of each, column t % 4.
+__device__ __forceinline__ void ld_pairs(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+
+__device__ __forceinline__ void st_words(uint32_t addr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(addr)
+                 : "memory");
+}
+
+// Four 8 x 8 blocks of 16-bit values in shared memory, transposed: lane l names
+// row l % 8 of block l / 8; thread t holds column t / 4 of rows 2 (t % 4) and the next.
+__device__ __forceinline__ void ld_blocks(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void st_blocks(uint32_t addr, const uint32_t (&r)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%4], {%0, %1, %2, %3};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(addr)
+                 : "memory");
+}
+
 // ---------------------------------------------------------------------------
 // products
 
@@ -161,19 +191,17 @@ __device__ __forceinline__ float2 rest_of(float2 v, uint32_t hi) {
     return pair_fma(make_float2(low_bf16(hi), high_bf16(hi)), make_float2(-1.0f, -1.0f), v);
 }
 
-// the first two (three) bf16 terms of a pair of values
-__device__ __forceinline__ void split2(float2 v, uint32_t& hi, uint32_t& lo) {
-    hi = pack_bf16(v.x, v.y);
-    const float2 r = rest_of(v, hi);
-    lo = pack_bf16(r.x, r.y);
+// The next bf16 term of a pair of values, which keeps what is left of them.
+__device__ __forceinline__ uint32_t take_term(float2& v) {
+    const uint32_t t = pack_bf16(v.x, v.y);
+    v = rest_of(v, t);
+    return t;
 }
 
-__device__ __forceinline__ void split3(float2 v, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
-    hi = pack_bf16(v.x, v.y);
-    const float2 r = rest_of(v, hi);
-    mid = pack_bf16(r.x, r.y);
-    const float2 q = rest_of(r, mid);
-    lo = pack_bf16(q.x, q.y);
+// the first two bf16 terms of a pair of values
+__device__ __forceinline__ void split2(float2 v, uint32_t& hi, uint32_t& lo) {
+    hi = take_term(v);
+    lo = pack_bf16(v.x, v.y);
 }
 
 __device__ __forceinline__ float exp2_approx(float v) {

@@ -1,21 +1,22 @@
 // k_attn_tc.cu -- linear attention in chunks of 64 tokens on the tensor cores.
 //
 // One CTA takes one (batch row, head), or a segment of its tokens, through the
-// chunks in order; its 28 warps are a pipeline of roles linked by mbarriers:
+// chunks in order; its 32 warps are a pipeline of roles linked by mbarriers:
 //
 //     warp 2       TMA loads of the operands' tiles (X, Y, Z, and W for the
 //                  decays' gradient), 128-byte swizzled panels of 64 values
-//     warp 7       hands a loaded stage on; in a row's last, ragged chunk it
-//                  first clears the rows of Y and Z past the length
-//     warp 6       the chunk's decays: G, the coefficients of read and update
-//     warp 3       issues every product (tcgen05.mma, one thread)
+//     warp 6       the chunk's decays (G, the coefficients of read and update);
+//                  hands a loaded stage on, after clearing the rows of Y and Z
+//                  past the length in a row's last, ragged chunk
+//     warps 3, 7   issue the products (tcgen05.mma, one thread each): the
+//                  scores' and the state's
 //     warps 0,1,4,5  scores -> P: mask and decay, split into bf16 terms, to
 //                  shared memory
-//     warps 8-11   Z scaled by its update coefficients and transposed into
-//                  tensor memory, three bf16 terms
-//     warps 12-19  the state: f32 in tensor memory, decayed once a chunk, and
+//     warps 8-15   Z scaled by its update coefficients and transposed into
+//                  tensor memory, two or three bf16 terms
+//     warps 16-23  the state: f32 in tensor memory, decayed once a chunk, and
 //                  its two bf16 terms for the read
-//     warps 20-27  the outputs: read, joined, rounded once, stored
+//     warps 24-31  the outputs: read, joined, rounded once, stored
 //
 // The state lies transposed, a value column a lane and a key column a column,
 // so that everything made from it or for it is the A operand, read from tensor
@@ -46,7 +47,7 @@ namespace es {
 namespace {
 
 constexpr int C = kAttnTcChunk;               // 64 tokens
-constexpr int kThreads = 896;
+constexpr int kThreads = 1024;
 constexpr int kAnchorChunks = kAttnAnchorTokens / C;
 constexpr int kMaxStages = 4;
 constexpr uint32_t kPanel = C * 128;          // bytes of a panel: 64 rows of 64 bf16
@@ -100,7 +101,7 @@ struct TcArgs {
 
 struct Shared {
     uint64_t full[kMaxStages], ready[kMaxStages], empty[kMaxStages];
-    uint64_t s_done, p_ready, zh_ready, kv_done, o_done, o_read, drained;
+    uint64_t s_done, p_ready, zh_ready, kv_done, o_done, o_read, drained[2];
     uint32_t tmem;
     int abort_flag;
     Coef coef[kMaxStages];
@@ -111,7 +112,7 @@ struct Shared {
 // the abort flag are looked at after every 64 tries; what runs in between is
 // kept short, for the roles' loops together have to stay in the instruction
 // caches.
-__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, uint64_t limit_ns, volatile int* abort_flag) {
+__device__ __noinline__ bool wait_more(uint64_t* bar, uint32_t parity, uint64_t limit_ns, volatile int* abort_flag) {
     const uint32_t at = smem_u32(bar);
     uint64_t t0 = 0;
 #pragma unroll 1
@@ -151,32 +152,30 @@ struct Ring {
     }
 };
 
+// one thread's wait
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, uint64_t limit_ns, volatile int* abort_flag) {
+    return mbar_try_wait(bar, parity) || wait_more(bar, parity, limit_ns, abort_flag);
+}
+
+// The whole warp's wait when its first try found the barrier not yet due.
+__device__ __noinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint64_t limit_ns, volatile int* abort_flag,
+                                       unsigned int* status) {
+    const bool ok = wait_more(bar, parity, limit_ns, abort_flag);
+    if (__all_sync(0xffffffffu, ok)) return true;
+    if (!ok && !*abort_flag) report_timeout(status, abort_flag);
+    return false;
+}
+
 struct Wait {
     uint64_t ns;
     volatile int* flag;
     unsigned int* status;
     // the whole warp waits; false: leave the loop
     __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
-        const bool ok = wait_bounded(bar, parity & 1, ns, flag);
-        if (__all_sync(0xffffffffu, ok)) return true;
-        if (!ok && !*flag) report_timeout(status, flag);
-        return false;
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity & 1))) return true;
+        return wait_warp(bar, parity & 1, ns, flag, status);
     }
 };
-
-// named barrier of 128 threads with an OR vote
-__device__ __forceinline__ bool any_of(uint32_t id, bool failed) {
-    uint32_t any;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 q, %2, 0;\n\t"
-        "bar.red.or.pred p, %1, 128, q;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(any)
-        : "r"(id), "r"(static_cast<uint32_t>(failed))
-        : "memory");
-    return any != 0;
-}
 
 __device__ __forceinline__ void arrive_warp(uint64_t* bar, int lane) {
     __syncwarp();
@@ -235,16 +234,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
     if (threadIdx.x == 0) {
         for (int s = 0; s < A.stages; ++s) {
             mbar_init(&sh.full[s], 1);
-            mbar_init(&sh.ready[s], 2);                              // the tiles, the coefficients
-            mbar_init(&sh.empty[s], 1 + 4 + 8 + (kStateOnly ? 0 : 4 + 8));   // products, Z, state, P, outputs
+            mbar_init(&sh.ready[s], 1);
+            mbar_init(&sh.empty[s], 1 + 8 + 8 + (kStateOnly ? 0 : 1 + 4 + 8));   // products, Z, state; products, P, outputs
         }
         mbar_init(&sh.s_done, 1);
         mbar_init(&sh.p_ready, 4);
-        mbar_init(&sh.zh_ready, 4 + 8);
+        mbar_init(&sh.zh_ready, 8 + 8);
         mbar_init(&sh.kv_done, 1);
         mbar_init(&sh.o_done, 1);
         mbar_init(&sh.o_read, 8);
-        mbar_init(&sh.drained, 1);
+        mbar_init(&sh.drained[0], 1);
+        mbar_init(&sh.drained[1], 1);
         sh.abort_flag = 0;
         mbar_fence_init();
     }
@@ -298,17 +298,76 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             }
         }
         __syncwarp();
-    } else if (warp == 7) {
-        // ---- hand the stages on
+    } else if (warp == 6) {
+        // ---- the chunks' decays, tokens 2 lane and 2 lane + 1; then the stage is handed on
+        const float* G = A.g != nullptr ? A.g + b * A.gb + h * A.gh : nullptr;
+        auto load = [&](int k) {
+            float2 g = make_float2(0.0f, 0.0f);
+            if (G == nullptr || k >= n) return g;
+            const int64_t t = static_cast<int64_t>(chunk_of(k)) * C + 2 * lane;
+            if (t < len) g.x = __ldg(G + t * A.gt);
+            if (t + 1 < len) g.y = __ldg(G + (t + 1) * A.gt);
+            return g;
+        };
+        float2 g = load(0);
+        float all = 1.0f;
         Ring ring;
 #pragma unroll 1
         for (int k = 0; k < n; ++k, ring.next(A.stages)) {
-            const int s = ring.s;
-            if (!wait(&sh.full[s], ring.parity)) break;
+            const float2 next = load(k + 1);
+            const bool cut0 = g.x < -104.0f, cut1 = g.y < -104.0f;
+            const float v0 = cut0 ? 0.0f : g.x * 1.4426950408889634f, v1 = cut1 ? 0.0f : g.y * 1.4426950408889634f;
+            // inclusive sums of the pairs before, exclusive sums of the pairs after
+            float pre = v0 + v1, suf = pre;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float p = __shfl_up_sync(0xffffffffu, pre, o);
+                const float q = __shfl_down_sync(0xffffffffu, suf, o);
+                if (lane >= o) pre += p;
+                if (lane + o < 32) suf += q;
+            }
+            const float whole = __shfl_sync(0xffffffffu, pre, 31);
+            float before = __shfl_up_sync(0xffffffffu, pre, 1), after = __shfl_down_sync(0xffffffffu, suf, 1);
+            if (lane == 0) before = 0.0f;
+            if (lane == 31) after = 0.0f;
+            const float2 g2 = make_float2(before + v0, pre);
+            float2 from_start = make_float2(tc::exp2_approx(g2.x), tc::exp2_approx(g2.y));
+            float2 to_end = make_float2(tc::exp2_approx(after + v1), tc::exp2_approx(after));
+            float decay = tc::exp2_approx(whole);
+            int2 bound = R.reverse ? make_int2(63, 63) : make_int2(0, 0);
+            if (__any_sync(0xffffffffu, cut0 || cut1)) {
+                // some token starts afresh: coefficients that reach across it are zero, and rows end there
+                const unsigned m0 = __ballot_sync(0xffffffffu, cut0), m1 = __ballot_sync(0xffffffffu, cut1);
+                const unsigned upto = 0xffffffffu >> (31 - lane), below = upto >> 1, above = ~upto;
+                // the last cut at or before each token, the first one after it
+                auto last = [](unsigned even, unsigned odd) {
+                    return max(even ? 2 * (31 - __clz(even)) : -1, odd ? 2 * (31 - __clz(odd)) + 1 : -1);
+                };
+                auto first = [](unsigned even, unsigned odd) {
+                    return min(even ? 2 * (__ffs(even) - 1) : 64, odd ? 2 * (__ffs(odd) - 1) + 1 : 64);
+                };
+                const int l0 = last(m0 & upto, m1 & below), l1 = last(m0 & upto, m1 & upto);
+                const int f0 = first(m0 & above, m1 & ~below), f1 = first(m0 & above, m1 & above);
+                if (l0 >= 0) from_start.x = 0.0f;
+                if (l1 >= 0) from_start.y = 0.0f;
+                if (f0 < 64) to_end.x = 0.0f;
+                if (f1 < 64) to_end.y = 0.0f;
+                bound = R.reverse ? make_int2(f0 - 1, f1 - 1) : make_int2(max(l0, 0), max(l1, 0));
+                decay = 0.0f;
+            }
+            all *= decay;
+            if (k >= A.stages && !wait(&sh.empty[ring.s], ring.parity ^ 1)) break;
+            Coef& c = sh.coef[ring.s];
+            *reinterpret_cast<float2*>(&c.g2[2 * lane]) = g2;
+            *reinterpret_cast<float2*>(&c.read[2 * lane]) = R.reverse ? to_end : from_start;
+            *reinterpret_cast<float2*>(&c.upd[2 * lane]) = R.reverse ? from_start : to_end;
+            *reinterpret_cast<int2*>(&c.bound[2 * lane]) = bound;
+            if (lane == 0) c.decay = decay;
+            if (!wait(&sh.full[ring.s], ring.parity)) break;
             const int left = static_cast<int>(min(static_cast<int64_t>(C), len - static_cast<int64_t>(chunk_of(k)) * C));
             if (left < C) {
                 // rows past the length may hold anything (a NaN times a zero of P is a NaN): cleared
-                unsigned char* st = tiles + s * A.stage_bytes;
+                unsigned char* st = tiles + ring.s * A.stage_bytes;
                 const int rows = C - left;
 #pragma unroll 1
                 for (int p = 0; p < px + pz; ++p) {
@@ -318,127 +377,68 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 }
                 fence_proxy_async_smem();
             }
-            arrive_warp(&sh.ready[s], lane);
-        }
-    } else if (warp == 6) {
-        // ---- the chunks' decays, tokens lane and lane + 32
-        const float* G = A.g != nullptr ? A.g + b * A.gb + h * A.gh : nullptr;
-        auto load = [&](int k, float (&g)[2]) {
-            g[0] = g[1] = 0.0f;
-            if (G == nullptr || k >= n) return;
-            const int64_t t0 = static_cast<int64_t>(chunk_of(k)) * C;
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-                if (t0 + lane + 32 * u < len) g[u] = __ldg(G + (t0 + lane + 32 * u) * A.gt);
-        };
-        float g[2], next[2];
-        float all = 1.0f;
-        load(0, g);
-        Ring ring;
-#pragma unroll 1
-        for (int k = 0; k < n; ++k, ring.next(A.stages)) {
-            load(k + 1, next);
-            const bool cut0 = g[0] < -104.0f, cut1 = g[1] < -104.0f;
-            const uint64_t cuts = static_cast<uint64_t>(__ballot_sync(0xffffffffu, cut0)) |
-                                  (static_cast<uint64_t>(__ballot_sync(0xffffffffu, cut1)) << 32);
-            float pre[2], suf[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const float v = (u ? cut1 : cut0) ? 0.0f : g[u] * 1.4426950408889634f;
-                pre[u] = v;
-                suf[u] = __shfl_down_sync(0xffffffffu, v, 1);
-                if (lane == 31) suf[u] = 0.0f;
-                if (u == 1) {
-                    // token 32 follows token 31
-                    const float first = __shfl_sync(0xffffffffu, v, 0);
-                    if (lane == 31) suf[0] = first;
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const float p = __shfl_up_sync(0xffffffffu, pre[u], o);
-                    const float q = __shfl_down_sync(0xffffffffu, suf[u], o);
-                    if (lane >= o) pre[u] += p;
-                    if (lane + o < 32) suf[u] += q;
-                }
-            pre[1] += __shfl_sync(0xffffffffu, pre[0], 31);
-            suf[0] += __shfl_sync(0xffffffffu, suf[1], 0);
-            if (k >= A.stages && !wait(&sh.empty[ring.s], ring.parity ^ 1)) break;
-            Coef& c = sh.coef[ring.s];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int t = lane + 32 * u;
-                const uint64_t upto = cuts & (~0ull >> (63 - t));
-                const uint64_t after = t == 63 ? 0ull : cuts >> (t + 1);
-                const float er = upto ? 0.0f : tc::exp2_approx(pre[u]), eu = after ? 0.0f : tc::exp2_approx(suf[u]);
-                c.g2[t] = pre[u];
-                c.read[t] = R.reverse ? eu : er;
-                c.upd[t] = R.reverse ? er : eu;
-                c.bound[t] = R.reverse ? (after ? t + __ffsll(static_cast<long long>(after)) - 1 : 63)
-                                       : (upto ? 63 - __clzll(static_cast<long long>(upto)) : 0);
-            }
-            const float whole = cuts ? 0.0f : tc::exp2_approx(__shfl_sync(0xffffffffu, pre[1], 31));
-            if (lane == 0) c.decay = whole;
-            all *= whole;
             arrive_warp(&sh.ready[ring.s], lane);
-            g[0] = next[0];
-            g[1] = next[1];
+            g = next;
         }
         if constexpr (kStateOnly) {
             if (lane == 0 && blockIdx.y == 0) A.seg_decays[bh * A.n_segs + seg] = all;
         }
-    } else if (warp == 3) {
-        // ---- products
-        const uint32_t i_s = tc::instr_bf16(C, false, false), i_o1 = tc::instr_bf16(C, true, false);
+    } else if (warp == 3 || warp == 7) {
+        // ---- products: warp 7 those of the state, warp 3 those of the scores, so that neither waits for the other's turn
+        const uint32_t i_64 = tc::instr_bf16(C, false, false), i_o1 = tc::instr_bf16(C, true, false);
         const uint32_t i_kv = tc::instr_bf16(static_cast<uint32_t>(dxp), false, true);
         const uint32_t base = smem_u32(tiles);
-        const uint64_t d_phi = tc::smem_desc(smem_u32(p_hi), 16, 1024);
-        bool ok = true;
         Ring ring;
+        if (warp == 7) {
 #pragma unroll 1
-        for (int k = 0; k < n; ++k, ring.next(A.stages)) {
-            const int s = ring.s;
-            const uint32_t sx = base + s * A.stage_bytes;
-            const uint64_t d_x = tc::smem_desc(sx, 16, 1024), d_y = tc::smem_desc(sx + off_y, 16, 1024);
-            const uint64_t d_yt = tc::smem_desc(sx + off_y, kPanel, 1024), d_zt = tc::smem_desc(sx + off_z, kPanel, 1024);
-            if (!(ok = wait(&sh.ready[s], ring.parity))) break;
-            if constexpr (!kStateOnly) {
+            for (int k = 0; k < n; ++k, ring.next(A.stages)) {
+                const uint32_t sx = base + ring.s * A.stage_bytes;
+                const uint64_t d_x = tc::smem_desc(sx, 16, 1024), d_yt = tc::smem_desc(sx + off_y, kPanel, 1024);
+                if (!wait(&sh.ready[ring.s], ring.parity)) break;
+                if (!wait(&sh.zh_ready, k)) break;
+                // O2's region: the last chunk's has to be read
+                if (!kStateOnly && k > 0 && !wait(&sh.o_read, k - 1)) break;
+                tc::fence_after();
+                if (tc::elect()) {
+                    if constexpr (!kStateOnly) {
+#pragma unroll 1
+                        for (int p = 0; p < 2 * px; ++p) {
+                            const uint64_t d = d_x + (p < px ? p : p - px) * (kPanel >> 4);
+#pragma unroll 1
+                            for (int q = 0; q < 4; ++q) tc::mma_ts(t_o2, t_hb + 32 * p + 8 * q, d + q * 2, i_64, p + q > 0);
+                        }
+                    }
+#pragma unroll 1
+                    for (int m = 0; m < R.terms; ++m)
+#pragma unroll 1
+                        for (int q = 0; q < C / 16; ++q) tc::mma_ts(t_h, t_zt + m * (C / 2) + q * 8, d_yt + q * 128, i_kv, true);
+                    tc::commit(&sh.kv_done);
+                    tc::commit(&sh.empty[ring.s]);
+                }
+                __syncwarp();
+            }
+        } else if constexpr (!kStateOnly) {
+            const uint64_t d_phi = tc::smem_desc(smem_u32(p_hi), 16, 1024);
+#pragma unroll 1
+            for (int k = 0; k < n; ++k, ring.next(A.stages)) {
+                const uint32_t sx = base + ring.s * A.stage_bytes;
+                const uint64_t d_x = tc::smem_desc(sx, 16, 1024), d_y = tc::smem_desc(sx + off_y, 16, 1024);
+                const uint64_t d_zt = tc::smem_desc(sx + off_z, kPanel, 1024);
+                if (!wait(&sh.ready[ring.s], ring.parity)) break;
                 // with three terms of Z the scores' region holds the last chunk's O1 until it is read
-                if (R.terms == 3 && k > 0 && !(ok = wait(&sh.o_read, k - 1))) break;
+                if (R.terms == 3 && k > 0 && !wait(&sh.o_read, k - 1)) break;
                 tc::fence_after();
                 if (tc::elect()) {
 #pragma unroll 1
                     for (int p = 0; p < px; ++p)
 #pragma unroll 1
                         for (int q = 0; q < 4; ++q)
-                            tc::mma_ss(t_s, d_x + p * (kPanel >> 4) + q * 2, d_y + p * (kPanel >> 4) + q * 2, i_s, p + q > 0);
+                            tc::mma_ss(t_s, d_x + p * (kPanel >> 4) + q * 2, d_y + p * (kPanel >> 4) + q * 2, i_64, p + q > 0);
                     tc::commit(&sh.s_done);
                 }
                 __syncwarp();
-                if (R.terms == 2 && k > 0 && !(ok = wait(&sh.o_read, k - 1))) break;
-            }
-            if (!(ok = wait(&sh.zh_ready, k))) break;
-            tc::fence_after();
-            if (tc::elect()) {
-                if constexpr (!kStateOnly) {
-#pragma unroll 1
-                    for (int p = 0; p < 2 * px; ++p) {
-                        const uint64_t d = d_x + (p < px ? p : p - px) * (kPanel >> 4);
-#pragma unroll 1
-                        for (int q = 0; q < 4; ++q) tc::mma_ts(t_o2, t_hb + 32 * p + 8 * q, d + q * 2, i_s, p + q > 0);
-                    }
-                }
-#pragma unroll 1
-                for (int m = 0; m < R.terms; ++m)
-#pragma unroll 1
-                    for (int q = 0; q < C / 16; ++q) tc::mma_ts(t_h, t_zt + m * (C / 2) + q * 8, d_yt + q * 128, i_kv, true);
-                tc::commit(&sh.kv_done);
-            }
-            __syncwarp();
-            if constexpr (!kStateOnly) {
-                if (!(ok = wait(&sh.p_ready, k))) break;
+                if (R.terms == 2 && k > 0 && !wait(&sh.o_read, k - 1)) break;
+                if (!wait(&sh.p_ready, k)) break;
                 tc::fence_after();
                 if (tc::elect()) {
 #pragma unroll 1
@@ -447,15 +447,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                         for (int q = 0; q < C / 16; ++q)
                             tc::mma_ss(t_o1, d_zt + q * 128, d_phi + m * (kPanel >> 4) + q * 2, i_o1, m + q > 0);
                     tc::commit(&sh.o_done);
+                    tc::commit(&sh.empty[ring.s]);
                 }
+                __syncwarp();
             }
-            if (tc::elect()) tc::commit(&sh.empty[s]);
-            __syncwarp();
         }
         // nothing of this CTA's may still run when its tensor memory goes
-        if (lane == 0) tc::commit(&sh.drained);
+        uint64_t* drained = &sh.drained[warp == 7];
+        if (tc::elect()) tc::commit(drained);
         __syncwarp();
-        if (!__all_sync(0xffffffffu, wait_bounded(&sh.drained, 0, A.wait_ns, nullptr)) && lane == 0)
+        if (!__all_sync(0xffffffffu, wait_bounded(drained, 0, A.wait_ns, nullptr)) && lane == 0)
             atomicOr(A.status, ES_DEVICE_TIMEOUT);
     } else if (warp < 8) {
         // ---- P: row i, 32 columns
@@ -517,45 +518,43 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 }
             }
         }
-    } else if (warp < 12) {
-        // ---- Z scaled and transposed: lane = value column, token pairs along the columns
-        const int c = (warp - 8) * 32 + lane;
-        const uint32_t to = t_zt + (static_cast<uint32_t>((warp - 8) * 32) << 16);
-        const bool on = (warp - 8) * 32 < R.dz;
-        uint32_t off[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) off[u] = (c / 64) * kPanel + ((((c % 64) >> 3) ^ u) << 4) + (c & 7) * 2 + u * 128;
+    } else if (warp < 16) {
+        // ---- Z scaled and transposed: 32 value columns (lanes) and 32 of the tokens (pairs along the columns)
+        const int slice = warp & 3, side = (warp - 8) / 4;
+        const uint32_t to = t_zt + 16 * side + (static_cast<uint32_t>(slice * 32) << 16);
+        const bool on = slice * 32 < R.dz;
+        // lane l names row l % 8 of block l / 8: two blocks of columns, two of tokens
+        const uint32_t row = 32 * side + 8 * (lane / 16) + lane % 8, piece = 4 * (slice & 1) + (lane / 8) % 2;
+        const uint32_t at0 = smem_u32(tiles) + off_z + (slice / 2) * kPanel + row * 128 + ((piece ^ (row & 7)) << 4);
         Ring ring;
 #pragma unroll 1
         for (int k = 0; k < n; ++k, ring.next(A.stages)) {
-            const int s = ring.s;
-            if (!wait(&sh.ready[s], ring.parity)) break;
+            if (!wait(&sh.ready[ring.s], ring.parity)) break;
             if (k > 0 && !wait(&sh.kv_done, k - 1)) break;
             tc::fence_after();
             if (on) {
-                const unsigned char* z = tiles + s * A.stage_bytes + off_z;
-                const Coef& cf = sh.coef[s];
+                const float* upd = sh.coef[ring.s].upd + 32 * side + 2 * (lane % 4);
+                const uint32_t at = at0 + ring.s * A.stage_bytes;
 #pragma unroll 1
-                for (int q = 0; q < 8; ++q) {
-                    uint32_t t0[4], t1[4], t2[4];
-                    float2 v[4];
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t z[2][4], t[8];
+                    float2 v[8];
+                    // pieces 2 half and 2 half + 1 (the swizzle only flips that bit of the address)
+                    tc::ld_blocks(at ^ (half << 5), z[0]);
+                    tc::ld_blocks((at ^ (half << 5)) + 16 * 128, z[1]);
+                    const uint32_t lanes = to + (static_cast<uint32_t>(16 * half) << 16);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 w = *reinterpret_cast<const float2*>(&cf.upd[8 * q + 2 * e]);
-                        const uint32_t z0 = *reinterpret_cast<const unsigned short*>(z + q * 1024 + off[2 * e]);
-                        const uint32_t z1 = *reinterpret_cast<const unsigned short*>(z + q * 1024 + off[2 * e + 1]);
-                        v[e] = pair_mul(make_float2(__uint_as_float(z0 << 16), __uint_as_float(z1 << 16)), w);
+                    for (int e = 0; e < 8; ++e) {
+                        const float2 w = *reinterpret_cast<const float2*>(upd + 8 * (e / 2));
+                        const uint32_t u = z[e / 4][e % 4];
+                        v[e] = pair_mul(make_float2(tc::low_bf16(u), tc::high_bf16(u)), w);
                     }
-                    if (R.terms == 2) {
+#pragma unroll 1
+                    for (int m = 0; m < R.terms; ++m) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) tc::split2(v[e], t0[e], t1[e]);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) tc::split3(v[e], t0[e], t1[e], t2[e]);
-                        tc::st(to + 64 + 4 * q, t2);
+                        for (int e = 0; e < 8; ++e) t[e] = tc::take_term(v[e]);
+                        tc::st_words(lanes + 32 * m, t);
                     }
-                    tc::st(to + 4 * q, t0);
-                    tc::st(to + 32 + 4 * q, t1);
                 }
                 tc::wait_st();
             }
@@ -563,12 +562,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&sh.zh_ready);
-                mbar_arrive(&sh.empty[s]);
+                mbar_arrive(&sh.empty[ring.s]);
             }
         }
-    } else if (warp < 20) {
+    } else if (warp < 24) {
         // ---- the state: lane = value column c, half of the key columns along
-        const int slice = warp & 3, side = (warp - 12) / 4, a_lo = side * (dxp / 2), a_hi = a_lo + dxp / 2;
+        const int slice = warp & 3, side = (warp - 16) / 4, a_lo = side * (dxp / 2), a_hi = a_lo + dxp / 2;
         const int c = slice * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>(slice * 32) << 16;
         const bool on = slice * 32 < R.dz, real = c < R.dz;
@@ -667,35 +666,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                     }
                 }
             if (on && k < n) {
-                // pieces of 16 columns, an even number: one on its way while the other is split
-                auto piece = [&](int a0, uint32_t (&r)[16]) {
-                    uint32_t hi[8], lo[8];
+#pragma unroll 1
+                for (int a0 = a_lo; a0 < a_hi; a0 += 16) {
+                    uint32_t r[16], t[8], u[8];
+                    tc::ld(t_h + lanes + a0, r);
+                    tc::wait_ld();
+                    tc::loaded(r);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const float2 v = make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
-                        if constexpr (!kStateOnly) tc::split2(v, hi[e], lo[e]);
+                        if constexpr (!kStateOnly) tc::split2(v, t[e], u[e]);
                         const float2 d = pair_mul(v, make_float2(decay, decay));
                         r[2 * e] = __float_as_uint(d.x);
                         r[2 * e + 1] = __float_as_uint(d.y);
                     }
                     if constexpr (!kStateOnly) {
-                        tc::st(t_hb + lanes + a0 / 2, hi);
-                        tc::st(t_hb + lanes + dxp / 2 + a0 / 2, lo);
+                        tc::st(t_hb + lanes + a0 / 2, t);
+                        tc::st(t_hb + lanes + dxp / 2 + a0 / 2, u);
                     }
                     tc::st(t_h + lanes + a0, r);
-                };
-                uint32_t r0[16], r1[16];
-                tc::ld(t_h + lanes + a_lo, r0);
-#pragma unroll 1
-                for (int a0 = a_lo; a0 < a_hi; a0 += 32) {
-                    tc::wait_ld();
-                    tc::loaded(r0);
-                    tc::ld(t_h + lanes + a0 + 16, r1);
-                    piece(a0, r0);
-                    tc::wait_ld();
-                    tc::loaded(r1);
-                    if (a0 + 32 < a_hi) tc::ld(t_h + lanes + a0 + 32, r0);
-                    piece(a0 + 16, r1);
                 }
             }
             if (anchor_to != nullptr) {
@@ -716,92 +705,88 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
     } else {
         // ---- outputs: lane = value column c, tokens along the columns
         if constexpr (!kStateOnly) {
-            const int slice = warp & 3, side = (warp - 20) / 4;       // 32 value columns, 32 of the tokens
+            const int slice = warp & 3, side = (warp - 24) / 4;       // 32 value columns, 32 of the tokens
             const int c = slice * 32 + lane;
             const uint32_t lanes = static_cast<uint32_t>(slice * 32) << 16;
             const bool on = slice * 32 < R.dz, real = c < R.dz;
-            float* of = static_cast<float*>(R.out) + b * R.ob + static_cast<int64_t>(h) * R.oh + c;
-            uint32_t off[8];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) off[u] = (c / 64) * kPanel + ((((c % 64) >> 3) ^ u) << 4) + (c & 7) * 2 + u * 128;
-            const int wt = (threadIdx.x - 640) & 127;
-            // pieces of 16 bytes a row, and the rows of a pass over the tile
-            const int cols = dzp / 8, rows = 128 / cols;
+            float* of = static_cast<float*>(R.out) + b * R.ob + static_cast<int64_t>(h) * R.oh;
+            unsigned short* o16 = static_cast<unsigned short*>(R.out) + b * R.ob + static_cast<int64_t>(h) * R.oh;
             const bool wide = !R.out_f32 && R.wide;
+            // the warp's part of the tile: lane l names row l % 8 of block l / 8 (blocks of 8 columns)
+            const uint32_t row0 = 32 * side + lane % 8, w0 = off_w + (slice / 2) * kPanel;
+            const uint32_t at0 = w0 + row0 * 128 + ((((4 * (slice & 1)) + lane / 8) ^ (row0 & 7)) << 4);
+            const float2 scale = make_float2(R.out_scale, R.out_scale);
             Ring ring;
 #pragma unroll 1
             for (int k = 0; k < n; ++k, ring.next(A.stages)) {
-                const int s = ring.s;
-                // (ready: the W tile is there, and its place is the output tile's from here on)
-                const bool go = wait(&sh.ready[s], ring.parity) && wait(&sh.o_done, k);
-                // a side's four warps leave together: they meet at a barrier below
-                if (any_of(side + 1, !go)) break;
+                // (kv_done: O2 is there too)
+                if (!wait(&sh.ready[ring.s], ring.parity) || !wait(&sh.kv_done, k) || !wait(&sh.o_done, k)) break;
                 tc::fence_after();
                 const int64_t t0 = static_cast<int64_t>(chunk_of(k)) * C;
                 const int left = static_cast<int>(min(static_cast<int64_t>(C), len - t0));
-                const Coef& cf = sh.coef[s];
-                unsigned char* w = tiles + s * A.stage_bytes + off_w;
+                const float* rd = sh.coef[ring.s].read + 32 * side + 2 * (lane % 4);
+                unsigned char* st = tiles + ring.s * A.stage_bytes;
                 if (on) {
-                    const float2 scale = make_float2(R.out_scale, R.out_scale);
 #pragma unroll 1
-                    for (int q = 2 * side; q < 2 * side + 2; ++q) {
-                        uint32_t r1[16], r2[16];
-                        tc::ld(t_o1 + lanes + 16 * q, r1);
-                        tc::ld(t_o2 + lanes + 16 * q, r2);
+                    for (int q = 0; q < 4; ++q) {
+                        // 8 tokens: columns t / 4 of four blocks, two tokens
+                        uint32_t o1[2][4], o2[2][4];
+                        const uint32_t col = lanes + 32 * side + 8 * q;
+                        tc::ld_pairs(t_o1 + col, o1[0]);
+                        tc::ld_pairs(t_o1 + col + (16u << 16), o1[1]);
+                        tc::ld_pairs(t_o2 + col, o2[0]);
+                        tc::ld_pairs(t_o2 + col + (16u << 16), o2[1]);
+                        const float2 r = *reinterpret_cast<const float2*>(rd + 8 * q);
                         tc::wait_ld();
-                        tc::loaded(r1);
-                        tc::loaded(r2);
-                        if (q == 2 * side + 1) {
+                        tc::loaded(o1[0]);
+                        tc::loaded(o1[1]);
+                        tc::loaded(o2[0]);
+                        tc::loaded(o2[1]);
+                        if (q == 3) {
                             // the products of the next chunk may overwrite what was read
                             tc::fence_before();
                             __syncwarp();
                             if (lane == 0) mbar_arrive(&sh.o_read);
                         }
-                        float v[16];
+                        float2 v[4];
 #pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            const float2 rd = *reinterpret_cast<const float2*>(&cf.read[16 * q + e]);
-                            const float2 o = pair_mul(pair_fma(make_float2(__uint_as_float(r2[e]), __uint_as_float(r2[e + 1])), rd,
-                                                               make_float2(__uint_as_float(r1[e]), __uint_as_float(r1[e + 1]))), scale);
-                            v[e] = o.x;
-                            v[e + 1] = o.y;
+                        for (int m = 0; m < 4; ++m) {
+                            const uint32_t* x1 = &o1[m / 2][2 * (m & 1)];
+                            const uint32_t* x2 = &o2[m / 2][2 * (m & 1)];
+                            v[m] = pair_mul(pair_fma(make_float2(__uint_as_float(x2[0]), __uint_as_float(x2[1])), r,
+                                                     make_float2(__uint_as_float(x1[0]), __uint_as_float(x1[1]))),
+                                            scale);
                         }
-                        unsigned char* at = w + q * 2048;
+                        const uint32_t at = smem_u32(st) + at0 + 8 * q * 128;
+                        const int row = 32 * side + 8 * q + 2 * (lane % 4);
                         if (dots) {
-                            // out . w over the warp's columns: products, then halves of the tokens are
-                            // exchanged until lane l holds token l / 2's sum (padded columns hold zeros)
-                            float m[16];
+                            // out . w over the warp's columns (padded columns hold zeros)
+                            uint32_t w[4];
+                            tc::ld_blocks(at, w);
+                            float2 d = make_float2(0.0f, 0.0f);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const uint32_t raw16 = *reinterpret_cast<const unsigned short*>(at + (e / 8) * 1024 + off[e % 8]);
-                                m[e] = v[e] * __uint_as_float(raw16 << 16);
+                            for (int m = 0; m < 4; ++m) d = pair_fma(v[m], make_float2(tc::low_bf16(w[m]), tc::high_bf16(w[m])), d);
+#pragma unroll
+                            for (int o = 4; o <= 16; o <<= 1) {
+                                d.x += __shfl_xor_sync(0xffffffffu, d.x, o);
+                                d.y += __shfl_xor_sync(0xffffffffu, d.y, o);
                             }
-#pragma unroll
-                            for (int o = 16; o >= 2; o >>= 1) {
-                                const bool up = lane & o;
-#pragma unroll
-                                for (int e = 0; e < o / 2; ++e) {
-                                    const float give = up ? m[e] : m[e + o / 2], keep = up ? m[e + o / 2] : m[e];
-                                    m[e] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-                                }
-                            }
-                            m[0] += __shfl_xor_sync(0xffffffffu, m[0], 1);
-                            const int row = 16 * q + lane / 2;
-                            if (row < left && !(lane & 1)) R.dots[(slice * A.BH + bh) * A.T + t0 + row] = m[0];
+                            float* to = R.dots + (slice * A.BH + bh) * A.T + t0 + row;
+                            if (lane < 4 && row < left) to[0] = d.x;
+                            if (lane < 4 && row + 1 < left) to[1] = d.y;
+                            __syncwarp();      // W's rows are read before the results take their place
                         }
-                        if (R.out_f32) {
-                            if (real) {
+                        if (!R.out_f32) {
+                            uint32_t p[4];
 #pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    if (16 * q + e < left) of[(t0 + 16 * q + e) * R.ot] = v[e];
-                            }
+                            for (int m = 0; m < 4; ++m) p[m] = tc::pack_bf16(v[m].x, v[m].y);
+                            tc::st_blocks(at, p);
                         } else {
 #pragma unroll
-                            for (int e = 0; e < 16; e += 2) {
-                                const uint32_t two = tc::pack_bf16(v[e], v[e + 1]);
-                                *reinterpret_cast<unsigned short*>(at + (e / 8) * 1024 + off[e % 8]) = static_cast<unsigned short>(two);
-                                *reinterpret_cast<unsigned short*>(at + (e / 8) * 1024 + off[(e + 1) % 8]) =
-                                    static_cast<unsigned short>(two >> 16);
+                            for (int m = 0; m < 4; ++m) {
+                                const int cc = 32 * slice + 8 * m + lane / 4;
+                                if (cc < R.dz && row < left) of[(t0 + row) * R.ot + cc] = v[m].x;
+                                if (cc < R.dz && row + 1 < left) of[(t0 + row + 1) * R.ot + cc] = v[m].y;
                             }
                         }
                     }
@@ -810,41 +795,40 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 }
                 // the next load of this place comes through the async proxy
                 fence_proxy_async_smem();
-                if (!R.out_f32) {
-                    named_barrier_sync(side + 1, 128);
-                    // rows out, 16 bytes a thread where the result's addresses allow it
-                    const int piece = wt & (cols - 1);
-                    unsigned short* base = static_cast<unsigned short*>(R.out) + b * R.ob + static_cast<int64_t>(h) * R.oh + t0 * R.ot + piece * 8;
-#pragma unroll 2
-                    for (int row = 32 * side + (wt >> (cols == 16 ? 4 : 3)); row < min(left, 32 * side + 32); row += rows) {
-                        const uint4 u = *reinterpret_cast<const uint4*>(w + (piece / 8) * kPanel + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
-                        unsigned short* to = base + row * R.ot;
+                __syncwarp();
+                if (on && !R.out_f32) {
+                    // the warp's rows out, 64 bytes each, 16 a thread where the result's addresses allow it
+                    const int piece = 4 * (slice & 1) + lane % 4, cc = 32 * slice + 8 * (lane % 4);
+#pragma unroll 1
+                    for (int row = 32 * side + lane / 4; row < min(left, 32 * side + 32); row += 8) {
+                        const uint4 u = *reinterpret_cast<const uint4*>(st + w0 + row * 128 + ((piece ^ (row & 7)) << 4));
+                        unsigned short* to = o16 + (t0 + row) * R.ot + cc;
                         if (wide) {
-                            if (piece * 8 < R.dz) *reinterpret_cast<uint4*>(to) = u;
+                            if (cc < R.dz) *reinterpret_cast<uint4*>(to) = u;
                         } else {
                             const uint32_t x[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
-                                if (piece * 8 + e < R.dz)
-                                    to[e] = static_cast<unsigned short>(e % 2 ? x[e / 2] >> 16 : x[e / 2]);
+                                if (cc + e < R.dz) to[e] = static_cast<unsigned short>(e % 2 ? x[e / 2] >> 16 : x[e / 2]);
                         }
                     }
                 }
-                arrive_warp(&sh.empty[s], lane);
+                arrive_warp(&sh.empty[ring.s], lane);
             }
             // this segment's rows past the length are zero
             const int64_t lo = max(len, static_cast<int64_t>(c0) * C);
             const int64_t hi = seg == A.n_segs - 1 ? A.T : min(A.T, static_cast<int64_t>(c0 + A.seg_chunks) * C);
             if (wide) {
-                unsigned short* to = static_cast<unsigned short*>(R.out) + b * R.ob + static_cast<int64_t>(h) * R.oh + (wt & (cols - 1)) * 8;
-                if ((wt & (cols - 1)) * 8 < R.dz)
+                const int cc = 32 * slice + 8 * (lane % 4);
+                if (cc < R.dz)
 #pragma unroll 4
-                    for (int64_t t = lo + side * rows + wt / cols; t < hi; t += 2 * rows) *reinterpret_cast<uint4*>(to + t * R.ot) = make_uint4(0, 0, 0, 0);
+                    for (int64_t t = lo + 8 * side + lane / 4; t < hi; t += 16)
+                        *reinterpret_cast<uint4*>(o16 + t * R.ot + cc) = make_uint4(0, 0, 0, 0);
             } else if (real) {
 #pragma unroll 1
                 for (int64_t t = lo + side; t < hi; t += 2) {
-                    if (R.out_f32) of[t * R.ot] = 0.0f;
-                    else static_cast<unsigned short*>(R.out)[b * R.ob + static_cast<int64_t>(h) * R.oh + t * R.ot + c] = 0;
+                    if (R.out_f32) of[t * R.ot + c] = 0.0f;
+                    else o16[t * R.ot + c] = 0;
                 }
             }
         }
