@@ -45,12 +45,10 @@ struct AttnRun {
     // columns, [slices, B*H, T]; null: not wanted.
     AttnOperand w;
     float* dots;
-    // A forward run writes its state after every `anchor_every` chunks (and
-    // after the last one) to anchors[(bh*n + m)*dx*dz + a*dz + c]; a reversed
-    // run instead writes out_scale * <its state there, the anchor> per slice
-    // to anchor_dots [slices, B*H, n] (the tensor-core kernel has two parts a slice).
+    // The run's state at the end of every anchor block (kAttnAnchorTokens) and
+    // of the row: a forward run's after the block, a reversed run's before it;
+    // value (a, c) at anchors[((b*H + h)*n + m)*dx*dz + a*dz + c].
     float* anchors;
-    float* anchor_dots;
     int dx, dz;
 };
 
@@ -63,7 +61,6 @@ struct AttnLaunch {
     const float* g;              // log decays, strides in elements; null: none
     int64_t gb, gt, gh;
     const int* lengths;          // [B] or null
-    int64_t anchor_every;        // in chunks
     int64_t n_anchors;           // per (b, h)
     // segments of tokens (tensor-core path): see k_attn_tc.cu
     int64_t seg_chunks;          // chunks a segment
@@ -94,17 +91,20 @@ constexpr int kAttnTcChunk = 64;
 bool attn_tc_operand_ok(const AttnOperand& o, int heads, int d, int64_t T, int64_t B);
 cudaError_t launch_attn_tc(const AttnLaunch& L, int* kernels, const char** err);
 
-// The decays' gradient from the two runs' dots: for each token t of anchor
-// block m, sum over s >= t of the block of (dq[s] - dk[s]) + e[m].
+// The decays' gradient from the two runs' dots and states: for each token t of
+// anchor block m, sum over s >= t of the block of (dq[s] - dk[s]) + e[m], with
+// e[m] = scale <state_q, state_k> at the block's end.
 struct AttnDecayGrad {
-    const float* dots_q;         // [slices_q, B*H, T]
+    const float* dots_q;         // [slices, B*H, T]
     const float* dots_k;
-    const float* ends;           // [slices_e, B*H, n]
-    int slices_q, slices_k, slices_e;
+    const float* states_q;       // [B*H, n, size]
+    const float* states_k;
+    float scale;
+    int slices;
+    int64_t size;
     int64_t B, T;
     int H;
     const int* lengths;
-    int64_t block;               // tokens of an anchor block
     int64_t n;                   // anchor blocks per (b, h)
     float* grad;                 // [B, T, H], or null
     float* partial;              // per head: [H, B*n] block sums, then summed to `grad_h`

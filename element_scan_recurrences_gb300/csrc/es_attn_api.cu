@@ -91,8 +91,8 @@ struct AttnPlan {
     int path;
     bool empty;
     // backward: byte offsets into the workspace
-    size_t seg_states, seg_decays, dots_q, dots_k, anchors, ends, partial, fold_q, fold_k, fold_v, bytes;
-    int slices_k, slices_v;      // slices of the runs that produce key- and value-wide outputs
+    size_t seg_states, seg_decays, dots_q, dots_k, states_q, states_k, partial, fold_q, fold_k, fold_v, bytes;
+    int slices_k;                // slices of the runs that give the dots (key-wide outputs)
 };
 
 // Segments a sequence is cut into (tensor-core path).  One CTA runs one (batch
@@ -108,9 +108,6 @@ int segments(int64_t ctas, int64_t chunks, int64_t* seg_chunks) {
     *seg_chunks = each;
     return static_cast<int>((chunks + each - 1) / each);
 }
-
-// parts of a slice's product of a state and an anchor
-int ends_parts(const AttnPlan& P) { return P.path == ES_PATH_TENSOR ? 2 : 1; }
 
 size_t take(size_t* at, int64_t bytes) {
     const size_t here = *at;
@@ -279,14 +276,12 @@ es_status plan_attn(const char* fn, const es_linear_attention_args* a, const es_
 
     // workspace
     const int64_t chunk = P->path == ES_PATH_TENSOR ? kAttnTcChunk : kAttnChunk;
-    L.anchor_every = kAttnAnchorTokens / chunk;
     L.n_anchors = (T + kAttnAnchorTokens - 1) / kAttnAnchorTokens;
     L.n_segs = 1;
     const int64_t chunks = (T + chunk - 1) / chunk;
     L.seg_chunks = chunks > 0 ? chunks : 1;
     if (P->path == ES_PATH_TENSOR) L.n_segs = segments(bh * L.runs, chunks, &L.seg_chunks);
     P->slices_k = static_cast<int>((dk + kAttnSlice - 1) / kAttnSlice);
-    P->slices_v = static_cast<int>((dv + kAttnSlice - 1) / kAttnSlice);
     size_t at = 0;
     if (L.n_segs > 1) {
         P->seg_states = take(&at, 4 * L.runs * bh * L.n_segs * dk * dv);
@@ -296,8 +291,8 @@ es_status plan_attn(const char* fn, const es_linear_attention_args* a, const es_
         if (g->grad_log_decay != nullptr) {
             P->dots_q = take(&at, 4 * P->slices_k * bh * T);
             P->dots_k = take(&at, 4 * P->slices_k * bh * T);
-            P->anchors = take(&at, 4 * bh * L.n_anchors * dk * dv);
-            P->ends = take(&at, 4 * ends_parts(*P) * P->slices_k * bh * L.n_anchors);
+            P->states_q = take(&at, 4 * bh * L.n_anchors * dk * dv);
+            P->states_k = take(&at, 4 * bh * L.n_anchors * dk * dv);
             P->partial = take(&at, 4 * bh * L.n_anchors);
         }
         if (a->q.heads < H) P->fold_q = take(&at, 4 * bh * T * dk);
@@ -369,7 +364,7 @@ es_status launch_runs(const char* fn, const AttnPlan& P, AttnLaunch L, void* wor
 es_status run_backward(const char* fn, const es_linear_attention_args* a, const es_linear_attention_grads* g, AttnPlan& P) {
     AttnLaunch& L = P.L;
     char* ws = static_cast<char*>(a->workspace);
-    const int64_t H = a->heads, bh = a->batch * H;
+    const int64_t H = a->heads;
     const int dk = static_cast<int>(a->key_dim), dv = static_cast<int>(a->value_dim);
     cudaError_t e;
     AttnRun &rq = L.run[0], &rv = L.run[1], &rk = L.run[2];
@@ -377,11 +372,10 @@ es_status run_backward(const char* fn, const es_linear_attention_args* a, const 
     if (decay) {
         rq.w = operand(a->q, H);
         rq.dots = reinterpret_cast<float*>(ws + P.dots_q);
-        rq.anchors = reinterpret_cast<float*>(ws + P.anchors);
+        rq.anchors = reinterpret_cast<float*>(ws + P.states_q);
         rk.w = operand(a->k, H);
         rk.dots = reinterpret_cast<float*>(ws + P.dots_k);
-        rk.anchors = rq.anchors;
-        rk.anchor_dots = reinterpret_cast<float*>(ws + P.ends);
+        rk.anchors = reinterpret_cast<float*>(ws + P.states_k);
     }
     AttnFold fold[3];
     int folds = 0;
@@ -399,26 +393,21 @@ es_status run_backward(const char* fn, const es_linear_attention_args* a, const 
     shared(rq, g->grad_q, P.fold_q, dk);
     shared(rv, g->grad_v, P.fold_v, dv);
     shared(rk, g->grad_k, P.fold_k, dk);
+    const es_status st = launch_runs(fn, P, L, a->workspace);
+    if (st != ES_OK) return st;
     if (decay) {
-        // the keys' run reads the states that the queries' run leaves
-        AttnLaunch first = L;
-        first.runs = 2;
-        es_status st = launch_runs(fn, P, first, a->workspace);
-        if (st != ES_OK) return st;
-        first.run[0] = rk;
-        first.runs = 1;
-        if ((st = launch_runs(fn, P, first, a->workspace)) != ES_OK) return st;
         AttnDecayGrad D{};
         D.dots_q = rq.dots;
         D.dots_k = rk.dots;
-        D.ends = rk.anchor_dots;
-        D.slices_q = D.slices_k = P.slices_k;
-        D.slices_e = ends_parts(P) * P.slices_k;
+        D.states_q = rq.anchors;
+        D.states_k = rk.anchors;
+        D.scale = rk.out_scale;
+        D.slices = P.slices_k;
+        D.size = static_cast<int64_t>(dk) * dv;
         D.B = L.B;
         D.T = L.T;
         D.H = L.H;
         D.lengths = L.lengths;
-        D.block = kAttnAnchorTokens;
         D.n = L.n_anchors;
         D.stream = L.stream;
         if (a->decay_per_head) {
@@ -430,18 +419,14 @@ es_status run_backward(const char* fn, const es_linear_attention_args* a, const 
         int n = 0;
         if ((e = launch_attn_decay_grad(D, &n)) != cudaSuccess) return cuda_fail(fn, e);
         count_launch(n);
-    } else {
-        const es_status st = launch_runs(fn, P, L, a->workspace);
-        if (st != ES_OK) return st;
-        if (g->grad_log_decay != nullptr && a->decay_per_head &&
-            (e = cudaMemsetAsync(g->grad_log_decay, 0, H * 4, L.stream)) != cudaSuccess)
-            return cuda_fail(fn, e);      // no tokens: a sum of nothing
+    } else if (g->grad_log_decay != nullptr && a->decay_per_head) {
+        // no tokens: a sum of nothing
+        if ((e = cudaMemsetAsync(g->grad_log_decay, 0, H * 4, L.stream)) != cudaSuccess) return cuda_fail(fn, e);
     }
     for (int i = 0; i < folds; ++i) {
         if ((e = launch_attn_fold(fold[i])) != cudaSuccess) return cuda_fail(fn, e);
         count_launch();
     }
-    (void)bh;
     return ES_OK;
 }
 

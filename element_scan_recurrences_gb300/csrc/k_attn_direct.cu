@@ -23,6 +23,7 @@ namespace {
 constexpr int C = kAttnChunk;
 constexpr int ZS = kAttnSlice;
 constexpr int kThreads = 256;
+constexpr int kAnchorChunks = kAttnAnchorTokens / C;
 
 template <typename T>
 __device__ __forceinline__ float to_f32(T v) {
@@ -36,7 +37,7 @@ struct DirectArgs {
     const float* g;
     int64_t gb, gt, gh;
     const int* lengths;
-    int64_t anchor_every, n_anchors;
+    int64_t n_anchors;
     int64_t BH;
 };
 
@@ -106,26 +107,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_consta
         const int64_t t0 = ci * C;
         const int n = static_cast<int>(len - t0 < C ? len - t0 : C);
         __syncthreads();
-        // the gradient of the decays: the state at the end of an anchor block
-        const bool at_anchor = (ci + 1) % A.anchor_every == 0 || ci == n_chunks - 1;
-        if (R.anchor_dots != nullptr && at_anchor) {
-            const int64_t m = ci / A.anchor_every;
-            const float* an = R.anchors + (bh * A.n_anchors + m) * R.dx * static_cast<int64_t>(R.dz);
-            float s = 0.0f;
+        // for the decays' gradient: the state at the end of an anchor block
+        const bool at_anchor = R.anchors != nullptr && ((ci + 1) % kAnchorChunks == 0 || ci == n_chunks - 1);
+        auto keep = [&]() {
+            float* an = R.anchors + (bh * A.n_anchors + ci / kAnchorChunks) * R.dx * static_cast<int64_t>(R.dz);
             for (int e = tid; e < dx * ZS; e += kThreads) {
                 const int a = e / ZS, c = e % ZS;
-                if (c < nz) s += sS[e] * an[static_cast<int64_t>(a) * R.dz + z0 + c];
+                if (c < nz) an[static_cast<int64_t>(a) * R.dz + z0 + c] = sS[e];
             }
-            for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            if (tid % 32 == 0) sP[tid / 32] = s;
-            __syncthreads();
-            if (tid == 0) {
-                float all = 0.0f;
-                for (int w = 0; w < kThreads / 32; ++w) all += sP[w];
-                R.anchor_dots[(slice * A.BH + bh) * A.n_anchors + m] = all * R.out_scale;
-            }
-            __syncthreads();
-        }
+        };
+        if (at_anchor && R.reverse) keep();
         for (int e = tid; e < C * dxp; e += kThreads) {
             const int t = e / dxp, a = e % dxp;
             const bool in = t < n && a < dx;
@@ -270,13 +261,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_consta
             for (int r = 0; r < 4; ++r)
                 *reinterpret_cast<float4*>(sS + (a + r) * ZS + c) = make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
         }
-        if (R.anchors != nullptr && R.anchor_dots == nullptr && at_anchor) {
+        if (at_anchor && !R.reverse) {
             __syncthreads();
-            float* an = R.anchors + (bh * A.n_anchors + ci / A.anchor_every) * R.dx * static_cast<int64_t>(R.dz);
-            for (int e = tid; e < dx * ZS; e += kThreads) {
-                const int a = e / ZS, c = e % ZS;
-                if (c < nz) an[static_cast<int64_t>(a) * R.dz + z0 + c] = sS[e];
-            }
+            keep();
         }
     }
     __syncthreads();
@@ -287,51 +274,75 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_consta
         }
 }
 
-// One warp an anchor block: the block's tokens from its end in groups of 32,
-// each group summed from its end by shuffles and carried in f32.  Reads the
-// rows' dots once (4 bytes a token and slice), so it is a small fraction of
-// the runs before it.
-__global__ void __launch_bounds__(256) k_attn_decay_grad(const AttnDecayGrad G) {
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32;
-    const int lane = threadIdx.x % 32;
-    const int64_t BH = G.B * G.H;
-    if (unit >= BH * G.n) return;
-    const int64_t bh = unit / G.n, m = unit % G.n, b = bh / G.H;
+// One CTA an anchor block.  The product of the two states at its end (all 256
+// threads: 8 bytes a value read once, the bulk of this kernel's traffic), then
+// the block's tokens from its end, thread t the t-th from the end: summed by
+// shuffles within a warp and across the warps through shared memory.
+__global__ void __launch_bounds__(kAttnAnchorTokens) k_attn_decay_grad(const __grid_constant__ AttnDecayGrad G) {
+    constexpr int kWarps = kAttnAnchorTokens / 32;
+    __shared__ float part[kWarps], total[kWarps];
+    const int64_t bh = blockIdx.x / G.n, m = blockIdx.x % G.n, BH = G.B * G.H, b = bh / G.H;
     const int h = static_cast<int>(bh % G.H);
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     int64_t len = G.T;
     if (G.lengths != nullptr) {
         const int64_t l = G.lengths[b];
         len = l < 0 ? 0 : l < G.T ? l : G.T;
     }
-    const int64_t lo = m * G.block, full = lo + G.block < G.T ? lo + G.block : G.T, hi = full < len ? full : len;
-    float carry = 0.0f, sum = 0.0f;
-    if (lo < hi)
-        for (int s = 0; s < G.slices_e; ++s) carry += G.ends[(s * BH + bh) * G.n + m];
-    for (int64_t top = hi; top > lo; top -= 32) {
-        const int64_t t = top - 32 + lane;
-        float v = 0.0f;
-        if (t >= lo) {
-            for (int s = 0; s < G.slices_q; ++s) v += G.dots_q[(s * BH + bh) * G.T + t];
-            for (int s = 0; s < G.slices_k; ++s) v -= G.dots_k[(s * BH + bh) * G.T + t];
+    const int64_t lo = m * kAttnAnchorTokens, full = lo + kAttnAnchorTokens < G.T ? lo + kAttnAnchorTokens : G.T;
+    const int64_t hi = full < len ? full : len;
+    float v = 0.0f, end = 0.0f;
+    if (lo < hi) {
+        const int64_t at = (bh * G.n + m) * G.size;
+        if (G.size % 4 == 0) {
+            const float4* a = reinterpret_cast<const float4*>(G.states_q + at);
+            const float4* c = reinterpret_cast<const float4*>(G.states_k + at);
+#pragma unroll 8
+            for (int64_t e = tid; e < G.size / 4; e += kAttnAnchorTokens) {
+                const float4 x = a[e], y = c[e];
+                end += x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
+            }
+        } else {
+            for (int64_t e = tid; e < G.size; e += kAttnAnchorTokens) end += G.states_q[at + e] * G.states_k[at + e];
         }
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const float q = __shfl_down_sync(0xffffffffu, v, o);
-            if (lane + o < 32) v += q;
-        }
-        v += carry;
-        if (t >= lo) {
-            if (G.grad != nullptr) G.grad[(b * G.T + t) * G.H + h] = v;
-            sum += v;
-        }
-        carry = __shfl_sync(0xffffffffu, v, 0);
     }
+    const int64_t t = hi - 1 - tid;
+    if (t >= lo) {
+        for (int s = 0; s < G.slices; ++s) v += G.dots_q[(s * BH + bh) * G.T + t];
+        for (int s = 0; s < G.slices; ++s) v -= G.dots_k[(s * BH + bh) * G.T + t];
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) end += __shfl_xor_sync(0xffffffffu, end, o);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const float q = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += q;
+    }
+    if (lane == 31) total[warp] = v;
+    if (lane == 0) part[warp] = end;
+    __syncthreads();
+    float carry = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) carry += part[w];
+    carry *= G.scale;
+    for (int w = 0; w < warp; ++w) carry += total[w];
+    v += carry;
+    if (t >= lo && G.grad != nullptr) G.grad[(b * G.T + t) * G.H + h] = v;
     if (G.grad != nullptr)
-        for (int64_t t = (hi > lo ? hi : lo) + lane; t < full; t += 32) G.grad[(b * G.T + t) * G.H + h] = 0.0f;
+        for (int64_t p = (hi > lo ? hi : lo) + tid; p < full; p += kAttnAnchorTokens) G.grad[(b * G.T + p) * G.H + h] = 0.0f;
     if (G.partial != nullptr) {
+        float sum = t >= lo ? v : 0.0f;
 #pragma unroll
         for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane == 0) G.partial[h * (G.B * G.n) + b * G.n + m] = sum;
+        __syncthreads();
+        if (lane == 0) part[warp] = sum;
+        __syncthreads();
+        if (tid == 0) {
+            float all = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) all += part[w];
+            G.partial[h * (G.B * G.n) + b * G.n + m] = all;
+        }
     }
 }
 
@@ -387,7 +398,6 @@ cudaError_t launch_attn_direct(const AttnLaunch& L) {
     A.gt = L.gt;
     A.gh = L.gh;
     A.lengths = L.lengths;
-    A.anchor_every = L.anchor_every;
     A.n_anchors = L.n_anchors;
     A.BH = L.B * L.H;
     const auto kernel = L.bf16 ? k_attn_direct<__nv_bfloat16> : k_attn_direct<float>;
@@ -400,9 +410,8 @@ cudaError_t launch_attn_direct(const AttnLaunch& L) {
 }
 
 cudaError_t launch_attn_decay_grad(const AttnDecayGrad& G, int* kernels) {
-    const int64_t units = G.B * G.H * G.n;
     *kernels = 1;
-    k_attn_decay_grad<<<static_cast<unsigned>((units + 7) / 8), 256, 0, G.stream>>>(G);
+    k_attn_decay_grad<<<static_cast<unsigned>(G.B * G.H * G.n), kAttnAnchorTokens, 0, G.stream>>>(G);
     if (G.grad_h != nullptr) {
         k_attn_sum_rows<<<G.H, 256, 0, G.stream>>>(G.partial, G.B * G.n, G.grad_h);
         ++*kernels;

@@ -56,6 +56,8 @@ constexpr uint32_t kTmemCols = 512;
 struct alignas(16) Coef {
     float g2[C];                              // inclusive sums of the log decays, base 2
     float read[C], upd[C];
+    float near_end[C];                        // decay between token j and the edge of its block of 8 that later (reversed: earlier) rows see
+    float edge[8];                            // g2 at that edge
     int bound[C];                             // forward: the first token row i sees; reversed: the last
     float decay;
     float pad[3];
@@ -71,7 +73,6 @@ struct TcRun {
     float init_scale, fin_scale, out_scale;
     float* dots;
     float* anchors;
-    float* anchor_dots;
     int xdiv, ydiv, zdiv, wdiv;
     int xb, yb, zb, wb;                       // 1; 0: one batch row for all
     int dx, dz;                               // real widths
@@ -184,7 +185,7 @@ __device__ __forceinline__ void arrive_warp(uint64_t* bar, int lane) {
 
 // kStateOnly: a segment's own state and decay, from zero (the first segment's
 // from the call's initial state): only Y and Z are read.
-template <bool kStateOnly>
+template <bool kStateOnly, bool kDots>
 __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__ TcArgs A) {
     extern __shared__ __align__(1024) unsigned char raw[];
     __shared__ Shared sh;
@@ -223,7 +224,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
     }
     const int dxp = (R.dx + 63) & ~63, dzp = (R.dz + 63) & ~63;
     const int px = dxp / 64, pz = dzp / 64;
-    const bool dots = !kStateOnly && R.dots != nullptr;
+    const bool dots = kDots && R.dots != nullptr;
+    // (the decays' gradient takes differences of the results: its terms are rounded to nearest)
+    constexpr bool kCut = !kDots;
 
     // a stage: X, Y, Z, and W's place, which is then the output tile's
     const uint32_t off_y = kStateOnly ? 0 : px * kPanel, off_z = off_y + px * kPanel, off_w = off_z + pz * kPanel;
@@ -358,6 +361,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             all *= decay;
             if (k >= A.stages && !wait(&sh.empty[ring.s], ring.parity ^ 1)) break;
             Coef& c = sh.coef[ring.s];
+            // the edge of the block of 8 tokens (4 lanes): after its last token, or (reversed) before its first
+            const float edge = R.reverse ? __shfl_sync(0xffffffffu, before, lane & ~3) : __shfl_sync(0xffffffffu, pre, lane | 3);
+            const float es = R.reverse ? -1.0f : 1.0f;
+            *reinterpret_cast<float2*>(&c.near_end[2 * lane]) =
+                make_float2(tc::exp2_approx(es * (edge - g2.x)), tc::exp2_approx(es * (edge - g2.y)));
+            if (lane % 4 == 0) c.edge[lane / 4] = edge;
             *reinterpret_cast<float2*>(&c.g2[2 * lane]) = g2;
             *reinterpret_cast<float2*>(&c.read[2 * lane]) = R.reverse ? to_end : from_start;
             *reinterpret_cast<float2*>(&c.upd[2 * lane]) = R.reverse ? from_start : to_end;
@@ -491,18 +500,31 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                         uint32_t r[8], hi[4], lo[4];
                         tc::ld(from + 8 * q, r);
                         const uint32_t mask = seen >> (8 * q);
+                        const int j0 = 32 * half + 8 * q;
+                        float2 d[4];
+                        if ((i & ~7) == j0) {
+                            // the row's own block: each difference by itself
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float2 gj = *reinterpret_cast<const float2*>(&c.g2[j0 + 2 * e]);
+                                d[e] = make_float2(tc::exp2_approx(sign * (gi - gj.x)), tc::exp2_approx(sign * (gi - gj.y)));
+                            }
+                        } else {
+                            // row to block edge, and block edge to column: neither grows
+                            const float row = tc::exp2_approx(sign * (gi - c.edge[j0 / 8]));
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                d[e] = pair_mul(*reinterpret_cast<const float2*>(&c.near_end[j0 + 2 * e]), make_float2(row, row));
+                        }
                         tc::wait_ld();
                         tc::loaded(r);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int j = 2 * e;
-                            const float2 gj = *reinterpret_cast<const float2*>(&c.g2[32 * half + 8 * q + j]);
-                            const float2 d = pair_fma(gj, make_float2(-sign, -sign), make_float2(gi * sign, gi * sign));
-                            float2 v = pair_mul(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])),
-                                                make_float2(tc::exp2_approx(d.x), tc::exp2_approx(d.y)));
+                            float2 v = pair_mul(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), d[e]);
                             if (!(mask & (1u << j))) v.x = 0.0f;
                             if (!(mask & (2u << j))) v.y = 0.0f;
-                            tc::split2(v, hi[e], lo[e]);
+                            tc::split2<kCut>(v, hi[e], lo[e]);
                         }
                         const uint32_t at = i * 128 + (((4 * half + q) ^ swz) << 4);
                         *reinterpret_cast<uint4*>(p_hi + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -550,11 +572,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                         v[e] = pair_mul(make_float2(tc::low_bf16(u), tc::high_bf16(u)), w);
                     }
 #pragma unroll 1
-                    for (int m = 0; m < R.terms; ++m) {
+                    for (int m = 0; m < R.terms - 1; ++m) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) t[e] = tc::take_term(v[e]);
+                        for (int e = 0; e < 8; ++e) t[e] = tc::take_term<kCut>(v[e]);
                         tc::st_words(lanes + 32 * m, t);
                     }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) t[e] = tc::pack_bf16(v[e].x, v[e].y);
+                    tc::st_words(lanes + 32 * (R.terms - 1), t);
                 }
                 tc::wait_st();
             }
@@ -591,7 +616,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 fa = R.dz;
             }
         }
-        const int slices = (R.dz + 31) / 32;
         bool ok = true;
         Ring ring;
         // n + 1 visits: the last one only takes the final state out
@@ -607,19 +631,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 if (!(ok = wait(&sh.ready[ring.s], ring.parity))) break;
                 decay = sh.coef[ring.s].decay;
             }
-            // the state between trip k - 1 and trip k is an anchor's
-            const int done = k > 0 ? chunk_of(k - 1) : 0, next = k < n ? chunk_of(k) : 0;
+            // the state between trip k - 1 and trip k, at the end of an anchor block
             float* dump = nullptr;
-            const float* anchor = nullptr;
-            float* anchor_to = nullptr;
-            if (!kStateOnly && on && R.anchors != nullptr) {
-                if (R.anchor_dots == nullptr) {
-                    if (k > 0 && ((done + 1) % kAnchorChunks == 0 || done == chunks - 1))
-                        dump = R.anchors + (bh * A.n_anchors + done / kAnchorChunks) * size + c;
-                } else if (k < n && ((next + 1) % kAnchorChunks == 0 || next == chunks - 1)) {
-                    anchor = R.anchors + (bh * A.n_anchors + next / kAnchorChunks) * size + c;
-                    anchor_to = R.anchor_dots + ((side * slices + slice) * A.BH + bh) * A.n_anchors + next / kAnchorChunks;
-                }
+            if (!kStateOnly && R.anchors != nullptr && (R.reverse ? k < n : k > 0)) {
+                const int at = chunk_of(R.reverse ? k : k - 1);
+                if ((at + 1) % kAnchorChunks == 0 || at == chunks - 1)
+                    dump = R.anchors + (bh * A.n_anchors + at / kAnchorChunks) * size + c;
             }
             float* out = nullptr;
             int64_t oa = 0;
@@ -645,9 +662,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 }
                 tc::wait_st();
             }
-            // now and then the state leaves, or meets an anchor
-            float dot = 0.0f;
-            const bool leaves = __any_sync(0xffffffffu, out != nullptr || dump != nullptr || anchor != nullptr);
+            // now and then the state leaves
+            const bool leaves = __any_sync(0xffffffffu, out != nullptr || dump != nullptr);
             if (leaves && on)
 #pragma unroll 1
                 for (int a0 = a_lo; a0 < min(a_hi, R.dx); a0 += 8) {
@@ -661,7 +677,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                         const int64_t row = static_cast<int64_t>(a0 + e) * R.dz;
                         if (!real) continue;
                         if (dump != nullptr) dump[row] = v;
-                        if (anchor != nullptr) dot += anchor[row] * v;
                         if (out != nullptr) out[(a0 + e) * oa] = v * os;
                     }
                 }
@@ -675,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const float2 v = make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
-                        if constexpr (!kStateOnly) tc::split2(v, t[e], u[e]);
+                        if constexpr (!kStateOnly) tc::split2<kCut>(v, t[e], u[e]);
                         const float2 d = pair_mul(v, make_float2(decay, decay));
                         r[2 * e] = __float_as_uint(d.x);
                         r[2 * e + 1] = __float_as_uint(d.y);
@@ -686,11 +701,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                     }
                     tc::st(t_h + lanes + a0, r);
                 }
-            }
-            if (anchor_to != nullptr) {
-#pragma unroll
-                for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-                if (lane == 0) *anchor_to = dot * R.out_scale;
             }
             if (k < n) {
                 tc::wait_st();
@@ -759,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                         }
                         const uint32_t at = smem_u32(st) + at0 + 8 * q * 128;
                         const int row = 32 * side + 8 * q + 2 * (lane % 4);
-                        if (dots) {
+                        if (kDots && dots) {
                             // out . w over the warp's columns (padded columns hold zeros)
                             uint32_t w[4];
                             tc::ld_blocks(at, w);
@@ -894,6 +904,7 @@ bool attn_tc_operand_ok(const AttnOperand& o, int heads, int d, int64_t T, int64
 cudaError_t launch_attn_tc(const AttnLaunch& L, int* kernels, const char** err) {
     TcArgs A{};
     uint32_t stage = 0;
+    bool any_dots = false;
     for (int r = 0; r < L.runs; ++r) {
         const AttnRun& f = L.run[r];
         TcRun& t = A.run[r];
@@ -917,8 +928,8 @@ cudaError_t launch_attn_tc(const AttnLaunch& L, int* kernels, const char** err) 
         t.fin_scale = f.fin_scale;
         t.out_scale = f.out_scale;
         t.dots = f.dots;
+        any_dots = any_dots || f.dots != nullptr;
         t.anchors = f.anchors;
-        t.anchor_dots = f.anchor_dots;
         t.xdiv = f.x.sh > 0 ? f.x.div : L.H;
         t.xb = f.x.sb > 0;
         t.ydiv = f.y.sh > 0 ? f.y.div : L.H;
@@ -964,18 +975,21 @@ cudaError_t launch_attn_tc(const AttnLaunch& L, int* kernels, const char** err) 
     *kernels = 0;
     cudaError_t e;
     const unsigned blocks = static_cast<unsigned>(A.BH * A.n_segs);
-    if (A.n_segs > 1) {
-        e = cudaFuncSetAttribute(k_attn_tc<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    auto launch = [&](void (*kernel)(TcArgs)) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e != cudaSuccess) return e;
-        k_attn_tc<true><<<dim3(blocks, L.runs), kThreads, smem, L.stream>>>(A);
+        kernel<<<dim3(blocks, L.runs), kThreads, smem, L.stream>>>(A);
+        return cudaGetLastError();
+    };
+    if (A.n_segs > 1) {
+        if ((e = launch(k_attn_tc<true, false>)) != cudaSuccess) return e;
         int most = 0;
         for (int r = 0; r < L.runs; ++r) most = L.run[r].dx * L.run[r].dz > most ? L.run[r].dx * L.run[r].dz : most;
         k_attn_tc_join<<<dim3((most + 255) / 256, L.runs, static_cast<unsigned>(A.BH)), 256, 0, L.stream>>>(A);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
         *kernels += 2;
     }
-    e = cudaFuncSetAttribute(k_attn_tc<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-    k_attn_tc<false><<<dim3(blocks, L.runs), kThreads, smem, L.stream>>>(A);
+    if ((e = launch(any_dots ? k_attn_tc<false, true> : k_attn_tc<false, false>)) != cudaSuccess) return e;
     ++*kernels;
     return cudaGetLastError();
 }
