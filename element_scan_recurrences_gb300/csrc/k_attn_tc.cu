@@ -183,6 +183,22 @@ __device__ __forceinline__ void arrive_warp(uint64_t* bar, int lane) {
     if (lane == 0) mbar_arrive(bar);
 }
 
+// Columns [lo, hi) of the warp's lanes of the state, scaled, to `to` (one value
+// column; null: none) and on every `stride` floats.
+__device__ __noinline__ void state_out(uint32_t state, int lo, int hi, float* to, int64_t stride, float scale) {
+#pragma unroll 1
+    for (int a0 = lo; a0 < hi; a0 += 8) {
+        uint32_t r[8];
+        tc::ld(state + a0, r);
+        tc::wait_ld();
+        tc::loaded(r);
+        if (to != nullptr) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) to[(a0 + e) * stride] = __uint_as_float(r[e]) * scale;
+        }
+    }
+}
+
 // kStateOnly: a segment's own state and decay, from zero (the first segment's
 // from the call's initial state): only Y and Z are read.
 template <bool kStateOnly, bool kDots>
@@ -244,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         mbar_init(&sh.p_ready, 4);
         mbar_init(&sh.zh_ready, 8 + 8);
         mbar_init(&sh.kv_done, 1);
-        mbar_init(&sh.o_done, 1);
+        mbar_init(&sh.o_done, 2);                                    // O1, O2
         mbar_init(&sh.o_read, 8);
         mbar_init(&sh.drained[0], 1);
         mbar_init(&sh.drained[1], 1);
@@ -397,6 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         const uint32_t i_64 = tc::instr_bf16(C, false, false), i_o1 = tc::instr_bf16(C, true, false);
         const uint32_t i_kv = tc::instr_bf16(static_cast<uint32_t>(dxp), false, true);
         const uint32_t base = smem_u32(tiles);
+        const uint32_t lead = tc::elect();
         Ring ring;
         if (warp == 7) {
 #pragma unroll 1
@@ -404,27 +421,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 const uint32_t sx = base + ring.s * A.stage_bytes;
                 const uint64_t d_x = tc::smem_desc(sx, 16, 1024), d_yt = tc::smem_desc(sx + off_y, kPanel, 1024);
                 if (!wait(&sh.ready[ring.s], ring.parity)) break;
-                if (!wait(&sh.zh_ready, k)) break;
                 // O2's region: the last chunk's has to be read
                 if (!kStateOnly && k > 0 && !wait(&sh.o_read, k - 1)) break;
+                if (!wait(&sh.zh_ready, k)) break;
                 tc::fence_after();
-                if (tc::elect()) {
-                    if constexpr (!kStateOnly) {
+                if constexpr (!kStateOnly) {
 #pragma unroll 1
-                        for (int p = 0; p < 2 * px; ++p) {
-                            const uint64_t d = d_x + (p < px ? p : p - px) * (kPanel >> 4);
-#pragma unroll 1
-                            for (int q = 0; q < 4; ++q) tc::mma_ts(t_o2, t_hb + 32 * p + 8 * q, d + q * 2, i_64, p + q > 0);
-                        }
+                    for (int p = 0; p < 2 * px; ++p) {
+                        const uint64_t d = d_x + (p < px ? p : p - px) * (kPanel >> 4);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) tc::mma_ts(lead, t_o2, t_hb + 32 * p + 8 * q, d + q * 2, i_64, p + q > 0);
                     }
-#pragma unroll 1
-                    for (int m = 0; m < R.terms; ++m)
-#pragma unroll 1
-                        for (int q = 0; q < C / 16; ++q) tc::mma_ts(t_h, t_zt + m * (C / 2) + q * 8, d_yt + q * 128, i_kv, true);
-                    tc::commit(&sh.kv_done);
-                    tc::commit(&sh.empty[ring.s]);
                 }
-                __syncwarp();
+#pragma unroll 1
+                for (int m = 0; m < R.terms; ++m)
+#pragma unroll
+                    for (int q = 0; q < C / 16; ++q)
+                        tc::mma_ts(lead, t_h, t_zt + m * (C / 2) + q * 8, d_yt + q * 128, i_kv, true);
+                tc::commit(lead, &sh.kv_done);
+                if constexpr (!kStateOnly) tc::commit(lead, &sh.o_done);
+                tc::commit(lead, &sh.empty[ring.s]);
             }
         } else if constexpr (!kStateOnly) {
             const uint64_t d_phi = tc::smem_desc(smem_u32(p_hi), 16, 1024);
@@ -437,34 +453,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 // with three terms of Z the scores' region holds the last chunk's O1 until it is read
                 if (R.terms == 3 && k > 0 && !wait(&sh.o_read, k - 1)) break;
                 tc::fence_after();
-                if (tc::elect()) {
 #pragma unroll 1
-                    for (int p = 0; p < px; ++p)
-#pragma unroll 1
-                        for (int q = 0; q < 4; ++q)
-                            tc::mma_ss(t_s, d_x + p * (kPanel >> 4) + q * 2, d_y + p * (kPanel >> 4) + q * 2, i_64, p + q > 0);
-                    tc::commit(&sh.s_done);
-                }
-                __syncwarp();
+                for (int p = 0; p < px; ++p)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        tc::mma_ss(lead, t_s, d_x + p * (kPanel >> 4) + q * 2, d_y + p * (kPanel >> 4) + q * 2, i_64, p + q > 0);
+                tc::commit(lead, &sh.s_done);
                 if (R.terms == 2 && k > 0 && !wait(&sh.o_read, k - 1)) break;
                 if (!wait(&sh.p_ready, k)) break;
                 tc::fence_after();
-                if (tc::elect()) {
 #pragma unroll 1
-                    for (int m = 0; m < 2; ++m)
-#pragma unroll 1
-                        for (int q = 0; q < C / 16; ++q)
-                            tc::mma_ss(t_o1, d_zt + q * 128, d_phi + m * (kPanel >> 4) + q * 2, i_o1, m + q > 0);
-                    tc::commit(&sh.o_done);
-                    tc::commit(&sh.empty[ring.s]);
-                }
-                __syncwarp();
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int q = 0; q < C / 16; ++q)
+                        tc::mma_ss(lead, t_o1, d_zt + q * 128, d_phi + m * (kPanel >> 4) + q * 2, i_o1, m + q > 0);
+                tc::commit(lead, &sh.o_done);
+                tc::commit(lead, &sh.empty[ring.s]);
             }
         }
         // nothing of this CTA's may still run when its tensor memory goes
         uint64_t* drained = &sh.drained[warp == 7];
-        if (tc::elect()) tc::commit(drained);
-        __syncwarp();
+        tc::commit(lead, drained);
         if (!__all_sync(0xffffffffu, wait_bounded(drained, 0, A.wait_ns, nullptr)) && lane == 0)
             atomicOr(A.status, ES_DEVICE_TIMEOUT);
     } else if (warp < 8) {
@@ -474,11 +483,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             const uint32_t from = t_s + (static_cast<uint32_t>(32 * (warp & 1)) << 16) + 32 * half;
             // rows of one half never see the columns of the other: forward rows 0-31 the late columns
             const float sign = R.reverse ? -1.0f : 1.0f;
+            const bool diagonal = (warp & 1) == half;
             const bool none = R.reverse ? (warp & 1) > half : (warp & 1) < half;
             Ring ring;
 #pragma unroll 1
             for (int k = 0; k < n; ++k, ring.next(A.stages)) {
-                if (!wait(&sh.ready[ring.s], ring.parity) || !wait(&sh.s_done, k)) break;
+                // (the products waited for the stage, so its coefficients are there)
+                if (!wait(&sh.s_done, k)) break;
                 const Coef& c = sh.coef[ring.s];
                 const uint32_t swz = i & 7;
                 if (none) {
@@ -502,12 +513,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                         const uint32_t mask = seen >> (8 * q);
                         const int j0 = 32 * half + 8 * q;
                         float2 d[4];
-                        if ((i & ~7) == j0) {
-                            // the row's own block: each difference by itself
+                        if (diagonal) {
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 const float2 gj = *reinterpret_cast<const float2*>(&c.g2[j0 + 2 * e]);
-                                d[e] = make_float2(tc::exp2_approx(sign * (gi - gj.x)), tc::exp2_approx(sign * (gi - gj.y)));
+                                const float2 x = pair_fma(gj, make_float2(-sign, -sign), make_float2(gi * sign, gi * sign));
+                                d[e] = make_float2(tc::exp2_approx(x.x), tc::exp2_approx(x.y));
                             }
                         } else {
                             // row to block edge, and block edge to column: neither grows
@@ -518,14 +529,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                         }
                         tc::wait_ld();
                         tc::loaded(r);
+                        float2 v[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int j = 2 * e;
-                            float2 v = pair_mul(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), d[e]);
-                            if (!(mask & (1u << j))) v.x = 0.0f;
-                            if (!(mask & (2u << j))) v.y = 0.0f;
-                            tc::split2<kCut>(v, hi[e], lo[e]);
+                        for (int e = 0; e < 4; ++e)
+                            v[e] = pair_mul(make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), d[e]);
+                        if (!__all_sync(0xffffffffu, (mask & 0xffu) == 0xffu)) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                if (!(mask & (1u << (2 * e)))) v[e].x = 0.0f;
+                                if (!(mask & (2u << (2 * e)))) v[e].y = 0.0f;
+                            }
                         }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) tc::split2<kCut>(v[e], hi[e], lo[e]);
                         const uint32_t at = i * 128 + (((4 * half + q) ^ swz) << 4);
                         *reinterpret_cast<uint4*>(p_hi + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                         *reinterpret_cast<uint4*>(p_lo + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -616,71 +632,34 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 fa = R.dz;
             }
         }
-        bool ok = true;
+        // the chunk's state leaves for its anchor block
+        auto keep = [&](int at) {
+            if ((at + 1) % kAnchorChunks == 0 || at == chunks - 1)
+                state_out(t_h + lanes, a_lo, min(a_hi, R.dx), real ? R.anchors + (bh * A.n_anchors + at / kAnchorChunks) * size + c : nullptr,
+                          R.dz, 1.0f);
+        };
+        if (on) {
+#pragma unroll 1
+            for (int a0 = a_lo; a0 < a_hi; a0 += 8) {
+                uint32_t r[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    r[e] = __float_as_uint(from != nullptr && a0 + e < R.dx ? from[(a0 + e) * fa] * fs : 0.0f);
+                tc::st(t_h + lanes + a0, r);
+            }
+            tc::wait_st();
+        }
+        const bool anchored = !kStateOnly && R.anchors != nullptr && on;
         Ring ring;
-        // n + 1 visits: the last one only takes the final state out
+        int k = 0;
 #pragma unroll 1
-        for (int k = 0; k <= n && ok; ++k, ring.next(A.stages)) {
-            if (k > 0) {
-                ok = wait(&sh.kv_done, k - 1);
-                if (!ok) break;
-                tc::fence_after();
-            }
-            float decay = 0.0f;
-            if (k < n) {
-                if (!(ok = wait(&sh.ready[ring.s], ring.parity))) break;
-                decay = sh.coef[ring.s].decay;
-            }
-            // the state between trip k - 1 and trip k, at the end of an anchor block
-            float* dump = nullptr;
-            if (!kStateOnly && R.anchors != nullptr && (R.reverse ? k < n : k > 0)) {
-                const int at = chunk_of(R.reverse ? k : k - 1);
-                if ((at + 1) % kAnchorChunks == 0 || at == chunks - 1)
-                    dump = R.anchors + (bh * A.n_anchors + at / kAnchorChunks) * size + c;
-            }
-            float* out = nullptr;
-            int64_t oa = 0;
-            float os = 1.0f;
-            if (k == n && real) {
-                if (kStateOnly) {
-                    out = A.seg_states + blockIdx.y * A.seg_stride + (bh * A.n_segs + seg) * size + c;
-                    oa = R.dz;
-                } else if (ends && R.fin != nullptr) {
-                    out = R.fin + bh * size + c * R.sc;
-                    oa = R.sa;
-                    os = R.fin_scale;
-                }
-            }
-            if (k == 0 && on) {
-#pragma unroll 1
-                for (int a0 = a_lo; a0 < a_hi; a0 += 8) {
-                    uint32_t r[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        r[e] = __float_as_uint(from != nullptr && a0 + e < R.dx ? from[(a0 + e) * fa] * fs : 0.0f);
-                    tc::st(t_h + lanes + a0, r);
-                }
-                tc::wait_st();
-            }
-            // now and then the state leaves
-            const bool leaves = __any_sync(0xffffffffu, out != nullptr || dump != nullptr);
-            if (leaves && on)
-#pragma unroll 1
-                for (int a0 = a_lo; a0 < min(a_hi, R.dx); a0 += 8) {
-                    uint32_t r[8];
-                    tc::ld(t_h + lanes + a0, r);
-                    tc::wait_ld();
-                    tc::loaded(r);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float v = __uint_as_float(r[e]);
-                        const int64_t row = static_cast<int64_t>(a0 + e) * R.dz;
-                        if (!real) continue;
-                        if (dump != nullptr) dump[row] = v;
-                        if (out != nullptr) out[(a0 + e) * oa] = v * os;
-                    }
-                }
-            if (on && k < n) {
+        for (; k < n; ++k, ring.next(A.stages)) {
+            if (!wait(&sh.ready[ring.s], ring.parity)) break;
+            const float decay = sh.coef[ring.s].decay;
+            if (k > 0 && !wait(&sh.kv_done, k - 1)) break;
+            tc::fence_after();
+            if (anchored && (R.reverse || k > 0)) keep(chunk_of(R.reverse ? k : k - 1));
+            if (on) {
 #pragma unroll 1
                 for (int a0 = a_lo; a0 < a_hi; a0 += 16) {
                     uint32_t r[16], t[8], u[8];
@@ -702,15 +681,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                     tc::st(t_h + lanes + a0, r);
                 }
             }
-            if (k < n) {
-                tc::wait_st();
-                tc::fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&sh.zh_ready);
-                    mbar_arrive(&sh.empty[ring.s]);
-                }
+            tc::wait_st();
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&sh.zh_ready);
+                mbar_arrive(&sh.empty[ring.s]);
             }
+        }
+        // the last state
+        if (k == n && (n == 0 || wait(&sh.kv_done, n - 1))) {
+            tc::fence_after();
+            if (anchored && !R.reverse && n > 0) keep(chunk_of(n - 1));
+            if (on && kStateOnly)
+                state_out(t_h + lanes, a_lo, min(a_hi, R.dx),
+                          real ? A.seg_states + blockIdx.y * A.seg_stride + (bh * A.n_segs + seg) * size + c : nullptr, R.dz, 1.0f);
+            else if (on && ends && R.fin != nullptr)
+                state_out(t_h + lanes, a_lo, min(a_hi, R.dx), real ? R.fin + bh * size + c * R.sc : nullptr, R.sa, R.fin_scale);
         }
     } else {
         // ---- outputs: lane = value column c, tokens along the columns
@@ -729,8 +716,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             Ring ring;
 #pragma unroll 1
             for (int k = 0; k < n; ++k, ring.next(A.stages)) {
-                // (kv_done: O2 is there too)
-                if (!wait(&sh.ready[ring.s], ring.parity) || !wait(&sh.kv_done, k) || !wait(&sh.o_done, k)) break;
+                // (the products waited for the stage, so what came with it is there)
+                if (!wait(&sh.o_done, k)) break;
                 tc::fence_after();
                 const int64_t t0 = static_cast<int64_t>(chunk_of(k)) * C;
                 const int left = static_cast<int>(min(static_cast<int64_t>(C), len - t0));
