@@ -102,7 +102,7 @@ struct TcArgs {
 
 struct Shared {
     uint64_t full[kMaxStages], ready[kMaxStages], empty[kMaxStages];
-    uint64_t s_done, p_ready, zh_ready, kv_done, o_done, o_read, drained[2];
+    uint64_t s_done, p_ready, p_free, zh_ready, kv_done, o_done, o_read, drained[2];
     uint32_t tmem;
     int abort_flag;
     Coef coef[kMaxStages];
@@ -258,6 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         }
         mbar_init(&sh.s_done, 1);
         mbar_init(&sh.p_ready, 4);
+        mbar_init(&sh.p_free, 1);
         mbar_init(&sh.zh_ready, 8 + 8);
         mbar_init(&sh.kv_done, 1);
         mbar_init(&sh.o_done, 2);                                    // O1, O2
@@ -272,8 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
     tc::fence_after();
     // all of the SM's tensor memory is this CTA's, so its address is 0
     constexpr uint32_t tmem = 0;
-    const uint32_t t_h = tmem, t_hb = t_h + dxp, t_zt = t_hb + dxp, t_s = t_zt + R.terms * (C / 2), t_o2 = t_s + C;
-    const uint32_t t_o1 = R.terms == 2 ? t_o2 + C : t_s;
+    const uint32_t t_h = tmem, t_hb = t_h + dxp, t_zt = t_hb + dxp, t_s = t_zt + C, t_o1 = t_s + C, t_o2 = t_o1 + C;
     const Wait wait{A.wait_ns, &sh.abort_flag, A.status};
     auto chunk_of = [&](int k) { return R.reverse ? c1 - 1 - k : c0 + k; };
 
@@ -412,18 +412,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         // ---- products: warp 7 those of the state, warp 3 those of the scores, so that neither waits for the other's turn
         const uint32_t i_64 = tc::instr_bf16(C, false, false), i_o1 = tc::instr_bf16(C, true, false);
         const uint32_t i_kv = tc::instr_bf16(static_cast<uint32_t>(dxp), false, true);
+        const uint32_t i_kv3 = tc::instr_bf16(static_cast<uint32_t>(dxp), true, true);
         const uint32_t base = smem_u32(tiles);
         const uint32_t lead = tc::elect();
         Ring ring;
+        int last = 0;
         if (warp == 7) {
 #pragma unroll 1
             for (int k = 0; k < n; ++k, ring.next(A.stages)) {
                 const uint32_t sx = base + ring.s * A.stage_bytes;
                 const uint64_t d_x = tc::smem_desc(sx, 16, 1024), d_yt = tc::smem_desc(sx + off_y, kPanel, 1024);
                 if (!wait(&sh.ready[ring.s], ring.parity)) break;
+                if (!wait(&sh.zh_ready, k)) break;
                 // O2's region: the last chunk's has to be read
                 if (!kStateOnly && k > 0 && !wait(&sh.o_read, k - 1)) break;
-                if (!wait(&sh.zh_ready, k)) break;
                 tc::fence_after();
                 if constexpr (!kStateOnly) {
 #pragma unroll 1
@@ -434,41 +436,52 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                     }
                 }
 #pragma unroll 1
-                for (int m = 0; m < R.terms; ++m)
+                for (int m = 0; m < 2; ++m)
 #pragma unroll
                     for (int q = 0; q < C / 16; ++q)
                         tc::mma_ts(lead, t_h, t_zt + m * (C / 2) + q * 8, d_yt + q * 128, i_kv, true);
+                if (R.terms == 3) {
+                    const uint64_t d_w = tc::smem_desc(sx + off_w, kPanel, 1024);
+#pragma unroll
+                    for (int q = 0; q < C / 16; ++q) tc::mma_ss(lead, t_h, d_w + q * 128, d_yt + q * 128, i_kv3, true);
+                }
                 tc::commit(lead, &sh.kv_done);
                 if constexpr (!kStateOnly) tc::commit(lead, &sh.o_done);
                 tc::commit(lead, &sh.empty[ring.s]);
             }
         } else if constexpr (!kStateOnly) {
             const uint64_t d_phi = tc::smem_desc(smem_u32(p_hi), 16, 1024);
+            // a chunk's scores go ahead of the last chunk's O1: P is on the longest way around
 #pragma unroll 1
-            for (int k = 0; k < n; ++k, ring.next(A.stages)) {
-                const uint32_t sx = base + ring.s * A.stage_bytes;
-                const uint64_t d_x = tc::smem_desc(sx, 16, 1024), d_y = tc::smem_desc(sx + off_y, 16, 1024);
-                const uint64_t d_zt = tc::smem_desc(sx + off_z, kPanel, 1024);
-                if (!wait(&sh.ready[ring.s], ring.parity)) break;
-                // with three terms of Z the scores' region holds the last chunk's O1 until it is read
-                if (R.terms == 3 && k > 0 && !wait(&sh.o_read, k - 1)) break;
-                tc::fence_after();
+            for (int k = 0; k <= n; ++k) {
+                if (k > 0 && !wait(&sh.p_ready, k - 1)) break;
+                if (k < n) {
+                    if (!wait(&sh.ready[ring.s], ring.parity)) break;
+                    const uint32_t sx = base + ring.s * A.stage_bytes;
+                    const uint64_t d_x = tc::smem_desc(sx, 16, 1024), d_y = tc::smem_desc(sx + off_y, 16, 1024);
+                    tc::fence_after();
 #pragma unroll 1
-                for (int p = 0; p < px; ++p)
+                    for (int p = 0; p < px; ++p)
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        tc::mma_ss(lead, t_s, d_x + p * (kPanel >> 4) + q * 2, d_y + p * (kPanel >> 4) + q * 2, i_64, p + q > 0);
-                tc::commit(lead, &sh.s_done);
-                if (R.terms == 2 && k > 0 && !wait(&sh.o_read, k - 1)) break;
-                if (!wait(&sh.p_ready, k)) break;
-                tc::fence_after();
+                        for (int q = 0; q < 4; ++q)
+                            tc::mma_ss(lead, t_s, d_x + p * (kPanel >> 4) + q * 2, d_y + p * (kPanel >> 4) + q * 2, i_64, p + q > 0);
+                    tc::commit(lead, &sh.s_done);
+                }
+                if (k > 0) {
+                    const uint64_t d_zt = tc::smem_desc(base + last * A.stage_bytes + off_z, kPanel, 1024);
+                    if (k > 1 && !wait(&sh.o_read, k - 2)) break;
+                    tc::fence_after();
 #pragma unroll 1
-                for (int m = 0; m < 2; ++m)
+                    for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int q = 0; q < C / 16; ++q)
-                        tc::mma_ss(lead, t_o1, d_zt + q * 128, d_phi + m * (kPanel >> 4) + q * 2, i_o1, m + q > 0);
-                tc::commit(lead, &sh.o_done);
-                tc::commit(lead, &sh.empty[ring.s]);
+                        for (int q = 0; q < C / 16; ++q)
+                            tc::mma_ss(lead, t_o1, d_zt + q * 128, d_phi + m * (kPanel >> 4) + q * 2, i_o1, m + q > 0);
+                    tc::commit(lead, &sh.o_done);
+                    tc::commit(lead, &sh.p_free);
+                    tc::commit(lead, &sh.empty[last]);
+                }
+                last = ring.s;
+                ring.next(A.stages);
             }
         }
         // nothing of this CTA's may still run when its tensor memory goes
@@ -490,6 +503,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             for (int k = 0; k < n; ++k, ring.next(A.stages)) {
                 // (the products waited for the stage, so its coefficients are there)
                 if (!wait(&sh.s_done, k)) break;
+                // P's place: the last chunk's O1 has read it
+                if (k > 0 && !wait(&sh.p_free, k - 1)) break;
                 const Coef& c = sh.coef[ring.s];
                 const uint32_t swz = i & 7;
                 if (none) {
@@ -587,15 +602,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                         const uint32_t u = z[e / 4][e % 4];
                         v[e] = pair_mul(make_float2(tc::low_bf16(u), tc::high_bf16(u)), w);
                     }
-#pragma unroll 1
-                    for (int m = 0; m < R.terms - 1; ++m) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) t[e] = tc::take_term<kCut>(v[e]);
+                    tc::st_words(lanes, t);
+                    if (R.terms == 3) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e) t[e] = tc::take_term<kCut>(v[e]);
-                        tc::st_words(lanes + 32 * m, t);
-                    }
+                        tc::st_words(lanes + 32, t);
+                        // the third goes back as it came, to W's place, which this run leaves to the results
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) t[e] = tc::pack_bf16(v[e].x, v[e].y);
-                    tc::st_words(lanes + 32 * (R.terms - 1), t);
+                        for (int e = 0; e < 8; ++e) z[e / 4][e % 4] = tc::pack_bf16(v[e].x, v[e].y);
+                        tc::st_blocks((at ^ (half << 5)) + off_w - off_z, z[0]);
+                        tc::st_blocks((at ^ (half << 5)) + off_w - off_z + 16 * 128, z[1]);
+                        fence_proxy_async_smem();
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) t[e] = tc::pack_bf16(v[e].x, v[e].y);
+                        tc::st_words(lanes + 32, t);
+                    }
                 }
                 tc::wait_st();
             }
