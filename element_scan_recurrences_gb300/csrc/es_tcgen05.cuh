@@ -127,14 +127,10 @@ __device__ __forceinline__ void st_blocks(uint32_t addr, const uint32_t (&r)[4])
 // ---------------------------------------------------------------------------
 // products
 
-// Shared-memory operand descriptor, 128-byte swizzle: rows of 64 16-bit values
-// in groups of 8 (1024 bytes).  K innermost: `sbo` is the step between groups
-// of 8 rows, `lbo` unused.  Rows innermost (a transposed operand): `sbo` is the
-// step between groups of 8 along K, `lbo` between panels of 64 rows.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-    return static_cast<uint64_t>((addr >> 4) & 0x3fffu) | (static_cast<uint64_t>((lbo >> 4) & 0x3fffu) << 16) |
-           (static_cast<uint64_t>((sbo >> 4) & 0x3fffu) << 32) | (1ull << 46) | (2ull << 61);
-}
+// Shared-memory operand descriptors, 128-byte swizzle: rows of 64 16-bit values
+// in groups of 8 (1024 bytes, `sbo`).  K innermost: sbo is the step between
+// groups of 8 rows, `lbo` unused.  Rows innermost (a transposed operand): sbo is
+// the step between groups of 8 along K, lbo between panels of 64 rows.
 
 // Instruction descriptor of bf16 operands with f32 sums, M = 128.
 __host__ __device__ constexpr uint32_t instr_bf16(uint32_t n, bool a_rows_inner, bool b_rows_inner) {
@@ -154,21 +150,32 @@ __device__ __forceinline__ uint32_t elect() {
     return r;
 }
 
-// d (+)= a b, 16 along K; both operands in shared memory
-__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t instr, bool add) {
+// Shared-memory descriptors differ in their low words only, which the callers
+// count up; the high word holds `sbo` and the kind.
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lbo) {
+    return ((addr >> 4) & 0x3fffu) | (((lbo >> 4) & 0x3fffu) << 16);
+}
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);     // sbo 1024, 128-byte swizzle
+
+// d = a b (first) or d += a b, 16 along K; both operands in shared memory
+template <bool kFirst = false>
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t instr) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(instr), "r"(static_cast<uint32_t>(add)), "r"(lead)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %6};\n\tmov.b64 b, {%2, %6};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(instr), "n"(kFirst ? 0 : 1), "r"(lead), "r"(kDescHigh)
         : "memory");
 }
 
-// d (+)= a b with a in tensor memory (a row a lane, two bf16 a column)
-__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t instr, bool add) {
+// the same with a in tensor memory (a row a lane, two bf16 a column)
+template <bool kFirst = false>
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t instr) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(instr), "r"(static_cast<uint32_t>(add)), "r"(lead)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %6};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(instr), "n"(kFirst ? 0 : 1), "r"(lead), "r"(kDescHigh)
         : "memory");
 }
 

@@ -102,7 +102,7 @@ struct TcArgs {
 
 struct Shared {
     uint64_t full[kMaxStages], ready[kMaxStages], empty[kMaxStages];
-    uint64_t s_done, p_ready, p_free, zh_ready, kv_done, o_done, o_read, drained[2];
+    uint64_t s_done, p_ready, zh_ready, kv_done, o_done, o_read, drained[2];
     uint32_t tmem;
     int abort_flag;
     Coef coef[kMaxStages];
@@ -258,7 +258,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         }
         mbar_init(&sh.s_done, 1);
         mbar_init(&sh.p_ready, 4);
-        mbar_init(&sh.p_free, 1);
         mbar_init(&sh.zh_ready, 8 + 8);
         mbar_init(&sh.kv_done, 1);
         mbar_init(&sh.o_done, 2);                                    // O1, O2
@@ -415,70 +414,78 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         const uint32_t i_kv3 = tc::instr_bf16(static_cast<uint32_t>(dxp), true, true);
         const uint32_t base = smem_u32(tiles);
         const uint32_t lead = tc::elect();
+        constexpr uint32_t kPanelStep = kPanel >> 4, kRows16 = 2048 >> 4;      // in descriptors' units
         Ring ring;
-        int last = 0;
         if (warp == 7) {
 #pragma unroll 1
             for (int k = 0; k < n; ++k, ring.next(A.stages)) {
                 const uint32_t sx = base + ring.s * A.stage_bytes;
-                const uint64_t d_x = tc::smem_desc(sx, 16, 1024), d_yt = tc::smem_desc(sx + off_y, kPanel, 1024);
                 if (!wait(&sh.ready[ring.s], ring.parity)) break;
                 if (!wait(&sh.zh_ready, k)) break;
-                // O2's region: the last chunk's has to be read
-                if (!kStateOnly && k > 0 && !wait(&sh.o_read, k - 1)) break;
-                tc::fence_after();
+                const uint32_t y = tc::desc_low(sx + off_y, kPanel);
                 if constexpr (!kStateOnly) {
-#pragma unroll 1
-                    for (int p = 0; p < 2 * px; ++p) {
-                        const uint64_t d = d_x + (p < px ? p : p - px) * (kPanel >> 4);
+                    // O2's region: the last chunk's has to be read
+                    if (k > 0 && !wait(&sh.o_read, k - 1)) break;
+                    tc::fence_after();
+                    const uint32_t x = tc::desc_low(sx, 16);
+                    tc::mma_ts<true>(lead, t_o2, t_hb, x, i_64);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) tc::mma_ts(lead, t_o2, t_hb + 32 * p + 8 * q, d + q * 2, i_64, p + q > 0);
+                    for (int q = 1; q < 4; ++q) tc::mma_ts(lead, t_o2, t_hb + 8 * q, x + 2 * q, i_64);
+#pragma unroll 1
+                    for (int p = 1; p < 2 * px; ++p) {
+                        const uint32_t xp = x + (p < px ? p : p - px) * kPanelStep;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) tc::mma_ts(lead, t_o2, t_hb + 32 * p + 8 * q, xp + 2 * q, i_64);
                     }
+                } else {
+                    tc::fence_after();
                 }
 #pragma unroll 1
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int q = 0; q < C / 16; ++q)
-                        tc::mma_ts(lead, t_h, t_zt + m * (C / 2) + q * 8, d_yt + q * 128, i_kv, true);
+                    for (int q = 0; q < C / 16; ++q) tc::mma_ts(lead, t_h, t_zt + m * (C / 2) + q * 8, y + q * kRows16, i_kv);
                 if (R.terms == 3) {
-                    const uint64_t d_w = tc::smem_desc(sx + off_w, kPanel, 1024);
+                    const uint32_t w = tc::desc_low(sx + off_w, kPanel);
 #pragma unroll
-                    for (int q = 0; q < C / 16; ++q) tc::mma_ss(lead, t_h, d_w + q * 128, d_yt + q * 128, i_kv3, true);
+                    for (int q = 0; q < C / 16; ++q) tc::mma_ss(lead, t_h, w + q * kRows16, y + q * kRows16, i_kv3);
                 }
                 tc::commit(lead, &sh.kv_done);
                 if constexpr (!kStateOnly) tc::commit(lead, &sh.o_done);
                 tc::commit(lead, &sh.empty[ring.s]);
             }
         } else if constexpr (!kStateOnly) {
-            const uint64_t d_phi = tc::smem_desc(smem_u32(p_hi), 16, 1024);
-            // a chunk's scores go ahead of the last chunk's O1: P is on the longest way around
+            const uint32_t phi = tc::desc_low(smem_u32(p_hi), 16);
+            int last = 0;
 #pragma unroll 1
             for (int k = 0; k <= n; ++k) {
-                if (k > 0 && !wait(&sh.p_ready, k - 1)) break;
-                if (k < n) {
-                    if (!wait(&sh.ready[ring.s], ring.parity)) break;
-                    const uint32_t sx = base + ring.s * A.stage_bytes;
-                    const uint64_t d_x = tc::smem_desc(sx, 16, 1024), d_y = tc::smem_desc(sx + off_y, 16, 1024);
-                    tc::fence_after();
-#pragma unroll 1
-                    for (int p = 0; p < px; ++p)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            tc::mma_ss(lead, t_s, d_x + p * (kPanel >> 4) + q * 2, d_y + p * (kPanel >> 4) + q * 2, i_64, p + q > 0);
-                    tc::commit(lead, &sh.s_done);
-                }
                 if (k > 0) {
-                    const uint64_t d_zt = tc::smem_desc(base + last * A.stage_bytes + off_z, kPanel, 1024);
+                    // O1 of the last chunk
+                    if (!wait(&sh.p_ready, k - 1)) break;
                     if (k > 1 && !wait(&sh.o_read, k - 2)) break;
                     tc::fence_after();
-#pragma unroll 1
-                    for (int m = 0; m < 2; ++m)
+                    const uint32_t z = tc::desc_low(base + last * A.stage_bytes + off_z, kPanel);
+                    tc::mma_ss<true>(lead, t_o1, z, phi, i_o1);
 #pragma unroll
-                        for (int q = 0; q < C / 16; ++q)
-                            tc::mma_ss(lead, t_o1, d_zt + q * 128, d_phi + m * (kPanel >> 4) + q * 2, i_o1, m + q > 0);
+                    for (int q = 1; q < C / 16; ++q) tc::mma_ss(lead, t_o1, z + q * kRows16, phi + 2 * q, i_o1);
+#pragma unroll
+                    for (int q = 0; q < C / 16; ++q) tc::mma_ss(lead, t_o1, z + q * kRows16, phi + kPanelStep + 2 * q, i_o1);
                     tc::commit(lead, &sh.o_done);
-                    tc::commit(lead, &sh.p_free);
                     tc::commit(lead, &sh.empty[last]);
+                }
+                if (k < n) {
+                    // this chunk's scores; their commit stands for O1 too, so P's place is free by then
+                    if (!wait(&sh.ready[ring.s], ring.parity)) break;
+                    tc::fence_after();
+                    const uint32_t sx = base + ring.s * A.stage_bytes;
+                    const uint32_t x = tc::desc_low(sx, 16), y = tc::desc_low(sx + off_y, 16);
+                    tc::mma_ss<true>(lead, t_s, x, y, i_64);
+#pragma unroll
+                    for (int q = 1; q < 4; ++q) tc::mma_ss(lead, t_s, x + 2 * q, y + 2 * q, i_64);
+                    if (px == 2)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            tc::mma_ss(lead, t_s, x + kPanelStep + 2 * q, y + kPanelStep + 2 * q, i_64);
+                    tc::commit(lead, &sh.s_done);
                 }
                 last = ring.s;
                 ring.next(A.stages);
@@ -503,8 +510,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             for (int k = 0; k < n; ++k, ring.next(A.stages)) {
                 // (the products waited for the stage, so its coefficients are there)
                 if (!wait(&sh.s_done, k)) break;
-                // P's place: the last chunk's O1 has read it
-                if (k > 0 && !wait(&sh.p_free, k - 1)) break;
                 const Coef& c = sh.coef[ring.s];
                 const uint32_t swz = i & 7;
                 if (none) {
@@ -516,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                     }
                 } else {
                     tc::fence_after();
-                    const float gi = c.g2[i];
+                    const float gs = sign * c.g2[i];
                     const int bound = c.bound[i];
                     // the half's columns that row i sees, as bits
                     const int first = max(0, (R.reverse ? i : bound) - 32 * half), last = min(31, (R.reverse ? bound : i) - 32 * half);
@@ -530,17 +535,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                         float2 d[4];
                         if (diagonal) {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float2 gj = *reinterpret_cast<const float2*>(&c.g2[j0 + 2 * e]);
-                                const float2 x = pair_fma(gj, make_float2(-sign, -sign), make_float2(gi * sign, gi * sign));
+                            for (int e = 0; e < 4; e += 2) {
+                                const float4 gj = *reinterpret_cast<const float4*>(&c.g2[j0 + 2 * e]);
+                                const float2 x = pair_fma(make_float2(gj.x, gj.y), make_float2(-sign, -sign), make_float2(gs, gs));
+                                const float2 y = pair_fma(make_float2(gj.z, gj.w), make_float2(-sign, -sign), make_float2(gs, gs));
                                 d[e] = make_float2(tc::exp2_approx(x.x), tc::exp2_approx(x.y));
+                                d[e + 1] = make_float2(tc::exp2_approx(y.x), tc::exp2_approx(y.y));
                             }
                         } else {
                             // row to block edge, and block edge to column: neither grows
-                            const float row = tc::exp2_approx(sign * (gi - c.edge[j0 / 8]));
+                            const float row = tc::exp2_approx(gs - sign * c.edge[j0 / 8]);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                d[e] = pair_mul(*reinterpret_cast<const float2*>(&c.near_end[j0 + 2 * e]), make_float2(row, row));
+                            for (int e = 0; e < 4; e += 2) {
+                                const float4 near = *reinterpret_cast<const float4*>(&c.near_end[j0 + 2 * e]);
+                                d[e] = pair_mul(make_float2(near.x, near.y), make_float2(row, row));
+                                d[e + 1] = pair_mul(make_float2(near.z, near.w), make_float2(row, row));
+                            }
                         }
                         tc::wait_ld();
                         tc::loaded(r);
