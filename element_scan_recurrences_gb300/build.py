@@ -5,7 +5,9 @@ object file, then linked into ``_build/libes.so`` with the static CUDA runtime
 (the driver's ``cuTensorMapEncodeTiled`` and module API are fetched at run
 time, so the library loads on machines without a GPU driver as well) and
 NVRTC, which compiles body programs at run time.  The headers NVRTC needs are
-embedded into the library as text (``write_jit_headers``).
+embedded into the library as text (``write_jit_headers``).  Beside it
+``_build/es_torch.so``, a Python module that marshals the sequence operators'
+tensors, is compiled against the installed PyTorch.
 """
 from __future__ import annotations
 
@@ -22,6 +24,9 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libes.so")
+# the tensor marshalling of the sequence operators (a Python module over libes.so and PyTorch)
+TORCH_SRC = os.path.join(CSRC, "torch", "es_torch.cpp")
+TORCH_LIB = os.path.join(BUILD, "es_torch.so")
 
 GEN = os.path.join(BUILD, "gen")
 
@@ -81,14 +86,39 @@ def write_jit_headers() -> str:
 
 def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
-        [os.path.join(INCLUDE, "es.h"), os.path.abspath(__file__)]
+        [os.path.join(INCLUDE, "es.h"), os.path.abspath(__file__), TORCH_SRC]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(TORCH_LIB)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(TORCH_LIB))
     return all(os.path.getmtime(p) <= t for p in _deps())
+
+
+def _compile_torch(obj: str):
+    """g++ on es_torch.cpp against the installed PyTorch's headers."""
+    import sysconfig
+
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cmd = ["g++", "-O1", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+           "-I", INCLUDE, "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda_home(), "include"),
+           "-c", TORCH_SRC, "-o", obj]
+    return TORCH_SRC, subprocess.run(cmd, capture_output=True, text=True)
+
+
+def _link_torch(obj: str):
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = TORCH_LIB + ".%d.tmp" % os.getpid()
+    r = subprocess.run(["g++", "-shared", "-o", tmp, obj, "-L", BUILD, "-les", "-L", lib, "-ltorch_python", "-ltorch", "-ltorch_cpu",
+                        "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib], capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("linking es_torch.so failed")
+    os.replace(tmp, TORCH_LIB)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -106,14 +136,18 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         return src, r
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
-        results = list(ex.map(compile_one, zip(srcs, objs)))
+    torch_obj = os.path.join(BUILD, "es_torch.torch.o")
+    # the longest compilations first, so that none of them is left alone at the end
+    order = sorted(zip(srcs, objs), key=lambda p: -os.path.getsize(p[0]))
+    with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
+        bound = ex.submit(_compile_torch, torch_obj)
+        results = list(ex.map(compile_one, order)) + [bound.result()]
     failed = [(s, r) for s, r in results if r.returncode != 0]
     for s, r in results:
         if verbose or r.returncode != 0:
             sys.stderr.write(r.stdout + r.stderr)
     if failed:
-        raise RuntimeError("nvcc failed for: " + ", ".join(os.path.basename(s) for s, _ in failed))
+        raise RuntimeError("compilation failed for: " + ", ".join(os.path.basename(s) for s, _ in failed))
     tmp = LIB + ".%d.tmp" % os.getpid()
     lib64 = os.path.join(cuda_home(), "lib64")
     link = ["-L", lib64, "-lnvrtc", "-Xlinker", "-rpath," + lib64]
@@ -122,6 +156,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("linking libes.so failed")
     os.replace(tmp, LIB)
+    _link_torch(torch_obj)
     return LIB
 
 

@@ -5,10 +5,10 @@
 //
 //     warp 2       TMA loads of the operands' tiles (X, Y, Z, and W for the
 //                  decays' gradient), 128-byte swizzled panels of 64 values
-//     warp 6       the chunk's decays (G, the coefficients of read and update);
+//     warp 7       the chunk's decays (G, the coefficients of read and update);
 //                  hands a loaded stage on, after clearing the rows of Y and Z
 //                  past the length in a row's last, ragged chunk
-//     warps 3, 7   issue the products (tcgen05.mma, one thread each): the
+//     warps 3, 6   issue the products (tcgen05.mma, one thread each): the
 //                  scores' and the state's
 //     warps 0,1,4,5  scores -> P: mask and decay, split into bf16 terms, to
 //                  shared memory
@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             }
         }
         __syncwarp();
-    } else if (warp == 6) {
+    } else if (warp == 7) {
         // ---- the chunks' decays, tokens 2 lane and 2 lane + 1; then the stage is handed on
         const float* G = A.g != nullptr ? A.g + b * A.gb + h * A.gh : nullptr;
         auto load = [&](int k) {
@@ -407,8 +407,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         if constexpr (kStateOnly) {
             if (lane == 0 && blockIdx.y == 0) A.seg_decays[bh * A.n_segs + seg] = all;
         }
-    } else if (warp == 3 || warp == 7) {
-        // ---- products: warp 7 those of the state, warp 3 those of the scores, so that neither waits for the other's turn
+    } else if (warp == 3 || warp == 6) {
+        // ---- products: warp 6 those of the state, warp 3 those of the scores, so that neither waits for the other's turn
         const uint32_t i_64 = tc::instr_bf16(C, false, false), i_o1 = tc::instr_bf16(C, true, false);
         const uint32_t i_kv = tc::instr_bf16(static_cast<uint32_t>(dxp), false, true);
         const uint32_t i_kv3 = tc::instr_bf16(static_cast<uint32_t>(dxp), true, true);
@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         const uint32_t lead = tc::elect();
         constexpr uint32_t kPanelStep = kPanel >> 4, kRows16 = 2048 >> 4;      // in descriptors' units
         Ring ring;
-        if (warp == 7) {
+        if (warp == 6) {
 #pragma unroll 1
             for (int k = 0; k < n; ++k, ring.next(A.stages)) {
                 const uint32_t sx = base + ring.s * A.stage_bytes;
@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             }
         }
         // nothing of this CTA's may still run when its tensor memory goes
-        uint64_t* drained = &sh.drained[warp == 7];
+        uint64_t* drained = &sh.drained[warp == 6];
         tc::commit(lead, drained);
         if (!__all_sync(0xffffffffu, wait_bounded(drained, 0, A.wait_ns, nullptr)) && lane == 0)
             atomicOr(A.status, ES_DEVICE_TIMEOUT);
