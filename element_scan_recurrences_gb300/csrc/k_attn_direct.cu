@@ -45,7 +45,11 @@ struct DirectArgs {
 // chunk and slice, dx = 128, 426 K FMAs (the 32 x 32 products of x and y are
 // formed again in every slice).  It serves the calls the tensor-core kernel
 // cannot take.
-template <typename T>
+//
+// The next chunk's operands are on their way in registers (XR values a thread
+// of x and of y) while this one's are worked on; widths above 128 would take too
+// many (XR = 0) and wait for theirs.
+template <typename T, int XR>
 __global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_constant__ DirectArgs A) {
     extern __shared__ __align__(16) float sm[];
     const AttnRun& R = A.run[blockIdx.z];
@@ -102,6 +106,49 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_consta
     const int64_t n_chunks = (len + C - 1) / C;
     const int ty = tid / 16, tx = tid % 16;
 
+    // Thread (t8, a) of 8 rows holds rows t8, t8 + 8, .. of columns a, a + 32, .. of x and y
+    constexpr int XC = XR > 0 ? XR / 4 : 1;
+    T px[XC][4], py[XC][4], pz[4];
+    float pg = 0.0f, cur_g = 0.0f;
+    const int t8 = tid / 32, al = tid % 32;
+    auto fetch = [&](int64_t k) {
+        const int64_t t0 = (R.reverse ? n_chunks - 1 - k : k) * C;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int64_t t = t0 + t8 + 8 * r;
+            const bool live = t < len;
+            const T* xr = X + t * R.x.st;
+            const T* yr = Y + t * R.y.st;
+#pragma unroll
+            for (int c = 0; c < XC; ++c) {
+                const int a = al + 32 * c;
+                px[c][r] = live && a < dx ? xr[a] : static_cast<T>(0.0f);
+                py[c][r] = live && a < dx ? yr[a] : static_cast<T>(0.0f);
+            }
+            pz[r] = live && al < nz ? Z[t * R.z.st + al] : static_cast<T>(0.0f);
+        }
+        if (tid < 32) pg = G != nullptr && t0 + tid < len ? G[(t0 + tid) * A.gt] : 0.0f;
+    };
+    auto put = [&]() {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int t = t8 + 8 * r;
+#pragma unroll
+            for (int c = 0; c < XC; ++c) {
+                const int a = al + 32 * c;
+                if (a < dxp) {
+                    sX[t * ld + a] = to_f32(px[c][r]);
+                    sY[t * ld + a] = to_f32(py[c][r]);
+                }
+            }
+            sZ[t * ZS + al] = to_f32(pz[r]);
+        }
+        cur_g = pg;
+    };
+    if constexpr (XR > 0) {
+        if (n_chunks > 0) fetch(0);
+    }
+
     for (int64_t k = 0; k < n_chunks; ++k) {
         const int64_t ci = R.reverse ? n_chunks - 1 - k : k;
         const int64_t t0 = ci * C;
@@ -117,20 +164,25 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_consta
             }
         };
         if (at_anchor && R.reverse) keep();
-        for (int e = tid; e < C * dxp; e += kThreads) {
-            const int t = e / dxp, a = e % dxp;
-            const bool in = t < n && a < dx;
-            sX[t * ld + a] = in ? to_f32(X[(t0 + t) * R.x.st + a]) : 0.0f;
-            sY[t * ld + a] = in ? to_f32(Y[(t0 + t) * R.y.st + a]) : 0.0f;
-        }
-        for (int e = tid; e < C * ZS; e += kThreads) {
-            const int t = e / ZS, c = e % ZS;
-            sZ[e] = (t < n && c < nz) ? to_f32(Z[(t0 + t) * R.z.st + c]) : 0.0f;
+        if constexpr (XR > 0) {
+            put();
+            if (k + 1 < n_chunks) fetch(k + 1);
+        } else {
+            for (int e = tid; e < C * dxp; e += kThreads) {
+                const int t = e / dxp, a = e % dxp;
+                const bool in = t < n && a < dx;
+                sX[t * ld + a] = in ? to_f32(X[(t0 + t) * R.x.st + a]) : 0.0f;
+                sY[t * ld + a] = in ? to_f32(Y[(t0 + t) * R.y.st + a]) : 0.0f;
+            }
+            for (int e = tid; e < C * ZS; e += kThreads) {
+                const int t = e / ZS, c = e % ZS;
+                sZ[e] = (t < n && c < nz) ? to_f32(Z[(t0 + t) * R.z.st + c]) : 0.0f;
+            }
         }
         if (tid < 32) {
             // one token a lane: G, the sum after it, and its group
-            float g = 0.0f;
-            if (G != nullptr && tid < n) g = G[(t0 + tid) * A.gt];
+            float g = cur_g;
+            if constexpr (XR == 0) g = G != nullptr && tid < n ? G[(t0 + tid) * A.gt] : 0.0f;
             const bool cut = g < -104.0f;
             if (cut) g = 0.0f;
             float pre = g, nxt = __shfl_down_sync(0xffffffffu, g, 1);
@@ -400,7 +452,9 @@ cudaError_t launch_attn_direct(const AttnLaunch& L) {
     A.lengths = L.lengths;
     A.n_anchors = L.n_anchors;
     A.BH = L.B * L.H;
-    const auto kernel = L.bf16 ? k_attn_direct<__nv_bfloat16> : k_attn_direct<float>;
+    const auto kernel = dx <= 64    ? (L.bf16 ? k_attn_direct<__nv_bfloat16, 8> : k_attn_direct<float, 8>)
+                        : dx <= 128 ? (L.bf16 ? k_attn_direct<__nv_bfloat16, 16> : k_attn_direct<float, 16>)
+                                    : (L.bf16 ? k_attn_direct<__nv_bfloat16, 0> : k_attn_direct<float, 0>);
     const size_t smem = direct_smem(dx);
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;

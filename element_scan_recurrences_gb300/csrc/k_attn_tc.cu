@@ -279,6 +279,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
     if (warp == 2) {
         // ---- loads
         if (lane == 0) {
+            if constexpr (!kStateOnly) tma_prefetch_desc(&R.x);
+            tma_prefetch_desc(&R.y);
+            tma_prefetch_desc(&R.z);
             const uint64_t pol = l2_policy_stream();
             const int hx = h / R.xdiv, hy = h / R.ydiv, hz = h / R.zdiv, hw = h / R.wdiv;
             const int bx = b * R.xb, by = b * R.yb, bz = b * R.zb, bw = b * R.wb;
@@ -673,12 +676,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                           R.dz, 1.0f);
         };
         if (on) {
+            // 32 loads in flight: a short sequence is mostly this and the way in and out
 #pragma unroll 1
-            for (int a0 = a_lo; a0 < a_hi; a0 += 8) {
-                uint32_t r[8];
+            for (int a0 = a_lo; a0 < a_hi; a0 += 32) {
+                uint32_t r[32];
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    r[e] = __float_as_uint(from != nullptr && a0 + e < R.dx ? from[(a0 + e) * fa] * fs : 0.0f);
+                for (int e = 0; e < 32; ++e) r[e] = 0u;
+                if (from != nullptr) {
+                    const float* p = from + a0 * fa;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (a0 + e < R.dx) r[e] = __float_as_uint(p[e * fa] * fs);
+                }
                 tc::st(t_h + lanes + a0, r);
             }
             tc::wait_st();
