@@ -93,12 +93,16 @@ cudaError_t launch_attn_tc(const AttnLaunch& L, int* kernels, const char** err);
 
 // The decays' gradient from the two runs' dots and states: for each token t of
 // anchor block m, sum over s >= t of the block of (dq[s] - dk[s]) + e[m], with
-// e[m] = scale <state_q, state_k> at the block's end.
+// e[m] = scale <state_q, state_k> at the block's end, corrected in proportion
+// so that it meets e[m - 1] at the block's start.
 struct AttnDecayGrad {
     const float* dots_q;         // [slices, B*H, T]
     const float* dots_k;
     const float* states_q;       // [B*H, n, size]
     const float* states_k;
+    const float* initial;        // [B*H, size]: the first state and its gradient, or null
+    const float* grad_initial;
+    float* ends;                 // [B*H, n + 1]: e[-1], e[0], ..
     float scale;
     int slices;
     int64_t size;

@@ -91,7 +91,7 @@ struct AttnPlan {
     int path;
     bool empty;
     // backward: byte offsets into the workspace
-    size_t seg_states, seg_decays, dots_q, dots_k, states_q, states_k, partial, fold_q, fold_k, fold_v, bytes;
+    size_t seg_states, seg_decays, dots_q, dots_k, states_q, states_k, ends, partial, fold_q, fold_k, fold_v, bytes;
     int slices_k;                // slices of the runs that give the dots (key-wide outputs)
 };
 
@@ -293,6 +293,7 @@ es_status plan_attn(const char* fn, const es_linear_attention_args* a, const es_
             P->dots_k = take(&at, 4 * P->slices_k * bh * T);
             P->states_q = take(&at, 4 * bh * L.n_anchors * dk * dv);
             P->states_k = take(&at, 4 * bh * L.n_anchors * dk * dv);
+            P->ends = take(&at, 4 * bh * (L.n_anchors + 1));
             P->partial = take(&at, 4 * bh * L.n_anchors);
         }
         if (a->q.heads < H) P->fold_q = take(&at, 4 * bh * T * dk);
@@ -401,6 +402,9 @@ es_status run_backward(const char* fn, const es_linear_attention_args* a, const 
         D.dots_k = rk.dots;
         D.states_q = rq.anchors;
         D.states_k = rk.anchors;
+        D.initial = a->initial_state;
+        D.grad_initial = g->grad_initial_state;
+        D.ends = reinterpret_cast<float*>(ws + P.ends);
         D.scale = rk.out_scale;
         D.slices = P.slices_k;
         D.size = static_cast<int64_t>(dk) * dv;

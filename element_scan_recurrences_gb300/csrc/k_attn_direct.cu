@@ -326,10 +326,60 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_consta
         }
 }
 
-// One CTA an anchor block.  The product of the two states at its end (all 256
-// threads: 8 bytes a value read once, the bulk of this kernel's traffic), then
-// the block's tokens from its end, thread t the t-th from the end: summed by
-// shuffles within a warp and across the warps through shared memory.
+// The decays' gradient meets, between the anchor blocks, the product of the
+// state and its gradient.  One CTA a product: 8 bytes a value read once, all of
+// this kernel's time.  Place 0 is the first state's (zero without one).
+__global__ void __launch_bounds__(256) k_attn_state_products(const __grid_constant__ AttnDecayGrad G) {
+    __shared__ float part[8];
+    const int64_t bh = blockIdx.x / (G.n + 1), m = blockIdx.x % (G.n + 1) - 1;
+    const int tid = threadIdx.x;
+    int64_t len = G.T;
+    if (G.lengths != nullptr) {
+        const int64_t l = G.lengths[bh / G.H];
+        len = l < 0 ? 0 : l < G.T ? l : G.T;
+    }
+    const float *a = nullptr, *c = nullptr;
+    if (m >= 0) {
+        if (m * kAttnAnchorTokens < len) {
+            a = G.states_q + (bh * G.n + m) * G.size;
+            c = G.states_k + (bh * G.n + m) * G.size;
+        }
+    } else if (G.initial != nullptr && G.grad_initial != nullptr) {
+        a = G.initial + bh * G.size;
+        c = G.grad_initial + bh * G.size;
+    }
+    float s = 0.0f;
+    if (a != nullptr) {
+        if (G.size % 4 == 0 && reinterpret_cast<uintptr_t>(a) % 16 == 0 && reinterpret_cast<uintptr_t>(c) % 16 == 0) {
+            const float4* a4 = reinterpret_cast<const float4*>(a);
+            const float4* c4 = reinterpret_cast<const float4*>(c);
+#pragma unroll 8
+            for (int64_t e = tid; e < G.size / 4; e += 256) {
+                const float4 x = a4[e], y = c4[e];
+                s += x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
+            }
+        } else {
+            for (int64_t e = tid; e < G.size; e += 256) s += a[e] * c[e];
+        }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (tid % 32 == 0) part[tid / 32] = s;
+    __syncthreads();
+    if (tid == 0) {
+        float all = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) all += part[w];
+        G.ends[blockIdx.x] = m >= 0 ? all * G.scale : all;
+    }
+}
+
+// One CTA an anchor block: its tokens from its end, thread t the t-th from the
+// end, summed by shuffles within a warp and across the warps through shared
+// memory.  The sums are of differences whose terms cancel, so the terms'
+// rounding drifts along the block; both of its ends are known, and what is
+// missing at the start is spread over the block in proportion (a third of the
+// drift's variance is left).
 __global__ void __launch_bounds__(kAttnAnchorTokens) k_attn_decay_grad(const __grid_constant__ AttnDecayGrad G) {
     constexpr int kWarps = kAttnAnchorTokens / 32;
     __shared__ float part[kWarps], total[kWarps];
@@ -343,50 +393,40 @@ __global__ void __launch_bounds__(kAttnAnchorTokens) k_attn_decay_grad(const __g
     }
     const int64_t lo = m * kAttnAnchorTokens, full = lo + kAttnAnchorTokens < G.T ? lo + kAttnAnchorTokens : G.T;
     const int64_t hi = full < len ? full : len;
-    float v = 0.0f, end = 0.0f;
-    if (lo < hi) {
-        const int64_t at = (bh * G.n + m) * G.size;
-        if (G.size % 4 == 0) {
-            const float4* a = reinterpret_cast<const float4*>(G.states_q + at);
-            const float4* c = reinterpret_cast<const float4*>(G.states_k + at);
-#pragma unroll 8
-            for (int64_t e = tid; e < G.size / 4; e += kAttnAnchorTokens) {
-                const float4 x = a[e], y = c[e];
-                end += x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
-            }
-        } else {
-            for (int64_t e = tid; e < G.size; e += kAttnAnchorTokens) end += G.states_q[at + e] * G.states_k[at + e];
-        }
-    }
     const int64_t t = hi - 1 - tid;
-    if (t >= lo) {
+    const bool in = t >= lo;
+    float v = 0.0f;
+    if (in) {
         for (int s = 0; s < G.slices; ++s) v += G.dots_q[(s * BH + bh) * G.T + t];
         for (int s = 0; s < G.slices; ++s) v -= G.dots_k[(s * BH + bh) * G.T + t];
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) end += __shfl_xor_sync(0xffffffffu, end, o);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const float q = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += q;
     }
     if (lane == 31) total[warp] = v;
-    if (lane == 0) part[warp] = end;
     __syncthreads();
-    float carry = 0.0f;
+    float whole = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) carry += part[w];
-    carry *= G.scale;
-    for (int w = 0; w < warp; ++w) carry += total[w];
-    v += carry;
-    if (t >= lo && G.grad != nullptr) G.grad[(b * G.T + t) * G.H + h] = v;
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) v += total[w];
+        whole += total[w];
+    }
+    if (lo < hi) {
+        const float end = G.ends[bh * (G.n + 1) + m + 1], start = G.ends[bh * (G.n + 1) + m];
+        // the first block's start is known unless a first state's gradient is not asked for
+        const bool known = m > 0 || G.initial == nullptr || G.grad_initial != nullptr;
+        const float missing = known ? start - (end + whole) : 0.0f;
+        v += end + missing * (static_cast<float>(tid + 1) / static_cast<float>(hi - lo));
+    }
+    if (in && G.grad != nullptr) G.grad[(b * G.T + t) * G.H + h] = v;
     if (G.grad != nullptr)
         for (int64_t p = (hi > lo ? hi : lo) + tid; p < full; p += kAttnAnchorTokens) G.grad[(b * G.T + p) * G.H + h] = 0.0f;
     if (G.partial != nullptr) {
-        float sum = t >= lo ? v : 0.0f;
+        float sum = in ? v : 0.0f;
 #pragma unroll
         for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        __syncthreads();
         if (lane == 0) part[warp] = sum;
         __syncthreads();
         if (tid == 0) {
@@ -464,7 +504,8 @@ cudaError_t launch_attn_direct(const AttnLaunch& L) {
 }
 
 cudaError_t launch_attn_decay_grad(const AttnDecayGrad& G, int* kernels) {
-    *kernels = 1;
+    *kernels = 2;
+    k_attn_state_products<<<static_cast<unsigned>(G.B * G.H * (G.n + 1)), 256, 0, G.stream>>>(G);
     k_attn_decay_grad<<<static_cast<unsigned>(G.B * G.H * G.n), kAttnAnchorTokens, 0, G.stream>>>(G);
     if (G.grad_h != nullptr) {
         k_attn_sum_rows<<<G.H, 256, 0, G.stream>>>(G.partial, G.B * G.n, G.grad_h);
