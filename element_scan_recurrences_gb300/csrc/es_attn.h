@@ -127,7 +127,7 @@ struct AttnFold {
     int heads, div, d;
     cudaStream_t stream;
 };
-cudaError_t launch_attn_fold(const AttnFold& F);
+cudaError_t launch_attn_folds(const AttnFold* folds, int n);      // one launch for all
 
 struct AttnStep {
     AttnOperand q, k, v;         // st unused

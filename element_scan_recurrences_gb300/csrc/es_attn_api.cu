@@ -427,8 +427,8 @@ es_status run_backward(const char* fn, const es_linear_attention_args* a, const 
         // no tokens: a sum of nothing
         if ((e = cudaMemsetAsync(g->grad_log_decay, 0, H * 4, L.stream)) != cudaSuccess) return cuda_fail(fn, e);
     }
-    for (int i = 0; i < folds; ++i) {
-        if ((e = launch_attn_fold(fold[i])) != cudaSuccess) return cuda_fail(fn, e);
+    if (folds > 0) {
+        if ((e = launch_attn_folds(fold, folds)) != cudaSuccess) return cuda_fail(fn, e);
         count_launch();
     }
     return ES_OK;

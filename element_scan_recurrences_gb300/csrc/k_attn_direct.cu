@@ -454,17 +454,39 @@ __global__ void __launch_bounds__(256) k_attn_sum_rows(const float* __restrict__
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) k_attn_fold(const AttnFold F) {
-    const int64_t n = F.B * F.T * F.heads * static_cast<int64_t>(F.d);
+// One thread four values (VEC) of an operand head: the f32 rows of the heads
+// that read it, 16 bytes each, summed in order.  Bounded by their bytes.  grid y:
+// which of the call's folds.
+struct AttnFolds {
+    AttnFold fold[3];
+};
+template <typename T, int VEC>
+__global__ void __launch_bounds__(256) k_attn_fold(const __grid_constant__ AttnFolds A) {
+    const AttnFold& F = A.fold[blockIdx.y];
+    const uint32_t per = F.d / VEC, heads = F.heads;
+    const int64_t n = F.B * F.T * heads * static_cast<int64_t>(per);
     for (int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; e < n; e += static_cast<int64_t>(gridDim.x) * 256) {
-        const int c = static_cast<int>(e % F.d);
-        const int j = static_cast<int>(e / F.d % F.heads);
-        const int64_t bt = e / F.d / F.heads;
-        const float* p = F.part + (bt * F.heads + j) * F.div * static_cast<int64_t>(F.d) + c;
-        float s = 0.0f;
-        for (int r = 0; r < F.div; ++r) s += p[static_cast<int64_t>(r) * F.d];
-        static_cast<T*>(F.out)[bt / F.T * F.ob + bt % F.T * F.ot + j * F.oh + c] = static_cast<T>(s);
+        const int64_t row = e / per, bt = row / heads, b = bt / F.T;
+        const int c = static_cast<int>(e - row * per) * VEC, j = static_cast<int>(row - bt * heads);
+        const float* p = F.part + row * F.div * F.d + c;
+        float s[VEC];
+#pragma unroll
+        for (int u = 0; u < VEC; ++u) s[u] = 0.0f;
+#pragma unroll 4
+        for (int r = 0; r < F.div; ++r) {
+            if constexpr (VEC == 4) {
+                const float4 v = *reinterpret_cast<const float4*>(p + static_cast<int64_t>(r) * F.d);
+                s[0] += v.x;
+                s[1] += v.y;
+                s[2] += v.z;
+                s[3] += v.w;
+            } else {
+                s[0] += p[static_cast<int64_t>(r) * F.d];
+            }
+        }
+        T* to = static_cast<T*>(F.out) + b * F.ob + (bt - b * F.T) * F.ot + j * F.oh + c;
+#pragma unroll
+        for (int u = 0; u < VEC; ++u) to[u] = static_cast<T>(s[u]);
     }
 }
 
@@ -514,11 +536,21 @@ cudaError_t launch_attn_decay_grad(const AttnDecayGrad& G, int* kernels) {
     return cudaGetLastError();
 }
 
-cudaError_t launch_attn_fold(const AttnFold& F) {
-    const int64_t n = F.B * F.T * F.heads * static_cast<int64_t>(F.d);
-    const unsigned blocks = static_cast<unsigned>((n + 255) / 256 < 152 * 16 ? (n + 255) / 256 : 152 * 16);
-    if (F.bf16) k_attn_fold<__nv_bfloat16><<<blocks, 256, 0, F.stream>>>(F);
-    else k_attn_fold<float><<<blocks, 256, 0, F.stream>>>(F);
+cudaError_t launch_attn_folds(const AttnFold* folds, int n) {
+    AttnFolds A{};
+    int64_t most = 0;
+    bool vec = true;
+    for (int i = 0; i < n; ++i) {
+        A.fold[i] = folds[i];
+        const int64_t values = folds[i].B * folds[i].T * folds[i].heads * static_cast<int64_t>(folds[i].d);
+        most = values > most ? values : most;
+        vec = vec && folds[i].d % 4 == 0 && reinterpret_cast<uintptr_t>(folds[i].part) % 16 == 0;
+    }
+    const int64_t blocks = (most / (vec ? 4 : 1) + 255) / 256;
+    const dim3 grid(static_cast<unsigned>(blocks < 152 * 8 ? blocks : 152 * 8), n);
+    const auto kernel = folds[0].bf16 ? (vec ? k_attn_fold<__nv_bfloat16, 4> : k_attn_fold<__nv_bfloat16, 1>)
+                                      : (vec ? k_attn_fold<float, 4> : k_attn_fold<float, 1>);
+    kernel<<<grid, 256, 0, folds[0].stream>>>(A);
     return cudaGetLastError();
 }
 

@@ -56,8 +56,6 @@ constexpr uint32_t kTmemCols = 512;
 struct alignas(16) Coef {
     float g2[C];                              // inclusive sums of the log decays, base 2
     float read[C], upd[C];
-    float near_end[C];                        // decay between token j and the edge of its block of 8 that later (reversed: earlier) rows see
-    float edge[8];                            // g2 at that edge
     int bound[C];                             // forward: the first token row i sees; reversed: the last
     float decay;
     float pad[3];
@@ -379,12 +377,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             all *= decay;
             if (k >= A.stages && !wait(&sh.empty[ring.s], ring.parity ^ 1)) break;
             Coef& c = sh.coef[ring.s];
-            // the edge of the block of 8 tokens (4 lanes): after its last token, or (reversed) before its first
-            const float edge = R.reverse ? __shfl_sync(0xffffffffu, before, lane & ~3) : __shfl_sync(0xffffffffu, pre, lane | 3);
-            const float es = R.reverse ? -1.0f : 1.0f;
-            *reinterpret_cast<float2*>(&c.near_end[2 * lane]) =
-                make_float2(tc::exp2_approx(es * (edge - g2.x)), tc::exp2_approx(es * (edge - g2.y)));
-            if (lane % 4 == 0) c.edge[lane / 4] = edge;
             *reinterpret_cast<float2*>(&c.g2[2 * lane]) = g2;
             *reinterpret_cast<float2*>(&c.read[2 * lane]) = R.reverse ? to_end : from_start;
             *reinterpret_cast<float2*>(&c.upd[2 * lane]) = R.reverse ? from_start : to_end;
@@ -506,7 +498,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             const uint32_t from = t_s + (static_cast<uint32_t>(32 * (warp & 1)) << 16) + 32 * half;
             // rows of one half never see the columns of the other: forward rows 0-31 the late columns
             const float sign = R.reverse ? -1.0f : 1.0f;
-            const bool diagonal = (warp & 1) == half;
             const bool none = R.reverse ? (warp & 1) > half : (warp & 1) < half;
             Ring ring;
 #pragma unroll 1
@@ -536,24 +527,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                         const uint32_t mask = seen >> (8 * q);
                         const int j0 = 32 * half + 8 * q;
                         float2 d[4];
-                        if (diagonal) {
 #pragma unroll
-                            for (int e = 0; e < 4; e += 2) {
-                                const float4 gj = *reinterpret_cast<const float4*>(&c.g2[j0 + 2 * e]);
-                                const float2 x = pair_fma(make_float2(gj.x, gj.y), make_float2(-sign, -sign), make_float2(gs, gs));
-                                const float2 y = pair_fma(make_float2(gj.z, gj.w), make_float2(-sign, -sign), make_float2(gs, gs));
-                                d[e] = make_float2(tc::exp2_approx(x.x), tc::exp2_approx(x.y));
-                                d[e + 1] = make_float2(tc::exp2_approx(y.x), tc::exp2_approx(y.y));
-                            }
-                        } else {
-                            // row to block edge, and block edge to column: neither grows
-                            const float row = tc::exp2_approx(gs - sign * c.edge[j0 / 8]);
-#pragma unroll
-                            for (int e = 0; e < 4; e += 2) {
-                                const float4 near = *reinterpret_cast<const float4*>(&c.near_end[j0 + 2 * e]);
-                                d[e] = pair_mul(make_float2(near.x, near.y), make_float2(row, row));
-                                d[e + 1] = pair_mul(make_float2(near.z, near.w), make_float2(row, row));
-                            }
+                        for (int e = 0; e < 4; e += 2) {
+                            const float4 gj = *reinterpret_cast<const float4*>(&c.g2[j0 + 2 * e]);
+                            const float2 x = pair_fma(make_float2(gj.x, gj.y), make_float2(-sign, -sign), make_float2(gs, gs));
+                            const float2 y = pair_fma(make_float2(gj.z, gj.w), make_float2(-sign, -sign), make_float2(gs, gs));
+                            d[e] = make_float2(tc::exp2_approx(x.x), tc::exp2_approx(x.y));
+                            d[e + 1] = make_float2(tc::exp2_approx(y.x), tc::exp2_approx(y.y));
                         }
                         tc::wait_ld();
                         tc::loaded(r);
