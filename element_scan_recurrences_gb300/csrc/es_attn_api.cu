@@ -285,7 +285,7 @@ es_status plan_attn(const char* fn, const es_linear_attention_args* a, const es_
     size_t at = 0;
     if (L.n_segs > 1) {
         P->seg_states = take(&at, 4 * L.runs * bh * L.n_segs * dk * dv);
-        P->seg_decays = take(&at, 4 * bh * L.n_segs);
+        P->seg_decays = take(&at, 4 * L.runs * bh * L.n_segs);
     }
     if (backward && T > 0) {
         if (g->grad_log_decay != nullptr) {
