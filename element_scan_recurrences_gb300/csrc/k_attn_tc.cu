@@ -200,7 +200,7 @@ __device__ __noinline__ void state_out(uint32_t state, int lo, int hi, float* to
 // kStateOnly: a segment's own state and decay, from zero: only Y and Z are read.
 // It goes through the segment backwards, with the decays from each chunk to the
 // segment's end in Z's coefficients, so the state is a plain sum and no role has
-// to look at it on the way (65536 tokens x 16 heads of 128: 153 -> 95 us).
+// to look at it on the way (65536 tokens x 16 heads of 128: 153 -> 113 us).
 template <bool kStateOnly, bool kDots>
 __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__ TcArgs A) {
     extern __shared__ __align__(1024) unsigned char raw[];
@@ -275,6 +275,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
     constexpr uint32_t tmem = 0;
     const uint32_t t_h = tmem, t_hb = t_h + dxp, t_zt = t_hb + dxp, t_s = t_zt + C, t_o1 = t_s + C, t_o2 = t_o1 + C;
     const Wait wait{A.wait_ns, &sh.abort_flag, A.status};
+    // Z's terms and the barrier of the state's products: a segment's own state has room for two chunks' terms (in the
+    // place of the state's), which take turns
+    auto zt_of = [&](int k) { return kStateOnly ? t_hb + (k & 1) * C : t_zt; };
+    auto kv_of = [&](int k) { return kStateOnly && (k & 1) ? &sh.s_done : &sh.kv_done; };
     auto chunk_of = [&](int k) { return (R.reverse != 0) != kStateOnly ? c1 - 1 - k : c0 + k; };
 
     if (warp == 2) {
@@ -445,16 +449,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 } else {
                     tc::fence_after();
                 }
-                if (kStateOnly && k == 0) tc::mma_ts<true>(lead, t_h, t_zt, y, i_kv);
-                else tc::mma_ts(lead, t_h, t_zt, y, i_kv);
+                const uint32_t zt = zt_of(k);
+                if (kStateOnly && k == 0) tc::mma_ts<true>(lead, t_h, zt, y, i_kv);
+                else tc::mma_ts(lead, t_h, zt, y, i_kv);
 #pragma unroll
-                for (int q = 1; q < 2 * C / 16; ++q) tc::mma_ts(lead, t_h, t_zt + q * 8, y + q % (C / 16) * kRows16, i_kv);
+                for (int q = 1; q < 2 * C / 16; ++q) tc::mma_ts(lead, t_h, zt + q * 8, y + q % (C / 16) * kRows16, i_kv);
                 if (R.terms == 3) {
                     const uint32_t w = tc::desc_low(sx + off_w, kPanel);
 #pragma unroll
                     for (int q = 0; q < C / 16; ++q) tc::mma_ss(lead, t_h, w + q * kRows16, y + q * kRows16, i_kv3);
                 }
-                tc::commit(lead, &sh.kv_done);
+                tc::commit(lead, kv_of(k));
                 if constexpr (kStateOnly) {
                     if (k == n - 1) tc::commit(lead, &sh.state_done);
                 } else {
@@ -581,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
     } else if (warp < 16) {
         // ---- Z scaled and transposed: 32 value columns (lanes) and 32 of the tokens (pairs along the columns)
         const int slice = warp & 3, side = (warp - 8) / 4;
-        const uint32_t to = t_zt + 16 * side + (static_cast<uint32_t>(slice * 32) << 16);
+        const uint32_t to = 16 * side + (static_cast<uint32_t>(slice * 32) << 16);
         const bool on = slice * 32 < R.dz;
         // lane l names row l % 8 of block l / 8: two blocks of columns, two of tokens
         const uint32_t row = 32 * side + 8 * (lane / 16) + lane % 8, piece = 4 * (slice & 1) + (lane / 8) % 2;
@@ -590,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
 #pragma unroll 1
         for (int k = 0; k < n; ++k, ring.next(A.stages)) {
             if (!wait(&sh.ready[ring.s], ring.parity)) break;
-            if (k > 0 && !wait(&sh.kv_done, k - 1)) break;
+            if (kStateOnly ? k > 1 && !wait(kv_of(k), k / 2 - 1) : k > 0 && !wait(&sh.kv_done, k - 1)) break;
             tc::fence_after();
             if (on) {
                 const float* upd = sh.coef[ring.s].upd + 32 * side + 2 * (lane % 4);
@@ -602,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                     // pieces 2 half and 2 half + 1 (the swizzle only flips that bit of the address)
                     tc::ld_blocks(at ^ (half << 5), z[0]);
                     tc::ld_blocks((at ^ (half << 5)) + 16 * 128, z[1]);
-                    const uint32_t lanes = to + (static_cast<uint32_t>(16 * half) << 16);
+                    const uint32_t lanes = zt_of(k) + to + (static_cast<uint32_t>(16 * half) << 16);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const float2 w = *reinterpret_cast<const float2*>(upd + 8 * (e / 2));
