@@ -71,8 +71,16 @@ es_status check_dense(const char* fn, const char* name, const void* p, int64_t e
     return ES_OK;
 }
 
-// No output may touch another span; `same[i] >= 0` lets output i be exactly that input.
-es_status check_outputs(const char* fn, const Span* in, int n_in, const Span* out, int n_out) {
+// No output may touch another span, nor the workspace any of them.
+es_status check_outputs(const char* fn, const Span* in, int n_in, const Span* out, int n_out, const void* ws = nullptr,
+                        size_t ws_bytes = 0) {
+    if (ws != nullptr && ws_bytes > 0) {
+        const Span w{"workspace", ws, static_cast<int64_t>(ws_bytes)};
+        for (int i = 0; i < n_in; ++i)
+            if (overlap(w, in[i])) return api_fail(ES_E_ARG, "%s: the workspace overlaps `%s`", fn, in[i].name);
+        for (int i = 0; i < n_out; ++i)
+            if (overlap(w, out[i])) return api_fail(ES_E_ARG, "%s: the workspace overlaps `%s`", fn, out[i].name);
+    }
     for (int i = 0; i < n_out; ++i) {
         for (int j = 0; j < n_in; ++j)
             if (overlap(out[i], in[j])) return api_fail(ES_E_ARG, "%s: `%s` overlaps `%s`", fn, out[i].name, in[j].name);
@@ -142,7 +150,7 @@ es_status plan_attn(const char* fn, const es_linear_attention_args* a, const es_
     if (!std::isfinite(a->scale) || static_cast<float>(a->scale) == 0.0f || !std::isfinite(static_cast<float>(a->scale)))
         return api_fail(ES_E_ARG, "%s: scale %g; it must be finite and not zero", fn, a->scale);
     const int64_t size = a->dtype == ES_BF16 ? 2 : 4;
-    Span in[10], out[8];
+    Span in[12], out[8];
     int n_in = 0, n_out = 0;
     es_status st;
     const int64_t dims[3] = {dk, dk, dv};
@@ -301,7 +309,7 @@ es_status plan_attn(const char* fn, const es_linear_attention_args* a, const es_
         if (a->v.heads < H) P->fold_v = take(&at, 4 * bh * T * dv);
     }
     P->bytes = at;
-    return ES_OK;
+    return check_outputs(fn, in, n_in, out, n_out, a->workspace, at);
 }
 
 es_status check_workspace(const char* fn, void* ws, int64_t bytes, size_t need) {
@@ -462,7 +470,7 @@ es_status plan_rotate(const char* fn, const es_qk_norm_rotate_args* a, const es_
         return api_fail(ES_E_UNSUPPORTED, "%s: too many tokens", fn);
     const int64_t size = a->dtype == ES_BF16 ? 2 : 4, wsize = a->weight_dtype == ES_BF16 ? 2 : 4;
     const bool backward = g != nullptr;
-    Span in[12], out[4];
+    Span in[18], out[4];
     int n_in = 0, n_out = 0;
     es_status st;
     const es_heads* xs[2] = {&a->q, &a->k};
@@ -573,7 +581,12 @@ es_status plan_rotate(const char* fn, const es_qk_norm_rotate_args* a, const es_
         return api_fail(ES_E_UNSUPPORTED, "%s: %lld tokens are too many", fn, static_cast<long long>(rows));
     if (!P->empty && (gw[0] != nullptr || gw[1] != nullptr))
         P->bytes = static_cast<size_t>(rotate_blocks(L, 0) + rotate_blocks(L, 1)) * d * 4;
-    return ES_OK;
+    for (int i = 0; i < 2; ++i) {
+        in[n_in++] = xsp[i];
+        in[n_in++] = osp[i];
+        if (backward) in[n_in++] = gsp[i];
+    }
+    return check_outputs(fn, in, n_in, out, n_out, a->workspace, P->bytes);
 }
 
 es_status run_rotate(const char* fn, const es_qk_norm_rotate_args* a, const es_qk_norm_rotate_grads* g, es_stream_t stream) {

@@ -23,12 +23,13 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-// CTAs an SM.  The forward's warps are many (6 CTAs) and wait for their own
-// loads; the backward's rows take twice the registers, so it has fewer warps (4
-// CTAs) that fetch the next unit's rows before they work on this one's.  Measured
-// the other way round: forward 61.5 -> 68.6 us for 16384 tokens x 40 heads of 128
-// bf16, backward 98 -> 132 us for 16384 x 32.
-constexpr int resident(bool bwd) { return bwd ? 4 : 6; }
+// CTAs an SM.  The forward's warps are many (6 CTAs, two rows a lane) and wait for
+// their own loads; the backward's rows take twice the registers, so it has fewer
+// warps (3 CTAs, two rows a lane) that fetch the next unit's rows before they work
+// on this one's.  Measured, 16384 tokens x 40 heads of 128 bf16: forward 66 us (8
+// CTAs 79, 5 CTAs 74, fetching ahead with 4 CTAs 69), backward 113 us (one row and
+// 4 CTAs 125, without fetching ahead 165, 2 CTAs 148).
+constexpr int resident(bool bwd) { return bwd ? 3 : 6; }
 
 template <typename T>
 __device__ __forceinline__ float to_f32(T v) {
@@ -477,8 +478,8 @@ __global__ void __launch_bounds__(kThreads, resident(BWD)) k_rotate(const __grid
 }
 
 // Both weights' gradients from the blocks' sums, in a fixed order: a CTA a
-// side and 8 columns, 128 threads a column, so that a column's 608 sums at most
-// are five loads a thread.
+// side and 8 columns, 128 threads a column, so that a column's 456 sums at most
+// are four loads a thread.
 constexpr int kSumParts = 128;
 __global__ void __launch_bounds__(8 * kSumParts) k_rotate_sum(const __grid_constant__ RotateArgs A, int total) {
     const RotateLaunch& L = A.L;
@@ -543,12 +544,12 @@ struct Grid {
     int per[2];
 };
 
-constexpr int unroll_of(bool bwd, bool vec) { return vec ? (bwd ? 1 : 2) : 1; }
+constexpr int unroll_of(bool vec) { return vec ? 2 : 1; }
 
 Grid grid_of(const RotateLaunch& L) {
     Grid g{};
     const bool vec = vectors(L);
-    const int hb = 32 / lanes(L, vec) * unroll_of(L.backward, vec);
+    const int hb = 32 / lanes(L, vec) * unroll_of(vec);
     int64_t heads = L.side[0].heads + L.side[1].heads;
     for (int s = 0; s < 2; ++s) {
         g.per[s] = (L.side[s].heads + hb - 1) / hb;
@@ -571,7 +572,7 @@ cudaError_t go(const RotateArgs& A, int total) {
 template <typename T, bool NEIGH, bool BWD>
 cudaError_t pick(const RotateArgs& A, int total, bool vec, int g) {
     constexpr int VEC = sizeof(T) == 2 ? 8 : 4;
-    constexpr int U = unroll_of(BWD, true);
+    constexpr int U = unroll_of(true);
     if (!vec) return go<T, 1, NEIGH, BWD, 32, 4, 1>(A, total);
     switch (g) {
         case 1: return go<T, VEC, NEIGH, BWD, 1, 1, U>(A, total);

@@ -661,7 +661,8 @@ typedef struct es_heads {
  *   log_decay         device f32 g: [B, T, H] by element strides, or [H] with
  *                     decay_per_head = 1 (decay_b and decay_t unused); null:
  *                     no decay.  Meant to be <= 0.  Below -104 (where e^g is
- *                     zero in f32; -inf included) the token starts afresh.
+ *                     zero in f32; -inf included) the token starts afresh from
+ *                     a state of finite values.
  *   lengths           device i32 [B], or null: tokens at and past a row's
  *                     length (clamped to 0..T) are not read, their `out` is 0.
  *   scale             finite, not zero.
@@ -670,8 +671,8 @@ typedef struct es_heads {
  *                     state after each row's last token.  It may be
  *                     initial_state itself.
  *   out               [B, T, H, value_dim]; may not overlap an input.
- *   workspace         es_linear_attention_workspace bytes, 16-byte aligned
- *                     (may be null where that is 0).
+ *   workspace         es_linear_attention_workspace bytes, 16-byte aligned, apart
+ *                     from every operand (may be null where that is 0).
  * bf16 with widths of at most 128 that are multiples of 8, 16-byte addresses
  * and strides: ES_PATH_TENSOR, chunks of tokens as products on the tensor
  * cores; anything else ES_PATH_GENERIC, the same chunk form on the FMA units.

@@ -121,3 +121,24 @@ def test_rotate_refusals(kw, code):
     with pytest.raises(es.EsError) as e:
         rotate(**kw)
     assert e.value.status == code, e.value
+
+
+def test_a_workspace_over_an_operand_is_refused():
+    """The backward's workspace begins in q, in a gradient; the rotation's in its gradient of q."""
+    es.set_path_override("generic")
+    B, T, H, D = Q
+    view = lambda i: ((i + 1) << 44, T * H * D, H * D, D, H)  # noqa: E731
+    for at in ((1 << 44) + 256, (11 << 44) + 4096):
+        args = sequence._ATTN.pack(1, B, T, H, D, D, 1.0, *view(0), *view(1), *view(2), *view(3), 5 << 44, T * H, H, 1, 0, 0, 0, 0,
+                                   at, 1 << 40)
+        grads = sequence._ATTN_GRADS.pack(*view(9), *view(10), *view(11), *view(12), 0, 15 << 44, 0)
+        with pytest.raises(es.EsError) as e:
+            binding._check(binding.lib().es_plan_linear_attention(args, grads, None))
+        assert e.value.status == 3 and "workspace" in e.value.message
+    args = sequence._ROTATE.pack(1, 1, 2, 5, 64, 64, 0, 1e-6, *((1 << 44, 1280, 256, 64, 4)), *((2 << 44, 640, 128, 64, 2)),
+                                 *((3 << 44, 1280, 256, 64, 4)), *((4 << 44, 640, 128, 64, 2)), 5 << 44, 6 << 44, 7 << 44, 8 << 44,
+                                 50, 0, 0, 0, 0, (3 << 44) + 16, 1 << 30)
+    grads = sequence._ROTATE_GRADS.pack(*((10 << 44, 1280, 256, 64, 4)), *((11 << 44, 640, 128, 64, 2)), 20 << 44, 21 << 44)
+    with pytest.raises(es.EsError) as e:
+        binding._check(binding.lib().es_plan_qk_norm_rotate(args, grads, None))
+    assert e.value.status == 3 and "workspace" in e.value.message
