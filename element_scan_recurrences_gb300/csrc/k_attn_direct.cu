@@ -16,6 +16,7 @@
 // precision and a decay of -inf needs no other care.
 #include "es_attn.h"
 #include "es_device.cuh"
+#include "es_pairs.cuh"
 
 namespace es {
 namespace {
@@ -25,9 +26,56 @@ constexpr int ZS = kAttnSlice;
 constexpr int kThreads = 256;
 constexpr int kAnchorChunks = kAttnAnchorTokens / C;
 
+// 2^v, 2 ulp: what the exponentials cost beside the sums' own roundings
+__device__ __forceinline__ float exp2_approx(float v) {
+    float r;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
 template <typename T>
 __device__ __forceinline__ float to_f32(T v) {
     return static_cast<float>(v);
+}
+
+// state = decay state + sum over the chunk's tokens of y u^T, a thread tiles of A rows by 4 columns
+template <int A>
+__device__ __forceinline__ void update(float* sS, const float* sY, const float* sU, int dxp, int ld, float decay, int tid) {
+    for (int tile = tid; tile < (dxp / A) * (ZS / 4); tile += kThreads) {
+        const int a = (tile / (ZS / 4)) * A, c = (tile % (ZS / 4)) * 4;
+        float2 acc[A][2];
+        const float2 d = make_float2(decay, decay);
+#pragma unroll
+        for (int r = 0; r < A; ++r) {
+            const float4 v = *reinterpret_cast<const float4*>(sS + (a + r) * ZS + c);
+            acc[r][0] = pair_mul(d, make_float2(v.x, v.y));
+            acc[r][1] = pair_mul(d, make_float2(v.z, v.w));
+        }
+#pragma unroll 4
+        for (int j = 0; j < C; ++j) {
+            float ya[A];
+            if constexpr (A == 4) {
+                const float4 yv = *reinterpret_cast<const float4*>(sY + j * ld + a);
+                ya[0] = yv.x;
+                ya[1] = yv.y;
+                ya[2] = yv.z;
+                ya[3] = yv.w;
+            } else {
+                const float2 yv = *reinterpret_cast<const float2*>(sY + j * ld + a);
+                ya[0] = yv.x;
+                ya[1] = yv.y;
+            }
+            const float4 uv = *reinterpret_cast<const float4*>(sU + j * ZS + c);
+#pragma unroll
+            for (int r = 0; r < A; ++r) {
+                acc[r][0] = pair_fma(make_float2(ya[r], ya[r]), make_float2(uv.x, uv.y), acc[r][0]);
+                acc[r][1] = pair_fma(make_float2(ya[r], ya[r]), make_float2(uv.z, uv.w), acc[r][1]);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < A; ++r)
+            *reinterpret_cast<float4*>(sS + (a + r) * ZS + c) = make_float4(acc[r][0].x, acc[r][0].y, acc[r][1].x, acc[r][1].y);
+    }
 }
 
 struct DirectArgs {
@@ -184,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_consta
             float g = cur_g;
             if constexpr (XR == 0) g = G != nullptr && tid < n ? G[(t0 + tid) * A.gt] : 0.0f;
             const bool cut = g < -104.0f;
-            if (cut) g = 0.0f;
+            g = cut ? 0.0f : g * 1.4426950408889634f;
             float pre = g, nxt = __shfl_down_sync(0xffffffffu, g, 1);
             float suf = tid == 31 ? 0.0f : nxt;
 #pragma unroll
@@ -199,15 +247,18 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_consta
             const unsigned after = tid == 31 ? 0u : cuts >> (tid + 1);
             sG[tid] = pre;
             sLo[tid] = upto ? 31 - __clz(upto) : 0;
-            const float er = upto ? 0.0f : expf(pre), eu = after ? 0.0f : expf(suf);
+            const float er = upto ? 0.0f : exp2_approx(pre), eu = after ? 0.0f : exp2_approx(suf);
             sRead[tid] = R.reverse ? eu : er;
             sUpd[tid] = R.reverse ? er : eu;
-            if (tid == 31) *sDecay = cuts ? 0.0f : expf(pre);
+            if (tid == 31) *sDecay = cuts ? 0.0f : exp2_approx(pre);
         }
         __syncthreads();
         // x_i . y_j with its decay: thread (ty, tx) rows ty, ty+16, columns tx, tx+16
         {
-            float s[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+            float2 s[2][2];       // even and odd values apart
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s[r / 2][r % 2] = make_float2(0.0f, 0.0f);
+#pragma unroll 2
             for (int a = 0; a < dxp; a += 4) {
                 float4 xv[2], yv[2];
 #pragma unroll
@@ -218,8 +269,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_consta
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                        s[r][c] += xv[r].x * yv[c].x + xv[r].y * yv[c].y + xv[r].z * yv[c].z + xv[r].w * yv[c].w;
+                    for (int c = 0; c < 2; ++c) {
+                        s[r][c] = pair_fma(make_float2(xv[r].x, xv[r].y), make_float2(yv[c].x, yv[c].y), s[r][c]);
+                        s[r][c] = pair_fma(make_float2(xv[r].z, xv[r].w), make_float2(yv[c].z, yv[c].w), s[r][c]);
+                    }
             }
 #pragma unroll
             for (int r = 0; r < 2; ++r)
@@ -228,14 +281,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_consta
                     const int i = ty + 16 * r, j = tx + 16 * c;
                     const int late = R.reverse ? j : i, early = R.reverse ? i : j;
                     const bool in = early <= late && early >= sLo[late];
-                    sP[i * (C + 1) + j] = in ? s[r][c] * expf(sG[late] - sG[early]) : 0.0f;
+                    sP[i * (C + 1) + j] = in ? (s[r][c].x + s[r][c].y) * exp2_approx(sG[late] - sG[early]) : 0.0f;
                 }
         }
         for (int e = tid; e < C * ZS; e += kThreads) sU[e] = sZ[e] * sUpd[e / ZS];
         __syncthreads();
         // out: thread (ty, tx) rows ty, ty+16, columns 2tx, 2tx+1
         {
-            float o[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}}, q[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+            const float2 zero = make_float2(0.0f, 0.0f);
+            float2 o[2] = {zero, zero}, q[2] = {zero, zero};      // two columns
+#pragma unroll 2
             for (int a = 0; a < dxp; a += 4) {
                 const float4 x0 = *reinterpret_cast<const float4*>(sX + ty * ld + a);
                 const float4 x1 = *reinterpret_cast<const float4*>(sX + (ty + 16) * ld + a);
@@ -244,10 +299,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_consta
                 for (int u = 0; u < 4; ++u) {
                     const float2 st = *reinterpret_cast<const float2*>(sS + (a + u) * ZS + 2 * tx);
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        q[r][0] += xs[r][u] * st.x;
-                        q[r][1] += xs[r][u] * st.y;
-                    }
+                    for (int r = 0; r < 2; ++r) q[r] = pair_fma(make_float2(xs[r][u], xs[r][u]), st, q[r]);
                 }
             }
 #pragma unroll 4
@@ -256,8 +308,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_consta
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const float p = sP[(ty + 16 * r) * (C + 1) + j];
-                    o[r][0] += p * zv.x;
-                    o[r][1] += p * zv.y;
+                    o[r] = pair_fma(make_float2(p, p), zv, o[r]);
                 }
             }
 #pragma unroll
@@ -266,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_consta
                 float dot = 0.0f;
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const float v = (o[r][c] + sRead[i] * q[r][c]) * R.out_scale;
+                    const float v = (c ? fmaf(sRead[i], q[r].y, o[r].y) : fmaf(sRead[i], q[r].x, o[r].x)) * R.out_scale;
                     const int zc = 2 * tx + c;
                     if (i < n && zc < nz) {
                         const int64_t at = out_at + (t0 + i) * R.ot + zc;
@@ -283,36 +334,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_consta
             }
         }
         __syncthreads();
-        // the state: 4 x 4 tiles
-        const float decay = *sDecay;
-        for (int tile = tid; tile < (dxp / 4) * (ZS / 4); tile += kThreads) {
-            const int a = (tile / (ZS / 4)) * 4, c = (tile % (ZS / 4)) * 4;
-            float acc[4][4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float4 v = *reinterpret_cast<const float4*>(sS + (a + r) * ZS + c);
-                acc[r][0] = decay * v.x;
-                acc[r][1] = decay * v.y;
-                acc[r][2] = decay * v.z;
-                acc[r][3] = decay * v.w;
-            }
-#pragma unroll 4
-            for (int j = 0; j < C; ++j) {
-                const float4 yv = *reinterpret_cast<const float4*>(sY + j * ld + a);
-                const float4 uv = *reinterpret_cast<const float4*>(sU + j * ZS + c);
-                const float ya[4] = {yv.x, yv.y, yv.z, yv.w};
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    acc[r][0] += ya[r] * uv.x;
-                    acc[r][1] += ya[r] * uv.y;
-                    acc[r][2] += ya[r] * uv.z;
-                    acc[r][3] += ya[r] * uv.w;
-                }
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                *reinterpret_cast<float4*>(sS + (a + r) * ZS + c) = make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
-        }
+        // the state, in tiles of 4 key rows (2 where those would leave threads idle) by 4 columns
+        if (dxp <= 64) update<2>(sS, sY, sU, dxp, ld, *sDecay, tid);
+        else update<4>(sS, sY, sU, dxp, ld, *sDecay, tid);
         if (at_anchor && !R.reverse) {
             __syncthreads();
             keep();
