@@ -62,7 +62,7 @@ struct AttnLaunch {
     int64_t gb, gt, gh;
     const int* lengths;          // [B] or null
     int64_t n_anchors;           // per (b, h)
-    // segments of tokens (tensor-core path): see k_attn_tc.cu
+    // segments of tokens: each a CTA's, with a pass before for the states between them
     int64_t seg_chunks;          // chunks a segment
     int n_segs;
     float* seg_states;
@@ -80,7 +80,7 @@ constexpr int kAttnChunk = 32;
 constexpr int kAttnSlice = 32;
 constexpr int kAttnMaxDim = 256;
 
-cudaError_t launch_attn_direct(const AttnLaunch& L);
+cudaError_t launch_attn_direct(const AttnLaunch& L, int* kernels);
 
 // Tokens between the states the decays' gradient starts from: its sums of
 // differences run within such a block (see k_attn_decay_grad).
@@ -90,6 +90,18 @@ constexpr int kAttnAnchorTokens = 256;
 constexpr int kAttnTcChunk = 64;
 bool attn_tc_operand_ok(const AttnOperand& o, int heads, int d, int64_t T, int64_t B);
 cudaError_t launch_attn_tc(const AttnLaunch& L, int* kernels, const char** err);
+
+// The states between segments from each segment's own (launch_attn_join).
+struct AttnJoin {
+    int reverse[3], init[3];     // of each run: direction, and whether a first state came
+    int64_t size, T, BH;
+    int H, chunk, n_segs;
+    int64_t seg_chunks;
+    const int* lengths;
+    float* states;               // [runs][BH][n_segs][size]
+    const float* decays;         // [runs][BH][n_segs]
+};
+cudaError_t launch_attn_join(const AttnLaunch& L, int chunk);
 
 // The decays' gradient from the two runs' dots and states: for each token t of
 // anchor block m, sum over s >= t of the block of (dq[s] - dk[s]) + e[m], with

@@ -103,16 +103,19 @@ struct AttnPlan {
     int slices_k;                // slices of the runs that give the dots (key-wide outputs)
 };
 
-// Segments a sequence is cut into (tensor-core path).  One CTA runs one (batch
-// row, head, run), one CTA an SM; with few of them the chunks are shared out
-// among more CTAs, which costs a pass over the keys and values for the states
-// between segments (0.42 of a main pass a chunk: 113 of 268 us for 65536 tokens x
-// 16 heads of 128) and two launches (about 5 chunks' time).
-int segments(int64_t ctas, int64_t chunks, int64_t* seg_chunks) {
-    const int64_t most = 152 / ctas;
+// Segments a sequence is cut into.  One CTA runs one (batch row, head, run, and on
+// the direct path slice); with fewer of them than the GPU has places, the chunks
+// are shared out among more CTAs, which costs a pass for the states between
+// segments and two launches.  In hundredths of a main pass's chunk: on the tensor
+// cores (one CTA an SM) 42 a chunk (113 of 268 us for 65536 tokens x 16 heads of
+// 128) and 500 for the launches; on the direct path (two CTAs an SM, chunks of 32
+// tokens, 5 to 6 us each) 65 and 300: f32, 4000 tokens x 4 heads of 128 802 -> 114 us
+// in segments, 4 x 300 x 12 heads of 96 62 us whole and 75 in two segments.
+int segments(bool tensor, int64_t ctas, int64_t chunks, int64_t* seg_chunks) {
+    const int64_t most = (tensor ? 152 : 304) / ctas;
     if (most < 2) return 1;
     const int64_t each = (chunks + most - 1) / most;
-    if (142 * each + 500 >= 100 * chunks) return 1;
+    if ((tensor ? 142 : 165) * each + (tensor ? 500 : 300) >= 100 * chunks) return 1;
     *seg_chunks = each;
     return static_cast<int>((chunks + each - 1) / each);
 }
@@ -288,7 +291,9 @@ es_status plan_attn(const char* fn, const es_linear_attention_args* a, const es_
     L.n_segs = 1;
     const int64_t chunks = (T + chunk - 1) / chunk;
     L.seg_chunks = chunks > 0 ? chunks : 1;
-    if (P->path == ES_PATH_TENSOR) L.n_segs = segments(bh * L.runs, chunks, &L.seg_chunks);
+    const int64_t slices = ((dk > dv ? dk : dv) + kAttnSlice - 1) / kAttnSlice;
+    if (chunks > 1 && !step)
+        L.n_segs = segments(P->path == ES_PATH_TENSOR, bh * L.runs * (P->path == ES_PATH_TENSOR ? 1 : slices), chunks, &L.seg_chunks);
     P->slices_k = static_cast<int>((dk + kAttnSlice - 1) / kAttnSlice);
     size_t at = 0;
     if (L.n_segs > 1) {
@@ -351,23 +356,23 @@ void fill_info(es_plan_info* info, int64_t O, int64_t T, int64_t J, int64_t W, i
 // one launch of P's path over `runs` of L
 es_status launch_runs(const char* fn, const AttnPlan& P, AttnLaunch L, void* workspace) {
     cudaError_t e;
+    int n = 0;
+    if (L.n_segs > 1) {
+        L.seg_states = reinterpret_cast<float*>(static_cast<char*>(workspace) + P.seg_states);
+        L.seg_decays = reinterpret_cast<float*>(static_cast<char*>(workspace) + P.seg_decays);
+    }
     if (P.path == ES_PATH_TENSOR) {
         es_status st = api_encoder(&L.encode);
         if (st != ES_OK) return st;
-        if (L.n_segs > 1) {
-            L.seg_states = reinterpret_cast<float*>(static_cast<char*>(workspace) + P.seg_states);
-            L.seg_decays = reinterpret_cast<float*>(static_cast<char*>(workspace) + P.seg_decays);
-        }
-        int n = 0;
         const char* msg = nullptr;
         e = launch_attn_tc(L, &n, &msg);
         if (msg != nullptr) return api_fail(ES_E_CUDA, "%s: %s", fn, msg);
-        count_launch(n);
     } else {
-        e = launch_attn_direct(L);
-        count_launch();
+        e = launch_attn_direct(L, &n);
     }
-    return e == cudaSuccess ? ES_OK : cuda_fail(fn, e);
+    if (e != cudaSuccess) return cuda_fail(fn, e);
+    count_launch(n);
+    return ES_OK;
 }
 
 es_status run_backward(const char* fn, const es_linear_attention_args* a, const es_linear_attention_grads* g, AttnPlan& P) {

@@ -87,6 +87,10 @@ struct DirectArgs {
     const int* lengths;
     int64_t n_anchors;
     int64_t BH;
+    int n_segs;
+    int64_t seg_chunks;
+    float* seg_states;           // [runs][BH][n_segs][dx * dz]: the state entering each segment's successor
+    float* seg_decays;           // [runs][BH][n_segs]
 };
 
 // Bounded on GB300 by shared-memory reads and FMA issue, not by HBM: for one
@@ -97,14 +101,17 @@ struct DirectArgs {
 // The next chunk's operands are on their way in registers (XR values a thread
 // of x and of y) while this one's are worked on; widths above 128 would take too
 // many (XR = 0) and wait for theirs.
-template <typename T, int XR>
+//
+// kStateOnly: a segment's own state, from zero, and its decay (slice 0); x is not read.
+template <typename T, int XR, bool kStateOnly>
 __global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_constant__ DirectArgs A) {
     extern __shared__ __align__(16) float sm[];
     const AttnRun& R = A.run[blockIdx.z];
     const int slice = blockIdx.y;
     const int z0 = slice * ZS;
     if (z0 >= R.dz) return;
-    const int64_t bh = blockIdx.x;
+    const int64_t bh = blockIdx.x / A.n_segs;
+    const int seg = static_cast<int>(blockIdx.x % A.n_segs);
     const int64_t b = bh / A.H;
     const int h = static_cast<int>(bh % A.H);
     const int tid = threadIdx.x;
@@ -133,25 +140,54 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_consta
     const T* Z = static_cast<const T*>(R.z.p) + b * R.z.sb + (h / R.z.div) * R.z.sh + z0;
     const T* Wd = R.dots != nullptr ? static_cast<const T*>(R.w.p) + b * R.w.sb + (h / R.w.div) * R.w.sh + z0 : nullptr;
     const float* G = A.g != nullptr ? A.g + b * A.gb + h * A.gh : nullptr;
+    // the segment's chunks [c0, c1) of the row's `chunks`, and whether they begin or end the run
+    const int64_t chunks = (len + C - 1) / C, c0 = seg * A.seg_chunks, c1 = chunks < c0 + A.seg_chunks ? chunks : c0 + A.seg_chunks;
+    const int last_seg = chunks > 0 ? static_cast<int>((chunks - 1) / A.seg_chunks) : 0;
+    const int64_t n_chunks = c1 > c0 ? c1 - c0 : 0;
+    const bool begins = R.reverse ? seg == last_seg : seg == 0, ends = R.reverse ? seg == 0 : seg == last_seg;
     float* dots = R.dots != nullptr ? R.dots + (slice * A.BH + bh) * A.T : nullptr;
     const int64_t out_at = b * R.ob + static_cast<int64_t>(h) * R.oh + z0;
     const bool store_f32 = R.out_f32 != 0;
 
     // the first state
     const int64_t sbase = bh * R.dx * static_cast<int64_t>(R.dz);
+    float* slots = A.n_segs > 1 ? A.seg_states + (blockIdx.z * A.BH + bh) * A.n_segs * R.dx * static_cast<int64_t>(R.dz) : nullptr;
+    auto slot = [&](int s) { return slots + s * (R.dx * static_cast<int64_t>(R.dz)) + z0; };
+    if constexpr (kStateOnly) {
+        if (seg > last_seg) return;
+        if (ends) {
+            // no successor: its place keeps the first state, which the last one may take the place of
+            if (R.init != nullptr)
+                for (int e = tid; e < dx * ZS; e += kThreads)
+                    if (e % ZS < nz)
+                        slot(seg)[(e / ZS) * static_cast<int64_t>(R.dz) + e % ZS] =
+                            R.init[sbase + (e / ZS) * R.sa + (z0 + e % ZS) * R.sc] * R.init_scale;
+            return;
+        }
+    }
+    const float* from = nullptr;
+    if (A.n_segs > 1 && !kStateOnly && seg <= last_seg && (!begins || R.init != nullptr))
+        from = slot(begins ? (R.reverse ? 0 : last_seg) : R.reverse ? seg + 1 : seg - 1);
     for (int e = tid; e < dxp * ZS; e += kThreads) {
         const int a = e / ZS, c = e % ZS;
         float v = 0.0f;
-        if (R.init != nullptr && a < dx && c < nz) v = R.init[sbase + a * R.sa + (z0 + c) * R.sc] * R.init_scale;
+        if (!kStateOnly && a < dx && c < nz) {
+            if (from != nullptr) v = from[a * static_cast<int64_t>(R.dz) + c];
+            else if (A.n_segs == 1 && R.init != nullptr) v = R.init[sbase + a * R.sa + (z0 + c) * R.sc] * R.init_scale;
+        }
         sS[e] = v;
     }
-    // rows past the length: zero
-    for (int64_t e = len * nz + tid; e < A.T * nz; e += kThreads) {
-        const int64_t t = e / nz, at = out_at + t * R.ot + e % nz;
-        if (store_f32) static_cast<float*>(R.out)[at] = 0.0f;
-        else static_cast<T*>(R.out)[at] = static_cast<T>(0.0f);
+    // the segment's rows past the length: zero
+    if constexpr (!kStateOnly) {
+        const int64_t lo = len > c0 * C ? len : c0 * C;
+        const int64_t hi = seg == A.n_segs - 1 || (c0 + A.seg_chunks) * C > A.T ? A.T : (c0 + A.seg_chunks) * C;
+        for (int64_t e = lo * nz + tid; e < hi * nz; e += kThreads) {
+            const int64_t t = e / nz, at = out_at + t * R.ot + e % nz;
+            if (store_f32) static_cast<float*>(R.out)[at] = 0.0f;
+            else static_cast<T*>(R.out)[at] = static_cast<T>(0.0f);
+        }
     }
-    const int64_t n_chunks = (len + C - 1) / C;
+    float all_decay = 1.0f;
     const int ty = tid / 16, tx = tid % 16;
 
     // Thread (t8, a) of 8 rows holds rows t8, t8 + 8, .. of columns a, a + 32, .. of x and y
@@ -160,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_consta
     float pg = 0.0f, cur_g = 0.0f;
     const int t8 = tid / 32, al = tid % 32;
     auto fetch = [&](int64_t k) {
-        const int64_t t0 = (R.reverse ? n_chunks - 1 - k : k) * C;
+        const int64_t t0 = (R.reverse ? c1 - 1 - k : c0 + k) * C;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int64_t t = t0 + t8 + 8 * r;
@@ -170,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_consta
 #pragma unroll
             for (int c = 0; c < XC; ++c) {
                 const int a = al + 32 * c;
-                px[c][r] = live && a < dx ? xr[a] : static_cast<T>(0.0f);
+                if constexpr (!kStateOnly) px[c][r] = live && a < dx ? xr[a] : static_cast<T>(0.0f);
                 py[c][r] = live && a < dx ? yr[a] : static_cast<T>(0.0f);
             }
             pz[r] = live && al < nz ? Z[t * R.z.st + al] : static_cast<T>(0.0f);
@@ -185,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_consta
             for (int c = 0; c < XC; ++c) {
                 const int a = al + 32 * c;
                 if (a < dxp) {
-                    sX[t * ld + a] = to_f32(px[c][r]);
+                    if constexpr (!kStateOnly) sX[t * ld + a] = to_f32(px[c][r]);
                     sY[t * ld + a] = to_f32(py[c][r]);
                 }
             }
@@ -198,12 +234,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_consta
     }
 
     for (int64_t k = 0; k < n_chunks; ++k) {
-        const int64_t ci = R.reverse ? n_chunks - 1 - k : k;
+        const int64_t ci = R.reverse ? c1 - 1 - k : c0 + k;
         const int64_t t0 = ci * C;
         const int n = static_cast<int>(len - t0 < C ? len - t0 : C);
         __syncthreads();
         // for the decays' gradient: the state at the end of an anchor block
-        const bool at_anchor = R.anchors != nullptr && ((ci + 1) % kAnchorChunks == 0 || ci == n_chunks - 1);
+        const bool at_anchor = !kStateOnly && R.anchors != nullptr && ((ci + 1) % kAnchorChunks == 0 || ci == chunks - 1);
         auto keep = [&]() {
             float* an = R.anchors + (bh * A.n_anchors + ci / kAnchorChunks) * R.dx * static_cast<int64_t>(R.dz);
             for (int e = tid; e < dx * ZS; e += kThreads) {
@@ -219,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_consta
             for (int e = tid; e < C * dxp; e += kThreads) {
                 const int t = e / dxp, a = e % dxp;
                 const bool in = t < n && a < dx;
-                sX[t * ld + a] = in ? to_f32(X[(t0 + t) * R.x.st + a]) : 0.0f;
+                if constexpr (!kStateOnly) sX[t * ld + a] = in ? to_f32(X[(t0 + t) * R.x.st + a]) : 0.0f;
                 sY[t * ld + a] = in ? to_f32(Y[(t0 + t) * R.y.st + a]) : 0.0f;
             }
             for (int e = tid; e < C * ZS; e += kThreads) {
@@ -254,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_consta
         }
         __syncthreads();
         // x_i . y_j with its decay: thread (ty, tx) rows ty, ty+16, columns tx, tx+16
-        {
+        if constexpr (!kStateOnly) {
             float2 s[2][2];       // even and odd values apart
 #pragma unroll
             for (int r = 0; r < 4; ++r) s[r / 2][r % 2] = make_float2(0.0f, 0.0f);
@@ -287,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_consta
         for (int e = tid; e < C * ZS; e += kThreads) sU[e] = sZ[e] * sUpd[e / ZS];
         __syncthreads();
         // out: thread (ty, tx) rows ty, ty+16, columns 2tx, 2tx+1
-        {
+        if constexpr (!kStateOnly) {
             const float2 zero = make_float2(0.0f, 0.0f);
             float2 o[2] = {zero, zero}, q[2] = {zero, zero};      // two columns
 #pragma unroll 2
@@ -334,6 +370,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_consta
             }
         }
         __syncthreads();
+        if constexpr (kStateOnly) all_decay *= *sDecay;
         // the state, in tiles of 4 key rows (2 where those would leave threads idle) by 4 columns
         if (dxp <= 64) update<2>(sS, sY, sU, dxp, ld, *sDecay, tid);
         else update<4>(sS, sY, sU, dxp, ld, *sDecay, tid);
@@ -343,11 +380,42 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_consta
         }
     }
     __syncthreads();
-    if (R.fin != nullptr)
+    if constexpr (kStateOnly) {
+        for (int e = tid; e < dx * ZS; e += kThreads)
+            if (e % ZS < nz) slot(seg)[(e / ZS) * static_cast<int64_t>(R.dz) + e % ZS] = sS[e];
+        if (slice == 0 && tid == 0) A.seg_decays[(blockIdx.z * A.BH + bh) * A.n_segs + seg] = all_decay;
+    } else if (R.fin != nullptr && ends) {
         for (int e = tid; e < dx * ZS; e += kThreads) {
             const int a = e / ZS, c = e % ZS;
             if (c < nz) R.fin[sbase + a * R.sa + (z0 + c) * R.sc] = sS[e] * R.fin_scale;
         }
+    }
+}
+
+// State entering each segment from the one before: in order along the run,
+// what came in times segment s's decay, plus its own state.  The first state
+// lies in the place of the run's last segment, which has no successor.
+__global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ AttnJoin J) {
+    const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (e >= J.size) return;
+    const int64_t bh = blockIdx.z;
+    int64_t len = J.T;
+    if (J.lengths != nullptr) {
+        const int64_t l = J.lengths[bh / J.H];
+        len = l < 0 ? 0 : l < J.T ? l : J.T;
+    }
+    const int64_t chunks = (len + J.chunk - 1) / J.chunk;
+    const int last_seg = chunks > 0 ? static_cast<int>((chunks - 1) / J.seg_chunks) : 0;
+    const bool reverse = J.reverse[blockIdx.y];
+    float* st = J.states + (blockIdx.y * J.BH + bh) * J.n_segs * J.size + e;
+    const float* d = J.decays + (blockIdx.y * J.BH + bh) * J.n_segs;
+    float v = J.init[blockIdx.y] ? st[(reverse ? 0 : last_seg) * J.size] : 0.0f;
+#pragma unroll 4
+    for (int s = 0; s < last_seg; ++s) {
+        const int at = reverse ? last_seg - s : s;
+        v = fmaf(d[at], v, st[at * J.size]);
+        st[at * J.size] = v;
+    }
 }
 
 // The decays' gradient meets, between the anchor blocks, the product of the
@@ -521,7 +589,42 @@ size_t direct_smem(int dx) {
 
 }  // namespace
 
-cudaError_t launch_attn_direct(const AttnLaunch& L) {
+cudaError_t launch_attn_join(const AttnLaunch& L, int chunk) {
+    AttnJoin J{};
+    for (int r = 0; r < L.runs; ++r) {
+        J.reverse[r] = L.run[r].reverse;
+        J.init[r] = L.run[r].init != nullptr;
+    }
+    J.size = static_cast<int64_t>(L.run[0].dx) * L.run[0].dz;     // the same for every run of a call
+    J.T = L.T;
+    J.BH = L.B * L.H;
+    J.H = L.H;
+    J.chunk = chunk;
+    J.n_segs = L.n_segs;
+    J.seg_chunks = L.seg_chunks;
+    J.lengths = L.lengths;
+    J.states = L.seg_states;
+    J.decays = L.seg_decays;
+    k_attn_join<<<dim3(static_cast<unsigned>((J.size + 255) / 256), L.runs, static_cast<unsigned>(J.BH)), 256, 0, L.stream>>>(J);
+    return cudaGetLastError();
+}
+
+template <typename T, int XR>
+cudaError_t launch_direct(const DirectArgs& A, const AttnLaunch& L, dim3 grid, size_t smem) {
+    cudaError_t e;
+    if (A.n_segs > 1) {
+        const auto state = k_attn_direct<T, XR, true>;
+        if ((e = cudaFuncSetAttribute(state, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem))) != cudaSuccess) return e;
+        state<<<grid, kThreads, smem, L.stream>>>(A);
+        if ((e = cudaGetLastError()) != cudaSuccess || (e = launch_attn_join(L, C)) != cudaSuccess) return e;
+    }
+    const auto kernel = k_attn_direct<T, XR, false>;
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem))) != cudaSuccess) return e;
+    kernel<<<grid, kThreads, smem, L.stream>>>(A);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_attn_direct(const AttnLaunch& L, int* kernels) {
     DirectArgs A{};
     int dx = 0, dz = 0;
     for (int r = 0; r < L.runs; ++r) {
@@ -538,15 +641,20 @@ cudaError_t launch_attn_direct(const AttnLaunch& L) {
     A.lengths = L.lengths;
     A.n_anchors = L.n_anchors;
     A.BH = L.B * L.H;
-    const auto kernel = dx <= 64    ? (L.bf16 ? k_attn_direct<__nv_bfloat16, 8> : k_attn_direct<float, 8>)
-                        : dx <= 128 ? (L.bf16 ? k_attn_direct<__nv_bfloat16, 16> : k_attn_direct<float, 16>)
-                                    : (L.bf16 ? k_attn_direct<__nv_bfloat16, 0> : k_attn_direct<float, 0>);
+    A.n_segs = L.n_segs;
+    A.seg_chunks = L.seg_chunks;
+    A.seg_states = L.seg_states;
+    A.seg_decays = L.seg_decays;
+    *kernels = L.n_segs > 1 ? 3 : 1;
     const size_t smem = direct_smem(dx);
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-    const dim3 grid(static_cast<unsigned>(A.BH), (dz + ZS - 1) / ZS, L.runs);
-    kernel<<<grid, kThreads, smem, L.stream>>>(A);
-    return cudaGetLastError();
+    const dim3 grid(static_cast<unsigned>(A.BH * A.n_segs), (dz + ZS - 1) / ZS, L.runs);
+    if (L.bf16)
+        return dx <= 64    ? launch_direct<__nv_bfloat16, 8>(A, L, grid, smem)
+               : dx <= 128 ? launch_direct<__nv_bfloat16, 16>(A, L, grid, smem)
+                           : launch_direct<__nv_bfloat16, 0>(A, L, grid, smem);
+    return dx <= 64    ? launch_direct<float, 8>(A, L, grid, smem)
+           : dx <= 128 ? launch_direct<float, 16>(A, L, grid, smem)
+                       : launch_direct<float, 0>(A, L, grid, smem);
 }
 
 cudaError_t launch_attn_decay_grad(const AttnDecayGrad& G, int* kernels) {

@@ -881,33 +881,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
     }
 }
 
-// State entering each segment from the one before: in order along the run,
-// segment s's own state plus its decay times what came into it.
-__global__ void __launch_bounds__(256) k_attn_tc_join(const __grid_constant__ TcArgs A) {
-    const TcRun& R = A.run[blockIdx.y];
-    const int64_t size = static_cast<int64_t>(R.dx) * R.dz;
-    const int64_t bh = blockIdx.z;
-    const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (e >= size) return;
-    const int b = static_cast<int>(bh / A.H);
-    int64_t len = A.T;
-    if (A.lengths != nullptr) {
-        const int64_t l = A.lengths[b];
-        len = l < 0 ? 0 : l < A.T ? l : A.T;
-    }
-    const int chunks = static_cast<int>((len + C - 1) / C);
-    const int last_seg = chunks > 0 ? (chunks - 1) / A.seg_chunks : 0;
-    float* st = A.seg_states + blockIdx.y * A.seg_stride + bh * A.n_segs * size + e;
-    const float* d = A.seg_decays + (blockIdx.y * A.BH + bh) * A.n_segs;
-    // the first state lies in the place of the run's last segment, which has no successor
-    float v = R.init != nullptr ? st[(R.reverse ? 0 : last_seg) * size] : 0.0f;
-    for (int s = 0; s < last_seg; ++s) {
-        const int at = R.reverse ? last_seg - s : s;
-        v = fmaf(d[at], v, st[at * size]);
-        st[at * size] = v;
-    }
-}
-
 bool encode(EncodeTiledFn fn, CUtensorMap* m, const AttnOperand& o, int heads, int d, int64_t T, int64_t B) {
     // a broadcast axis (stride 0) has an extent of one; extents of one take a stride that keeps the map valid
     if (o.sb == 0) B = 1;
@@ -1014,10 +987,7 @@ cudaError_t launch_attn_tc(const AttnLaunch& L, int* kernels, const char** err) 
     };
     if (A.n_segs > 1) {
         if ((e = launch(k_attn_tc<true, false>)) != cudaSuccess) return e;
-        int most = 0;
-        for (int r = 0; r < L.runs; ++r) most = L.run[r].dx * L.run[r].dz > most ? L.run[r].dx * L.run[r].dz : most;
-        k_attn_tc_join<<<dim3((most + 255) / 256, L.runs, static_cast<unsigned>(A.BH)), 256, 0, L.stream>>>(A);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if ((e = launch_attn_join(L, C)) != cudaSuccess) return e;
         *kernels += 2;
     }
     if ((e = launch(any_dots ? k_attn_tc<false, true> : k_attn_tc<false, false>)) != cudaSuccess) return e;

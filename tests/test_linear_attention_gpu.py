@@ -394,3 +394,25 @@ def test_refusals():
         es.linear_attention_step(c.q[:, 0], c.k[:, 0], c.v[:, 0], c.g[:, 0], None)
     with pytest.raises(es.EsError):
         es.linear_attention_step(c.q[:, 0], c.k[:, 0], c.v[:, 0], c.g[:, 0], c.init[:1])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("heads", [(1, 1, 1, 1), (2, 1, 2, 2)], ids=str)
+def test_long_rows_in_segments(heads, dtype):
+    """Few heads and many tokens: the row is cut into segments (a workspace is
+    asked for), with lengths that end in the first, a middle and the last of
+    them, a carried state in place, and decays of zero at and near the cuts."""
+    lengths = [1500, 64, 700]
+    c = Case(dtype, 3, 1500, heads, 64, 64, lengths=lengths)
+    assert es.plan_linear_attention(c.q.shape, c.k.shape, c.v.shape, "f32" if dtype == F32 else "bf16", decay="token",
+                                    heads=heads[3])["workspace"] > 0
+    c.g[0, 640, 0] = float("-inf")
+    c.g[2, 512, 0] = float("-inf")
+    out, state = check_forward(c)
+    check_backward(c)
+    place = c.init.clone()
+    es.linear_attention(c.q, c.k, c.v, c.g, initial_state=place, lengths=c.lengths, scale=c.scale, final_state=place)
+    assert torch.equal(place, state)
+    c = Case(dtype, 1, 900, heads, 64, 64, decay="head", carry=False)
+    check_forward(c)
+    check_backward(c)
