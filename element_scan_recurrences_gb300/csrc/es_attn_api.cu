@@ -108,14 +108,17 @@ struct AttnPlan {
 // are shared out among more CTAs, which costs a pass for the states between
 // segments and two launches.  In hundredths of a main pass's chunk: on the tensor
 // cores (one CTA an SM) 42 a chunk (113 of 268 us for 65536 tokens x 16 heads of
-// 128) and 500 for the launches; on the direct path (two CTAs an SM, chunks of 32
-// tokens, 5 to 6 us each) 65 and 300: f32, 4000 tokens x 4 heads of 128 802 -> 114 us
-// in segments, 4 x 300 x 12 heads of 96 62 us whole and 75 in two segments.
-int segments(bool tensor, int64_t ctas, int64_t chunks, int64_t* seg_chunks) {
-    const int64_t most = (tensor ? 152 : 304) / ctas;
+// 128) and 500 for the launches; on the direct path (four CTAs an SM at widths to
+// 64, three to 128, two above; chunks of 32 tokens, 5 to 7 us each) 65 and 600.
+// f32, whole against in segments: 4000 tokens x 4 heads of 128 851 and 107 us,
+// 256 tokens x 4 heads of 64 48 and 24, 8 x 200 x 8 heads of 64 44 and 46,
+// 8 x 1000 x 16 heads of 64 221 and 227.  With two CTAs an SM at all widths
+// 4 x 1000 x 16 heads of 64 took 146 us instead of 120.
+int segments(bool tensor, int64_t width, int64_t ctas, int64_t chunks, int64_t* seg_chunks) {
+    const int64_t most = 152 * (tensor ? 1 : width <= 64 ? 4 : width <= 128 ? 3 : 2) / ctas;
     if (most < 2) return 1;
     const int64_t each = (chunks + most - 1) / most;
-    if ((tensor ? 142 : 165) * each + (tensor ? 500 : 300) >= 100 * chunks) return 1;
+    if ((tensor ? 142 : 165) * each + (tensor ? 500 : 600) >= 100 * chunks) return 1;
     *seg_chunks = each;
     return static_cast<int>((chunks + each - 1) / each);
 }
@@ -293,7 +296,8 @@ es_status plan_attn(const char* fn, const es_linear_attention_args* a, const es_
     L.seg_chunks = chunks > 0 ? chunks : 1;
     const int64_t slices = ((dk > dv ? dk : dv) + kAttnSlice - 1) / kAttnSlice;
     if (chunks > 1 && !step)
-        L.n_segs = segments(P->path == ES_PATH_TENSOR, bh * L.runs * (P->path == ES_PATH_TENSOR ? 1 : slices), chunks, &L.seg_chunks);
+        L.n_segs = segments(P->path == ES_PATH_TENSOR, dk > dv ? dk : dv, bh * L.runs * (P->path == ES_PATH_TENSOR ? 1 : slices),
+                            chunks, &L.seg_chunks);
     P->slices_k = static_cast<int>((dk + kAttnSlice - 1) / kAttnSlice);
     size_t at = 0;
     if (L.n_segs > 1) {

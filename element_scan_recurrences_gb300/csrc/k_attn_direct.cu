@@ -23,7 +23,8 @@ namespace {
 
 constexpr int C = kAttnChunk;
 constexpr int ZS = kAttnSlice;
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+constexpr int kPLd = C + 4;          // rows of P: on 16 bytes
 constexpr int kAnchorChunks = kAttnAnchorTokens / C;
 
 // 2^v, 2 ulp: what the exponentials cost beside the sums' own roundings
@@ -51,7 +52,7 @@ __device__ __forceinline__ void update(float* sS, const float* sY, const float* 
             acc[r][0] = pair_mul(d, make_float2(v.x, v.y));
             acc[r][1] = pair_mul(d, make_float2(v.z, v.w));
         }
-#pragma unroll 4
+#pragma unroll 8
         for (int j = 0; j < C; ++j) {
             float ya[A];
             if constexpr (A == 4) {
@@ -93,18 +94,23 @@ struct DirectArgs {
     float* seg_decays;           // [runs][BH][n_segs]
 };
 
-// Bounded on GB300 by shared-memory reads and FMA issue, not by HBM: for one
-// chunk and slice, dx = 128, 426 K FMAs (the 32 x 32 products of x and y are
-// formed again in every slice).  It serves the calls the tensor-core kernel
-// cannot take.
+// Bounded on GB300 by the latency of shared-memory reads and by their number
+// (in the main pass shared memory is 64 % busy and 47 % of issue slots are used),
+// not by HBM: for one chunk and slice, dx = 128, 426 K FMAs (the 32 x 32 products
+// of x and y are formed again in every slice).  So few threads with 4 rows of the
+// products each: 256 threads with 2 rows read half as much again, and the training
+// pass of 4 x 1000 x 16 heads of 128 took 1451 us instead of 1183 (2 x 501 x 8
+// heads of 64: 122 instead of 105; a lone CTA an SM favours them, 4 x 300 x 12
+// heads of 96 took 62 instead of 72).  It serves the calls the tensor-core
+// kernel cannot take.
 //
-// The next chunk's operands are on their way in registers (XR values a thread
-// of x and of y) while this one's are worked on; widths above 128 would take too
-// many (XR = 0) and wait for theirs.
+// The next chunk's operands are on their way in registers (XC columns of 8 rows a
+// thread of x and of y) while this one's are worked on; widths above 128 would take
+// too many (XC = 0) and wait for theirs.
 //
 // kStateOnly: a segment's own state, from zero, and its decay (slice 0); x is not read.
-template <typename T, int XR, bool kStateOnly>
-__global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_constant__ DirectArgs A) {
+template <typename T, int XC, bool kStateOnly>
+__global__ void __launch_bounds__(kThreads, XC == 2 ? 4 : XC == 4 ? 3 : 2) k_attn_direct(const __grid_constant__ DirectArgs A) {
     extern __shared__ __align__(16) float sm[];
     const AttnRun& R = A.run[blockIdx.z];
     const int slice = blockIdx.y;
@@ -123,8 +129,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_consta
     float* sS = sY + C * ld;              // state slice [dxp][ZS]
     float* sZ = sS + dxp * ZS;            // [C][ZS]
     float* sU = sZ + C * ZS;              // z scaled by its chunk coefficient
-    float* sP = sU + C * ZS;              // [C][C + 1]
-    float* sG = sP + C * (C + 1);         // G, and per token: coefficient of the read, of the update
+    float* sP = sU + C * ZS;              // [C][kPLd]
+    float* sG = sP + C * kPLd;            // G, and per token: coefficient of the read, of the update
     float* sRead = sG + C;
     float* sUpd = sRead + C;
     int* sLo = reinterpret_cast<int*>(sUpd + C);    // first token of the group of token i
@@ -190,21 +196,21 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_consta
     float all_decay = 1.0f;
     const int ty = tid / 16, tx = tid % 16;
 
-    // Thread (t8, a) of 8 rows holds rows t8, t8 + 8, .. of columns a, a + 32, .. of x and y
-    constexpr int XC = XR > 0 ? XR / 4 : 1;
-    T px[XC][4], py[XC][4], pz[4];
+    // Thread (t4, a) of 4 rows holds rows t4, t4 + 4, .. of columns a, a + 32, .. of x and y
+    constexpr int PC = XC > 0 ? XC : 1, PR = C / 4;
+    T px[PC][PR], py[PC][PR], pz[PR];
     float pg = 0.0f, cur_g = 0.0f;
-    const int t8 = tid / 32, al = tid % 32;
+    const int t4 = tid / 32, al = tid % 32;
     auto fetch = [&](int64_t k) {
         const int64_t t0 = (R.reverse ? c1 - 1 - k : c0 + k) * C;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int64_t t = t0 + t8 + 8 * r;
+        for (int r = 0; r < PR; ++r) {
+            const int64_t t = t0 + t4 + 4 * r;
             const bool live = t < len;
             const T* xr = X + t * R.x.st;
             const T* yr = Y + t * R.y.st;
 #pragma unroll
-            for (int c = 0; c < XC; ++c) {
+            for (int c = 0; c < PC; ++c) {
                 const int a = al + 32 * c;
                 if constexpr (!kStateOnly) px[c][r] = live && a < dx ? xr[a] : static_cast<T>(0.0f);
                 py[c][r] = live && a < dx ? yr[a] : static_cast<T>(0.0f);
@@ -215,10 +221,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_consta
     };
     auto put = [&]() {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int t = t8 + 8 * r;
+        for (int r = 0; r < PR; ++r) {
+            const int t = t4 + 4 * r;
 #pragma unroll
-            for (int c = 0; c < XC; ++c) {
+            for (int c = 0; c < PC; ++c) {
                 const int a = al + 32 * c;
                 if (a < dxp) {
                     if constexpr (!kStateOnly) sX[t * ld + a] = to_f32(px[c][r]);
@@ -229,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_consta
         }
         cur_g = pg;
     };
-    if constexpr (XR > 0) {
+    if constexpr (XC > 0) {
         if (n_chunks > 0) fetch(0);
     }
 
@@ -248,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_consta
             }
         };
         if (at_anchor && R.reverse) keep();
-        if constexpr (XR > 0) {
+        if constexpr (XC > 0) {
             put();
             if (k + 1 < n_chunks) fetch(k + 1);
         } else {
@@ -266,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_consta
         if (tid < 32) {
             // one token a lane: G, the sum after it, and its group
             float g = cur_g;
-            if constexpr (XR == 0) g = G != nullptr && tid < n ? G[(t0 + tid) * A.gt] : 0.0f;
+            if constexpr (XC == 0) g = G != nullptr && tid < n ? G[(t0 + tid) * A.gt] : 0.0f;
             const bool cut = g < -104.0f;
             g = cut ? 0.0f : g * 1.4426950408889634f;
             float pre = g, nxt = __shfl_down_sync(0xffffffffu, g, 1);
@@ -289,21 +295,20 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_consta
             if (tid == 31) *sDecay = cuts ? 0.0f : exp2_approx(pre);
         }
         __syncthreads();
-        // x_i . y_j with its decay: thread (ty, tx) rows ty, ty+16, columns tx, tx+16
+        // x_i . y_j with its decay: thread (ty, tx) rows ty + 8r, columns tx, tx + 16
         if constexpr (!kStateOnly) {
-            float2 s[2][2];       // even and odd values apart
+            float2 s[4][2];       // even and odd values apart
 #pragma unroll
-            for (int r = 0; r < 4; ++r) s[r / 2][r % 2] = make_float2(0.0f, 0.0f);
-#pragma unroll 2
+            for (int r = 0; r < 8; ++r) s[r / 2][r % 2] = make_float2(0.0f, 0.0f);
+#pragma unroll 4
             for (int a = 0; a < dxp; a += 4) {
-                float4 xv[2], yv[2];
+                float4 xv[4], yv[2];
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    xv[r] = *reinterpret_cast<const float4*>(sX + (ty + 16 * r) * ld + a);
-                    yv[r] = *reinterpret_cast<const float4*>(sY + (tx + 16 * r) * ld + a);
-                }
+                for (int r = 0; r < 4; ++r) xv[r] = *reinterpret_cast<const float4*>(sX + (ty + 8 * r) * ld + a);
 #pragma unroll
-                for (int r = 0; r < 2; ++r)
+                for (int c = 0; c < 2; ++c) yv[c] = *reinterpret_cast<const float4*>(sY + (tx + 16 * c) * ld + a);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         s[r][c] = pair_fma(make_float2(xv[r].x, xv[r].y), make_float2(yv[c].x, yv[c].y), s[r][c]);
@@ -311,55 +316,67 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_consta
                     }
             }
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
+            for (int r = 0; r < 4; ++r)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const int i = ty + 16 * r, j = tx + 16 * c;
+                    const int i = ty + 8 * r, j = tx + 16 * c;
                     const int late = R.reverse ? j : i, early = R.reverse ? i : j;
                     const bool in = early <= late && early >= sLo[late];
-                    sP[i * (C + 1) + j] = in ? (s[r][c].x + s[r][c].y) * exp2_approx(sG[late] - sG[early]) : 0.0f;
+                    sP[i * kPLd + j] = in ? (s[r][c].x + s[r][c].y) * exp2_approx(sG[late] - sG[early]) : 0.0f;
                 }
         }
         for (int e = tid; e < C * ZS; e += kThreads) sU[e] = sZ[e] * sUpd[e / ZS];
         __syncthreads();
-        // out: thread (ty, tx) rows ty, ty+16, columns 2tx, 2tx+1
+        // out: thread (ty, tx) rows ty + 8r, columns 2tx, 2tx + 1; what the state gives first, then the chunk
         if constexpr (!kStateOnly) {
-            const float2 zero = make_float2(0.0f, 0.0f);
-            float2 o[2] = {zero, zero}, q[2] = {zero, zero};      // two columns
-#pragma unroll 2
-            for (int a = 0; a < dxp; a += 4) {
-                const float4 x0 = *reinterpret_cast<const float4*>(sX + ty * ld + a);
-                const float4 x1 = *reinterpret_cast<const float4*>(sX + (ty + 16) * ld + a);
-                const float xs[2][4] = {{x0.x, x0.y, x0.z, x0.w}, {x1.x, x1.y, x1.z, x1.w}};
+            float2 o[4];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const float2 st = *reinterpret_cast<const float2*>(sS + (a + u) * ZS + 2 * tx);
+            for (int r = 0; r < 4; ++r) o[r] = make_float2(0.0f, 0.0f);
+            T wv[4][2];           // on their way meanwhile
+            if (Wd != nullptr) {
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) q[r] = pair_fma(make_float2(xs[r][u], xs[r][u]), st, q[r]);
-                }
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        wv[r][c] = ty + 8 * r < n && 2 * tx + c < nz ? Wd[(t0 + ty + 8 * r) * R.w.st + 2 * tx + c] : static_cast<T>(0.0f);
             }
+            auto add = [&](const float* left, int stride, const float* right) {      // 4 terms
+                float4 lv[4];
+                float2 rv[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) lv[r] = *reinterpret_cast<const float4*>(left + (ty + 8 * r) * stride);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) rv[u] = *reinterpret_cast<const float2*>(right + u * ZS + 2 * tx);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    o[r] = pair_fma(make_float2(lv[r].x, lv[r].x), rv[0], o[r]);
+                    o[r] = pair_fma(make_float2(lv[r].y, lv[r].y), rv[1], o[r]);
+                    o[r] = pair_fma(make_float2(lv[r].z, lv[r].z), rv[2], o[r]);
+                    o[r] = pair_fma(make_float2(lv[r].w, lv[r].w), rv[3], o[r]);
+                }
+            };
 #pragma unroll 4
-            for (int j = 0; j < C; ++j) {
-                const float2 zv = *reinterpret_cast<const float2*>(sZ + j * ZS + 2 * tx);
+            for (int a = 0; a < dxp; a += 4) add(sX + a, ld, sS + a * ZS);
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const float p = sP[(ty + 16 * r) * (C + 1) + j];
-                    o[r] = pair_fma(make_float2(p, p), zv, o[r]);
-                }
+            for (int r = 0; r < 4; ++r) {
+                const float rd = sRead[ty + 8 * r];
+                o[r] = pair_mul(o[r], make_float2(rd, rd));
             }
+#pragma unroll 2
+            for (int j = 0; j < C; j += 4) add(sP + j, kPLd, sZ + j * ZS);
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int i = ty + 16 * r;
+            for (int r = 0; r < 4; ++r) {
+                const int i = ty + 8 * r;
                 float dot = 0.0f;
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const float v = (c ? fmaf(sRead[i], q[r].y, o[r].y) : fmaf(sRead[i], q[r].x, o[r].x)) * R.out_scale;
+                    const float v = (c ? o[r].y : o[r].x) * R.out_scale;
                     const int zc = 2 * tx + c;
                     if (i < n && zc < nz) {
                         const int64_t at = out_at + (t0 + i) * R.ot + zc;
                         if (store_f32) static_cast<float*>(R.out)[at] = v;
                         else static_cast<T*>(R.out)[at] = static_cast<T>(v);
-                        if (Wd != nullptr) dot += v * to_f32(Wd[(t0 + i) * R.w.st + zc]);
+                        if (Wd != nullptr) dot += v * to_f32(wv[r][c]);
                     }
                 }
                 if (dots != nullptr) {
@@ -372,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_direct(const __grid_consta
         __syncthreads();
         if constexpr (kStateOnly) all_decay *= *sDecay;
         // the state, in tiles of 4 key rows (2 where those would leave threads idle) by 4 columns
-        if (dxp <= 64) update<2>(sS, sY, sU, dxp, ld, *sDecay, tid);
+        if (dxp <= 32) update<2>(sS, sY, sU, dxp, ld, *sDecay, tid);
         else update<4>(sS, sY, sU, dxp, ld, *sDecay, tid);
         if (at_anchor && !R.reverse) {
             __syncthreads();
@@ -584,7 +601,7 @@ __global__ void __launch_bounds__(256) k_attn_fold(const __grid_constant__ AttnF
 
 size_t direct_smem(int dx) {
     const size_t dxp = (dx + 3) & ~3;
-    return sizeof(float) * (2 * C * (dxp + 4) + dxp * ZS + 2 * C * ZS + C * (C + 1) + 4 * C + 4);
+    return sizeof(float) * (2 * C * (dxp + 4) + dxp * ZS + 2 * C * ZS + C * kPLd + 4 * C + 4);
 }
 
 }  // namespace
@@ -609,16 +626,16 @@ cudaError_t launch_attn_join(const AttnLaunch& L, int chunk) {
     return cudaGetLastError();
 }
 
-template <typename T, int XR>
+template <typename T, int XC>
 cudaError_t launch_direct(const DirectArgs& A, const AttnLaunch& L, dim3 grid, size_t smem) {
     cudaError_t e;
     if (A.n_segs > 1) {
-        const auto state = k_attn_direct<T, XR, true>;
+        const auto state = k_attn_direct<T, XC, true>;
         if ((e = cudaFuncSetAttribute(state, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem))) != cudaSuccess) return e;
         state<<<grid, kThreads, smem, L.stream>>>(A);
         if ((e = cudaGetLastError()) != cudaSuccess || (e = launch_attn_join(L, C)) != cudaSuccess) return e;
     }
-    const auto kernel = k_attn_direct<T, XR, false>;
+    const auto kernel = k_attn_direct<T, XC, false>;
     if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem))) != cudaSuccess) return e;
     kernel<<<grid, kThreads, smem, L.stream>>>(A);
     return cudaGetLastError();
@@ -649,11 +666,11 @@ cudaError_t launch_attn_direct(const AttnLaunch& L, int* kernels) {
     const size_t smem = direct_smem(dx);
     const dim3 grid(static_cast<unsigned>(A.BH * A.n_segs), (dz + ZS - 1) / ZS, L.runs);
     if (L.bf16)
-        return dx <= 64    ? launch_direct<__nv_bfloat16, 8>(A, L, grid, smem)
-               : dx <= 128 ? launch_direct<__nv_bfloat16, 16>(A, L, grid, smem)
+        return dx <= 64    ? launch_direct<__nv_bfloat16, 2>(A, L, grid, smem)
+               : dx <= 128 ? launch_direct<__nv_bfloat16, 4>(A, L, grid, smem)
                            : launch_direct<__nv_bfloat16, 0>(A, L, grid, smem);
-    return dx <= 64    ? launch_direct<float, 8>(A, L, grid, smem)
-           : dx <= 128 ? launch_direct<float, 16>(A, L, grid, smem)
+    return dx <= 64    ? launch_direct<float, 2>(A, L, grid, smem)
+           : dx <= 128 ? launch_direct<float, 4>(A, L, grid, smem)
                        : launch_direct<float, 0>(A, L, grid, smem);
 }
 
