@@ -100,7 +100,7 @@ struct TcArgs {
 
 struct Shared {
     uint64_t full[kMaxStages], ready[kMaxStages], empty[kMaxStages];
-    uint64_t s_done, p_ready, zh_ready, kv_done, state_done, o_done, o_read, drained[2];
+    uint64_t s_done, p_ready, zh_ready[2], kv_done, state_done, o_done, o_read, drained[2];
     uint32_t tmem;
     int abort_flag;
     Coef coef[kMaxStages];
@@ -258,7 +258,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         }
         mbar_init(&sh.s_done, 1);
         mbar_init(&sh.p_ready, 4);
-        mbar_init(&sh.zh_ready, kStateOnly ? 8 : 8 + 8);
+        mbar_init(&sh.zh_ready[0], kStateOnly ? 8 : 8 + 8);
+        mbar_init(&sh.zh_ready[1], 8);
         mbar_init(&sh.kv_done, 1);
         mbar_init(&sh.state_done, 1);
         mbar_init(&sh.o_done, 2);                                    // O1, O2
@@ -275,9 +276,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
     constexpr uint32_t tmem = 0;
     const uint32_t t_h = tmem, t_hb = t_h + dxp, t_zt = t_hb + dxp, t_s = t_zt + C, t_o1 = t_s + C, t_o2 = t_o1 + C;
     const Wait wait{A.wait_ns, &sh.abort_flag, A.status};
-    // Z's terms and the barrier of the state's products: a segment's own state has room for two chunks' terms (in the
-    // place of the state's), which take turns
+    // Z's terms, the barrier that says they are there and the one of the state's products: a segment's own state has room
+    // for two chunks' terms (in the place of the state's), which take turns.  So do their barriers: a warp may be one chunk
+    // ahead of another (those past the value columns have nothing to do), and its arrival must not count for the other's.
     auto zt_of = [&](int k) { return kStateOnly ? t_hb + (k & 1) * C : t_zt; };
+    auto zh_of = [&](int k) { return &sh.zh_ready[kStateOnly ? k & 1 : 0]; };
     auto kv_of = [&](int k) { return kStateOnly && (k & 1) ? &sh.s_done : &sh.kv_done; };
     auto chunk_of = [&](int k) { return (R.reverse != 0) != kStateOnly ? c1 - 1 - k : c0 + k; };
 
@@ -430,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             for (int k = 0; k < n; ++k, ring.next(A.stages)) {
                 const uint32_t sx = base + ring.s * A.stage_bytes;
                 if (!wait(&sh.ready[ring.s], ring.parity)) break;
-                if (!wait(&sh.zh_ready, k)) break;
+                if (!wait(zh_of(k), kStateOnly ? k / 2 : k)) break;
                 const uint32_t y = tc::desc_low(sx + off_y, kPanel);
                 if constexpr (!kStateOnly) {
                     // O2's region: the last chunk's has to be read
@@ -638,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             tc::fence_before();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&sh.zh_ready);
+                mbar_arrive(zh_of(k));
                 mbar_arrive(&sh.empty[ring.s]);
             }
         }
@@ -725,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             tc::fence_before();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&sh.zh_ready);
+                mbar_arrive(zh_of(k));
                 mbar_arrive(&sh.empty[ring.s]);
             }
         }
