@@ -17,6 +17,7 @@
 #include "es_attn.h"
 #include "es_device.cuh"
 #include "es_pairs.cuh"
+#include "es_segments.h"
 
 namespace es {
 namespace {
@@ -147,10 +148,9 @@ __global__ void __launch_bounds__(kThreads, XC == 2 ? 4 : XC == 4 ? 3 : 2) k_att
     const T* Wd = R.dots != nullptr ? static_cast<const T*>(R.w.p) + b * R.w.sb + (h / R.w.div) * R.w.sh + z0 : nullptr;
     const float* G = A.g != nullptr ? A.g + b * A.gb + h * A.gh : nullptr;
     // the segment's chunks [c0, c1) of the row's `chunks`, and whether they begin or end the run
-    const int64_t chunks = (len + C - 1) / C, c0 = seg * A.seg_chunks, c1 = chunks < c0 + A.seg_chunks ? chunks : c0 + A.seg_chunks;
-    const int last_seg = chunks > 0 ? static_cast<int>((chunks - 1) / A.seg_chunks) : 0;
-    const int64_t n_chunks = c1 > c0 ? c1 - c0 : 0;
-    const bool begins = R.reverse ? seg == last_seg : seg == 0, ends = R.reverse ? seg == 0 : seg == last_seg;
+    const int chunks = static_cast<int>((len + C - 1) / C);
+    const SegmentPart part = segment_part(seg, A.n_segs, static_cast<int>(A.seg_chunks), chunks, R.reverse != 0);
+    const int64_t c0 = part.c0, c1 = part.c1, n_chunks = c1 > c0 ? c1 - c0 : 0;
     float* dots = R.dots != nullptr ? R.dots + (slice * A.BH + bh) * A.T : nullptr;
     const int64_t out_at = b * R.ob + static_cast<int64_t>(h) * R.oh + z0;
     const bool store_f32 = R.out_f32 != 0;
@@ -160,8 +160,8 @@ __global__ void __launch_bounds__(kThreads, XC == 2 ? 4 : XC == 4 ? 3 : 2) k_att
     float* slots = A.n_segs > 1 ? A.seg_states + (blockIdx.z * A.BH + bh) * A.n_segs * R.dx * static_cast<int64_t>(R.dz) : nullptr;
     auto slot = [&](int s) { return slots + s * (R.dx * static_cast<int64_t>(R.dz)) + z0; };
     if constexpr (kStateOnly) {
-        if (seg > last_seg) return;
-        if (ends) {
+        if (seg > part.last) return;
+        if (part.ends) {
             // no successor: its place keeps the first state, which the last one may take the place of
             if (R.init != nullptr)
                 for (int e = tid; e < dx * ZS; e += kThreads)
@@ -172,8 +172,7 @@ __global__ void __launch_bounds__(kThreads, XC == 2 ? 4 : XC == 4 ? 3 : 2) k_att
         }
     }
     const float* from = nullptr;
-    if (A.n_segs > 1 && !kStateOnly && seg <= last_seg && (!begins || R.init != nullptr))
-        from = slot(begins ? (R.reverse ? 0 : last_seg) : R.reverse ? seg + 1 : seg - 1);
+    if (!kStateOnly && part.entry >= 0 && (!part.begins || R.init != nullptr)) from = slot(part.entry);
     for (int e = tid; e < dxp * ZS; e += kThreads) {
         const int a = e / ZS, c = e % ZS;
         float v = 0.0f;
@@ -401,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, XC == 2 ? 4 : XC == 4 ? 3 : 2) k_att
         for (int e = tid; e < dx * ZS; e += kThreads)
             if (e % ZS < nz) slot(seg)[(e / ZS) * static_cast<int64_t>(R.dz) + e % ZS] = sS[e];
         if (slice == 0 && tid == 0) A.seg_decays[(blockIdx.z * A.BH + bh) * A.n_segs + seg] = all_decay;
-    } else if (R.fin != nullptr && ends) {
+    } else if (R.fin != nullptr && part.ends) {
         for (int e = tid; e < dx * ZS; e += kThreads) {
             const int a = e / ZS, c = e % ZS;
             if (c < nz) R.fin[sbase + a * R.sa + (z0 + c) * R.sc] = sS[e] * R.fin_scale;

@@ -41,6 +41,7 @@
 // waited for (bounded too), and tensor memory is freed.
 #include "es_attn.h"
 #include "es_device.cuh"
+#include "es_segments.h"
 #include "es_tcgen05.cuh"
 
 namespace es {
@@ -218,15 +219,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
     }
     // the segment's chunks [c0, c1) and whether they begin or end the run
     const int chunks = static_cast<int>((len + C - 1) / C);
-    const int c0 = seg * A.seg_chunks;
-    const int c1 = min(chunks, c0 + A.seg_chunks);
-    const int last_seg = chunks > 0 ? (chunks - 1) / A.seg_chunks : 0;
-    const int n = max(0, c1 - c0);
-    const bool begins = R.reverse ? seg == last_seg : seg == 0;
-    const bool ends = R.reverse ? seg == 0 : seg == last_seg;
+    const SegmentPart part = segment_part(seg, A.n_segs, A.seg_chunks, chunks, R.reverse != 0);
+    const int c0 = part.c0, c1 = part.c1, n = max(0, c1 - c0);
     if constexpr (kStateOnly) {
-        if (seg > last_seg) return;
-        if (ends) {
+        if (seg > part.last) return;
+        if (part.ends) {
             // No successor: its place keeps the initial state, which the main pass may find overwritten
             // (the last state may take its place) before its first segment reads it.
             if (R.init != nullptr) {
@@ -657,17 +654,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         int64_t fa = 0;
         float fs = 1.0f;
         if (real && !kStateOnly) {
-            if (begins && A.n_segs > 1) {
-                if (R.init != nullptr)
-                    from = A.seg_states + blockIdx.y * A.seg_stride + (bh * A.n_segs + (R.reverse ? 0 : last_seg)) * size + c;
-                fa = R.dz;
-            } else if (begins) {
+            if (A.n_segs == 1) {
                 if (R.init != nullptr) from = R.init + bh * size + c * R.sc;
                 fa = R.sa;
                 fs = R.init_scale;
-            } else {
-                const int prev = R.reverse ? seg + 1 : seg - 1;
-                from = A.seg_states + blockIdx.y * A.seg_stride + (bh * A.n_segs + prev) * size + c;
+            } else if (part.entry >= 0 && (!part.begins || R.init != nullptr)) {
+                from = A.seg_states + blockIdx.y * A.seg_stride + (bh * A.n_segs + part.entry) * size + c;
                 fa = R.dz;
             }
         }
@@ -742,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             if (on && kStateOnly)
                 state_out(t_h + lanes, a_lo, min(a_hi, R.dx),
                           real ? A.seg_states + blockIdx.y * A.seg_stride + (bh * A.n_segs + seg) * size + c : nullptr, R.dz, 1.0f);
-            else if (on && ends && R.fin != nullptr)
+            else if (on && part.ends && R.fin != nullptr)
                 state_out(t_h + lanes, a_lo, min(a_hi, R.dx), real ? R.fin + bh * size + c * R.sc : nullptr, R.sa, R.fin_scale);
         }
     } else {
