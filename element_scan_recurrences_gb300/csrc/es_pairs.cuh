@@ -1,4 +1,5 @@
-// es_pairs.cuh -- two f32 operations an instruction (sm_100 and later).
+// es_pairs.cuh -- two f32 operations an instruction (sm_100 and later), and sums
+// held in two floats.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -31,6 +32,13 @@ __device__ __forceinline__ float2 pair_fma(float2 a, float2 b, float2 c) {
         : "=f"(r.x), "=f"(r.y)
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
     return r;
+}
+
+// a + b rounded, and what the rounding lost, exactly (Knuth's two-sum)
+__device__ __forceinline__ float two_sum(float a, float b, float& lost) {
+    const float s = a + b, of_b = s - a;
+    lost = (a - (s - of_b)) + (b - of_b);
+    return s;
 }
 
 }  // namespace es

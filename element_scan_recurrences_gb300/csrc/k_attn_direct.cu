@@ -10,10 +10,13 @@
 //     out_i  = sum_{j<=i} e^{G_i-G_j} (x_i.y_j) z_j + e^{G_i} x_i state
 //     state' = e^{G_C} state + sum_j e^{G_C-G_j} y_j z_j^T
 //
-// (reversed: j >= i, e^{G_j-G_i}, and the two chunk coefficients swapped).  A
-// log decay below -104 makes e^g zero in f32: such a token starts a new group
-// and contributes nothing to G, so the sums of later tokens keep their
-// precision and a decay of -inf needs no other care.
+// (reversed: j >= i, e^{G_j-G_i}, and the two chunk coefficients swapped).  G
+// is held as two floats, the second what the first lost: after a few strong
+// decays it is in the thousands, while the weights that count are those between
+// later tokens some hundredths apart (in one float, half of the tokens at -100:
+// results off by 3e-5 instead of 1e-7).  A log decay below -104 makes e^g zero
+// in f32: such a token starts a new group and contributes nothing to G, so a
+// decay of -inf needs no other care.
 #include "es_attn.h"
 #include "es_device.cuh"
 #include "es_pairs.cuh"
@@ -27,13 +30,6 @@ constexpr int ZS = kAttnSlice;
 constexpr int kThreads = 128;
 constexpr int kPLd = C + 4;          // rows of P: on 16 bytes
 constexpr int kAnchorChunks = kAttnAnchorTokens / C;
-
-// 2^v, 2 ulp: what the exponentials cost beside the sums' own roundings
-__device__ __forceinline__ float exp2_approx(float v) {
-    float r;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
-}
 
 template <typename T>
 __device__ __forceinline__ float to_f32(T v) {
@@ -131,8 +127,9 @@ __global__ void __launch_bounds__(kThreads, XC == 2 ? 4 : XC == 4 ? 3 : 2) k_att
     float* sZ = sS + dxp * ZS;            // [C][ZS]
     float* sU = sZ + C * ZS;              // z scaled by its chunk coefficient
     float* sP = sU + C * ZS;              // [C][kPLd]
-    float* sG = sP + C * kPLd;            // G, and per token: coefficient of the read, of the update
-    float* sRead = sG + C;
+    float* sG = sP + C * kPLd;            // G and what it lost, and per token: coefficient of the read, of the update
+    float* sGl = sG + C;
+    float* sRead = sGl + C;
     float* sUpd = sRead + C;
     int* sLo = reinterpret_cast<int*>(sUpd + C);    // first token of the group of token i
     float* sDecay = reinterpret_cast<float*>(sLo + C);
@@ -273,25 +270,30 @@ __global__ void __launch_bounds__(kThreads, XC == 2 ? 4 : XC == 4 ? 3 : 2) k_att
             float g = cur_g;
             if constexpr (XC == 0) g = G != nullptr && tid < n ? G[(t0 + tid) * A.gt] : 0.0f;
             const bool cut = g < -104.0f;
-            g = cut ? 0.0f : g * 1.4426950408889634f;
-            float pre = g, nxt = __shfl_down_sync(0xffffffffu, g, 1);
+            g = cut ? 0.0f : g;
+            float pre = g, low = 0.0f, nxt = __shfl_down_sync(0xffffffffu, g, 1);
             float suf = tid == 31 ? 0.0f : nxt;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const float p = __shfl_up_sync(0xffffffffu, pre, o);
+                const float p = __shfl_up_sync(0xffffffffu, pre, o), pl = __shfl_up_sync(0xffffffffu, low, o);
                 const float q = __shfl_down_sync(0xffffffffu, suf, o);
-                if (tid >= o) pre += p;
+                if (tid >= o) {
+                    float lost;
+                    pre = two_sum(pre, p, lost);
+                    low += pl + lost;
+                }
                 if (tid + o < 32) suf += q;
             }
             const unsigned cuts = __ballot_sync(0xffffffffu, cut);
             const unsigned upto = cuts & (0xffffffffu >> (31 - tid));
             const unsigned after = tid == 31 ? 0u : cuts >> (tid + 1);
             sG[tid] = pre;
+            sGl[tid] = low;
             sLo[tid] = upto ? 31 - __clz(upto) : 0;
-            const float er = upto ? 0.0f : exp2_approx(pre), eu = after ? 0.0f : exp2_approx(suf);
+            const float er = upto ? 0.0f : expf(pre), eu = after ? 0.0f : expf(suf);
             sRead[tid] = R.reverse ? eu : er;
             sUpd[tid] = R.reverse ? er : eu;
-            if (tid == 31) *sDecay = cuts ? 0.0f : exp2_approx(pre);
+            if (tid == 31) *sDecay = cuts ? 0.0f : expf(pre);
         }
         __syncthreads();
         // x_i . y_j with its decay: thread (ty, tx) rows ty + 8r, columns tx, tx + 16
@@ -321,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, XC == 2 ? 4 : XC == 4 ? 3 : 2) k_att
                     const int i = ty + 8 * r, j = tx + 16 * c;
                     const int late = R.reverse ? j : i, early = R.reverse ? i : j;
                     const bool in = early <= late && early >= sLo[late];
-                    sP[i * kPLd + j] = in ? (s[r][c].x + s[r][c].y) * exp2_approx(sG[late] - sG[early]) : 0.0f;
+                    sP[i * kPLd + j] = in ? (s[r][c].x + s[r][c].y) * expf((sG[late] - sG[early]) + (sGl[late] - sGl[early])) : 0.0f;
                 }
         }
         for (int e = tid; e < C * ZS; e += kThreads) sU[e] = sZ[e] * sUpd[e / ZS];
@@ -600,7 +602,7 @@ __global__ void __launch_bounds__(256) k_attn_fold(const __grid_constant__ AttnF
 
 size_t direct_smem(int dx) {
     const size_t dxp = (dx + 3) & ~3;
-    return sizeof(float) * (2 * C * (dxp + 4) + dxp * ZS + 2 * C * ZS + C * kPLd + 4 * C + 4);
+    return sizeof(float) * (2 * C * (dxp + 4) + dxp * ZS + 2 * C * ZS + C * kPLd + 5 * C + 4);
 }
 
 }  // namespace

@@ -56,11 +56,21 @@ constexpr uint32_t kTmemCols = 512;
 
 struct alignas(16) Coef {
     float g2[C];                              // inclusive sums of the log decays, base 2
+    float low[C];                             // what they lost to rounding
     float read[C], upd[C];
     int bound[C];                             // forward: the first token row i sees; reversed: the last
     float decay;
-    float pad[3];
+    int wide;                                 // the sums are so large that what they lost counts
+    float pad[2];
 };
+
+// Half of an ulp of a sum below 32 is 2^-20, and a weight is off by a few of them: less
+// than the 2^-16 to which P is kept.  Above (half of the tokens at -100: 2^-12) the
+// weights take the sums' second floats too.  With the decays' gradient only there
+// (8 x 4096 x 16 x 128 both ways 762 us, for every chunk 769); without it for every
+// chunk, which is the faster way round by the code it leaves (65536 tokens x 16 heads of
+// 128 384 us, 391 with a branch).
+constexpr float kWideSum = 32.0f;
 
 struct TcRun {
     CUtensorMap x, y, z, w;
@@ -343,20 +353,30 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             const float2 next = load(k + 1);
             const bool cut0 = g.x < -104.0f, cut1 = g.y < -104.0f;
             const float v0 = cut0 ? 0.0f : g.x * 1.4426950408889634f, v1 = cut1 ? 0.0f : g.y * 1.4426950408889634f;
-            // inclusive sums of the pairs before, exclusive sums of the pairs after
-            float pre = v0 + v1, suf = pre;
+            // inclusive sums of the pairs before (and what they lose), exclusive sums of the pairs after
+            float lost;
+            float pre = two_sum(v0, v1, lost), low = lost, suf = pre;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const float p = __shfl_up_sync(0xffffffffu, pre, o);
+                const float p = __shfl_up_sync(0xffffffffu, pre, o), pl = __shfl_up_sync(0xffffffffu, low, o);
                 const float q = __shfl_down_sync(0xffffffffu, suf, o);
-                if (lane >= o) pre += p;
+                if (lane >= o) {
+                    if constexpr (kStateOnly) {
+                        pre += p;
+                    } else {
+                        pre = two_sum(pre, p, lost);
+                        low += pl + lost;
+                    }
+                }
                 if (lane + o < 32) suf += q;
             }
             const float whole = __shfl_sync(0xffffffffu, pre, 31);
             float before = __shfl_up_sync(0xffffffffu, pre, 1), after = __shfl_down_sync(0xffffffffu, suf, 1);
-            if (lane == 0) before = 0.0f;
+            float before_low = __shfl_up_sync(0xffffffffu, low, 1);
+            if (lane == 0) before = before_low = 0.0f;
             if (lane == 31) after = 0.0f;
-            const float2 g2 = make_float2(before + v0, pre);
+            const float2 g2 = make_float2(two_sum(before, v0, lost), pre);
+            const float2 g2_low = make_float2(before_low + lost, low);
             float2 from_start = make_float2(tc::exp2_approx(g2.x), tc::exp2_approx(g2.y));
             float2 to_end = make_float2(tc::exp2_approx(after + v1), tc::exp2_approx(after));
             float decay = tc::exp2_approx(whole);
@@ -391,11 +411,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             all *= decay;
             if (k >= A.stages && !wait(&sh.empty[ring.s], ring.parity ^ 1)) break;
             Coef& c = sh.coef[ring.s];
-            *reinterpret_cast<float2*>(&c.g2[2 * lane]) = g2;
+            if constexpr (!kStateOnly) {
+                *reinterpret_cast<float2*>(&c.g2[2 * lane]) = g2;
+                *reinterpret_cast<float2*>(&c.low[2 * lane]) = g2_low;
+            }
             *reinterpret_cast<float2*>(&c.read[2 * lane]) = R.reverse ? to_end : from_start;
             *reinterpret_cast<float2*>(&c.upd[2 * lane]) = R.reverse ? from_start : to_end;
             *reinterpret_cast<int2*>(&c.bound[2 * lane]) = bound;
-            if (lane == 0) c.decay = decay;
+            if (lane == 0) {
+                c.decay = decay;
+                c.wide = !(fabsf(whole) < kWideSum);
+            }
             if (!wait(&sh.full[ring.s], ring.parity)) break;
             const int left = static_cast<int>(min(static_cast<int64_t>(C), len - static_cast<int64_t>(chunk_of(k)) * C));
             if (left < C) {
@@ -534,8 +560,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                     }
                 } else {
                     tc::fence_after();
-                    const float gs = sign * c.g2[i];
-                    const int bound = c.bound[i];
+                    const float gs = sign * c.g2[i], gs_low = sign * c.low[i];
+                    const int bound = c.bound[i], wide = c.wide;
                     // the half's columns that row i sees, as bits
                     const int first = max(0, (R.reverse ? i : bound) - 32 * half), last = min(31, (R.reverse ? bound : i) - 32 * half);
                     const uint32_t seen = first <= last ? (0xffffffffu >> (31 - (last - first))) << first : 0u;
@@ -549,8 +575,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
 #pragma unroll
                         for (int e = 0; e < 4; e += 2) {
                             const float4 gj = *reinterpret_cast<const float4*>(&c.g2[j0 + 2 * e]);
-                            const float2 x = pair_fma(make_float2(gj.x, gj.y), make_float2(-sign, -sign), make_float2(gs, gs));
-                            const float2 y = pair_fma(make_float2(gj.z, gj.w), make_float2(-sign, -sign), make_float2(gs, gs));
+                            float2 x = pair_fma(make_float2(gj.x, gj.y), make_float2(-sign, -sign), make_float2(gs, gs));
+                            float2 y = pair_fma(make_float2(gj.z, gj.w), make_float2(-sign, -sign), make_float2(gs, gs));
+                            if (!kDots || wide) {
+                                const float4 lj = *reinterpret_cast<const float4*>(&c.low[j0 + 2 * e]);
+                                x = pair_add(x, pair_fma(make_float2(lj.x, lj.y), make_float2(-sign, -sign), make_float2(gs_low, gs_low)));
+                                y = pair_add(y, pair_fma(make_float2(lj.z, lj.w), make_float2(-sign, -sign), make_float2(gs_low, gs_low)));
+                            }
                             d[e] = make_float2(tc::exp2_approx(x.x), tc::exp2_approx(x.y));
                             d[e + 1] = make_float2(tc::exp2_approx(y.x), tc::exp2_approx(y.y));
                         }
