@@ -547,8 +547,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             Ring ring;
 #pragma unroll 1
             for (int k = 0; k < n; ++k, ring.next(A.stages)) {
-                // (the products waited for the stage, so its coefficients are there)
-                if (!wait(&sh.s_done, k)) break;
+                // the stage's coefficients, then the scores
+                if (!wait(&sh.ready[ring.s], ring.parity) || !wait(&sh.s_done, k)) break;
                 const Coef& c = sh.coef[ring.s];
                 const uint32_t swz = i & 7;
                 if (none) {
@@ -785,8 +785,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             Ring ring;
 #pragma unroll 1
             for (int k = 0; k < n; ++k, ring.next(A.stages)) {
-                // (the products waited for the stage, so what came with it is there)
-                if (!wait(&sh.o_done, k)) break;
+                // the stage's coefficients (and W), then the products
+                if (!wait(&sh.ready[ring.s], ring.parity) || !wait(&sh.o_done, k)) break;
                 tc::fence_after();
                 const int64_t t0 = static_cast<int64_t>(chunk_of(k)) * C;
                 const int left = static_cast<int>(min(static_cast<int64_t>(C), len - t0));
