@@ -19,14 +19,17 @@ struct AttnOperand {
 
 // One run of the recurrence over the sequences of a call:
 //
-//     state[t] = e^{g[t]} state[t-1] + y[t] z[t]^T,   out[t] = out_scale * x[t] state[t]
+//     state[t] = e^{g[t]} state[t-1] + u y[t] z[t]^T,   out[t] = r x[t] state[t]
 //
 // or, reversed, from the last token to the first,
 //
-//     state[t] = e^{g[t+1]} state[t+1] + y[t] z[t]^T, out[t] = out_scale * x[t] state[t]
+//     state[t] = e^{g[t+1]} state[t+1] + u y[t] z[t]^T, out[t] = r x[t] state[t]
 //
-// with a state of dx x dz values.  The forward pass is one run (x, y, z) =
-// (q, k, v); the gradients are three more over the same data:
+// with a state of dx x dz values.  u and r are update_scale and read_scale, one
+// of them the call's scale (out_scale, their product) and the other one: the
+// states are then the ones that the call takes and gives, at any scale.
+// The forward pass is one run (x, y, z) = (q, k, v); the gradients are three
+// more over the same data:
 //     grad_q  forward  (grad_out, v, k),  the state transposed
 //     grad_v  reversed (k, q, grad_out)
 //     grad_k  reversed (v, grad_out, q),  the state transposed
@@ -38,7 +41,7 @@ struct AttnRun {
     const float* init;           // value (a, c) of the state of (b, h) at [(b*H + h)*dx*dz + a*sa + c*sc], or null (zero)
     float* fin;                  // state after the last trip, the same layout, or null
     int64_t sa, sc;
-    float init_scale, fin_scale, out_scale;
+    float update_scale, read_scale, out_scale;
     int reverse;
     int state_result;            // the run's last state can be asked for (its results do not depend on whether it is)
     // For the decays' gradient: out[t] (unrounded) . w[t], per slice of dz
@@ -105,8 +108,8 @@ cudaError_t launch_attn_join(const AttnLaunch& L, int chunk);
 
 // The decays' gradient from the two runs' dots and states: for each token t of
 // anchor block m, sum over s >= t of the block of (dq[s] - dk[s]) + e[m], with
-// e[m] = scale <state_q, state_k> at the block's end, corrected in proportion
-// so that it meets e[m - 1] at the block's start.
+// e[m] = <state_q, state_k> at the block's end, corrected in proportion so that
+// it meets e[m - 1] at the block's start.
 struct AttnDecayGrad {
     const float* dots_q;         // [slices, B*H, T]
     const float* dots_k;
@@ -115,7 +118,6 @@ struct AttnDecayGrad {
     const float* initial;        // [B*H, size]: the first state and its gradient, or null
     const float* grad_initial;
     float* ends;                 // [B*H, n + 1]: e[-1], e[0], ..
-    float scale;
     int slices;
     int64_t size;
     int64_t B, T;

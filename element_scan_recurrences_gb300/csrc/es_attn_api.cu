@@ -240,8 +240,8 @@ es_status plan_attn(const char* fn, const es_linear_attention_args* a, const es_
         f.fin = a->final_state;
         f.sa = dv;
         f.sc = 1;
-        f.init_scale = f.fin_scale = 1.0f;
-        f.out_scale = scale;
+        f.update_scale = 1.0f;
+        f.read_scale = f.out_scale = scale;
         f.state_result = 1;
         f.dx = static_cast<int>(dk);
         f.dz = static_cast<int>(dv);
@@ -260,21 +260,22 @@ es_status plan_attn(const char* fn, const es_linear_attention_args* a, const es_
             r.oh = o.stride_h;
             r.sa = turned ? 1 : dv;
             r.sc = turned ? dv : 1;
-            r.out_scale = scale;
+            r.update_scale = 1.0f;
+            r.read_scale = r.out_scale = scale;
             r.dx = static_cast<int>(dx);
             r.dz = static_cast<int>(dz);
         };
         fill(rq, go, v, k, g->grad_q, dv, dk, true);
         rq.init = a->initial_state;
-        rq.init_scale = 1.0f;
         fill(rv, k, q, go, g->grad_v, dk, dv, false);
         fill(rk, v, go, q, g->grad_k, dv, dk, true);
         rv.reverse = rk.reverse = 1;
         rv.init = rk.init = g->grad_final_state;
-        rv.init_scale = rk.init_scale = 1.0f / scale;
+        // the states of these are the gradients of the states
+        rv.update_scale = rk.update_scale = scale;
+        rv.read_scale = rk.read_scale = 1.0f;
         rv.fin = g->grad_initial_state;
         rv.state_result = 1;
-        rv.fin_scale = scale;
     }
     // the path: every run's operands have to suit the tensor-core kernel's loads
     bool tensor = L.bf16 && T > 0 && !step;
@@ -422,7 +423,6 @@ es_status run_backward(const char* fn, const es_linear_attention_args* a, const 
         D.initial = a->initial_state;
         D.grad_initial = g->grad_initial_state;
         D.ends = reinterpret_cast<float*>(ws + P.ends);
-        D.scale = rk.out_scale;
         D.slices = P.slices_k;
         D.size = static_cast<int64_t>(dk) * dv;
         D.B = L.B;

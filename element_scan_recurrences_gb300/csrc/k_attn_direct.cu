@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, XC == 2 ? 4 : XC == 4 ? 3 : 2) k_att
                 for (int e = tid; e < dx * ZS; e += kThreads)
                     if (e % ZS < nz)
                         slot(seg)[(e / ZS) * static_cast<int64_t>(R.dz) + e % ZS] =
-                            R.init[sbase + (e / ZS) * R.sa + (z0 + e % ZS) * R.sc] * R.init_scale;
+                            R.init[sbase + (e / ZS) * R.sa + (z0 + e % ZS) * R.sc];
             return;
         }
     }
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, XC == 2 ? 4 : XC == 4 ? 3 : 2) k_att
         float v = 0.0f;
         if (!kStateOnly && a < dx && c < nz) {
             if (from != nullptr) v = from[a * static_cast<int64_t>(R.dz) + c];
-            else if (A.n_segs == 1 && R.init != nullptr) v = R.init[sbase + a * R.sa + (z0 + c) * R.sc] * R.init_scale;
+            else if (A.n_segs == 1 && R.init != nullptr) v = R.init[sbase + a * R.sa + (z0 + c) * R.sc];
         }
         sS[e] = v;
     }
@@ -291,8 +291,8 @@ __global__ void __launch_bounds__(kThreads, XC == 2 ? 4 : XC == 4 ? 3 : 2) k_att
             sGl[tid] = low;
             sLo[tid] = upto ? 31 - __clz(upto) : 0;
             const float er = upto ? 0.0f : expf(pre), eu = after ? 0.0f : expf(suf);
-            sRead[tid] = R.reverse ? eu : er;
-            sUpd[tid] = R.reverse ? er : eu;
+            sRead[tid] = (R.reverse ? eu : er) * R.read_scale;
+            sUpd[tid] = (R.reverse ? er : eu) * R.update_scale;
             if (tid == 31) *sDecay = cuts ? 0.0f : expf(pre);
         }
         __syncthreads();
@@ -323,7 +323,8 @@ __global__ void __launch_bounds__(kThreads, XC == 2 ? 4 : XC == 4 ? 3 : 2) k_att
                     const int i = ty + 8 * r, j = tx + 16 * c;
                     const int late = R.reverse ? j : i, early = R.reverse ? i : j;
                     const bool in = early <= late && early >= sLo[late];
-                    sP[i * kPLd + j] = in ? (s[r][c].x + s[r][c].y) * expf((sG[late] - sG[early]) + (sGl[late] - sGl[early])) : 0.0f;
+                    const float w = expf((sG[late] - sG[early]) + (sGl[late] - sGl[early])) * R.out_scale;
+                    sP[i * kPLd + j] = in ? (s[r][c].x + s[r][c].y) * w : 0.0f;
                 }
         }
         for (int e = tid; e < C * ZS; e += kThreads) sU[e] = sZ[e] * sUpd[e / ZS];
@@ -371,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, XC == 2 ? 4 : XC == 4 ? 3 : 2) k_att
                 float dot = 0.0f;
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const float v = (c ? o[r].y : o[r].x) * R.out_scale;
+                    const float v = c ? o[r].y : o[r].x;
                     const int zc = 2 * tx + c;
                     if (i < n && zc < nz) {
                         const int64_t at = out_at + (t0 + i) * R.ot + zc;
@@ -405,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, XC == 2 ? 4 : XC == 4 ? 3 : 2) k_att
     } else if (R.fin != nullptr && part.ends) {
         for (int e = tid; e < dx * ZS; e += kThreads) {
             const int a = e / ZS, c = e % ZS;
-            if (c < nz) R.fin[sbase + a * R.sa + (z0 + c) * R.sc] = sS[e] * R.fin_scale;
+            if (c < nz) R.fin[sbase + a * R.sa + (z0 + c) * R.sc] = sS[e];
         }
     }
 }
@@ -480,7 +481,7 @@ __global__ void __launch_bounds__(256) k_attn_state_products(const __grid_consta
         float all = 0.0f;
 #pragma unroll
         for (int w = 0; w < 8; ++w) all += part[w];
-        G.ends[blockIdx.x] = m >= 0 ? all * G.scale : all;
+        G.ends[blockIdx.x] = all;
     }
 }
 

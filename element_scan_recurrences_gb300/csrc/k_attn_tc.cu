@@ -28,7 +28,7 @@
 //                                     rows innermost
 //     O2^T[c, i] = H^T X^T            A = the state's terms, B = X
 //     O1^T[c, i] = Z^T P^T            A = Z rows innermost, B = P
-//     out_i      = scale (O1_i + read_i O2_i)
+//     out_i      = scale O1_i + read_i O2_i      (the scale of O2 in read)
 //
 // Precision: bf16 operands go in as they are.  Every f32 factor is split into
 // bf16 terms that are multiplied in turn and summed in f32: P and the state as
@@ -79,7 +79,7 @@ struct TcRun {
     const float* init;
     float* fin;
     int64_t sa, sc;
-    float init_scale, fin_scale, out_scale;
+    float update_scale, read_scale, out_scale;
     float* dots;
     float* anchors;
     int xdiv, ydiv, zdiv, wdiv;
@@ -192,9 +192,9 @@ __device__ __forceinline__ void arrive_warp(uint64_t* bar, int lane) {
     if (lane == 0) mbar_arrive(bar);
 }
 
-// Columns [lo, hi) of the warp's lanes of the state, scaled, to `to` (one value
-// column; null: none) and on every `stride` floats.
-__device__ __noinline__ void state_out(uint32_t state, int lo, int hi, float* to, int64_t stride, float scale) {
+// Columns [lo, hi) of the warp's lanes of the state to `to` (one value column;
+// null: none) and on every `stride` floats.
+__device__ __noinline__ void state_out(uint32_t state, int lo, int hi, float* to, int64_t stride) {
 #pragma unroll 1
     for (int a0 = lo; a0 < hi; a0 += 8) {
         uint32_t r[8];
@@ -203,7 +203,7 @@ __device__ __noinline__ void state_out(uint32_t state, int lo, int hi, float* to
         tc::loaded(r);
         if (to != nullptr) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) to[(a0 + e) * stride] = __uint_as_float(r[e]) * scale;
+            for (int e = 0; e < 8; ++e) to[(a0 + e) * stride] = __uint_as_float(r[e]);
         }
     }
 }
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 const int64_t size = static_cast<int64_t>(R.dx) * R.dz;
                 float* to = A.seg_states + blockIdx.y * A.seg_stride + (bh * A.n_segs + seg) * size;
                 for (int64_t e = threadIdx.x; e < size; e += kThreads)
-                    to[e] = R.init[bh * size + e / R.dz * R.sa + e % R.dz * R.sc] * R.init_scale;
+                    to[e] = R.init[bh * size + e / R.dz * R.sa + e % R.dz * R.sc];
             }
             return;
         }
@@ -415,8 +415,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                 *reinterpret_cast<float2*>(&c.g2[2 * lane]) = g2;
                 *reinterpret_cast<float2*>(&c.low[2 * lane]) = g2_low;
             }
-            *reinterpret_cast<float2*>(&c.read[2 * lane]) = R.reverse ? to_end : from_start;
-            *reinterpret_cast<float2*>(&c.upd[2 * lane]) = R.reverse ? from_start : to_end;
+            const float2 read = R.reverse ? to_end : from_start, upd = R.reverse ? from_start : to_end;
+            *reinterpret_cast<float2*>(&c.read[2 * lane]) = pair_mul(read, make_float2(R.read_scale, R.read_scale));
+            *reinterpret_cast<float2*>(&c.upd[2 * lane]) = pair_mul(upd, make_float2(R.update_scale, R.update_scale));
             *reinterpret_cast<int2*>(&c.bound[2 * lane]) = bound;
             if (lane == 0) {
                 c.decay = decay;
@@ -683,12 +684,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         // where the run's first state comes from
         const float* from = nullptr;
         int64_t fa = 0;
-        float fs = 1.0f;
         if (real && !kStateOnly) {
             if (A.n_segs == 1) {
                 if (R.init != nullptr) from = R.init + bh * size + c * R.sc;
                 fa = R.sa;
-                fs = R.init_scale;
             } else if (part.entry >= 0 && (!part.begins || R.init != nullptr)) {
                 from = A.seg_states + blockIdx.y * A.seg_stride + (bh * A.n_segs + part.entry) * size + c;
                 fa = R.dz;
@@ -698,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
         auto keep = [&](int at) {
             if ((at + 1) % kAnchorChunks == 0 || at == chunks - 1)
                 state_out(t_h + lanes, a_lo, min(a_hi, R.dx), real ? R.anchors + (bh * A.n_anchors + at / kAnchorChunks) * size + c : nullptr,
-                          R.dz, 1.0f);
+                          R.dz);
         };
         if (on && !kStateOnly) {
             // 32 loads in flight: a short sequence is mostly this and the way in and out
@@ -711,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                     const float* p = from + a0 * fa;
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
-                        if (a0 + e < R.dx) r[e] = __float_as_uint(p[e * fa] * fs);
+                        if (a0 + e < R.dx) r[e] = __float_as_uint(p[e * fa]);
                 }
                 tc::st(t_h + lanes + a0, r);
             }
@@ -764,9 +763,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
             if (anchored && !R.reverse && n > 0) keep(chunk_of(n - 1));
             if (on && kStateOnly)
                 state_out(t_h + lanes, a_lo, min(a_hi, R.dx),
-                          real ? A.seg_states + blockIdx.y * A.seg_stride + (bh * A.n_segs + seg) * size + c : nullptr, R.dz, 1.0f);
+                          real ? A.seg_states + blockIdx.y * A.seg_stride + (bh * A.n_segs + seg) * size + c : nullptr, R.dz);
             else if (on && part.ends && R.fin != nullptr)
-                state_out(t_h + lanes, a_lo, min(a_hi, R.dx), real ? R.fin + bh * size + c * R.sc : nullptr, R.sa, R.fin_scale);
+                state_out(t_h + lanes, a_lo, min(a_hi, R.dx), real ? R.fin + bh * size + c * R.sc : nullptr, R.sa);
         }
     } else {
         // ---- outputs: lane = value column c, tokens along the columns
@@ -819,9 +818,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const __grid_constant__
                         for (int m = 0; m < 4; ++m) {
                             const uint32_t* x1 = &o1[m / 2][2 * (m & 1)];
                             const uint32_t* x2 = &o2[m / 2][2 * (m & 1)];
-                            v[m] = pair_mul(pair_fma(make_float2(__uint_as_float(x2[0]), __uint_as_float(x2[1])), r,
-                                                     make_float2(__uint_as_float(x1[0]), __uint_as_float(x1[1]))),
-                                            scale);
+                            v[m] = pair_fma(make_float2(__uint_as_float(x2[0]), __uint_as_float(x2[1])), r,
+                                            pair_mul(make_float2(__uint_as_float(x1[0]), __uint_as_float(x1[1])), scale));
                         }
                         const uint32_t at = smem_u32(st) + at0 + 8 * q * 128;
                         const int row = 32 * side + 8 * q + 2 * (lane % 4);
@@ -954,8 +952,8 @@ cudaError_t launch_attn_tc(const AttnLaunch& L, int* kernels, const char** err) 
         t.fin = f.fin;
         t.sa = f.sa;
         t.sc = f.sc;
-        t.init_scale = f.init_scale;
-        t.fin_scale = f.fin_scale;
+        t.update_scale = f.update_scale;
+        t.read_scale = f.read_scale;
         t.out_scale = f.out_scale;
         t.dots = f.dots;
         any_dots = any_dots || f.dots != nullptr;
