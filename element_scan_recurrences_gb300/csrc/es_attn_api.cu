@@ -37,16 +37,26 @@ bool overlap(const Span& a, const Span& b) {
 }
 
 // Two views with the same batch and token strides whose tokens' rows lie side
-// by side (as the parts of one fused projection do) share no element.
-bool side_by_side(const es_heads& a, const es_heads& b, int64_t da, int64_t db, int64_t size, int64_t T) {
-    if (a.stride_t != b.stride_t || a.stride_b != b.stride_b || a.stride_t <= 0) return false;
-    if (a.stride_b < a.stride_t * T) return false;
+// by side (as the parts of one fused projection do) share no element.  The
+// stride of an axis with one entry means nothing; of two axes, one has to hold
+// the other's entries whole, in either order.
+bool side_by_side(const es_heads& a, const es_heads& b, int64_t da, int64_t db, int64_t size, int64_t B, int64_t T) {
+    int64_t period = INT64_MAX;           // elements from one token's row to the next
+    if (T > 1) {
+        if (a.stride_t != b.stride_t) return false;
+        period = a.stride_t;
+    }
+    if (B > 1) {
+        if (a.stride_b != b.stride_b) return false;
+        if (T > 1 && (a.stride_b >= a.stride_t ? a.stride_b < a.stride_t * T : a.stride_t < a.stride_b * B)) return false;
+        period = a.stride_b < period ? a.stride_b : period;
+    }
     const int64_t wa = (a.heads - 1) * a.stride_h + da, wb = (b.heads - 1) * b.stride_h + db;
     int64_t d = static_cast<int64_t>(reinterpret_cast<uintptr_t>(a.data) - reinterpret_cast<uintptr_t>(b.data));
     if (d % size != 0) return false;
     d /= size;
-    if (d >= 0) return d >= wb && d + wa <= a.stride_t;
-    return -d >= wa && -d + wb <= a.stride_t;
+    if (d >= 0) return d >= wb && d <= period - wa;
+    return -d >= wa && -d <= period - wb;
 }
 
 es_status check_view(const char* fn, const char* name, const es_heads& v, int64_t B, int64_t T, int64_t dim, int64_t size,
@@ -534,17 +544,17 @@ es_status plan_rotate(const char* fn, const es_qk_norm_rotate_args* a, const es_
         for (int j = 0; j < n_out; ++j)
             if (overlap(osp[i], out[j])) return api_fail(ES_E_ARG, "%s: `%s` overlaps `%s`", fn, on[i], out[j].name);
         for (int j = 0; j < 2; ++j) {
-            if (overlap(osp[i], xsp[j]) && !(i == j && same(*os[i], *xs[j])) && !side_by_side(*os[i], *xs[j], d, d, size, T))
+            if (overlap(osp[i], xsp[j]) && !(i == j && same(*os[i], *xs[j])) && !side_by_side(*os[i], *xs[j], d, d, size, B, T))
                 return api_fail(ES_E_ARG, "%s: `%s` overlaps `%s`", fn, on[i], xn[j]);
             if (backward && overlap(osp[i], gsp[j]) && !(i == j && same(*os[i], *gs[j])) &&
-                !side_by_side(*os[i], *gs[j], d, d, size, T))
+                !side_by_side(*os[i], *gs[j], d, d, size, B, T))
                 return api_fail(ES_E_ARG, "%s: `%s` overlaps `%s`", fn, on[i], gn[j]);
             for (int o = 0; o < n_out; ++o)
                 if (overlap(out[o], xsp[j]) || (backward && overlap(out[o], gsp[j])))
                     return api_fail(ES_E_ARG, "%s: `%s` overlaps an input", fn, out[o].name);
         }
     }
-    if (overlap(osp[0], osp[1]) && !side_by_side(*os[0], *os[1], d, d, size, T))
+    if (overlap(osp[0], osp[1]) && !side_by_side(*os[0], *os[1], d, d, size, B, T))
         return api_fail(ES_E_ARG, "%s: `%s` overlaps `%s`", fn, on[0], on[1]);
 
     *P = RotatePlan{};
