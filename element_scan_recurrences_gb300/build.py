@@ -7,12 +7,15 @@ time, so the library loads on machines without a GPU driver as well) and
 NVRTC, which compiles body programs at run time.  The headers NVRTC needs are
 embedded into the library as text (``write_jit_headers``).  Beside it
 ``_build/es_torch.so``, a Python module that marshals the sequence operators'
-tensors, is compiled against the installed PyTorch.
+tensors, is compiled against the installed PyTorch and again when that changes;
+without PyTorch there is libes.so alone, and what goes wrong with the module
+leaves libes.so built.
 """
 from __future__ import annotations
 
 import concurrent.futures
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -27,6 +30,7 @@ LIB = os.path.join(BUILD, "libes.so")
 # the tensor marshalling of the sequence operators (a Python module over libes.so and PyTorch)
 TORCH_SRC = os.path.join(CSRC, "torch", "es_torch.cpp")
 TORCH_LIB = os.path.join(BUILD, "es_torch.so")
+TORCH_STAMP = TORCH_LIB + ".built_for"
 
 GEN = os.path.join(BUILD, "gen")
 
@@ -86,14 +90,41 @@ def write_jit_headers() -> str:
 
 def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
-        [os.path.join(INCLUDE, "es.h"), os.path.abspath(__file__), TORCH_SRC]
+        [os.path.join(INCLUDE, "es.h"), os.path.abspath(__file__)]
+
+
+def _newer(product: str, deps) -> bool:
+    return os.path.exists(product) and all(os.path.getmtime(p) <= os.path.getmtime(product) for p in deps)
+
+
+def _installed_torch():
+    """What es_torch.so is built against: where PyTorch lies and its version (found without importing
+    it, which takes seconds), Python's ABI; None without PyTorch."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or spec.origin is None:
+        return None
+    home = os.path.dirname(spec.origin)
+    version = os.path.join(home, "version.py")
+    text = open(version).read() if os.path.exists(version) else ""
+    return "%s\n%s\n%s" % (home, sys.implementation.cache_tag, text)
+
+
+def _lib_up_to_date() -> bool:
+    return _newer(LIB, _deps())
+
+
+def _torch_up_to_date() -> bool:
+    installed = _installed_torch()
+    if installed is None:
+        return True
+    if not _newer(TORCH_LIB, [TORCH_SRC, os.path.join(INCLUDE, "es.h"), os.path.abspath(__file__)]) or not os.path.exists(TORCH_STAMP):
+        return False
+    with open(TORCH_STAMP) as f:
+        return f.read() == installed
 
 
 def up_to_date() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(TORCH_LIB)):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(TORCH_LIB))
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    return _lib_up_to_date() and _torch_up_to_date()
 
 
 def _compile_torch(obj: str):
@@ -119,15 +150,18 @@ def _link_torch(obj: str):
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("linking es_torch.so failed")
     os.replace(tmp, TORCH_LIB)
+    with open(TORCH_STAMP, "w") as f:
+        f.write(_installed_torch() or "")
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    if not force and up_to_date():
+    lib, module = force or not _lib_up_to_date(), (force and _installed_torch() is not None) or not _torch_up_to_date()
+    if not (lib or module):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     write_jit_headers()
     cc = nvcc()
-    srcs = _sources()
+    srcs = _sources() if lib else []
     objs = [os.path.join(BUILD, os.path.basename(s)[:-3] + ".o") for s in srcs]
 
     def compile_one(pair):
@@ -140,23 +174,30 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     # the longest compilations first, so that none of them is left alone at the end
     order = sorted(zip(srcs, objs), key=lambda p: -os.path.getsize(p[0]))
     with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
-        bound = ex.submit(_compile_torch, torch_obj)
-        results = list(ex.map(compile_one, order)) + [bound.result()]
+        bound = ex.submit(_compile_torch, torch_obj) if module else None
+        results = list(ex.map(compile_one, order))
     failed = [(s, r) for s, r in results if r.returncode != 0]
     for s, r in results:
         if verbose or r.returncode != 0:
             sys.stderr.write(r.stdout + r.stderr)
     if failed:
         raise RuntimeError("compilation failed for: " + ", ".join(os.path.basename(s) for s, _ in failed))
-    tmp = LIB + ".%d.tmp" % os.getpid()
-    lib64 = os.path.join(cuda_home(), "lib64")
-    link = ["-L", lib64, "-lnvrtc", "-Xlinker", "-rpath," + lib64]
-    r = subprocess.run([cc] + ARCH + ["-shared", "-o", tmp] + objs + link, capture_output=True, text=True)
-    if r.returncode != 0:
-        sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("linking libes.so failed")
-    os.replace(tmp, LIB)
-    _link_torch(torch_obj)
+    if lib:
+        tmp = LIB + ".%d.tmp" % os.getpid()
+        lib64 = os.path.join(cuda_home(), "lib64")
+        link = ["-L", lib64, "-lnvrtc", "-Xlinker", "-rpath," + lib64]
+        r = subprocess.run([cc] + ARCH + ["-shared", "-o", tmp] + objs + link, capture_output=True, text=True)
+        if r.returncode != 0:
+            sys.stderr.write(r.stdout + r.stderr)
+            raise RuntimeError("linking libes.so failed")
+        os.replace(tmp, LIB)
+    if module:
+        src, r = bound.result()
+        if verbose or r.returncode != 0:
+            sys.stderr.write(r.stdout + r.stderr)
+        if r.returncode != 0:
+            raise RuntimeError("compilation failed for: " + os.path.basename(src))
+        _link_torch(torch_obj)
     return LIB
 
 
