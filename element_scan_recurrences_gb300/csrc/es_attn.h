@@ -9,6 +9,10 @@
 
 namespace es {
 
+// GB300's SMs.  Workspaces and grids are counted by this number and not by the
+// device's, for a workspace may be asked for where there is no GPU.
+constexpr int kSms = 152;
+
 // [B, T, heads, dim] operand, innermost stride 1 (strides in elements); head h
 // of the call reads operand head h / div.
 struct AttnOperand {
@@ -74,7 +78,6 @@ struct AttnLaunch {
     uint64_t wait_ns;
     int64_t drop_tile;
     cudaStream_t stream;
-    int num_sms;
     EncodeTiledFn encode;
 };
 
@@ -156,7 +159,6 @@ struct AttnStep {
     int64_t B;
     int H, dk, dv;
     cudaStream_t stream;
-    int num_sms;
 };
 cudaError_t launch_attn_step(const AttnStep& S);
 
@@ -190,7 +192,6 @@ struct RotateLaunch {
     float* partial;              // backward: [blocks, d] partial sums of both weights' gradients
     int backward;
     cudaStream_t stream;
-    int num_sms;
 };
 int rotate_blocks(const RotateLaunch& L, int side);
 int64_t rotate_units(const RotateLaunch& L, int side);     // below 2^31 - 2^20: the kernel counts them in 32 bits

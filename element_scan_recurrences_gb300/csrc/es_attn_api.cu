@@ -125,7 +125,7 @@ struct AttnPlan {
 // 8 x 1000 x 16 heads of 64 221 and 227.  With two CTAs an SM at all widths
 // 4 x 1000 x 16 heads of 64 took 146 us instead of 120.
 int segments(bool tensor, int64_t width, int64_t ctas, int64_t chunks, int64_t* seg_chunks) {
-    const int64_t most = 152 * (tensor ? 1 : width <= 64 ? 4 : width <= 128 ? 3 : 2) / ctas;
+    const int64_t most = kSms * (tensor ? 1 : width <= 64 ? 4 : width <= 128 ? 3 : 2) / ctas;
     if (most < 2) return 1;
     const int64_t each = (chunks + most - 1) / most;
     if ((tensor ? 142 : 165) * each + (tensor ? 500 : 600) >= 100 * chunks) return 1;
@@ -341,7 +341,7 @@ es_status check_workspace(const char* fn, void* ws, int64_t bytes, size_t need) 
     return ES_OK;
 }
 
-es_status device_of(const char* fn, AttnLaunch* L, es_stream_t stream) {
+es_status device_of(AttnLaunch* L, es_stream_t stream) {
     int dev = 0;
     DeviceState* ds = nullptr;
     es_status st = api_device(&dev, &ds);
@@ -349,9 +349,7 @@ es_status device_of(const char* fn, AttnLaunch* L, es_stream_t stream) {
     L->status = ds->status;
     L->wait_ns = api_wait_ns();
     L->drop_tile = api_drop_tile();
-    L->num_sms = ds->num_sms;
     L->stream = reinterpret_cast<cudaStream_t>(stream);
-    (void)fn;
     return ES_OK;
 }
 
@@ -641,7 +639,7 @@ es_status es_linear_attention(const es_linear_attention_args* args, es_stream_t 
     es_status st = es::plan_attn(fn, args, nullptr, false, &P);
     if (st != ES_OK || P.empty) return st;
     if ((st = es::check_workspace(fn, args->workspace, args->workspace_bytes, P.bytes)) != ES_OK) return st;
-    if ((st = es::device_of(fn, &P.L, stream)) != ES_OK) return st;
+    if ((st = es::device_of(&P.L, stream)) != ES_OK) return st;
     return es::launch_runs(fn, P, P.L, args->workspace);
 }
 
@@ -660,7 +658,7 @@ es_status es_linear_attention_backward(const es_linear_attention_args* args, con
         return ES_OK;
     }
     if ((st = es::check_workspace(fn, args->workspace, args->workspace_bytes, P.bytes)) != ES_OK) return st;
-    if ((st = es::device_of(fn, &P.L, stream)) != ES_OK) return st;
+    if ((st = es::device_of(&P.L, stream)) != ES_OK) return st;
     return es::run_backward(fn, args, grads, P);
 }
 

@@ -37,12 +37,6 @@ __device__ __forceinline__ void loaded(uint32_t (&r)[N]) {
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // N columns of the warp's 32 lanes: lane l of the warp holds its lane's N values
-__device__ __forceinline__ void st(uint32_t addr, const uint32_t (&r)[4]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%4], {%0, %1, %2, %3};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
-                 "r"(addr)
-                 : "memory");
-}
-
 __device__ __forceinline__ void ld(uint32_t addr, uint32_t (&r)[8]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
@@ -69,18 +63,6 @@ __device__ __forceinline__ void st(uint32_t addr, const uint32_t (&r)[16]) {
                  ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
                  "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
                  : "memory");
-}
-
-__device__ __forceinline__ void ld(uint32_t addr, uint32_t (&r)[32]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-                 "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-                 "%30, %31}, [%32];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-                   "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
-                   "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
-                   "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-                 : "r"(addr));
 }
 
 __device__ __forceinline__ void st(uint32_t addr, const uint32_t (&r)[32]) {
@@ -206,8 +188,8 @@ __device__ __forceinline__ float2 rest_of(float2 v, uint32_t hi) {
 }
 
 // The next bf16 term of a pair of values, which keeps what is left of them.
-// Rounded to nearest (9 bits of the value), or cut off (8): the conversion runs
-// at a quarter of the rate of the byte permute that cuts.
+// Rounded to nearest (2^-8 of the value is left at most) or cut off (2^-7): the
+// conversion runs at a quarter of the rate of the byte permute that cuts.
 template <bool kCut>
 __device__ __forceinline__ uint32_t take_term(float2& v) {
     uint32_t t;
@@ -221,7 +203,7 @@ __device__ __forceinline__ uint32_t take_term(float2& v) {
     return t;
 }
 
-// the first two bf16 terms of a pair of values: 2^-18 of them is left at most, cut off 2^-17
+// the first two bf16 terms of a pair of values: 2^-17 of them is left at most, cut off 2^-16
 template <bool kCut>
 __device__ __forceinline__ void split2(float2 v, uint32_t& hi, uint32_t& lo) {
     hi = take_term<kCut>(v);

@@ -698,7 +698,7 @@ cudaError_t launch_attn_folds(const AttnFold* folds, int n) {
         vec = vec && folds[i].d % 4 == 0 && reinterpret_cast<uintptr_t>(folds[i].part) % 16 == 0;
     }
     const int64_t blocks = (most / (vec ? 4 : 1) + 255) / 256;
-    const dim3 grid(static_cast<unsigned>(blocks < 152 * 8 ? blocks : 152 * 8), n);
+    const dim3 grid(static_cast<unsigned>(blocks < kSms * 8 ? blocks : kSms * 8), n);
     const auto kernel = folds[0].bf16 ? (vec ? k_attn_fold<__nv_bfloat16, 4> : k_attn_fold<__nv_bfloat16, 1>)
                                       : (vec ? k_attn_fold<float, 4> : k_attn_fold<float, 1>);
     kernel<<<grid, 256, 0, folds[0].stream>>>(A);

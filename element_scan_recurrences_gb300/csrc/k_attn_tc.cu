@@ -32,9 +32,10 @@
 //
 // Precision: bf16 operands go in as they are.  Every f32 factor is split into
 // bf16 terms that are multiplied in turn and summed in f32: P and the state as
-// read in two (2^-16 of each factor, below the result's own rounding; the
-// decays' gradient takes differences of these results, which one term would
-// spoil), Z' in three (2^-24: the state is an f32 result).
+// read in two (2^-16 of each factor, below the result's own rounding; 2^-17
+// with the decays' gradient, which takes differences of these results that one
+// term would spoil), Z' in three where the state is an f32 result (all of its
+// 24 bits), else in two.
 //
 // Every wait is bounded: a role that gives up sets the status word and the
 // abort flag, all roles leave their loops, copies and products in flight are

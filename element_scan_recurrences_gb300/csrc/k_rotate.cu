@@ -555,7 +555,7 @@ Grid grid_of(const RotateLaunch& L) {
         g.per[s] = (L.side[s].heads + hb - 1) / hb;
         g.units[s] = L.B * L.T * g.per[s];
         int64_t n = (g.units[s] + kWarps - 1) / kWarps;
-        int64_t most = static_cast<int64_t>(152) * resident(L.backward) * L.side[s].heads / (heads > 0 ? heads : 1);
+        int64_t most = static_cast<int64_t>(kSms) * resident(L.backward) * L.side[s].heads / (heads > 0 ? heads : 1);
         if (most < 1) most = 1;
         n = n < most ? n : most;
         g.blocks[s] = static_cast<int>(n);
