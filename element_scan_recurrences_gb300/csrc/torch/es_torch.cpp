@@ -28,6 +28,9 @@ struct Refused {
     std::string what;
 };
 
+// A Python exception is set already.
+struct Raised {};
+
 [[noreturn]] void refuse(int status, const std::string& what) { throw Refused{status, what}; }
 [[noreturn]] void wrong_type(const std::string& what) { throw Refused{0, what}; }
 
@@ -65,6 +68,13 @@ at::Tensor tensor(PyObject* o, const char* name) {
     auto t = maybe(o, name);
     if (!t) wrong_type(std::string(name) + " must be a torch.Tensor");
     return *t;
+}
+
+// An argument's truth value, which an object may refuse to have.
+bool truth(PyObject* o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw Raised{};
+    return v != 0;
 }
 
 // The first operand fixes the type and the device.
@@ -237,7 +247,7 @@ PyObject* attention(PyObject* const* x) {
     a.lengths = static_cast<const int32_t*>(dense(lengths, "lengths", at::kInt, o.dev, {a.batch}));
     std::optional<at::Tensor> fin;
     if (THPVariable_Check(x[7])) fin = THPVariable_Unpack(x[7]);
-    else if (PyObject_IsTrue(x[7]) == 1) fin = empty(shape, o.q, at::kFloat);
+    else if (truth(x[7])) fin = empty(shape, o.q, at::kFloat);
     a.final_state = static_cast<float*>(dense(fin, "final_state", at::kFloat, o.dev, shape));
     auto out = maybe(x[8], "out");
     const std::array<int64_t, 4> want{a.batch, a.length, a.heads, a.value_dim};
@@ -271,7 +281,7 @@ PyObject* attention_backward(PyObject* const* x) {
     g.grad_k = view(gk, "grad_k", o.type, o.dev, 4);
     g.grad_v = view(gv, "grad_v", o.type, o.dev, 4);
     std::optional<at::Tensor> gg, gi;
-    if (o.g && PyObject_IsTrue(x[9]) == 1) {
+    if (truth(x[9]) && o.g) {
         gg = empty(o.g->sizes(), o.q, at::kFloat);
         g.grad_log_decay = static_cast<float*>(gg->data_ptr());
     }
@@ -368,7 +378,7 @@ struct Rotation {
             PyErr_Clear();
             wrong_type("eps must be a number");
         }
-        a.neighbours = PyObject_IsTrue(x[8]) == 1;
+        a.neighbours = truth(x[8]);
     }
     // a result's tensor (a new dense one unless given) and its view
     at::Tensor out(PyObject* given, const at::Tensor& like, const char* name, es_heads* v) {
@@ -434,6 +444,8 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
         return F(args);
     } catch (const Refused& r) {
         return raise(r);
+    } catch (const Raised&) {
+        return nullptr;
     } catch (const c10::Error& e) {
         PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
     } catch (const std::exception& e) {
