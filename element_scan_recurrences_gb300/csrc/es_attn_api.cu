@@ -510,8 +510,6 @@ es_status plan_rotate(const char* fn, const es_qk_norm_rotate_args* a, const es_
         if (backward && (st = check_view(fn, gn[i], *gs[i], B, T, d, size, false, &gsp[i])) != ES_OK) return st;
         if (reinterpret_cast<uintptr_t>(ws[i]) % wsize != 0 || reinterpret_cast<uintptr_t>(gw[i]) % wsize != 0)
             return api_fail(ES_E_ARG, "%s: `%s` or its gradient is not aligned to its elements", fn, wn[i]);
-        if (gw[i] != nullptr && xs[i]->heads == 0)
-            return api_fail(ES_E_ARG, "%s: `%s` without heads", fn, gwn[i]);
         in[n_in++] = Span{wn[i], ws[i], ws[i] == nullptr ? 0 : d * wsize};
         if (gw[i] != nullptr) out[n_out++] = Span{gwn[i], gw[i], d * wsize};
     }
