@@ -662,7 +662,8 @@ typedef struct es_heads {
  *                     decay_per_head = 1 (decay_b and decay_t unused); null:
  *                     no decay.  Meant to be <= 0.  Below -104 (where e^g is
  *                     zero in f32; -inf included) the token starts afresh from
- *                     a state of finite values.
+ *                     a state of finite values.  Strong decays above that cost
+ *                     the weights between later tokens no precision.
  *   lengths           device i32 [B], or null: tokens at and past a row's
  *                     length (clamped to 0..T) are not read, their `out` is 0.
  *   scale             finite, not zero.
@@ -676,7 +677,17 @@ typedef struct es_heads {
  * bf16 with widths of at most 128 that are multiples of 8, 16-byte addresses
  * and strides: ES_PATH_TENSOR, chunks of tokens as products on the tensor
  * cores; anything else ES_PATH_GENERIC, the same chunk form on the FMA units.
- * In both the states, sums and decays are f32.
+ * In both the states, sums and decays are f32.  bf16 results differ from exact
+ * ones by their rounding; ES_PATH_TENSOR's f32 factors keep 16 bits or more on
+ * the way to bf16 results and to the decays' gradient (about 5e-6 of it), and
+ * all 24 on the way to a state.
+ * Operands are meant to be finite.  Tokens are worked on in chunks of 64
+ * (ES_PATH_TENSOR) or 32 from the row's start, as products in which a later
+ * token has weight zero: an infinity or NaN in v at a token within the length
+ * makes NaNs of its column in the whole chunk's results, the tokens before it
+ * included (in the gradients, one in grad_out, q or k likewise), and on
+ * ES_PATH_TENSOR an infinity comes out as NaN.  Tokens past a row's length may
+ * hold anything.
  */
 typedef struct es_linear_attention_args {
     int64_t dtype, batch, length, heads, key_dim, value_dim;
