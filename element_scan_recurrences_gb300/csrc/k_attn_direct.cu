@@ -96,8 +96,8 @@ struct DirectArgs {
 // not by HBM: for one chunk and slice, dx = 128, 426 K FMAs (the 32 x 32 products
 // of x and y are formed again in every slice).  So few threads with 4 rows of the
 // products each: 256 threads with 2 rows read half as much again, and the training
-// pass of 4 x 1000 x 16 heads of 128 took 1451 us instead of 1183 (2 x 501 x 8
-// heads of 64: 122 instead of 105; a lone CTA an SM favours them, 4 x 300 x 12
+// pass of 4 x 1000 x 16 heads of 128 took 1451 us instead of 1165 (2 x 501 x 8
+// heads of 64: 122 instead of 103; a lone CTA an SM favours them, 4 x 300 x 12
 // heads of 96 took 62 instead of 72).  It serves the calls the tensor-core
 // kernel cannot take.
 //

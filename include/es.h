@@ -679,8 +679,9 @@ typedef struct es_heads {
  * cores; anything else ES_PATH_GENERIC, the same chunk form on the FMA units.
  * In both the states, sums and decays are f32.  bf16 results differ from exact
  * ones by their rounding; ES_PATH_TENSOR's f32 factors keep 16 bits or more on
- * the way to bf16 results and to the decays' gradient (about 5e-6 of it), and
- * all 24 on the way to a state.
+ * the way to bf16 results and to the decays' gradient (about 5e-6 of it, up to
+ * 5e-5 of a fixed decay's; f32 operands hold it to 1e-6 and 3e-6), and all 24
+ * on the way to a state.
  * Operands are meant to be finite.  Tokens are worked on in chunks of 64
  * (ES_PATH_TENSOR) or 32 from the row's start, as products in which a later
  * token has weight zero: an infinity or NaN in v at a token within the length
