@@ -5,7 +5,9 @@ for sm_103a, declared in ``include/es.h``); ``scan`` and friends are a thin
 ctypes binding over it that only marshals arguments.  The binding loads the
 library on first use and raises if it is missing: there is no CPU fallback.
 ``linear_attention`` and ``qk_norm_rotate`` (sequence.py) are the operators of
-a sequence layer whose recurrence has a matrix state per head.
+a sequence layer whose recurrence has a matrix state per head; ``causal_conv``,
+``selective_scan`` and ``group_norm`` those of one whose channels each carry a
+few states.
 """
 from . import workloads  # noqa: F401  (pure Python: seeded inputs only)
 
@@ -20,7 +22,9 @@ _BINDING_NAMES = {
 }
 _SEQUENCE_NAMES = {
     "linear_attention", "linear_attention_backward", "linear_attention_step", "plan_linear_attention", "qk_norm_rotate",
-    "qk_norm_rotate_backward",
+    "qk_norm_rotate_backward", "causal_conv", "causal_conv_backward", "causal_conv_step", "plan_causal_conv",
+    "selective_scan", "selective_scan_backward", "selective_scan_step", "plan_selective_scan", "group_norm",
+    "group_norm_backward", "plan_group_norm",
 }
 
 

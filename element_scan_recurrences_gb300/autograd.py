@@ -203,3 +203,89 @@ def qk_norm_rotate(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: Optiona
     """``sequence.qk_norm_rotate``, differentiable with respect to q, k and
     the weights; the tables take no gradient."""
     return _QkNormRotate.apply(q, k, q_weight, k_weight, cos, sin, positions, float(eps), bool(neighbours))
+
+
+class _CausalConv(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, initial_state, lengths, activation, final_state):
+        out, fin = sequence.causal_conv(x, weight, bias, initial_state=initial_state, lengths=lengths, activation=activation,
+                                        final_state=final_state)
+        ctx.save_for_backward(x, weight, bias, initial_state, lengths)
+        ctx.activation = activation
+        return out, fin
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_out, grad_fin):
+        x, weight, bias, initial_state, lengths = ctx.saved_tensors
+        gx, gw, gb, gi = sequence.causal_conv_backward(
+            x, weight, bias, grad_out if grad_out.stride(-1) == 1 else grad_out.contiguous(), initial_state=initial_state,
+            grad_final_state=None if grad_fin is None else grad_fin.contiguous(), lengths=lengths, activation=ctx.activation)
+        return gx, gw, gb, gi, None, None, None
+
+
+def causal_conv(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                initial_state: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None, activation: bool = True,
+                final_state: bool = False):
+    """``sequence.causal_conv``, differentiable with respect to x, the weights
+    and the initial state: (out, the last inputs or None)."""
+    return _CausalConv.apply(x, weight, bias, initial_state, lengths, bool(activation), bool(final_state))
+
+
+class _SelectiveScan(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, delta, A, B, C, D, gate, delta_bias, softplus, initial_state, lengths, final_state, keep):
+        keep = keep and any(ctx.needs_input_grad)
+        out, fin, kept = sequence.selective_scan(x, delta, A, B, C, D, gate, delta_bias, softplus=softplus,
+                                                 initial_state=initial_state, lengths=lengths, final_state=final_state,
+                                                 checkpoints=keep)
+        ctx.save_for_backward(x, delta, A, B, C, D, gate, delta_bias, initial_state, lengths)
+        ctx.softplus, ctx.kept = softplus, kept
+        return out, fin
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_out, grad_fin):
+        x, delta, A, B, C, D, gate, delta_bias, initial_state, lengths = ctx.saved_tensors
+        gx, gdelta, gA, gB, gC, gD, ggate, gbias, gi = sequence.selective_scan_backward(
+            x, delta, A, B, C, D, gate, delta_bias, grad_out if grad_out.stride(-1) == 1 else grad_out.contiguous(),
+            softplus=ctx.softplus, initial_state=initial_state,
+            grad_final_state=None if grad_fin is None else grad_fin.contiguous(), lengths=lengths, checkpoints=ctx.kept)
+        return gx, gdelta, gA, gB, gC, gD, ggate, gbias, None, gi, None, None, None
+
+
+def selective_scan(x: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
+                   D: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                   delta_bias: Optional[torch.Tensor] = None, softplus: bool = True,
+                   initial_state: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None,
+                   final_state: bool = False, checkpoints: bool = True):
+    """``sequence.selective_scan``, differentiable with respect to every
+    floating operand: (out, the last state or None).  The forward keeps states
+    on the way for the backward (4 N bytes a channel every 16 tokens); with
+    ``checkpoints`` false it keeps none, and the backward finds them again."""
+    return _SelectiveScan.apply(x, delta, A, B, C, D, gate, delta_bias, bool(softplus), initial_state, lengths,
+                                bool(final_state), bool(checkpoints))
+
+
+class _GroupNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, gate, gate_first, center, activation, eps):
+        ctx.save_for_backward(x, weight, bias, gate)
+        ctx.options = dict(gate_first=gate_first, center=center, activation=activation, eps=eps)
+        return sequence.group_norm(x, weight, bias, gate, **ctx.options)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_out):
+        x, weight, bias, gate = ctx.saved_tensors
+        grads = sequence.group_norm_backward(x, weight, bias, gate,
+                                             grad_out if grad_out.stride(-1) == 1 else grad_out.contiguous(), **ctx.options)
+        return grads + (None, None, None, None)
+
+
+def group_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+               gate: Optional[torch.Tensor] = None, gate_first: bool = False, center: bool = True, activation: bool = False,
+               eps: float = 1e-5):
+    """``sequence.group_norm``, differentiable with respect to x, the weights
+    and the gate."""
+    return _GroupNorm.apply(x, weight, bias, gate, bool(gate_first), bool(center), bool(activation), float(eps))

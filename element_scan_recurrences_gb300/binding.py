@@ -41,7 +41,11 @@ EXPORTS = ("es_scan_f32", "es_plan_f32", "es_scan_backward_f32", "es_plan_backwa
            "es_scan_host_f32", "es_scan_body_host_f32", "es_matrix_scan_backward_ws_f32",
            "es_plan_matrix_scan_backward_ws_f32", "es_linear_attention", "es_linear_attention_backward",
            "es_linear_attention_workspace", "es_plan_linear_attention", "es_linear_attention_step", "es_qk_norm_rotate",
-           "es_qk_norm_rotate_backward", "es_qk_norm_rotate_workspace", "es_plan_qk_norm_rotate")
+           "es_qk_norm_rotate_backward", "es_qk_norm_rotate_workspace", "es_plan_qk_norm_rotate", "es_causal_conv",
+           "es_causal_conv_backward", "es_causal_conv_workspace", "es_plan_causal_conv", "es_causal_conv_step",
+           "es_selective_scan", "es_selective_scan_backward", "es_selective_scan_workspace", "es_selective_scan_checkpoints",
+           "es_plan_selective_scan", "es_selective_scan_step", "es_group_norm", "es_group_norm_backward",
+           "es_group_norm_workspace", "es_plan_group_norm")
 
 
 class LibraryMissing(ImportError):
@@ -176,13 +180,16 @@ def lib():
         L.es_plan_table_scan_i32.restype = ctypes.c_int
         # the sequence-layer operators (sequence.py): structs packed as bytes, then (workspace, plan) a result or a stream
         C, szp = ctypes.c_char_p, ctypes.POINTER(ctypes.c_size_t)
-        for op in ("linear_attention", "qk_norm_rotate"):
+        for op in ("linear_attention", "qk_norm_rotate", "causal_conv", "selective_scan", "group_norm"):
             for name, args in (("es_%s" % op, [C, P]), ("es_%s_backward" % op, [C, C, P]),
                                ("es_%s_workspace" % op, [C, C, szp]), ("es_plan_%s" % op, [C, C, ctypes.POINTER(PlanInfo)])):
                 getattr(L, name).argtypes = args
                 getattr(L, name).restype = ctypes.c_int
-        L.es_linear_attention_step.argtypes = [C, P]
-        L.es_linear_attention_step.restype = ctypes.c_int
+        for op in ("linear_attention", "causal_conv", "selective_scan"):
+            getattr(L, "es_%s_step" % op).argtypes = [C, P]
+            getattr(L, "es_%s_step" % op).restype = ctypes.c_int
+        L.es_selective_scan_checkpoints.argtypes = [C, szp]
+        L.es_selective_scan_checkpoints.restype = ctypes.c_int
         _lib = L
         return L
 

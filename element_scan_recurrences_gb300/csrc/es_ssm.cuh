@@ -1,0 +1,204 @@
+// es_ssm.cuh -- device helpers of the state-space layer's kernels: element
+// types, exponentials, the logistic function and log(1 + e^x), copies into
+// shared memory.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "es_pairs.cuh"
+
+namespace es {
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) {
+    return v;
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
+    return __float2bfloat16_rn(v);
+}
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLog2eLow = 1.92596299112661746887e-8f;      // log2(e) - kLog2e
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// The hardware's 2^x (relative error below 2^-22; results under 2^-126 are 0).
+__device__ __forceinline__ float exp2_hw(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ float rcp_hw(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// e^x for finite x: what x log2(e) loses in its rounding, |x| 2^-24 of the
+// result, goes back in to first order.
+__device__ __forceinline__ float exp_f32(float x) {
+    const float t = x * kLog2e;
+    const float lost = fmaf(x, kLog2eLow, fmaf(x, kLog2e, -t));
+    const float e = exp2_hw(t);
+    return fmaf(e, lost * kLn2, e);
+}
+
+// 1 / (1 + e^-z).  Below -87 it is 0 (e^87 = 6e37 keeps 1 + e^-z finite).
+__device__ __forceinline__ float logistic(float z) { return rcp_hw(1.0f + exp_f32(-fmaxf(z, -87.0f))); }
+
+// log(1 + e^x) = max(x, 0) + log(1 + e), e = e^-|x| in (0, 1].  log(1 + e) / e
+// is a polynomial of degree 9, fitted for the least relative error on [0, 1]
+// (5e-9; 1.3e-7 as evaluated in f32), so small results keep their bits.
+__device__ __forceinline__ float log1p_poly(float e) {
+    float p = -0.003244024235755205f;
+    p = fmaf(p, e, 0.019851457327604294f);
+    p = fmaf(p, e, -0.056959524750709534f);
+    p = fmaf(p, e, 0.10603653639554977f);
+    p = fmaf(p, e, -0.15305592119693756f);
+    p = fmaf(p, e, 0.1967593878507614f);
+    p = fmaf(p, e, -0.24954134225845337f);
+    p = fmaf(p, e, 0.3332996368408203f);
+    p = fmaf(p, e, -0.4999990165233612f);
+    p = fmaf(p, e, 1.0f);
+    return p * e;
+}
+
+// A NaN stays one through the first term.
+__device__ __forceinline__ float softplus(float x) {
+    const float m = fabsf(x);
+    return fmaf(0.5f, m, 0.5f * x) + log1p_poly(exp_f32(-fminf(m, 87.0f)));
+}
+
+// d/dz of z s(z), s = logistic(z)
+__device__ __forceinline__ float silu_slope(float z, float s) { return fmaf(z * s, 1.0f - s, s); }
+
+// V neighbouring values in one access
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Pack {
+    T v[V];
+};
+
+template <typename T, int V>
+__device__ __forceinline__ void load_pack(const T* p, float (&r)[V]) {
+    const Pack<T, V> q = *reinterpret_cast<const Pack<T, V>*>(p);
+#pragma unroll
+    for (int i = 0; i < V; ++i) r[i] = to_f32(q.v[i]);
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_pack(T* p, const float (&r)[V]) {
+    Pack<T, V> q;
+#pragma unroll
+    for (int i = 0; i < V; ++i) q.v[i] = from_f32<T>(r[i]);
+    *reinterpret_cast<Pack<T, V>*>(p) = q;
+}
+template <int V>
+__device__ __forceinline__ void zero(float (&r)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) r[i] = 0.0f;
+}
+
+// a weight of either type
+__device__ __forceinline__ float weight_at(const void* w, int bf16, int64_t i) {
+    return bf16 ? to_f32(static_cast<const __nv_bfloat16*>(w)[i]) : static_cast<const float*>(w)[i];
+}
+
+// 16 bytes into shared memory; the bytes past `n` (0..16) are zeros and not read.
+__device__ __forceinline__ void copy16(void* to, const void* from, int n) {
+    const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(to));
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(a), "l"(from), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+// a row's tokens that count
+__device__ __forceinline__ int64_t live_tokens(const int32_t* lengths, int64_t b, int64_t T) {
+    if (lengths == nullptr) return T;
+    const int64_t n = lengths[b];
+    return n < 0 ? 0 : n < T ? n : T;
+}
+
+// RN of a channel's N states from number n0 on (zeros past the last); `wide`: N is
+// a multiple of 4 and p of 16 bytes
+template <int RN>
+__device__ __forceinline__ void load_states(const float* p, int n0, int N, bool wide, float2 (&h)[RN / 2]) {
+    if constexpr (RN % 4 == 0) {
+        if (wide) {
+#pragma unroll
+            for (int i = 0; i < RN; i += 4) {
+                const float4 v = n0 + i < N ? *reinterpret_cast<const float4*>(p + n0 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+                h[i / 2] = make_float2(v.x, v.y);
+                h[i / 2 + 1] = make_float2(v.z, v.w);
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < RN; i += 2) {
+        h[i / 2].x = n0 + i < N ? p[n0 + i] : 0.0f;
+        h[i / 2].y = n0 + i + 1 < N ? p[n0 + i + 1] : 0.0f;
+    }
+}
+
+template <int RN>
+__device__ __forceinline__ void store_states(float* p, int n0, int N, bool wide, const float2 (&h)[RN / 2]) {
+    if constexpr (RN % 4 == 0) {
+        if (wide) {
+#pragma unroll
+            for (int i = 0; i < RN; i += 4)
+                if (n0 + i < N) *reinterpret_cast<float4*>(p + n0 + i) = make_float4(h[i / 2].x, h[i / 2].y, h[i / 2 + 1].x, h[i / 2 + 1].y);
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < RN; i += 2) {
+        if (n0 + i < N) p[n0 + i] = h[i / 2].x;
+        if (n0 + i + 1 < N) p[n0 + i + 1] = h[i / 2].y;
+    }
+}
+
+// Sums of the rows of a [rows][M] table, put(j, sum) for each column: a block takes
+// 32 columns, its 8 warps every eighth row, always in one order.
+constexpr int kSumLanes = 8;
+template <typename Put>
+__global__ void __launch_bounds__(32 * kSumLanes) k_sum_rows(const float* __restrict__ p, int64_t rows, int64_t M, const Put put) {
+    __shared__ float part[kSumLanes][32];
+    const int64_t j = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;
+    float s = 0.0f;
+    if (j < M) {
+        float t[4] = {0.f, 0.f, 0.f, 0.f};
+        int64_t r = threadIdx.y;
+        for (; r + 3 * kSumLanes < rows; r += 4 * kSumLanes)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t[i] += p[(r + i * kSumLanes) * M + j];
+        for (; r < rows; r += kSumLanes) t[0] += p[r * M + j];
+        s = (t[0] + t[1]) + (t[2] + t[3]);
+    }
+    part[threadIdx.y][threadIdx.x] = s;
+    __syncthreads();
+    if (threadIdx.y == 0 && j < M) {
+#pragma unroll
+        for (int i = 1; i < kSumLanes; ++i) s += part[i][threadIdx.x];
+        put(j, s);
+    }
+}
+template <typename Put>
+cudaError_t sum_rows(const float* p, int64_t rows, int64_t M, const Put& put, cudaStream_t stream) {
+    k_sum_rows<<<static_cast<unsigned>((M + 31) / 32), dim3(32, kSumLanes), 0, stream>>>(p, rows, M, put);
+    return cudaGetLastError();
+}
+
+__device__ __forceinline__ void put_weight(void* w, int bf16, int64_t i, float v) {
+    if (w == nullptr) return;
+    if (bf16) static_cast<__nv_bfloat16*>(w)[i] = from_f32<__nv_bfloat16>(v);
+    else static_cast<float*>(w)[i] = v;
+}
+
+}  // namespace es

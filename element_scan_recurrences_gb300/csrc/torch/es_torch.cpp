@@ -432,6 +432,356 @@ PyObject* rotate_backward(PyObject* const* x) {
     return result({gq, gk, gwq, gwk});
 }
 
+// ---------------------------------------------------------------------------
+// the state-space layer
+
+// [B, T, channels], or [B, channels] for a step
+es_rows rows(const at::Tensor& t, const char* name, at::ScalarType type, const at::Device& dev, int rank) {
+    like(t, name, type, dev);
+    if (t.dim() != rank)
+        refuse(ES_E_DIM_001, std::string("E-DIM-001 ") + name + " has rank " + std::to_string(t.dim()) + ", not " + std::to_string(rank));
+    const auto s = t.strides();
+    const auto n = t.sizes();
+    if (s[rank - 1] != 1 && n[rank - 1] > 1 && t.numel() > 0)
+        refuse(ES_E_ARG, std::string("the last axis of ") + name + " has stride " + std::to_string(s[rank - 1]) + "; it must be 1");
+    return es_rows{t.data_ptr(), s[0], rank == 2 ? 0 : s[1]};
+}
+
+// a tensor of rows of a known shape (null for None)
+es_rows rows_like(const std::optional<at::Tensor>& t, const char* name, const at::Tensor& x) {
+    if (!t) return es_rows{};
+    shaped(*t, name, x.sizes());
+    return rows(*t, name, x.scalar_type(), x.device(), static_cast<int>(x.dim()));
+}
+
+// a result of x's shape and dtype: a new one unless given
+at::Tensor rows_out(PyObject* given, const char* name, const at::Tensor& x, es_rows* v) {
+    auto t = maybe(given, name);
+    if (!t) t = empty(x.sizes(), x, x.scalar_type());
+    *v = rows_like(t, name, x);
+    return *t;
+}
+
+// f32 or bf16, one type for all that are there
+at::ScalarType weight_type(std::initializer_list<const std::optional<at::Tensor>*> ws, const char* names) {
+    std::optional<at::ScalarType> type;
+    for (const auto* w : ws)
+        if (*w) {
+            const auto t = (*w)->scalar_type();
+            if ((t != at::kFloat && t != at::kBFloat16) || (type && *type != t))
+                wrong_type(std::string(names) + " must be tensors of one dtype, float32 or bfloat16");
+            type = t;
+        }
+    return type ? *type : at::kFloat;
+}
+
+double number(PyObject* o, const char* name) {
+    const double v = PyFloat_AsDouble(o);
+    if (PyErr_Occurred()) {
+        PyErr_Clear();
+        wrong_type(std::string(name) + " must be a number");
+    }
+    return v;
+}
+
+// what every form of the convolution shares, from x[0..2]: x, weight, bias
+struct Conv {
+    at::Tensor x;
+    std::optional<at::Tensor> w, b, init, lengths;
+    at::Device dev{at::kCPU};
+    at::ScalarType type, wtype;
+    es_causal_conv_args a{};
+    Conv(PyObject* const* p, PyObject* act, bool step)
+        : x(first(p[0], "x")), w(tensor(p[1], "weight")), b(maybe(p[2], "bias")), dev(x.device()), type(x.scalar_type()),
+          wtype(weight_type({&w, &b}, "weight and bias")) {
+        const int rank = step ? 2 : 3;
+        a.dtype = dtype_of(x);
+        a.weight_dtype = wtype == at::kBFloat16 ? ES_BF16 : ES_F32;
+        a.x = rows(x, "x", type, dev, rank);
+        a.batch = x.size(0);
+        a.length = step ? 1 : x.size(1);
+        a.channels = x.size(rank - 1);
+        if (w->dim() != 2) refuse(ES_E_DIM_001, "E-DIM-001 weight must be [channels, taps], not " + shape_of(w->sizes()));
+        a.taps = w->size(1);
+        a.weight = dense(w, "weight", wtype, dev, {a.channels, a.taps});
+        a.bias = dense(b, "bias", wtype, dev, {a.channels});
+        a.activation = truth(act);
+    }
+    std::array<int64_t, 3> state_shape() const { return {a.batch, a.taps - 1, a.channels}; }
+    // a refusal of the taps comes before a state of a nonsensical shape is made
+    void taps_fit() const {
+        if (a.taps < 1) refuse(ES_E_UNSUPPORTED, "es_causal_conv: no taps");
+    }
+    void take(PyObject* pi, PyObject* pl) {
+        taps_fit();
+        init = maybe(pi, "initial_state");
+        lengths = maybe(pl, "lengths");
+        a.initial_state = dense(init, "initial_state", type, dev, state_shape());
+        a.lengths = static_cast<const int32_t*>(dense(lengths, "lengths", at::kInt, dev, {a.batch}));
+    }
+};
+
+// a state result: a tensor to write to, or a new one where the argument is true
+std::optional<at::Tensor> state_result(PyObject* o, at::IntArrayRef shape, const at::Tensor& x, at::ScalarType type) {
+    if (THPVariable_Check(o)) return THPVariable_Unpack(o);
+    if (truth(o)) return empty(shape, x, type);
+    return std::nullopt;
+}
+
+// x, weight, bias, initial_state, lengths, activation, final_state, out, stream
+PyObject* conv(PyObject* const* x) {
+    Conv o(x, x[5], false);
+    On on(o.dev, x[8]);
+    auto& a = o.a;
+    o.take(x[3], x[4]);
+    const auto fin = state_result(x[6], o.state_shape(), o.x, o.type);
+    a.final_state = dense(fin, "final_state", o.type, o.dev, o.state_shape());
+    const at::Tensor out = rows_out(x[7], "out", o.x, &a.out);
+    check(es_causal_conv(&a, on.handle));
+    return result({out, fin});
+}
+
+// x, weight, bias, grad_out, initial_state, grad_final_state, lengths, activation, workspace, stream
+PyObject* conv_backward(PyObject* const* x) {
+    Conv o(x, x[7], false);
+    On on(o.dev, x[9]);
+    auto& a = o.a;
+    o.take(x[4], x[6]);
+    const at::Tensor go = tensor(x[3], "grad_out");
+    const auto gfin = maybe(x[5], "grad_final_state");
+    es_causal_conv_grads g{};
+    g.grad_out = rows_like(go, "grad_out", o.x);
+    g.grad_final_state = dense(gfin, "grad_final_state", o.type, o.dev, o.state_shape());
+    const at::Tensor gx = rows_out(Py_None, "grad_x", o.x, &g.grad_x), gw = empty(o.w->sizes(), o.x, o.wtype);
+    g.grad_weight = gw.data_ptr();
+    std::optional<at::Tensor> gb, gi;
+    if (o.b) {
+        gb = empty(o.b->sizes(), o.x, o.wtype);
+        g.grad_bias = gb->data_ptr();
+    }
+    if (o.init) {
+        gi = empty(o.state_shape(), o.x, o.type);
+        g.grad_initial_state = gi->data_ptr();
+    }
+    size_t bytes = 0;
+    check(es_causal_conv_workspace(&a, &g, &bytes));
+    const auto ws = workspace(x[8], bytes, o.x, &a.workspace, &a.workspace_bytes);
+    check(es_causal_conv_backward(&a, &g, on.handle));
+    return result({gx, gw, gb, gi});
+}
+
+// x, weight, bias, state, state_out, activation, out, stream
+PyObject* conv_step(PyObject* const* x) {
+    Conv o(x, x[5], true);
+    On on(o.dev, x[7]);
+    auto& a = o.a;
+    o.taps_fit();
+    const at::Tensor state = tensor(x[3], "state");
+    auto next = maybe(x[4], "state_out");
+    if (!next) next = state;
+    a.initial_state = dense(state, "state", o.type, o.dev, o.state_shape());
+    a.final_state = dense(next, "state_out", o.type, o.dev, o.state_shape());
+    const at::Tensor out = rows_out(x[6], "out", o.x, &a.out);
+    check(es_causal_conv_step(&a, on.handle));
+    return result({out, next});
+}
+
+// what every form of the scan shares, from x[0..7]: x, delta, A, B, C, D, gate, delta_bias
+struct Scan {
+    at::Tensor x, delta, A, B, C;
+    std::optional<at::Tensor> D, gate, bias, init, lengths;
+    at::Device dev{at::kCPU};
+    at::ScalarType type;
+    es_selective_scan_args a{};
+    Scan(PyObject* const* p, PyObject* soft, bool step)
+        : x(first(p[0], "x")), delta(tensor(p[1], "delta")), A(tensor(p[2], "A")), B(tensor(p[3], "B")), C(tensor(p[4], "C")),
+          D(maybe(p[5], "D")), gate(maybe(p[6], "gate")), bias(maybe(p[7], "delta_bias")), dev(x.device()), type(x.scalar_type()) {
+        const int rank = step ? 2 : 3;
+        a.dtype = dtype_of(x);
+        a.x = rows(x, "x", type, dev, rank);
+        a.batch = x.size(0);
+        a.length = step ? 1 : x.size(1);
+        a.channels = x.size(rank - 1);
+        a.delta = rows_like(delta, "delta", x);
+        a.gate = rows_like(gate, "gate", x);
+        if (A.dim() != 2) refuse(ES_E_DIM_001, "E-DIM-001 A must be [channels, states], not " + shape_of(A.sizes()));
+        a.states = A.size(1);
+        a.a = static_cast<const float*>(dense(A, "A", at::kFloat, dev, {a.channels, a.states}));
+        a.skip = static_cast<const float*>(dense(D, "D", at::kFloat, dev, {a.channels}));
+        a.delta_bias = static_cast<const float*>(dense(bias, "delta_bias", at::kFloat, dev, {a.channels}));
+        a.b = view(B, "B", type, dev, rank + 1);
+        a.c = view(C, "C", type, dev, rank + 1);
+        a.groups = a.b.heads;
+        for (const auto* t : {&B, &C})
+            if (t->size(0) != a.batch || (!step && t->size(1) != a.length) || t->size(rank - 1) != a.groups || t->size(rank) != a.states)
+                refuse(ES_E_DIM_001, "E-DIM-001 x " + shape_of(x.sizes()) + ", A " + shape_of(A.sizes()) + ", B " + shape_of(B.sizes()) +
+                                         " and C " + shape_of(C.sizes()) + " do not fit");
+        a.softplus = truth(soft);
+    }
+    std::array<int64_t, 3> state_shape() const { return {a.batch, a.channels, a.states}; }
+    void take(PyObject* pi, PyObject* pl) {
+        init = maybe(pi, "initial_state");
+        lengths = maybe(pl, "lengths");
+        a.initial_state = static_cast<const float*>(dense(init, "initial_state", at::kFloat, dev, state_shape()));
+        a.lengths = static_cast<const int32_t*>(dense(lengths, "lengths", at::kInt, dev, {a.batch}));
+    }
+    // the caller's checkpoints
+    void kept(const std::optional<at::Tensor>& t) {
+        if (!t) return;
+        if (t->device() != dev || !t->is_contiguous()) wrong_type("checkpoints must be a contiguous tensor on " + dev.str());
+        a.checkpoints = t->data_ptr();
+        a.checkpoints_bytes = static_cast<int64_t>(t->numel() * t->element_size());
+    }
+};
+
+// x, delta, A, B, C, D, gate, delta_bias, softplus, initial_state, lengths, final_state, checkpoints, out, workspace, stream
+PyObject* scan(PyObject* const* x) {
+    Scan o(x, x[8], false);
+    On on(o.dev, x[15]);
+    auto& a = o.a;
+    o.take(x[9], x[10]);
+    const auto fin = state_result(x[11], o.state_shape(), o.x, at::kFloat);
+    a.final_state = static_cast<float*>(dense(fin, "final_state", at::kFloat, o.dev, o.state_shape()));
+    const at::Tensor out = rows_out(x[13], "out", o.x, &a.out);
+    size_t bytes = 0;
+    std::optional<at::Tensor> kept;
+    if (THPVariable_Check(x[12])) {
+        kept = THPVariable_Unpack(x[12]);
+    } else if (truth(x[12])) {
+        check(es_selective_scan_checkpoints(&a, &bytes));
+        kept = at::empty({static_cast<int64_t>(bytes)}, o.x.options().dtype(at::kByte));
+    }
+    o.kept(kept);
+    check(es_selective_scan_workspace(&a, nullptr, &bytes));
+    const auto ws = workspace(x[14], bytes, o.x, &a.workspace, &a.workspace_bytes);
+    check(es_selective_scan(&a, on.handle));
+    return result({out, fin, kept});
+}
+
+// x, delta, A, B, C, D, gate, delta_bias, grad_out, softplus, initial_state, grad_final_state, lengths, checkpoints, workspace, stream
+PyObject* scan_backward(PyObject* const* x) {
+    Scan o(x, x[9], false);
+    On on(o.dev, x[15]);
+    auto& a = o.a;
+    o.take(x[10], x[12]);
+    o.kept(maybe(x[13], "checkpoints"));
+    const at::Tensor go = tensor(x[8], "grad_out");
+    const auto gfin = maybe(x[11], "grad_final_state");
+    es_selective_scan_grads g{};
+    g.grad_out = rows_like(go, "grad_out", o.x);
+    g.grad_final_state = static_cast<const float*>(dense(gfin, "grad_final_state", at::kFloat, o.dev, o.state_shape()));
+    const at::Tensor gx = rows_out(Py_None, "grad_x", o.x, &g.grad_x), gdelta = rows_out(Py_None, "grad_delta", o.x, &g.grad_delta);
+    const at::Tensor gB = empty(o.B.sizes(), o.x, o.type), gC = empty(o.C.sizes(), o.x, o.type), gA = empty(o.A.sizes(), o.x, at::kFloat);
+    g.grad_b = view(gB, "grad_B", o.type, o.dev, 4);
+    g.grad_c = view(gC, "grad_C", o.type, o.dev, 4);
+    g.grad_a = static_cast<float*>(gA.data_ptr());
+    std::optional<at::Tensor> ggate, gD, gbias, gi;
+    if (o.gate) ggate = rows_out(Py_None, "grad_gate", o.x, &g.grad_gate);
+    if (o.D) {
+        gD = empty(o.D->sizes(), o.x, at::kFloat);
+        g.grad_skip = static_cast<float*>(gD->data_ptr());
+    }
+    if (o.bias) {
+        gbias = empty(o.bias->sizes(), o.x, at::kFloat);
+        g.grad_delta_bias = static_cast<float*>(gbias->data_ptr());
+    }
+    if (o.init) {
+        gi = empty(o.state_shape(), o.x, at::kFloat);
+        g.grad_initial_state = static_cast<float*>(gi->data_ptr());
+    }
+    size_t bytes = 0;
+    check(es_selective_scan_workspace(&a, &g, &bytes));
+    const auto ws = workspace(x[14], bytes, o.x, &a.workspace, &a.workspace_bytes);
+    check(es_selective_scan_backward(&a, &g, on.handle));
+    return result({gx, gdelta, gA, gB, gC, gD, ggate, gbias, gi});
+}
+
+// x, delta, A, B, C, D, gate, delta_bias, state, softplus, state_out, out, stream
+PyObject* scan_step(PyObject* const* x) {
+    Scan o(x, x[9], true);
+    On on(o.dev, x[12]);
+    auto& a = o.a;
+    const at::Tensor state = tensor(x[8], "state");
+    auto next = maybe(x[10], "state_out");
+    if (!next) next = state;
+    a.initial_state = static_cast<const float*>(dense(state, "state", at::kFloat, o.dev, o.state_shape()));
+    a.final_state = static_cast<float*>(dense(next, "state_out", at::kFloat, o.dev, o.state_shape()));
+    const at::Tensor out = rows_out(x[11], "out", o.x, &a.out);
+    check(es_selective_scan_step(&a, on.handle));
+    return result({out, next});
+}
+
+// what both directions of the group norm share, from x[0..7]: x, weight, bias, gate, gate_first, center, activation, eps
+struct Norm {
+    at::Tensor x;
+    std::optional<at::Tensor> w, b, gate;
+    at::Device dev{at::kCPU};
+    at::ScalarType type, wtype;
+    es_group_norm_args a{};
+    explicit Norm(PyObject* const* p)
+        : x(first(p[0], "x")), w(maybe(p[1], "weight")), b(maybe(p[2], "bias")), gate(maybe(p[3], "gate")), dev(x.device()),
+          type(x.scalar_type()), wtype(weight_type({&w, &b}, "weight and bias")) {
+        a.dtype = dtype_of(x);
+        a.weight_dtype = wtype == at::kBFloat16 ? ES_BF16 : ES_F32;
+        a.x = view(x, "x", type, dev, 4);
+        a.batch = x.size(0);
+        a.length = x.size(1);
+        a.dim = x.size(3);
+        a.weight = dense(w, "weight", wtype, dev, {x.size(2), x.size(3)});
+        a.bias = dense(b, "bias", wtype, dev, {x.size(2), x.size(3)});
+        if (gate) {
+            shaped(*gate, "gate", x.sizes());
+            a.gate = view(*gate, "gate", type, dev, 4);
+        }
+        a.gate_first = truth(p[4]);
+        a.center = truth(p[5]);
+        a.activation = truth(p[6]);
+        a.eps = number(p[7], "eps");
+    }
+    at::Tensor out(PyObject* given, const char* name, es_heads* v) {
+        auto t = maybe(given, name);
+        if (!t) t = empty(x.sizes(), x, type);
+        shaped(*t, name, x.sizes());
+        *v = view(*t, name, type, dev, 4);
+        return *t;
+    }
+};
+
+// ..., out, stream
+PyObject* norm(PyObject* const* x) {
+    Norm o(x);
+    On on(o.dev, x[9]);
+    const at::Tensor out = o.out(x[8], "out", &o.a.out);
+    check(es_group_norm(&o.a, on.handle));
+    return result({out});
+}
+
+// ..., grad_out, workspace, stream
+PyObject* norm_backward(PyObject* const* x) {
+    Norm o(x);
+    On on(o.dev, x[10]);
+    const at::Tensor go = tensor(x[8], "grad_out");
+    es_group_norm_grads g{};
+    shaped(go, "grad_out", o.x.sizes());
+    g.grad_out = view(go, "grad_out", o.type, o.dev, 4);
+    const at::Tensor gx = o.out(Py_None, "grad_x", &g.grad_x);
+    std::optional<at::Tensor> gw, gb, ggate;
+    if (o.gate) ggate = o.out(Py_None, "grad_gate", &g.grad_gate);
+    if (o.w) {
+        gw = empty(o.w->sizes(), o.x, o.wtype);
+        g.grad_weight = gw->data_ptr();
+    }
+    if (o.b) {
+        gb = empty(o.b->sizes(), o.x, o.wtype);
+        g.grad_bias = gb->data_ptr();
+    }
+    size_t bytes = 0;
+    check(es_group_norm_workspace(&o.a, &g, &bytes));
+    const auto ws = workspace(x[9], bytes, o.x, &o.a.workspace, &o.a.workspace_bytes);
+    check(es_group_norm_backward(&o.a, &g, on.handle));
+    return result({gx, gw, gb, ggate});
+}
+
 // One Python entry: the number of arguments is fixed (sequence.py passes them
 // all), every exception becomes a Python one.
 template <PyObject* (*F)(PyObject* const*), Py_ssize_t N>
@@ -469,6 +819,14 @@ PyMethodDef methods[] = {
     ENTRY("linear_attention_step", attention_step, 9),
     ENTRY("qk_norm_rotate", rotate, 12),
     ENTRY("qk_norm_rotate_backward", rotate_backward, 13),
+    ENTRY("causal_conv", conv, 9),
+    ENTRY("causal_conv_backward", conv_backward, 10),
+    ENTRY("causal_conv_step", conv_step, 8),
+    ENTRY("selective_scan", scan, 16),
+    ENTRY("selective_scan_backward", scan_backward, 16),
+    ENTRY("selective_scan_step", scan_step, 13),
+    ENTRY("group_norm", norm, 10),
+    ENTRY("group_norm_backward", norm_backward, 11),
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

@@ -1,6 +1,8 @@
 """The sequence-layer operators: linear attention with a decay for each head
 (chunked for prompts and training, recurrent for single tokens) and the norm
-of queries and keys with the position rotation.
+of queries and keys with the position rotation; the short causal convolution,
+the selective scan (each for prompts, training and single tokens) and the group
+norm with a gate.
 
 Thin wrappers like ``binding``'s (``include/es.h`` holds the contract): tensors
 are CUDA tensors in float32 or bfloat16, any strides with an innermost stride
@@ -30,12 +32,17 @@ from . import binding
 from . import build as _build
 from .binding import EsError, LibraryMissing, PATHS, _check
 
-# es_linear_attention_args, es_linear_attention_grads, es_qk_norm_rotate_args,
-# es_qk_norm_rotate_grads: every field is 64 bits wide (for the plans, which take no tensors)
+# The structs of include/es.h, in its order: every field is 64 bits wide (for the plans, which take no tensors)
 _ATTN = struct.Struct("6qd20q5q5q")
 _ATTN_GRADS = struct.Struct("20q3q")
 _ROTATE = struct.Struct("7qd20q4q5q2q")
 _ROTATE_GRADS = struct.Struct("10q2q")
+_CONV = struct.Struct("7q6q7q")
+_CONV_GRADS = struct.Struct("6q4q")
+_SCAN = struct.Struct("7q12q10q10q")
+_SCAN_GRADS = struct.Struct("12q10q5q")
+_NORM = struct.Struct("8qd15q4q")
+_NORM_GRADS = struct.Struct("15q2q")
 
 _lock = threading.Lock()
 _native_module = None
@@ -161,3 +168,190 @@ def qk_norm_rotate_backward(q, k, q_weight, k_weight, cos, sin, grad_q_out, grad
     grad_k_weight), None where there is no operand."""
     return (_native_module or _native()).qk_norm_rotate_backward(q, k, q_weight, k_weight, cos, sin, positions, eps,
                                                                  neighbours, grad_q_out, grad_k_out, workspace, stream)
+
+
+def causal_conv(x, weight, bias=None, initial_state=None, lengths=None, activation: bool = True,
+                final_state: Union[bool, torch.Tensor] = False, out=None, stream=None):
+    """The short causal convolution of each channel:
+
+        p[t] = bias + sum_j weight[:, j] * x[t - W + 1 + j],    out = p / (1 + exp(-p))
+
+    (or p, without ``activation``).  x [B, T, C]; ``weight`` [C, W], W 2..8, and
+    ``bias`` [C] in one dtype; ``initial_state`` [B, W - 1, C] in x's dtype: the
+    inputs before the first token, oldest first (None: zeros); ``lengths`` int32
+    [B]: tokens past a row's length are not read and give zeros.  Returns (out,
+    the last W - 1 inputs or None); ``final_state`` is True, or the tensor to
+    write them to (which may be ``initial_state``).
+    """
+    return (_native_module or _native()).causal_conv(x, weight, bias, initial_state, lengths, activation, final_state, out, stream)
+
+
+def causal_conv_backward(x, weight, bias, grad_out, initial_state=None, grad_final_state=None, lengths=None,
+                         activation: bool = True, workspace=None, stream=None):
+    """Gradients of ``causal_conv``: (grad_x, grad_weight, grad_bias or None,
+    grad_initial_state or None)."""
+    return (_native_module or _native()).causal_conv_backward(x, weight, bias, grad_out, initial_state, grad_final_state,
+                                                              lengths, activation, workspace, stream)
+
+
+def causal_conv_step(x, weight, bias, state, state_out=None, activation: bool = True, out=None, stream=None):
+    """One token of each batch row: x [B, C], ``state`` [B, W - 1, C].  Returns
+    (out [B, C], the new state): ``state`` itself, updated in place, unless
+    ``state_out`` is given."""
+    return (_native_module or _native()).causal_conv_step(x, weight, bias, state, state_out, activation, out, stream)
+
+
+def selective_scan(x, delta, A, B, C, D=None, gate=None, delta_bias=None, softplus: bool = True, initial_state=None,
+                   lengths=None, final_state: Union[bool, torch.Tensor] = False,
+                   checkpoints: Union[bool, torch.Tensor] = False, out=None, workspace=None, stream=None):
+    """The selective state-space scan: for each channel c, with N states,
+
+        d[t] = log(1 + exp(delta[t] + delta_bias))
+        h[t] = exp(d[t] * A[c]) * h[t-1] + d[t] * x[t] * B[t]
+        out[t] = (C[t] . h[t] + D[c] * x[t]) * gate[t] / (1 + exp(-gate[t]))
+
+    (d the sum itself without ``softplus``; no last factor without ``gate``).
+    x, delta, gate [B, T, channels]; A [channels, N] f32, N 1..64, meant to be
+    negative; B, C [B, T, groups, N], the groups dividing the channels; D,
+    ``delta_bias`` f32 [channels]; ``initial_state`` f32 [B, channels, N];
+    ``lengths`` int32 [B]: tokens past a row's length are not read and give
+    zeros.  Returns (out, the last state or None, checkpoints or None).
+    ``final_state`` is True, or the tensor to write it to (which may be
+    ``initial_state``); ``checkpoints`` likewise: states on the way, which
+    ``selective_scan_backward`` of the same operands takes.
+    """
+    return (_native_module or _native()).selective_scan(x, delta, A, B, C, D, gate, delta_bias, softplus, initial_state,
+                                                        lengths, final_state, checkpoints, out, workspace, stream)
+
+
+def selective_scan_backward(x, delta, A, B, C, D, gate, delta_bias, grad_out, softplus: bool = True, initial_state=None,
+                            grad_final_state=None, lengths=None, checkpoints=None, workspace=None, stream=None):
+    """Gradients of ``selective_scan``: (grad_x, grad_delta, grad_A, grad_B,
+    grad_C, grad_D, grad_gate, grad_delta_bias, grad_initial_state), None where
+    there is no operand.  Without ``checkpoints`` the states on the way are
+    found again first."""
+    return (_native_module or _native()).selective_scan_backward(x, delta, A, B, C, D, gate, delta_bias, grad_out, softplus,
+                                                                 initial_state, grad_final_state, lengths, checkpoints,
+                                                                 workspace, stream)
+
+
+def selective_scan_step(x, delta, A, B, C, D, gate, delta_bias, state, softplus: bool = True, state_out=None, out=None,
+                        stream=None):
+    """One token of each batch row: x, delta, gate [B, channels], B, C [B,
+    groups, N], ``state`` f32 [B, channels, N].  Returns (out [B, channels], the
+    new state): ``state`` itself, updated in place, unless ``state_out`` is
+    given."""
+    return (_native_module or _native()).selective_scan_step(x, delta, A, B, C, D, gate, delta_bias, state, softplus,
+                                                             state_out, out, stream)
+
+
+def group_norm(x, weight=None, bias=None, gate=None, gate_first: bool = False, center: bool = True, activation: bool = False,
+               eps: float = 1e-5, out=None, stream=None):
+    """The norm of each group (head) of a token's channels, with a gate: for x
+    [B, T, H, D], s(z) = z / (1 + exp(-z)),
+
+        (u - mean(u)) / sqrt(var(u) + eps) * weight + bias,   u = x
+
+    times s(gate), or with ``gate_first`` for u = x * s(gate); without
+    ``center`` u / sqrt(mean(u^2) + eps).  ``weight``, ``bias`` [H, D] in one
+    dtype, or None; without a gate, ``activation`` makes y into s(y).  D
+    1..8192."""
+    return (_native_module or _native()).group_norm(x, weight, bias, gate, gate_first, center, activation, eps, out, stream)[0]
+
+
+def group_norm_backward(x, weight, bias, gate, grad_out, gate_first: bool = False, center: bool = True,
+                        activation: bool = False, eps: float = 1e-5, workspace=None, stream=None):
+    """Gradients of ``group_norm``: (grad_x, grad_weight, grad_bias,
+    grad_gate), None where there is no operand."""
+    return (_native_module or _native()).group_norm_backward(x, weight, bias, gate, gate_first, center, activation, eps,
+                                                             grad_out, workspace, stream)
+
+
+_DTYPES = {"f32": 0, "bf16": 1}
+
+
+def _planned(op: str, args: bytes, grads: Optional[bytes]) -> dict:
+    info, n = binding.PlanInfo(), ctypes.c_size_t()
+    L = binding.lib()
+    _check(getattr(L, "es_plan_" + op)(args, grads, ctypes.byref(info)))
+    _check(getattr(L, "es_%s_workspace" % op)(args, grads, ctypes.byref(n)))
+    return {"O": info.O, "T": info.T, "J": info.J, "W": info.W, "elements": info.elements, "path": PATHS[info.path],
+            "workspace": n.value}
+
+
+class _Places:
+    """Stand-in addresses and dense views of a plan's operands; ``ptrs`` and
+    ``strides`` (by name) replace them."""
+
+    def __init__(self, ptrs, strides):
+        self.ptrs, self.strides, self.count = ptrs or {}, strides or {}, 0
+
+    def at(self, name, there=True):
+        self.count += 1
+        return self.ptrs.get(name, self.count << 44 if there else 0)
+
+    def rows(self, name, shape, there=True):
+        b, t, c = shape
+        return (self.at(name, there),) + tuple(self.strides.get(name, (t * c, c)))
+
+    def heads(self, name, shape, there=True):
+        b, t, h, d = shape
+        return (self.at(name, there),) + tuple(self.strides.get(name, (t * h * d, h * d, d))) + (h,)
+
+
+def plan_causal_conv(shape, taps: int, dtype="bf16", weight_dtype=None, bias=True, lengths=False, state=False, backward=False,
+                     ptrs=None, strides=None) -> dict:
+    """Validate and plan a call without a GPU (pure host logic): x's ``shape``
+    [B, T, C]; ``ptrs`` and ``strides`` ({"x": ...}) replace dense stand-ins."""
+    p = _Places(ptrs, strides)
+    b, t, c = shape
+    args = _CONV.pack(_DTYPES.get(dtype, 9), _DTYPES.get(weight_dtype or dtype, 9), b, t, c, taps, 1, *p.rows("x", shape),
+                      *p.rows("out", shape), p.at("weight"), p.at("bias", bias), p.at("lengths", lengths),
+                      p.at("initial_state", state), p.at("final_state", state and not backward), p.at("workspace", False),
+                      1 << 50)
+    grads = None
+    if backward:
+        grads = _CONV_GRADS.pack(*p.rows("grad_out", shape), *p.rows("grad_x", shape), p.at("grad_weight"),
+                                 p.at("grad_bias", bias), p.at("grad_final_state", state), p.at("grad_initial_state", state))
+    return _planned("causal_conv", args, grads)
+
+
+def plan_selective_scan(shape, states: int, groups: int = 1, dtype="bf16", gate=True, skip=True, delta_bias=True, lengths=False,
+                        state=False, checkpoints=False, backward=False, ptrs=None, strides=None) -> dict:
+    """Validate and plan a call without a GPU, as ``plan_causal_conv``; the
+    result also holds the bytes of its "checkpoints"."""
+    p = _Places(ptrs, strides)
+    b, t, c = shape
+    bc = (b, t, groups, states)
+    args = _SCAN.pack(_DTYPES.get(dtype, 9), b, t, c, states, groups, 1, *p.rows("x", shape), *p.rows("delta", shape),
+                      *p.rows("gate", shape, gate), *p.rows("out", shape), *p.heads("b", bc), *p.heads("c", bc), p.at("a"),
+                      p.at("skip", skip), p.at("delta_bias", delta_bias), p.at("lengths", lengths), p.at("initial_state", state),
+                      p.at("final_state", state and not backward), p.at("checkpoints", checkpoints), 1 << 50,
+                      p.at("workspace", False), 1 << 50)
+    grads = None
+    if backward:
+        grads = _SCAN_GRADS.pack(*p.rows("grad_out", shape), *p.rows("grad_x", shape), *p.rows("grad_delta", shape),
+                                 *p.rows("grad_gate", shape, gate), *p.heads("grad_b", bc), *p.heads("grad_c", bc),
+                                 p.at("grad_a"), p.at("grad_skip", skip), p.at("grad_delta_bias", delta_bias),
+                                 p.at("grad_final_state", state), p.at("grad_initial_state", state))
+    plan = _planned("selective_scan", args, grads)
+    n = ctypes.c_size_t()
+    _check(binding.lib().es_selective_scan_checkpoints(args, ctypes.byref(n)))
+    plan["checkpoints"] = n.value
+    return plan
+
+
+def plan_group_norm(shape, dtype="bf16", weight_dtype=None, weight=True, bias=True, gate=True, gate_first=False, center=True,
+                    activation=False, eps=1e-5, backward=False, ptrs=None, strides=None) -> dict:
+    """Validate and plan a call without a GPU, as ``plan_causal_conv``: x's
+    ``shape`` is [B, T, H, D]."""
+    p = _Places(ptrs, strides)
+    b, t, h, d = shape
+    args = _NORM.pack(_DTYPES.get(dtype, 9), _DTYPES.get(weight_dtype or dtype, 9), b, t, d, center, gate_first, activation, eps,
+                      *p.heads("x", shape), *p.heads("gate", shape, gate), *p.heads("out", shape), p.at("weight", weight),
+                      p.at("bias", bias), p.at("workspace", False), 1 << 50)
+    grads = None
+    if backward:
+        grads = _NORM_GRADS.pack(*p.heads("grad_out", shape), *p.heads("grad_x", shape), *p.heads("grad_gate", shape, gate),
+                                 p.at("grad_weight", weight), p.at("grad_bias", bias))
+    return _planned("group_norm", args, grads)

@@ -803,6 +803,219 @@ es_status es_qk_norm_rotate_workspace(const es_qk_norm_rotate_args *args,
 es_status es_plan_qk_norm_rotate(const es_qk_norm_rotate_args *args,
                                  const es_qk_norm_rotate_grads *grads, es_plan_info *info);
 
+/* ---------------------------------------------------------------------------
+ * The state-space layer: the short causal convolution, the selective scan and
+ * the group norm with a gate.
+ *
+ * Operands [B, T, channels] are es_rows: an innermost stride of 1 and any other
+ * strides (in elements, not negative; an output's not zero where its extent is
+ * above one), so halves of one projection's result are taken as they lie.
+ * Tokens at and past a row's length (lengths: device i32 [B], clamped to 0..T;
+ * null: all T) are not read, and their results and gradients are 0. */
+typedef struct es_rows {
+    void *data;
+    int64_t stride_b, stride_t;
+} es_rows;
+
+/*
+ * es_causal_conv -- for each channel, with `taps` weights w:
+ *
+ *     p[t] = bias + sum_j w[j] x[t - taps + 1 + j]
+ *     out[t] = p[t] / (1 + e^-p[t])   (activation), or p[t]
+ *
+ *   dtype, weight_dtype   of x, out and the states; of weight and bias (ES_F32 or
+ *                     ES_BF16; else ES_E_DIM_002).
+ *   taps              2..8.
+ *   weight, bias      [channels, taps] dense; [channels] or null (zero).
+ *   initial_state     [B, taps - 1, channels] dense, of dtype: the inputs before
+ *                     the first token, oldest first; null: zeros.
+ *   final_state       the same for the next call: the last taps - 1 inputs up to
+ *                     each row's length; null: not wanted.  It may be
+ *                     initial_state itself.
+ *   out               may not overlap an input.
+ * Sums are f32, rounded once.
+ */
+typedef struct es_causal_conv_args {
+    int64_t dtype, weight_dtype, batch, length, channels, taps, activation;
+    es_rows x, out;
+    const void *weight, *bias;
+    const int32_t *lengths;
+    const void *initial_state;
+    void *final_state;
+    void *workspace;
+    int64_t workspace_bytes;
+} es_causal_conv_args;
+
+es_status es_causal_conv(const es_causal_conv_args *args, es_stream_t stream);
+
+/*
+ * es_causal_conv_backward -- from grad_out and, where not null,
+ * grad_final_state: grad_x, grad_weight and grad_bias (of weight_dtype; null:
+ * not wanted), grad_initial_state (null: not wanted).  args->out and
+ * args->final_state are not used.  The weights' sums are f32, in a fixed order
+ * (the same bits each time), through the workspace.
+ */
+typedef struct es_causal_conv_grads {
+    es_rows grad_out, grad_x;
+    void *grad_weight, *grad_bias;
+    const void *grad_final_state;
+    void *grad_initial_state;
+} es_causal_conv_grads;
+
+es_status es_causal_conv_backward(const es_causal_conv_args *args, const es_causal_conv_grads *grads,
+                                  es_stream_t stream);
+
+/* Workspace bytes of a backward call (a forward call needs none). */
+es_status es_causal_conv_workspace(const es_causal_conv_args *args, const es_causal_conv_grads *grads,
+                                   size_t *bytes);
+
+/* Validate a forward (grads null) or backward call without a GPU: O, T, J =
+ * B, T, channels; W = taps; elements of `out`. */
+es_status es_plan_causal_conv(const es_causal_conv_args *args, const es_causal_conv_grads *grads,
+                              es_plan_info *info);
+
+/*
+ * es_causal_conv_step -- one token of each batch row: length 1, no lengths
+ * (x.stride_t and out.stride_t are unused); both states are required, and may
+ * be the same.
+ */
+es_status es_causal_conv_step(const es_causal_conv_args *args, es_stream_t stream);
+
+/*
+ * es_selective_scan -- for each batch row and channel c of group g, with a
+ * state of `states` values:
+ *
+ *     d[t] = log(1 + e^(delta[t] + delta_bias))   (softplus), or the sum itself
+ *     h[t, n] = e^(d[t] a[c, n]) h[t-1, n] + d[t] x[t] b[t, g, n]
+ *     y[t] = sum_n c[t, g, n] h[t, n] + skip[c] x[t]
+ *     out[t] = y[t] gate[t] / (1 + e^-gate[t])    (or y[t] without a gate)
+ *
+ *   dtype             of x, delta, gate, b, c, out (ES_F32 or ES_BF16).
+ *   states            1..64; a device f32 [channels, states] dense, meant to be
+ *                     <= 0 (with d >= 0 the decays are then at most 1; below
+ *                     e^-87 they are zero).
+ *   b, c              [B, T, groups, states]; the groups divide the channels, and
+ *                     channel i reads group i / (channels / groups).
+ *   skip, delta_bias  device f32 [channels], or null (zero).
+ *   gate              data null: no gate.
+ *   initial_state     device f32 [B, channels, states] dense, or null (zero);
+ *                     final_state the same, or null; it may be initial_state
+ *                     itself.
+ *   checkpoints       null, or es_selective_scan_checkpoints bytes, 16-byte
+ *                     aligned, written: states on the way, which the backward
+ *                     call of the same operands takes instead of finding them
+ *                     again.
+ *   out               may not overlap an input.
+ *   workspace         es_selective_scan_workspace bytes, 16-byte aligned (may be
+ *                     null where that is 0).
+ * States and sums are f32; results are rounded once.  Operands are meant to be
+ * finite: an infinity or NaN makes NaNs of its own channel's later tokens (in b
+ * or c of its group's), and in a backward call of its row's earlier ones too.
+ */
+typedef struct es_selective_scan_args {
+    int64_t dtype, batch, length, channels, states, groups, softplus;
+    es_rows x, delta, gate, out;
+    es_heads b, c;
+    const float *a, *skip, *delta_bias;
+    const int32_t *lengths;
+    const float *initial_state;
+    float *final_state;
+    void *checkpoints;
+    int64_t checkpoints_bytes;
+    void *workspace;
+    int64_t workspace_bytes;
+} es_selective_scan_args;
+
+es_status es_selective_scan(const es_selective_scan_args *args, es_stream_t stream);
+
+/*
+ * es_selective_scan_backward -- from grad_out and, where not null,
+ * grad_final_state: grad_x, grad_delta, grad_gate (data null exactly where
+ * there is no gate), grad_b, grad_c [B, T, groups, states] of dtype, summed
+ * over the group's channels; f32 grad_a [channels, states], grad_skip,
+ * grad_delta_bias [channels], grad_initial_state (each null: not wanted).
+ * args->checkpoints: those the forward call of the same operands wrote, or
+ * null (they are then found first, in the workspace).  args->out and
+ * args->final_state are not used.  All sums are taken in a fixed order.
+ */
+typedef struct es_selective_scan_grads {
+    es_rows grad_out, grad_x, grad_delta, grad_gate;
+    es_heads grad_b, grad_c;
+    float *grad_a, *grad_skip, *grad_delta_bias;
+    const float *grad_final_state;
+    float *grad_initial_state;
+} es_selective_scan_grads;
+
+es_status es_selective_scan_backward(const es_selective_scan_args *args, const es_selective_scan_grads *grads,
+                                     es_stream_t stream);
+
+/* Workspace bytes of a forward (grads null) or backward call, and the bytes of
+ * its checkpoints. */
+es_status es_selective_scan_workspace(const es_selective_scan_args *args, const es_selective_scan_grads *grads,
+                                      size_t *bytes);
+es_status es_selective_scan_checkpoints(const es_selective_scan_args *args, size_t *bytes);
+
+/* Validate a forward (grads null) or backward call without a GPU: O, T, J, W =
+ * B, T, channels, states; elements of `out`. */
+es_status es_plan_selective_scan(const es_selective_scan_args *args, const es_selective_scan_grads *grads,
+                                 es_plan_info *info);
+
+/*
+ * es_selective_scan_step -- one token of each batch row: length 1, no lengths,
+ * no checkpoints, no workspace (strides over tokens are unused); both states
+ * are required, and may be the same.
+ */
+es_status es_selective_scan_step(const es_selective_scan_args *args, es_stream_t stream);
+
+/*
+ * es_group_norm -- for each row u of `dim` values of a token's heads (the
+ * groups of its channels, side by side):
+ *
+ *     n = (u - mean(u)) / sqrt(var(u) + eps)     (center), or
+ *         u / sqrt(mean(u^2) + eps)
+ *     y = n * weight + bias                      (each [heads, dim] dense or null)
+ *
+ * with s(z) = z / (1 + e^-z):
+ *     gate, gate_first = 0:   u = x,         out = y s(gate)
+ *     gate, gate_first = 1:   u = x s(gate), out = y
+ *     no gate (data null):    u = x,         out = s(y) with activation, else y
+ *
+ *   dtype, weight_dtype   of x, gate, out; of weight and bias.
+ *   dim               1..8192 (var is the mean square distance from the mean).
+ *   out               may not overlap an input.
+ * activation goes without a gate only (ES_E_ARG).  Sums are f32.
+ */
+typedef struct es_group_norm_args {
+    int64_t dtype, weight_dtype, batch, length, dim, center, gate_first, activation;
+    double eps;
+    es_heads x, gate, out;
+    const void *weight, *bias;
+    void *workspace;
+    int64_t workspace_bytes;
+} es_group_norm_args;
+
+es_status es_group_norm(const es_group_norm_args *args, es_stream_t stream);
+
+/*
+ * es_group_norm_backward -- grad_x, grad_gate (data null exactly where there is
+ * no gate), grad_weight and grad_bias (of weight_dtype; null: not wanted; sums
+ * in a fixed order through the workspace).  args->out is not used.
+ */
+typedef struct es_group_norm_grads {
+    es_heads grad_out, grad_x, grad_gate;
+    void *grad_weight, *grad_bias;
+} es_group_norm_grads;
+
+es_status es_group_norm_backward(const es_group_norm_args *args, const es_group_norm_grads *grads,
+                                 es_stream_t stream);
+
+es_status es_group_norm_workspace(const es_group_norm_args *args, const es_group_norm_grads *grads,
+                                  size_t *bytes);
+
+/* Validate a forward (grads null) or backward call without a GPU. */
+es_status es_plan_group_norm(const es_group_norm_args *args, const es_group_norm_grads *grads,
+                             es_plan_info *info);
+
 /* Synchronise `stream`, then read and clear this device's status word.
  * Returns ES_E_TIMEOUT if a kernel since the last check gave up a bounded
  * wait (its outputs are then incomplete), ES_E_CUDA if the synchronisation
