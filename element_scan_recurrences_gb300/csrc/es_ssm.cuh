@@ -74,8 +74,53 @@ __device__ __forceinline__ float softplus(float x) {
     return fmaf(0.5f, m, 0.5f * x) + log1p_poly(exp_f32(-fminf(m, 87.0f)));
 }
 
+// The same of two values; without EXACT the exponent's rounding is left (|z| 2^-24
+// of e^-z, for results rounded to bf16).
+__device__ __forceinline__ float2 pair_of(float v) { return make_float2(v, v); }
+
+template <bool EXACT>
+__device__ __forceinline__ float2 pair_exp(float2 x) {
+    const float2 t = pair_mul(x, pair_of(kLog2e));
+    const float2 e = make_float2(exp2_hw(t.x), exp2_hw(t.y));
+    if constexpr (!EXACT) return e;
+    const float2 lost = pair_fma(x, pair_of(kLog2eLow), pair_fma(x, pair_of(kLog2e), make_float2(-t.x, -t.y)));
+    return pair_fma(e, pair_mul(lost, pair_of(kLn2)), e);
+}
+
+template <bool EXACT>
+__device__ __forceinline__ float2 pair_logistic(float2 z) {
+    const float2 e = pair_exp<EXACT>(make_float2(-fmaxf(z.x, -87.0f), -fmaxf(z.y, -87.0f)));
+    const float2 d = pair_add(e, pair_of(1.0f));
+    return make_float2(rcp_hw(d.x), rcp_hw(d.y));
+}
+
+__device__ __forceinline__ float2 pair_softplus(float2 x) {
+    const float2 m = make_float2(fabsf(x.x), fabsf(x.y));
+    const float2 e = pair_exp<true>(make_float2(-fminf(m.x, 87.0f), -fminf(m.y, 87.0f)));
+    float2 p = pair_fma(e, pair_of(-0.003244024235755205f), pair_of(0.019851457327604294f));
+    p = pair_fma(p, e, pair_of(-0.056959524750709534f));
+    p = pair_fma(p, e, pair_of(0.10603653639554977f));
+    p = pair_fma(p, e, pair_of(-0.15305592119693756f));
+    p = pair_fma(p, e, pair_of(0.1967593878507614f));
+    p = pair_fma(p, e, pair_of(-0.24954134225845337f));
+    p = pair_fma(p, e, pair_of(0.3332996368408203f));
+    p = pair_fma(p, e, pair_of(-0.4999990165233612f));
+    p = pair_fma(p, e, pair_of(1.0f));
+    return pair_fma(p, e, pair_fma(m, pair_of(0.5f), pair_mul(x, pair_of(0.5f))));
+}
+
 // d/dz of z s(z), s = logistic(z)
 __device__ __forceinline__ float silu_slope(float z, float s) { return fmaf(z * s, 1.0f - s, s); }
+
+// two neighbouring values in shared memory
+__device__ __forceinline__ float2 load_two(const float* p) { return *reinterpret_cast<const float2*>(p); }
+__device__ __forceinline__ float2 load_two(const __nv_bfloat16* p) {
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p));
+}
+__device__ __forceinline__ void store_two(float* p, float2 v) { *reinterpret_cast<float2*>(p) = v; }
+__device__ __forceinline__ void store_two(__nv_bfloat16* p, float2 v) {
+    *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v.x, v.y);
+}
 
 // V neighbouring values in one access
 template <typename T, int V>
@@ -113,9 +158,11 @@ __device__ __forceinline__ void copy16(void* to, const void* from, int n) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(a), "l"(from), "r"(n) : "memory");
 }
 __device__ __forceinline__ void copies_done() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// all groups but the LEFT last ones are there (0: every copy, in a group or not)
 template <int LEFT>
 __device__ __forceinline__ void copies_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+    if constexpr (LEFT == 0) asm volatile("cp.async.wait_all;" ::: "memory");
+    else asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
 }
 
 // a row's tokens that count

@@ -77,11 +77,10 @@ struct ScanBackward {
     float *part_c;              // [segs * B][C][N + 2]: of a, skip, bias
 };
 
-// channels one CTA of the kernels takes
-inline int scan_block_channels(int N) { return N <= 16 ? 128 : N <= 32 ? 64 : 32; }
-inline int64_t scan_blocks(int64_t C, int G, int N) {      // CTAs over a group's channels
-    return (C / G + scan_block_channels(N) - 1) / scan_block_channels(N);
-}
+// channels a CTA takes, forwards and backwards, and CTAs over the channels of a group
+inline int scan_channels(int N) { return N <= 8 ? 64 : N <= 16 ? 32 : N <= 32 ? 16 : 8; }
+inline int scan_bwd_channels(int N) { return 4 * scan_channels(N); }
+inline int64_t scan_blocks(int64_t C, int G, int channels) { return (C / G + channels - 1) / channels; }
 // `keep_only`: nothing but the kept states is computed
 cudaError_t launch_scan(const ScanLaunch& L, bool keep_only, int* kernels);
 // gradients that the segments' own tokens leave (seg_state, seg_sum, from the second segment on)

@@ -269,14 +269,15 @@ es_status plan_scan(const char* fn, const es_selective_scan_args* a, const es_se
     P->fwd_segs = 1;
     P->fwd_seg_chunks = L.seg_chunks;
     if (!P->empty) {
-        const int64_t ctas = G * scan_blocks(C, static_cast<int>(G), static_cast<int>(N)) * B;
+        const int g = static_cast<int>(G), n = static_cast<int>(N);
+        const int64_t ctas = G * scan_blocks(C, g, scan_channels(n)) * B, back = G * scan_blocks(C, g, scan_bwd_channels(n)) * B;
         size_t at = 0;
-        if (!step) P->fwd_segs = scan_segments(ctas, L.chunks, 4, &P->fwd_seg_chunks);
+        if (!step) P->fwd_segs = scan_segments(ctas, L.chunks, 8, &P->fwd_seg_chunks);
         if (!backward) {
             L.segs = P->fwd_segs;
             L.seg_chunks = P->fwd_seg_chunks;
         } else {
-            L.segs = scan_segments(ctas, L.chunks, 1, &L.seg_chunks);
+            L.segs = scan_segments(back, L.chunks, 1, &L.seg_chunks);
             P->find = L.kept == nullptr && L.chunks > 0;
         }
         int64_t segs = L.segs;
@@ -290,7 +291,7 @@ es_status plan_scan(const char* fn, const es_selective_scan_args* a, const es_se
         }
         if (backward) {
             if (P->find) P->kept = take(&at, static_cast<int64_t>(P->kept_bytes));
-            P->part_bc = take(&at, 4 * (ctas / B) * B * T * 2 * N);
+            P->part_bc = take(&at, 4 * back * T * 2 * N);
             P->part_c = take(&at, 4 * segs * B * C * (N + 2));
         }
         P->bytes = at;

@@ -6,12 +6,20 @@
 //
 // Each token, channel and state costs one exponential (32 a clock an SM) and
 // four products or sums (128 a clock), against 1/2 byte of traffic at 16 states
-// in bf16: the exponentials bound it, not HBM.  So a thread owns one channel and
-// up to 16 states in registers (more states: 2 or 4 lanes a channel): what is
-// made once a token and channel (d, the gate) is made by one thread, the sum over
-// states needs no exchange, and B and C are one broadcast read for the warp.
-// Tokens come in tiles of kScanChunk through two stages of shared memory
-// (cp.async; B and C widened to f32 on the way).
+// in bf16: the exponentials bound it, not HBM.  What else could: shared memory
+// gives a warp 128 bytes a clock whether its lanes read one address or many, so
+// B and C cost 2 of 32 words a state if a lane has one channel.  So a lane holds 4
+// states of each of 4 channels (as pairs of channels, two products an instruction)
+// and 12 words serve 16 states; sums over states cross NL lanes in exchanges
+// that halve the values.
+//
+// Tokens come in tiles of kScanChunk.  Half of a CTA's warps run the states through
+// a tile, where the only chain from token to token is one product and sum; the
+// other half at the same time make what the next tile's tokens and channels need once
+// (d and d x), and the last tile's results, two channels an instruction: 50 of the
+// 133 instructions a token and channel, and half of the warps that hide each
+// other's latencies (with every warp doing all three in turn 1.7 of them were there a
+// scheduler, and it issued in 38 of 100 clocks).  One barrier a tile.
 //
 // A channel's tokens are a chain, so few channels leave the GPU idle: then the
 // tokens are cut into segments, a first pass finds the state each segment makes
@@ -23,200 +31,310 @@
 namespace es {
 namespace {
 
-constexpr int kThreads = kScanThreads;
+constexpr int kThreads = 64, kHalf = 32;             // a CTA's threads, those of either kind
 constexpr int K = kScanChunk;
+constexpr int kStages = 4;                           // tiles arriving, made ready, run, finished
 
 enum Mode { kMain, kOwnState, kOwnGrad };
 
-template <typename T, int LANES, int RN>
+template <typename T, int NL>
 struct Tile {
-    static constexpr int CB = kThreads / LANES;      // channels a CTA
-    static constexpr int NP = LANES * RN;            // states, padded
-    T x[K][CB], delta[K][CB], gate[K][CB];
-    float b[K][NP], c[K][NP];
+    static constexpr int CB = kHalf / 32 * Lanes<NL>::CW, NP = Lanes<NL>::NP;
+    struct Stage {
+        T x[K][CB], delta[K][CB], gate[K][CB], b[K][NP], c[K][NP];
+    };
+    Stage stage[kStages];
+    float d[2][K][CB], v[2][K][CB];                  // v: d x, or the gradient of y
+    float y[2][K][CB];
 };
 
-template <typename T, int LANES, int RN, bool VEC, Mode MODE>
-__global__ void __launch_bounds__(kThreads) k_sscan(const __grid_constant__ ScanArgs A) {
-    using Buf = Tile<T, LANES, RN>;
-    constexpr int CB = Buf::CB, NP = Buf::NP, P = RN / 2;
-    extern __shared__ __align__(128) unsigned char smem[];
-    Buf* const buf = reinterpret_cast<Buf*>(smem);
-    const ScanLaunch& L = A.L;
-    Place p = place_of<CB>(A);
-    if constexpr (MODE == kOwnGrad) p.seg += 1;      // the first segment's gradient enters none
-    const int sub = threadIdx.x % LANES, ch = threadIdx.x / LANES, n0 = sub * RN;
-    const int64_t c = p.first + ch;
-    const bool mine = c < p.last, wide = L.wide;
-    const int64_t len = live_tokens(L.lengths, p.b, L.T);
-    const int64_t begin = p.seg * L.seg_chunks * K;
-    const int64_t stop = begin + L.seg_chunks * K < L.T ? begin + L.seg_chunks * K : L.T;
-    const int64_t end = stop < len ? stop : len;
-    const int tiles = end > begin ? static_cast<int>((end - begin + K - 1) / K) : 0;
+// What both kinds of warps know.
+struct Run {
+    Place p;
+    int64_t begin, stop, end;    // the segment's tokens, those that count
+    int tiles;
+    template <Mode MODE>
+    __device__ __forceinline__ int64_t start(int i) const {      // tile i of the pass: from the back for the gradient's
+        return begin + static_cast<int64_t>(MODE == kOwnGrad ? tiles - 1 - i : i) * K;
+    }
+    __device__ __forceinline__ int live(int64_t t0) const { return static_cast<int>(end - t0 < K ? end - t0 : K); }
+};
 
-    float2 h[P], a2[P];
-    float skip = 0.0f, bias = 0.0f, sum = 0.0f;
+// The warps that make steps and results.
+template <typename T, int NL, Mode MODE>
+__device__ __forceinline__ void help(const ScanArgs& A, const Run& R, Tile<T, NL>& buf) {
+    constexpr int CB = Tile<T, NL>::CB, NP = Tile<T, NL>::NP, CW = Lanes<NL>::CW, PAIRS = Lanes<NL>::PAIRS, STEP = Lanes<NL>::STEP;
+    constexpr bool kWide = sizeof(T) == 4, kReads = MODE != kOwnGrad;      // kReads: x and B; else the gradient, the gate and C
+    const ScanLaunch& L = A.L;
+    const Place& p = R.p;
+    const int id = threadIdx.x % kHalf, lane = id % 32, warp = id / 32;
+    const int two = warp * CW + lane % PAIRS * 2, at0 = lane / PAIRS;
+    const int64_t c2 = p.first + two;
+    const bool in0 = c2 < p.last, in1 = c2 + 1 < p.last;
+    float2 skip = pair_of(0.f), bias = pair_of(0.f), sum = pair_of(0.f);
+    if (L.skip != nullptr) skip = make_float2(in0 ? L.skip[c2] : 0.f, in1 ? L.skip[c2 + 1] : 0.f);
+    if (L.bias != nullptr) bias = make_float2(in0 ? L.bias[c2] : 0.f, in1 ? L.bias[c2 + 1] : 0.f);
+    const bool results = MODE == kMain && !A.keep_only, gated = L.gate.data != nullptr && (results || MODE == kOwnGrad);
+    const int width = static_cast<int>(p.last - p.first);
+    auto from = [&](const es_rows& r, int64_t t0) { return static_cast<const T*>(r.data) + p.b * r.stride_b + t0 * r.stride_t + p.first; };
+    auto of_group = [&](const es_heads& r, int64_t t0) {
+        return static_cast<const T*>(r.data) + p.b * r.stride_b + t0 * r.stride_t + p.group * r.stride_h;
+    };
+    auto fetch = [&](int i) {
+        const int64_t t0 = R.start<MODE>(i);
+        const int live = R.live(t0);
+        auto& to = buf.stage[i % kStages];
+        load_tile<T, CB, kHalf>(id, to.x, from(kReads ? L.x : A.g, t0), kReads ? L.x.stride_t : A.g.stride_t, width, live, A.vec);
+        load_tile<T, CB, kHalf>(id, to.delta, from(L.delta, t0), L.delta.stride_t, width, live, A.vec);
+        if (gated) load_tile<T, CB, kHalf>(id, to.gate, from(L.gate, t0), L.gate.stride_t, width, live, A.vec);
+        if (kReads) load_tile<T, NP, kHalf>(id, to.b, of_group(L.b, t0), L.b.stride_t, L.N, live, A.vec);
+        if (MODE != kOwnState) load_tile<T, NP, kHalf>(id, to.c, of_group(L.c, t0), L.c.stride_t, L.N, live, A.vec);
+    };
+    T* const out = static_cast<T*>(L.out.data) + p.b * L.out.stride_b + c2;
+    if (R.tiles > 0) fetch(0);
+    copies_wait<0>();
+    __syncthreads();
+    for (int i = 0; i < R.tiles + 2; ++i) {
+        if (i + 1 < R.tiles) fetch(i + 1);
+        if (i < R.tiles) {
+            const auto& at = buf.stage[i % kStages];
+            const int live = R.live(R.start<MODE>(i));
+            float2 d[K / STEP], v[K / STEP];
 #pragma unroll
-    for (int i = 0; i < P; ++i) h[i] = a2[i] = make_float2(0.f, 0.f);
-    const int64_t row = (p.b * L.C + c) * L.N;       // of a [B, C, N] tensor
-    const int64_t seg_row = L.B * L.C * L.N;
-    if (mine) {
-        load_states<RN>(L.a + c * L.N, n0, L.N, wide, a2);
+            for (int k = 0; k < K / STEP; ++k) {
+                d[k] = pair_add(load_two(&at.delta[at0 + k * STEP][two]), bias);
+                v[k] = load_two(&at.x[at0 + k * STEP][two]);
+            }
+            if (L.softplus) {
 #pragma unroll
-        for (int i = 0; i < P; ++i) a2[i] = pair_mul(a2[i], make_float2(kLog2e, kLog2e));
-        if (L.skip != nullptr) skip = L.skip[c];
-        if (L.bias != nullptr) bias = L.bias[c];
-        if constexpr (MODE == kOwnGrad) {
-            if (p.seg == L.segs - 1 && A.gfin != nullptr) load_states<RN>(A.gfin + row, n0, L.N, wide, h);
-        } else if (p.seg == 0) {
-            const float* from = MODE == kMain && L.first != nullptr ? L.first : L.init;
-            if (from != nullptr) load_states<RN>(from + row, n0, L.N, wide, h);
-            if (MODE == kOwnState && L.first != nullptr) store_states<RN>(L.first + row, n0, L.N, wide, h);
-        } else if constexpr (MODE == kMain) {
-            load_states<RN>(L.seg_state + row, n0, L.N, wide, h);
-            for (int s = 1; s < p.seg; ++s) {
-                const float d = L.seg_sum[(s * L.B + p.b) * L.C + c];
-                float2 own[P];
-                load_states<RN>(L.seg_state + s * seg_row + row, n0, L.N, wide, own);
+                for (int k = 0; k < K / STEP; ++k) d[k] = pair_softplus(d[k]);
+            }
+            if constexpr (MODE == kOwnGrad) {
+                if (gated) {
 #pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    const float2 q = pair_mul(make_float2(d, d), a2[i]);
-                    h[i] = pair_fma(make_float2(exp2_hw(q.x), exp2_hw(q.y)), h[i], own[i]);
+                    for (int k = 0; k < K / STEP; ++k) {
+                        const float2 z = load_two(&at.gate[at0 + k * STEP][two]);
+                        v[k] = pair_mul(v[k], pair_mul(z, pair_logistic<kWide>(z)));
+                    }
                 }
             }
-        }
-    }
-
-    constexpr bool kReads = MODE != kOwnGrad;        // x and B; else the gradient, the gate and C
-    const bool gated = L.gate.data != nullptr && MODE != kOwnState;
-    Ahead<T, NP> ab, ac;
-    // tile i of the pass: the i-th from the front, or from the back of the gradient's
-    auto start = [&](int i) { return begin + static_cast<int64_t>(MODE == kOwnGrad ? tiles - 1 - i : i) * K; };
-    auto count = [&](int64_t t0) { return static_cast<int>(end - t0 < K ? end - t0 : K); };
-    auto fetch = [&](int i) {
-        const int64_t t0 = start(i);
-        const int live = count(t0);
-        Buf& to = buf[i & 1];
-        load_rows<T, VEC, CB>(to.x, kReads ? L.x : A.g, p, t0, live);
-        load_rows<T, VEC, CB>(to.delta, L.delta, p, t0, live);
-        if (gated && !A.keep_only) load_rows<T, VEC, CB>(to.gate, L.gate, p, t0, live);
-        copies_done();
-        if (kReads) ab.load(L.b, p.b, p.group, L.N, t0, live);
-        if (MODE != kOwnState) ac.load(L.c, p.b, p.group, L.N, t0, live);
-    };
-    auto land = [&](int i) {
-        if (kReads) ab.put(buf[i & 1].b);
-        if (MODE != kOwnState) ac.put(buf[i & 1].c);
-    };
-    T* const out = static_cast<T*>(L.out.data) + p.b * L.out.stride_b + c;
-    if (tiles > 0) {
-        fetch(0);
-        land(0);
-    }
-    for (int i = 0; i < tiles; ++i) {
-        if (i + 1 < tiles) fetch(i + 1);
-        else copies_done();
-        copies_wait<1>();
-        __syncthreads();
-        const Buf& at = buf[i & 1];
-        const int64_t t0 = start(i);
-        const int live = count(t0);
-        if (MODE == kMain && L.kept != nullptr && mine)
-            store_states<RN>(L.kept + ((p.b * L.chunks + t0 / K) * L.C + c) * L.N, n0, L.N, wide, h);
-#pragma unroll 2
-        for (int k = 0; k < live; ++k) {
-            const int tt = MODE == kOwnGrad ? live - 1 - k : k;
-            const float xv = to_f32(at.x[tt][ch]);
-            float d = to_f32(at.delta[tt][ch]) + bias;
-            if (L.softplus) d = softplus(d);
-            if constexpr (MODE != kMain) sum += d;
-            const float2 dd = make_float2(d, d);
-            float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            if constexpr (MODE == kOwnGrad) {
-                float gy = xv;
-                if (gated) {
-                    const float z = to_f32(at.gate[tt][ch]);
-                    gy *= z * logistic(z);
-                }
-                const float2 gg = make_float2(gy, gy);
+            // tokens past the last take no step
 #pragma unroll
-                for (int j = 0; j < P; ++j) {
-                    const float2 q = pair_mul(dd, a2[j]);
-                    h[j] = pair_mul(make_float2(exp2_hw(q.x), exp2_hw(q.y)),
-                                    pair_fma(gg, *reinterpret_cast<const float2*>(&at.c[tt][n0 + 2 * j]), h[j]));
+            for (int k = 0; k < K / STEP; ++k) {
+                const int tt = at0 + k * STEP;
+                if (tt >= live) d[k] = v[k] = pair_of(0.f);
+                if (MODE != kMain) sum = pair_add(sum, d[k]);
+                store_two(&buf.d[i & 1][tt][two], d[k]);
+                store_two(&buf.v[i & 1][tt][two], MODE == kOwnGrad ? v[k] : pair_mul(d[k], v[k]));
+            }
+        }
+        if (results && i >= 2) {
+            const auto& at = buf.stage[(i - 2) % kStages];
+            const int64_t t0 = R.start<MODE>(i - 2);
+            const int live = R.live(t0);
+            float2 y[K / STEP];
+#pragma unroll
+            for (int k = 0; k < K / STEP; ++k) {
+                const int tt = at0 + k * STEP;
+                y[k] = pair_fma(skip, load_two(&at.x[tt][two]), load_two(&buf.y[i & 1][tt][two]));
+            }
+            if (gated) {
+#pragma unroll
+                for (int k = 0; k < K / STEP; ++k) {
+                    const float2 z = load_two(&at.gate[at0 + k * STEP][two]);
+                    y[k] = pair_mul(y[k], pair_mul(z, pair_logistic<kWide>(z)));
+                }
+            }
+            T* o = out + (t0 + at0) * L.out.stride_t;
+            if (A.pairs && in1) {
+#pragma unroll
+                for (int k = 0; k < K / STEP; ++k) {
+                    if (at0 + k * STEP < live) store_two(o, y[k]);
+                    o += STEP * L.out.stride_t;
                 }
             } else {
-                const float dx = d * xv;
-                const float2 xx = make_float2(dx, dx);
 #pragma unroll
-                for (int j = 0; j < P; ++j) {
-                    const float2 q = pair_mul(dd, a2[j]);
-                    h[j] = pair_fma(make_float2(exp2_hw(q.x), exp2_hw(q.y)), h[j],
-                                    pair_mul(xx, *reinterpret_cast<const float2*>(&at.b[tt][n0 + 2 * j])));
-                    if (MODE == kMain)
-                        acc[j & 1] = pair_fma(*reinterpret_cast<const float2*>(&at.c[tt][n0 + 2 * j]), h[j], acc[j & 1]);
-                }
-                if (MODE == kMain && !A.keep_only) {
-                    const float2 both = pair_add(acc[0], acc[1]);
-                    float y = both.x + both.y;
-#pragma unroll
-                    for (int m = 1; m < LANES; m *= 2) y += __shfl_xor_sync(0xffffffffu, y, m, LANES);
-                    y = fmaf(skip, xv, y);
-                    if (gated) {
-                        const float z = to_f32(at.gate[tt][ch]);
-                        y *= z * logistic(z);
-                    }
-                    if (sub == 0 && mine) out[(t0 + tt) * L.out.stride_t] = from_f32<T>(y);
+                for (int k = 0; k < K / STEP; ++k) {
+                    if (in0 && at0 + k * STEP < live) o[0] = from_f32<T>(y[k].x);
+                    if (in1 && at0 + k * STEP < live) o[1] = from_f32<T>(y[k].y);
+                    o += STEP * L.out.stride_t;
                 }
             }
         }
+        copies_wait<0>();
         __syncthreads();
-        if (i + 1 < tiles) land(i + 1);
     }
-    if (!mine) return;
-    if constexpr (MODE == kMain) {
-        if (!A.keep_only && sub == 0)
-            for (int64_t t = end > begin ? end : begin; t < stop; ++t) out[t * L.out.stride_t] = from_f32<T>(0.0f);
-        if (L.fin != nullptr && p.seg == L.segs - 1) store_states<RN>(L.fin + row, n0, L.N, wide, h);
-    } else {
-        store_states<RN>(L.seg_state + p.seg * seg_row + row, n0, L.N, wide, h);
-        if (sub == 0) L.seg_sum[(p.seg * L.B + p.b) * L.C + c] = sum;
+    if (results && in0)
+        for (int64_t t = (R.end > R.begin ? R.end : R.begin) + at0; t < R.stop; t += STEP) {
+            out[t * L.out.stride_t] = from_f32<T>(0.0f);
+            if (in1) out[t * L.out.stride_t + 1] = from_f32<T>(0.0f);
+        }
+    if constexpr (MODE != kMain) {
+        // the steps' sums, of the lanes that took every STEP-th token
+#pragma unroll
+        for (int m = PAIRS; m < 32; m *= 2) {
+            sum.x += __shfl_xor_sync(0xffffffffu, sum.x, m);
+            sum.y += __shfl_xor_sync(0xffffffffu, sum.y, m);
+        }
+        float* const to = L.seg_sum + (p.seg * L.B + p.b) * L.C + c2;
+        if (at0 == 0 && in0) to[0] = sum.x;
+        if (at0 == 0 && in1) to[1] = sum.y;
     }
 }
 
-template <typename T, int LANES, int RN, bool VEC, Mode MODE>
+// The warps that run the states.
+template <typename T, int NL, Mode MODE>
+__device__ __forceinline__ void run(const ScanArgs& A, const Run& R, Tile<T, NL>& buf) {
+    constexpr int CW = Lanes<NL>::CW;
+    constexpr bool kReads = MODE != kOwnGrad;
+    const ScanLaunch& L = A.L;
+    const Place& p = R.p;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x % kHalf / 32, sub = lane % NL, n0 = 4 * sub;
+    const int tile = warp * CW + lane / NL * 4;      // the lane's channels, from p.first
+    const int64_t c = p.first + tile;
+    const bool wide = L.wide;
+    Block h, a2;
+    const int64_t rows = L.C * L.N, seg_rows = L.B * rows;      // of a [C, N] table, of a segment's
+    load_block(L.a, c, p.last, n0, L.N, wide, a2);
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            a2[n][r] = pair_mul(a2[n][r], pair_of(kLog2e));
+            h[n][r] = pair_of(0.f);
+        }
+    if constexpr (MODE == kOwnGrad) {
+        if (p.seg == L.segs - 1 && A.gfin != nullptr) load_block(A.gfin + p.b * rows, c, p.last, n0, L.N, wide, h);
+    } else if (p.seg == 0) {
+        const float* from = MODE == kMain && L.first != nullptr ? L.first : L.init;
+        if (from != nullptr) load_block(from + p.b * rows, c, p.last, n0, L.N, wide, h);
+        if (MODE == kOwnState && L.first != nullptr) store_block(L.first + p.b * rows, L.N, c, p.last, n0, L.N, wide, h);
+    } else if constexpr (MODE == kMain) {
+        load_block(L.seg_state + p.b * rows, c, p.last, n0, L.N, wide, h);
+        for (int s = 1; s < p.seg; ++s) enter_segment(L, p, s, c, n0, a2, h);
+    }
+    __syncthreads();
+    for (int i = -1; i < R.tiles + 1; ++i) {
+        if (i >= 0 && i < R.tiles) {
+            const auto& at = buf.stage[i % kStages];
+            const int64_t t0 = R.start<MODE>(i);
+            const int live = R.live(t0);
+            const float *const ds = &buf.d[i & 1][0][tile], *const vs = &buf.v[i & 1][0][tile];
+            constexpr int CB = Tile<T, NL>::CB;
+            if (MODE == kMain && L.kept != nullptr)
+                store_block(L.kept + (p.b * L.chunks + t0 / K) * rows, L.N, c, p.last, n0, L.N, wide, h);
+            // what makes up for the exponentials' mean error, by their size in this tile
+            Block mend;
+            {
+                const float4 d = *reinterpret_cast<const float4*>(ds + (MODE == kOwnGrad ? live - 1 : 0) * CB);
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    mend[n][0] = decay_mend(pair_mul(make_float2(d.x, d.y), a2[n][0]));
+                    mend[n][1] = decay_mend(pair_mul(make_float2(d.z, d.w), a2[n][1]));
+                }
+            }
+            // kBlock tokens at a time: their reads come before the writes of their sums
+            constexpr int kBlock = 4;
+#pragma unroll 1
+            for (int k0 = 0; k0 < live; k0 += kBlock) {
+                float2 y[kBlock];
+#pragma unroll
+                for (int k = 0; k < kBlock; ++k) {
+                    const int tt = MODE == kOwnGrad ? (live - 1) / kBlock * kBlock - k0 + kBlock - 1 - k : k0 + k;
+                    const float4 d4 = *reinterpret_cast<const float4*>(ds + tt * CB), v4 = *reinterpret_cast<const float4*>(vs + tt * CB);
+                    const float2 d[2] = {make_float2(d4.x, d4.y), make_float2(d4.z, d4.w)};
+                    const float2 v[2] = {make_float2(v4.x, v4.y), make_float2(v4.z, v4.w)};
+                    float4 bv, cv;
+                    if (kReads) bv = load_four(&at.b[tt][n0]);
+                    if (MODE != kOwnState) cv = load_four(&at.c[tt][n0]);
+                    float2 part[2] = {pair_of(0.f), pair_of(0.f)};
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const float2 q = pair_fma(d[r], a2[n][r], mend[n][r]);
+                            const float2 a = make_float2(exp2_hw(q.x), exp2_hw(q.y));
+                            if constexpr (MODE == kOwnGrad) {
+                                h[n][r] = pair_mul(a, pair_fma(v[r], pair_of(of_four(cv, n)), h[n][r]));
+                            } else {
+                                h[n][r] = pair_fma(a, h[n][r], pair_mul(v[r], pair_of(of_four(bv, n))));
+                                if (MODE == kMain) {
+                                    const float2 cn = pair_of(of_four(cv, n));
+                                    part[r] = n == 0 ? pair_mul(cn, h[n][r]) : pair_fma(cn, h[n][r], part[r]);
+                                }
+                            }
+                        }
+                    if constexpr (MODE == kMain) y[k] = over_states<NL>(part, sub);
+                }
+                if constexpr (MODE == kMain) {
+#pragma unroll
+                    for (int k = 0; k < kBlock; ++k) put_sum<NL>(&buf.y[i & 1][k0 + k][tile], y[k], sub);
+                }
+            }
+        }
+        __syncthreads();
+    }
+    if constexpr (MODE == kMain) {
+        if (L.fin != nullptr && p.seg == L.segs - 1) store_block(L.fin + p.b * rows, L.N, c, p.last, n0, L.N, wide, h);
+    } else {
+        store_block(L.seg_state + p.seg * seg_rows + p.b * rows, L.N, c, p.last, n0, L.N, wide, h);
+    }
+}
+
+template <typename T, int NL, Mode MODE>
+__global__ void __launch_bounds__(kThreads, 8) k_sscan(const __grid_constant__ ScanArgs A) {
+    extern __shared__ __align__(128) unsigned char smem[];
+    auto& buf = *reinterpret_cast<Tile<T, NL>*>(smem);
+    const ScanLaunch& L = A.L;
+    Run R;
+    R.p = place_of<Tile<T, NL>::CB>(A);
+    if constexpr (MODE == kOwnGrad) R.p.seg += 1;    // the first segment's gradient enters none
+    const int64_t len = live_tokens(L.lengths, R.p.b, L.T);
+    R.begin = R.p.seg * L.seg_chunks * K;
+    R.stop = R.begin + L.seg_chunks * K < L.T ? R.begin + L.seg_chunks * K : L.T;
+    R.end = R.stop < len ? R.stop : len;
+    R.tiles = R.end > R.begin ? static_cast<int>((R.end - R.begin + K - 1) / K) : 0;
+    // A warp's place on the SM fixes its scheduler: neighbouring CTAs give the two kinds
+    // of warps the other way round, so that each scheduler has as much of both.
+    __shared__ uint32_t slot;
+    if (threadIdx.x == 0) asm volatile("mov.u32 %0, %%warpid;" : "=r"(slot));
+    __syncthreads();
+    if ((threadIdx.x < kHalf) == ((slot >> 2 & 1) == 0)) run<T, NL, MODE>(A, R, buf);
+    else help<T, NL, MODE>(A, R, buf);
+}
+
+template <typename T, int NL, Mode MODE>
 cudaError_t go(const ScanArgs& A, int64_t segs) {
-    const int bytes = 2 * static_cast<int>(sizeof(Tile<T, LANES, RN>));
-    auto* kernel = k_sscan<T, LANES, RN, VEC, MODE>;
+    const int bytes = static_cast<int>(sizeof(Tile<T, NL>));
+    auto* kernel = k_sscan<T, NL, MODE>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     kernel<<<static_cast<unsigned>(A.L.G * A.blocks * A.L.B * segs), kThreads, bytes, A.L.stream>>>(A);
     return cudaGetLastError();
 }
 
-template <typename T, bool VEC, Mode MODE>
+template <typename T, Mode MODE>
 cudaError_t by_states(const ScanArgs& A, int64_t segs) {
-    if (A.L.N <= 8) return go<T, 1, 8, VEC, MODE>(A, segs);
-    if (A.L.N <= 16) return go<T, 1, 16, VEC, MODE>(A, segs);
-    if (A.L.N <= 32) return go<T, 2, 16, VEC, MODE>(A, segs);
-    return go<T, 4, 16, VEC, MODE>(A, segs);
+    if (A.L.N <= 8) return go<T, 2, MODE>(A, segs);
+    if (A.L.N <= 16) return go<T, 4, MODE>(A, segs);
+    if (A.L.N <= 32) return go<T, 8, MODE>(A, segs);
+    return go<T, 16, MODE>(A, segs);
 }
 
 template <Mode MODE>
-cudaError_t by_type(const ScanArgs& A, bool vec, int64_t segs) {
-    if (A.L.bf16) return vec ? by_states<__nv_bfloat16, true, MODE>(A, segs) : by_states<__nv_bfloat16, false, MODE>(A, segs);
-    return vec ? by_states<float, true, MODE>(A, segs) : by_states<float, false, MODE>(A, segs);
+cudaError_t by_type(const ScanArgs& A, int64_t segs) {
+    return A.L.bf16 ? by_states<__nv_bfloat16, MODE>(A, segs) : by_states<float, MODE>(A, segs);
 }
 
 // ---------------------------------------------------------------------------
 // one token: bound by the states' bytes (read and written once).  A lane holds
 // VEC of a channel's states, `lanes` of them a channel, and takes ROWS batch rows
 // with the channel's A in registers, their states' loads all in flight.
-constexpr int ROWS = 4;
+constexpr int kStepThreads = 128, ROWS = 4;
 
 template <typename T, int VEC>
-__global__ void __launch_bounds__(kThreads) k_sscan_step(const __grid_constant__ ScanLaunch L, int lanes) {
-    const int64_t at = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+__global__ void __launch_bounds__(kStepThreads) k_sscan_step(const __grid_constant__ ScanLaunch L, int lanes) {
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * kStepThreads + threadIdx.x;
     const int sub = static_cast<int>(at % lanes), n0 = sub * VEC;
     const int64_t c = at / lanes;
     const bool mine = c < L.C && n0 < L.N;
@@ -270,7 +388,7 @@ __global__ void __launch_bounds__(kThreads) k_sscan_step(const __grid_constant__
         if constexpr (VEC == 1) {
             // 64 states of one value a lane are two warps
             if (lanes > 32) {
-                __shared__ float half[kThreads / 32];
+                __shared__ float half[kStepThreads / 32];
                 __syncthreads();
                 if (threadIdx.x % 32 == 0) half[threadIdx.x / 32] = y;
                 __syncthreads();
@@ -286,38 +404,40 @@ __global__ void __launch_bounds__(kThreads) k_sscan_step(const __grid_constant__
 }  // namespace
 
 cudaError_t launch_scan(const ScanLaunch& L, bool keep_only, int* kernels) {
-    ScanArgs A = scan_args(L);
+    ScanArgs A = scan_args(L, scan_channels(L.N));
     A.keep_only = keep_only;
-    const bool vec = scan_vectors(L, nullptr);
+    A.vec = scan_vectors(L, nullptr);
+    A.pairs = scan_pairs(L, L.out);
     cudaError_t e;
     *kernels = 0;
     if (L.segs > 1) {
-        if ((e = by_type<kOwnState>(A, vec, L.segs - 1)) != cudaSuccess) return e;
+        if ((e = by_type<kOwnState>(A, L.segs - 1)) != cudaSuccess) return e;
         ++*kernels;
     }
     ++*kernels;
-    return by_type<kMain>(A, vec, L.segs);
+    return by_type<kMain>(A, L.segs);
 }
 
 // the gradients that the segments' own tokens leave (seg_state, seg_sum; from the second segment on)
 cudaError_t launch_scan_own_grads(const ScanBackward& S) {
-    ScanArgs A = scan_args(S.f);
+    ScanArgs A = scan_args(S.f, scan_channels(S.f.N));
     A.g = S.g;
     A.gfin = S.gfin;
-    return by_type<kOwnGrad>(A, scan_vectors(S.f, &S.g), S.f.segs - 1);
+    A.vec = scan_vectors(S.f, &S.g);
+    return by_type<kOwnGrad>(A, S.f.segs - 1);
 }
 
 cudaError_t launch_scan_step(const ScanLaunch& L) {
     const bool vec = L.wide;
     int lanes = 1;
     while (lanes * (vec ? 4 : 1) < L.N) lanes *= 2;
-    const dim3 grid(static_cast<unsigned>((L.C * lanes + kThreads - 1) / kThreads), static_cast<unsigned>((L.B + ROWS - 1) / ROWS));
+    const dim3 grid(static_cast<unsigned>((L.C * lanes + kStepThreads - 1) / kStepThreads), static_cast<unsigned>((L.B + ROWS - 1) / ROWS));
     if (L.bf16) {
-        if (vec) k_sscan_step<__nv_bfloat16, 4><<<grid, kThreads, 0, L.stream>>>(L, lanes);
-        else k_sscan_step<__nv_bfloat16, 1><<<grid, kThreads, 0, L.stream>>>(L, lanes);
+        if (vec) k_sscan_step<__nv_bfloat16, 4><<<grid, kStepThreads, 0, L.stream>>>(L, lanes);
+        else k_sscan_step<__nv_bfloat16, 1><<<grid, kStepThreads, 0, L.stream>>>(L, lanes);
     } else {
-        if (vec) k_sscan_step<float, 4><<<grid, kThreads, 0, L.stream>>>(L, lanes);
-        else k_sscan_step<float, 1><<<grid, kThreads, 0, L.stream>>>(L, lanes);
+        if (vec) k_sscan_step<float, 4><<<grid, kStepThreads, 0, L.stream>>>(L, lanes);
+        else k_sscan_step<float, 1><<<grid, kStepThreads, 0, L.stream>>>(L, lanes);
     }
     return cudaGetLastError();
 }

@@ -4,293 +4,351 @@
 // last to the first:
 //
 //     dh = dh + gy C,   gC += gy h,   gB += dh d x,   gx = gy D + d (dh.B)
-//     u = dh a h' (h' the state before),  gA += u d,  gd = u.A + x (dh.B),   dh = a dh
+//     dh = a dh,   u = dh h' (h' the state before),   gA += u d,   gd = u.A + x (dh.B)
 //
 // The states come from those kept every kScanChunk tokens (by the forward call, or
-// found first): a chunk's states are formed again forwards, a h' of every token
-// stays in shared memory, and the reverse pass forms the decays anew.  A token,
-// channel and state costs 14 products and sums and two exponentials, and takes
-// part in sums along both the states (y, dh.B, u.A) and the channels (gB, gC).  So
-// a warp is 8 lanes of channels by 4 lanes of states, and a lane holds a tile of
-// RC channels by RN states of one batch row: sums within the tile are products
-// already made, and what is left crosses lanes in exchanges that halve the values
-// each time.  gB and gC are summed over the CTA's channels here and over the CTAs
-// by a second launch, always in one order.
+// found first): a chunk's states are formed again forwards and stay in tensor
+// memory, 16 words a thread and token, which no product uses here; the reverse pass
+// forms the decays anew.  A token, channel and state costs 13 products and sums
+// (128 a clock an SM) and two exponentials (32), and takes part in sums along both
+// the states (y, dh.B, u.A) and the channels (gB, gC): the products bound it, then
+// the instructions of the sums.  A lane holds 4 states of each of 4 channels: sums
+// within the tile are products already made, sums over states cross NL lanes in
+// exchanges, sums over the CTA's channels go through shared memory (each lane's 8
+// values of a token, four instructions to write and read them where exchanges took
+// 28), those over the CTAs of a group through a second launch, always in one order.
 #include "es_attn.h"
 #include "es_sscan.cuh"
+#include "es_tcgen05.cuh"
 
 namespace es {
 namespace {
 
-constexpr int kThreads = kScanThreads, kWarps = kThreads / 32;
+constexpr int kThreads = 128, kWarps = kThreads / 32;
 constexpr int K = kScanChunk;
+constexpr int kGroup = 8;                            // tokens whose sums over channels are taken at once
+constexpr int kPitch = kThreads + 4;                 // of a row of their terms: reads of neighbouring rows miss each other's banks
+constexpr uint32_t kColumns = 16 * K;                // tensor memory: two CTAs an SM
+constexpr int kLeastBytes = 77 * 1024;               // of shared memory, for the same reason
 
 struct BwdArgs {
     ScanArgs A;
     ScanBackward S;
 };
 
-template <typename T, int RN>
-struct Shape {
-    static constexpr int RC = RN <= 4 ? 4 : 16 / RN;     // channels a lane
-    static constexpr int CW = 8 * RC, CB = kWarps * CW;  // channels a warp, a CTA
-    static constexpr int NP = 4 * RN, P = RN / 2;
-    static constexpr int Q = RC * RN / 4;                // float4 of a lane's tile
-    struct Buf {
-        T x[K][CB], delta[K][CB], gate[K][CB], g[K][CB];
-        float b[K][NP], c[K][NP];
-        float d[K][CB], dx[K][CB], gy[K][CB], y[K][CB];
-        float part[K][kWarps][2 * NP];
-        float4 stash[K][Q][kThreads];
+template <typename T, int NL>
+struct BwdTile {
+    static constexpr int CB = kWarps * Lanes<NL>::CW, NP = Lanes<NL>::NP;
+    static constexpr int STAGES = sizeof(T) == 2 && NL >= 4 ? 2 : 1;      // two where two CTAs still fit an SM
+    struct Stage {
+        T x[K][CB], delta[K][CB], gate[K][CB], g[K][CB], b[K][NP], c[K][NP];
     };
+    Stage stage[STAGES];
+    float d[K][CB], dx[K][CB], gy[K][CB], of_b[K][CB], of_a[K][CB];       // dx: later y
+    float4 terms[kGroup][2][kPitch];
+    uint32_t tmem;
 };
 
-// v[r] summed over the 4 lanes of states; lane r of them (of RC) gets channel r's
-template <int RC>
-__device__ __forceinline__ float over_states(const float (&v)[RC], int lane) {
-    if constexpr (RC == 4) {
-        const bool hi = lane & 2, odd = lane & 1;
-        const float k0 = (hi ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[2], 2);
-        const float k1 = (hi ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, hi ? v[1] : v[3], 2);
-        return (odd ? k1 : k0) + __shfl_xor_sync(0xffffffffu, odd ? k0 : k1, 1);
-    } else {
-        float s;
-        if constexpr (RC == 2) {
-            const bool odd = lane & 1;
-            s = (odd ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, odd ? v[0] : v[1], 1);
-        } else {
-            s = v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
-        }
-        return s + __shfl_xor_sync(0xffffffffu, s, 2);
-    }
-}
-
-// w[0..N) summed over the lanes that differ in bits MASK, MASK / 2 .. 4 (those of
-// channels): each lane is left with every 8th part of the sums (one at least) in
-// w[0..), those from the returned index on
-template <int N, int MASK, int M>
-__device__ __forceinline__ int over_channels(float (&w)[M], int lane) {
-    if constexpr (MASK < 4) {
-        return 0;
-    } else if constexpr (N == 1) {
-        w[0] += __shfl_xor_sync(0xffffffffu, w[0], MASK);
-        return over_channels<1, MASK / 2>(w, lane);
-    } else {
-        const bool hi = lane & MASK;
+__device__ __forceinline__ void stash(uint32_t addr, const Block& h) {
+    uint32_t r[16];
 #pragma unroll
-        for (int i = 0; i < N / 2; ++i) {
-            const float keep = hi ? w[i + N / 2] : w[i], send = hi ? w[i] : w[i + N / 2];
-            w[i] = keep + __shfl_xor_sync(0xffffffffu, send, MASK);
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            r[4 * n + 2 * j] = __float_as_uint(h[n][j].x);
+            r[4 * n + 2 * j + 1] = __float_as_uint(h[n][j].y);
         }
-        return (hi ? N / 2 : 0) + over_channels<N / 2, MASK / 2>(w, lane);
-    }
+    tc::st(addr, r);
+}
+__device__ __forceinline__ float2 stashed(const uint32_t (&r)[16], int n, int j) {
+    return make_float2(__uint_as_float(r[4 * n + 2 * j]), __uint_as_float(r[4 * n + 2 * j + 1]));
 }
 
-template <typename T, int RN, bool VEC>
-__global__ void __launch_bounds__(kThreads) k_sscan_bwd(const __grid_constant__ BwdArgs B) {
-    using S = Shape<T, RN>;
-    constexpr int RC = S::RC, CW = S::CW, CB = S::CB, NP = S::NP, P = S::P;
+template <typename T, int NL>
+__global__ void __launch_bounds__(kThreads, 2) k_sscan_bwd(const __grid_constant__ BwdArgs B) {
+    using Buf = BwdTile<T, NL>;
+    constexpr int CB = Buf::CB, NP = Buf::NP, CW = Lanes<NL>::CW, PAIRS = Lanes<NL>::PAIRS, STEP = Lanes<NL>::STEP;
+    constexpr bool kWide = sizeof(T) == 4;
     extern __shared__ __align__(128) unsigned char smem[];
-    auto& at = *reinterpret_cast<typename S::Buf*>(smem);
+    Buf& buf = *reinterpret_cast<Buf*>(smem);
     const ScanLaunch& L = B.A.L;
     const Place p = place_of<CB>(B.A);
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, quad = lane & 3, n0 = quad * RN;
-    const int tile = warp * CW + (lane >> 2) * RC;          // the lane's channels, from p.first
-    const int own = tile + (quad < RC ? quad : 0);          // the channel whose sums over states the lane gets
-    const bool owner = quad < RC && p.first + own < p.last, wide = L.wide;
-    const bool gated = L.gate.data != nullptr;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, sub = lane % NL, n0 = 4 * sub;
+    const int tile = warp * CW + lane / NL * 4;      // the lane's channels, from p.first
+    const int two = warp * CW + lane % PAIRS * 2, at0 = lane / PAIRS;      // what it does once a token and channel
+    const int64_t c = p.first + tile, c2 = p.first + two;
+    const bool wide = L.wide, gated = L.gate.data != nullptr;
     const int64_t len = live_tokens(L.lengths, p.b, L.T);
     const int64_t begin = p.seg * L.seg_chunks * K;
     const int64_t stop = begin + L.seg_chunks * K < L.T ? begin + L.seg_chunks * K : L.T;
     const int64_t end = stop < len ? stop : len;
     const int tiles = end > begin ? static_cast<int>((end - begin + K - 1) / K) : 0;
-    const int64_t seg_row = L.B * L.C * L.N;
+    const int64_t rows = L.C * L.N;                  // of a [C, N] table
+    if (warp == 0) tc::alloc(&buf.tmem, kColumns);
 
-    float2 a2[RC][P], dh[RC][P], ga[RC][P];
-    float bias[RC];
+    Block a2, dh, ga;
+    float2 skip = pair_of(0.f), bias = pair_of(0.f), gskip = pair_of(0.f), gbias = pair_of(0.f);
+    if (L.skip != nullptr) skip = make_float2(c2 < p.last ? L.skip[c2] : 0.f, c2 + 1 < p.last ? L.skip[c2 + 1] : 0.f);
+    if (L.bias != nullptr) bias = make_float2(c2 < p.last ? L.bias[c2] : 0.f, c2 + 1 < p.last ? L.bias[c2 + 1] : 0.f);
+    load_block(L.a, c, p.last, n0, L.N, wide, a2);
 #pragma unroll
-    for (int r = 0; r < RC; ++r) {
-        const int64_t c = p.first + tile + r, row = (p.b * L.C + c) * L.N;
+    for (int n = 0; n < 4; ++n)
 #pragma unroll
-        for (int i = 0; i < P; ++i) a2[r][i] = dh[r][i] = ga[r][i] = make_float2(0.f, 0.f);
-        bias[r] = 0.0f;
-        if (c < p.last) {
-            load_states<RN>(L.a + c * L.N, n0, L.N, wide, a2[r]);
-#pragma unroll
-            for (int i = 0; i < P; ++i) a2[r][i] = pair_mul(a2[r][i], make_float2(kLog2e, kLog2e));
-            if (p.seg == L.segs - 1) {
-                if (B.S.gfin != nullptr) load_states<RN>(B.S.gfin + row, n0, L.N, wide, dh[r]);
-            } else {
-                load_states<RN>(L.seg_state + (L.segs - 1) * seg_row + row, n0, L.N, wide, dh[r]);
-                for (int s = L.segs - 2; s > p.seg; --s) {
-                    const float d = L.seg_sum[(s * L.B + p.b) * L.C + c];
-                    float2 own_grad[P];
-                    load_states<RN>(L.seg_state + s * seg_row + row, n0, L.N, wide, own_grad);
-#pragma unroll
-                    for (int i = 0; i < P; ++i) {
-                        const float2 q = pair_mul(make_float2(d, d), a2[r][i]);
-                        dh[r][i] = pair_fma(make_float2(exp2_hw(q.x), exp2_hw(q.y)), dh[r][i], own_grad[i]);
-                    }
-                }
-            }
+        for (int r = 0; r < 2; ++r) {
+            a2[n][r] = pair_mul(a2[n][r], pair_of(kLog2e));
+            dh[n][r] = ga[n][r] = pair_of(0.f);
         }
+    if (p.seg == L.segs - 1) {
+        if (B.S.gfin != nullptr) load_block(B.S.gfin + p.b * rows, c, p.last, n0, L.N, wide, dh);
+    } else {
+        load_block(L.seg_state + ((L.segs - 1) * L.B + p.b) * rows, c, p.last, n0, L.N, wide, dh);
+        for (int s = L.segs - 2; s > p.seg; --s) enter_segment(L, p, s, c, n0, a2, dh);
     }
-    const int64_t oc = p.first + own;
-    const float skip = L.skip != nullptr && owner ? L.skip[oc] : 0.0f, own_bias = L.bias != nullptr && owner ? L.bias[oc] : 0.0f;
-    float gskip = 0.0f, gbias = 0.0f;
-    T* const gx = static_cast<T*>(B.S.gx.data) + p.b * B.S.gx.stride_b + oc;
-    T* const gdelta = static_cast<T*>(B.S.gdelta.data) + p.b * B.S.gdelta.stride_b + oc;
-    T* const ggate = gated ? static_cast<T*>(B.S.ggate.data) + p.b * B.S.ggate.stride_b + oc : nullptr;
+
+    const int width = static_cast<int>(p.last - p.first);
+    auto start = [&](int i) { return begin + static_cast<int64_t>(i) * K; };
+    auto count = [&](int64_t t0) { return static_cast<int>(end - t0 < K ? end - t0 : K); };
+    auto from = [&](const es_rows& r, int64_t t0) { return static_cast<const T*>(r.data) + p.b * r.stride_b + t0 * r.stride_t + p.first; };
+    auto of_group = [&](const es_heads& r, int64_t t0) {
+        return static_cast<const T*>(r.data) + p.b * r.stride_b + t0 * r.stride_t + p.group * r.stride_h;
+    };
+    auto fetch = [&](int i) {
+        const int64_t t0 = start(i);
+        const int live = count(t0);
+        auto& to = buf.stage[i % Buf::STAGES];
+        load_tile<T, CB, kThreads>(threadIdx.x, to.x, from(L.x, t0), L.x.stride_t, width, live, B.A.vec);
+        load_tile<T, CB, kThreads>(threadIdx.x, to.delta, from(L.delta, t0), L.delta.stride_t, width, live, B.A.vec);
+        load_tile<T, CB, kThreads>(threadIdx.x, to.g, from(B.A.g, t0), B.A.g.stride_t, width, live, B.A.vec);
+        if (gated) load_tile<T, CB, kThreads>(threadIdx.x, to.gate, from(L.gate, t0), L.gate.stride_t, width, live, B.A.vec);
+        load_tile<T, NP, kThreads>(threadIdx.x, to.b, of_group(L.b, t0), L.b.stride_t, L.N, live, B.A.vec);
+        load_tile<T, NP, kThreads>(threadIdx.x, to.c, of_group(L.c, t0), L.c.stride_t, L.N, live, B.A.vec);
+    };
+    T* const gx = static_cast<T*>(B.S.gx.data) + p.b * B.S.gx.stride_b + c2;
+    T* const gdelta = static_cast<T*>(B.S.gdelta.data) + p.b * B.S.gdelta.stride_b + c2;
+    T* const ggate = gated ? static_cast<T*>(B.S.ggate.data) + p.b * B.S.ggate.stride_b + c2 : nullptr;
+    auto put = [&](T* o, float2 v) {
+        if (B.A.pairs && c2 + 1 < p.last) {
+            store_two(o, v);
+        } else {
+            if (c2 < p.last) o[0] = from_f32<T>(v.x);
+            if (c2 + 1 < p.last) o[1] = from_f32<T>(v.y);
+        }
+    };
     const int64_t across = L.G * B.A.blocks;
     float* const bc = B.S.part_bc + ((blockIdx.x % across) * L.B + p.b) * L.T * 2 * L.N;
 
+    if (tiles > 0) fetch(tiles - 1);
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = buf.tmem + (static_cast<uint32_t>(warp) << 21);      // the warp's 32 lanes
+
     for (int i = tiles - 1; i >= 0; --i) {
-        const int64_t t0 = begin + static_cast<int64_t>(i) * K;
-        const int live = static_cast<int>(end - t0 < K ? end - t0 : K);
-        load_rows<T, VEC, CB>(at.x, L.x, p, t0, live);
-        load_rows<T, VEC, CB>(at.delta, L.delta, p, t0, live);
-        load_rows<T, VEC, CB>(at.g, B.A.g, p, t0, live);
-        if (gated) load_rows<T, VEC, CB>(at.gate, L.gate, p, t0, live);
-        copies_done();
-        {
-            Ahead<T, NP> ab, ac;
-            ab.load(L.b, p.b, p.group, L.N, t0, live);
-            ac.load(L.c, p.b, p.group, L.N, t0, live);
-            ab.put(at.b);
-            ac.put(at.c);
-        }
-        float2 h[RC][P];
-#pragma unroll
-        for (int r = 0; r < RC; ++r) {
-#pragma unroll
-            for (int j = 0; j < P; ++j) h[r][j] = make_float2(0.f, 0.f);
-            const int64_t c = p.first + tile + r;
-            if (c < p.last) load_states<RN>(L.kept + ((p.b * L.chunks + t0 / K) * L.C + c) * L.N, n0, L.N, wide, h[r]);
-        }
+        const int64_t t0 = start(i);
+        const int live = count(t0);
+        Block h;
+        load_block(L.kept + (p.b * L.chunks + t0 / K) * rows, c, p.last, n0, L.N, wide, h);
         copies_wait<0>();
         __syncthreads();
-        // what the tile's lanes share: d, d x and gy of the warp's channels
-        for (int k = lane; k < K * CW; k += 32) {
-            const int tt = k / CW, ch = warp * CW + k % CW;
-            const int64_t c = p.first + ch;
-            float d = to_f32(at.delta[tt][ch]) + (L.bias != nullptr && c < p.last ? L.bias[c] : 0.0f);
-            if (L.softplus) d = softplus(d);
-            float gy = to_f32(at.g[tt][ch]);
+        // the other stage has been read by all: the next chunk's operands on their way
+        if (Buf::STAGES == 2 && i > 0) fetch(i - 1);
+        const auto& at = buf.stage[i % Buf::STAGES];
+#pragma unroll
+        for (int k = 0; k < K; k += STEP) {
+            const int tt = at0 + k;
+            float2 d = pair_add(load_two(&at.delta[tt][two]), bias), gy = load_two(&at.g[tt][two]);
+            if (L.softplus) d = pair_softplus(d);
             if (gated) {
-                const float z = to_f32(at.gate[tt][ch]);
-                gy *= z * logistic(z);
+                const float2 z = load_two(&at.gate[tt][two]);
+                gy = pair_mul(gy, pair_mul(z, pair_logistic<kWide>(z)));
             }
-            at.d[tt][ch] = d;
-            at.dx[tt][ch] = d * to_f32(at.x[tt][ch]);
-            at.gy[tt][ch] = gy;
+            store_two(&buf.d[tt][two], d);
+            store_two(&buf.dx[tt][two], pair_mul(d, load_two(&at.x[tt][two])));
+            store_two(&buf.gy[tt][two], gy);
         }
         __syncwarp();
+        Block mend;
+        {
+            const float4 d = *reinterpret_cast<const float4*>(&buf.d[0][tile]);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                mend[n][0] = decay_mend(pair_mul(make_float2(d.x, d.y), a2[n][0]));
+                mend[n][1] = decay_mend(pair_mul(make_float2(d.z, d.w), a2[n][1]));
+            }
+        }
+        // the states before each token
+#pragma unroll 4
         for (int tt = 0; tt < live; ++tt) {
-            float y[RC];
+            stash(tmem + 16 * tt, h);
+            const float4 d4 = *reinterpret_cast<const float4*>(&buf.d[tt][tile]), v4 = *reinterpret_cast<const float4*>(&buf.dx[tt][tile]);
+            const float2 d[2] = {make_float2(d4.x, d4.y), make_float2(d4.z, d4.w)};
+            const float2 v[2] = {make_float2(v4.x, v4.y), make_float2(v4.z, v4.w)};
+            const float4 bv = load_four(&at.b[tt][n0]);
 #pragma unroll
-            for (int r = 0; r < RC; ++r) {
-                const float d = at.d[tt][tile + r], dx = at.dx[tt][tile + r];
-                float2 acc = make_float2(0.f, 0.f);
+            for (int n = 0; n < 4; ++n)
 #pragma unroll
-                for (int j = 0; j < P; ++j) {
-                    const float2 q = pair_mul(make_float2(d, d), a2[r][j]);
-                    const float2 ah = pair_mul(make_float2(exp2_hw(q.x), exp2_hw(q.y)), h[r][j]);
-                    reinterpret_cast<float2*>(&at.stash[tt][(r * P + j) / 2][threadIdx.x])[(r * P + j) & 1] = ah;
-                    h[r][j] = pair_fma(make_float2(dx, dx), *reinterpret_cast<const float2*>(&at.b[tt][n0 + 2 * j]), ah);
-                    acc = pair_fma(*reinterpret_cast<const float2*>(&at.c[tt][n0 + 2 * j]), h[r][j], acc);
+                for (int r = 0; r < 2; ++r) {
+                    const float2 q = pair_fma(d[r], a2[n][r], mend[n][r]);
+                    h[n][r] = pair_fma(make_float2(exp2_hw(q.x), exp2_hw(q.y)), h[n][r], pair_mul(v[r], pair_of(of_four(bv, n))));
                 }
-                y[r] = acc.x + acc.y;
+        }
+        tc::wait_st();
+        uint32_t one[16], other[16];
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                one[4 * n + 2 * r] = __float_as_uint(h[n][r].x);
+                one[4 * n + 2 * r + 1] = __float_as_uint(h[n][r].y);
             }
+        tc::ld(tmem + 16 * (live - 1), other);
+        // token tt: `now` holds the state after it, `before` (on its way) the one before
+        auto step = [&](int tt, uint32_t(&now)[16], uint32_t(&before)[16]) {
+            const float4 d4 = *reinterpret_cast<const float4*>(&buf.d[tt][tile]), v4 = *reinterpret_cast<const float4*>(&buf.dx[tt][tile]),
+                         g4 = *reinterpret_cast<const float4*>(&buf.gy[tt][tile]);
+            const float2 d[2] = {make_float2(d4.x, d4.y), make_float2(d4.z, d4.w)};
+            const float2 v[2] = {make_float2(v4.x, v4.y), make_float2(v4.z, v4.w)};
+            const float2 g[2] = {make_float2(g4.x, g4.y), make_float2(g4.z, g4.w)};
+            const float4 bv = load_four(&at.b[tt][n0]), cv = load_four(&at.c[tt][n0]);
+            float2 y[2] = {pair_of(0.f), pair_of(0.f)}, of_b[2] = {pair_of(0.f), pair_of(0.f)}, of_a[2] = {pair_of(0.f), pair_of(0.f)};
+            float tb[4], tcv[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const float2 bn = pair_of(of_four(bv, n)), cn = pair_of(of_four(cv, n));
+                float2 wb, wc;
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float2 s = stashed(now, n, r), grad = pair_fma(g[r], cn, dh[n][r]);
+                    wc = r == 0 ? pair_mul(g[r], s) : pair_fma(g[r], s, wc);
+                    wb = r == 0 ? pair_mul(grad, v[r]) : pair_fma(grad, v[r], wb);
+                    y[r] = pair_fma(cn, s, y[r]);
+                    of_b[r] = pair_fma(grad, bn, of_b[r]);
+                    const float2 q = pair_fma(d[r], a2[n][r], mend[n][r]);
+                    dh[n][r] = pair_mul(grad, make_float2(exp2_hw(q.x), exp2_hw(q.y)));
+                }
+                tb[n] = wb.x + wb.y;
+                tcv[n] = wc.x + wc.y;
+            }
+            buf.terms[tt % kGroup][0][threadIdx.x] = make_float4(tb[0], tb[1], tb[2], tb[3]);
+            buf.terms[tt % kGroup][1][threadIdx.x] = make_float4(tcv[0], tcv[1], tcv[2], tcv[3]);
+            tc::wait_ld();
+            tc::loaded(before);
+            if (tt > 0) tc::ld(tmem + 16 * (tt - 1), now);
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float2 u = pair_mul(dh[n][r], stashed(before, n, r));
+                    of_a[r] = pair_fma(u, a2[n][r], of_a[r]);
+                    ga[n][r] = pair_fma(u, d[r], ga[n][r]);
+                }
+            put_sum<NL>(&buf.of_b[tt][tile], over_states<NL>(of_b, sub), sub);
+            put_sum<NL>(&buf.of_a[tt][tile], over_states<NL>(of_a, sub), sub);
             if (gated) {
-                const float whole = over_states<RC>(y, lane);
-                if (quad < RC) at.y[tt][own] = whole;
+                const float2 whole = over_states<NL>(y, sub);
+                __syncwarp();                        // every lane has read its d x of this token
+                put_sum<NL>(&buf.dx[tt][tile], whole, sub);
             }
-        }
-        for (int tt = live - 1; tt >= 0; --tt) {
-            float w[2 * RN], s1[RC], s2[RC];
-#pragma unroll
-            for (int j = 0; j < 2 * RN; ++j) w[j] = 0.0f;
-#pragma unroll
-            for (int r = 0; r < RC; ++r) {
-                const float d = at.d[tt][tile + r], dx = at.dx[tt][tile + r], gy = at.gy[tt][tile + r];
-                float2 sb = make_float2(0.f, 0.f), sa = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int j = 0; j < P; ++j) {
-                    const float2 bb = *reinterpret_cast<const float2*>(&at.b[tt][n0 + 2 * j]);
-                    const float2 cc = *reinterpret_cast<const float2*>(&at.c[tt][n0 + 2 * j]);
-                    const float2 ah = reinterpret_cast<const float2*>(&at.stash[tt][(r * P + j) / 2][threadIdx.x])[(r * P + j) & 1];
-                    const float2 q = pair_mul(make_float2(d, d), a2[r][j]);
-                    const float2 a = make_float2(exp2_hw(q.x), exp2_hw(q.y));
-                    const float2 now = pair_fma(make_float2(dx, dx), bb, ah);
-                    float2 g = pair_fma(make_float2(gy, gy), cc, dh[r][j]);
-                    const float2 pb = pair_fma(g, make_float2(dx, dx), make_float2(w[2 * j], w[2 * j + 1]));
-                    const float2 pc = pair_fma(now, make_float2(gy, gy), make_float2(w[RN + 2 * j], w[RN + 2 * j + 1]));
-                    w[2 * j] = pb.x, w[2 * j + 1] = pb.y, w[RN + 2 * j] = pc.x, w[RN + 2 * j + 1] = pc.y;
-                    sb = pair_fma(g, bb, sb);
-                    const float2 u = pair_mul(g, ah);
-                    sa = pair_fma(u, a2[r][j], sa);
-                    ga[r][j] = pair_fma(u, make_float2(d, d), ga[r][j]);
-                    dh[r][j] = pair_mul(g, a);
+        };
+        int tt = live - 1;
+        bool turned = false;
+        for (int k0 = (live - 1) / kGroup * kGroup; k0 >= 0; k0 -= kGroup) {
+            // pairs of tokens, so that the two registers' roles are fixed
+#pragma unroll 1
+            while (tt >= k0) {
+                if (!turned) {
+                    step(tt, one, other);
+                    if (--tt < k0) {
+                        turned = true;
+                        break;
+                    }
                 }
-                s1[r] = sb.x + sb.y;
-                s2[r] = sa.x + sa.y;
+                step(tt, other, one);
+                turned = false;
+                --tt;
             }
-            const float of_b = over_states<RC>(s1, lane), of_a = over_states<RC>(s2, lane);
-            if (owner) {
-                const float d = at.d[tt][own], x = to_f32(at.x[tt][own]), gy = at.gy[tt][own];
-                float gd = fmaf(of_a, kLn2, of_b * x);
-                if (L.softplus) gd *= logistic(to_f32(at.delta[tt][own]) + own_bias);
-                gskip = fmaf(gy, x, gskip);
-                gbias += gd;
-                const int64_t t = t0 + tt;
-                gx[t * B.S.gx.stride_t] = from_f32<T>(fmaf(of_b, d, gy * skip));
-                gdelta[t * B.S.gdelta.stride_t] = from_f32<T>(gd);
-                if (gated) {
-                    const float z = to_f32(at.gate[tt][own]);
-                    ggate[t * B.S.ggate.stride_t] =
-                        from_f32<T>(to_f32(at.g[tt][own]) * fmaf(skip, x, at.y[tt][own]) * silu_slope(z, logistic(z)));
+            __syncthreads();
+            // gB and gC of these tokens: 16 rows (a token's two) of NL float4 each, the sum of 128 / NL terms
+            constexpr int PARTS = 8 / NL > 0 ? 8 / NL : 1, TERMS = kThreads / NL / PARTS, EACH = kThreads / (NL * PARTS);
+#pragma unroll
+            for (int q = 0; q < 2 * kGroup; q += EACH) {
+                const int r = q + threadIdx.x / (NL * PARTS), s = threadIdx.x % NL, part = threadIdx.x / NL % PARTS;
+                const float4* const f = &buf.terms[r / 2][r % 2][s + NL * part];
+                float4 v = f[0];
+#pragma unroll 8
+                for (int j = 1; j < TERMS; ++j) {
+                    const float4 t = f[j * NL * PARTS];
+                    v.x += t.x, v.y += t.y, v.z += t.z, v.w += t.w;
+                }
+#pragma unroll
+                for (int m = NL; m < NL * PARTS; m *= 2) {
+                    v.x += __shfl_xor_sync(0xffffffffu, v.x, m);
+                    v.y += __shfl_xor_sync(0xffffffffu, v.y, m);
+                    v.z += __shfl_xor_sync(0xffffffffu, v.z, m);
+                    v.w += __shfl_xor_sync(0xffffffffu, v.w, m);
+                }
+                const int token = k0 + r / 2;
+                if (part == 0 && token < live) {
+                    float* const o = bc + ((t0 + token) * 2 + r % 2) * L.N + 4 * s;
+                    if (L.N % 4 == 0) {
+                        if (4 * s < L.N) *reinterpret_cast<float4*>(o) = v;
+                    } else {
+                        if (4 * s < L.N) o[0] = v.x;
+                        if (4 * s + 1 < L.N) o[1] = v.y;
+                        if (4 * s + 2 < L.N) o[2] = v.z;
+                        if (4 * s + 3 < L.N) o[3] = v.w;
+                    }
                 }
             }
-            const int first = over_channels<2 * RN, 16>(w, lane);
-            constexpr int LEFT = 2 * RN >= 8 ? 2 * RN / 8 : 1;
-#pragma unroll
-            for (int j = 0; j < LEFT; ++j) {
-                const int e = first + j;
-                at.part[tt][warp][(e / RN) * NP + n0 + e % RN] = w[j];
+            __syncthreads();
+        }
+#pragma unroll 2
+        for (int k = 0; k < K; k += STEP) {
+            const int t = at0 + k;
+            if (t >= live) break;
+            const float2 x = load_two(&at.x[t][two]), gy = load_two(&buf.gy[t][two]), ob = load_two(&buf.of_b[t][two]);
+            float2 gd = pair_fma(load_two(&buf.of_a[t][two]), pair_of(kLn2), pair_mul(ob, x));
+            if (L.softplus) gd = pair_mul(gd, pair_logistic<true>(pair_add(load_two(&at.delta[t][two]), bias)));
+            gskip = pair_fma(gy, x, gskip);
+            gbias = pair_add(gbias, gd);
+            put(gx + (t0 + t) * B.S.gx.stride_t, pair_fma(ob, load_two(&buf.d[t][two]), pair_mul(gy, skip)));
+            put(gdelta + (t0 + t) * B.S.gdelta.stride_t, gd);
+            if (gated) {
+                const float2 z = load_two(&at.gate[t][two]), s = pair_logistic<kWide>(z);
+                const float2 of_z = pair_mul(load_two(&at.g[t][two]), pair_fma(skip, x, load_two(&buf.dx[t][two])));
+                put(ggate + (t0 + t) * B.S.ggate.stride_t, pair_mul(of_z, make_float2(silu_slope(z.x, s.x), silu_slope(z.y, s.y))));
             }
         }
-        __syncthreads();
-        for (int k = threadIdx.x; k < K * 2 * NP; k += kThreads) {
-            const int tt = k / (2 * NP), e = k % (2 * NP), n = e % NP;
-            if (tt < live && n < L.N) {
-                float s = at.part[tt][0][e];
-#pragma unroll
-                for (int v = 1; v < kWarps; ++v) s += at.part[tt][v][e];
-                bc[(t0 + tt) * 2 * L.N + (e / NP) * L.N + n] = s;
-            }
+        if (Buf::STAGES == 1) {
+            __syncthreads();
+            if (i > 0) fetch(i - 1);
         }
-        __syncthreads();
     }
     // tokens past the row's length
-    if (owner)
-        for (int64_t t = end > begin ? end : begin; t < stop; ++t) {
-            gx[t * B.S.gx.stride_t] = from_f32<T>(0.0f);
-            gdelta[t * B.S.gdelta.stride_t] = from_f32<T>(0.0f);
-            if (gated) ggate[t * B.S.ggate.stride_t] = from_f32<T>(0.0f);
+    if (c2 < p.last)
+        for (int64_t t = (end > begin ? end : begin) + at0; t < stop; t += STEP) {
+            put(gx + t * B.S.gx.stride_t, pair_of(0.f));
+            put(gdelta + t * B.S.gdelta.stride_t, pair_of(0.f));
+            if (gated) put(ggate + t * B.S.ggate.stride_t, pair_of(0.f));
         }
-    const int64_t part_row = (static_cast<int64_t>(p.seg) * L.B + p.b) * L.C;
+    if (p.seg == 0 && B.S.ginit != nullptr) store_block(B.S.ginit + p.b * rows, L.N, c, p.last, n0, L.N, wide, dh);
+    float* const part = B.S.part_c + (static_cast<int64_t>(p.seg) * L.B + p.b) * L.C * (L.N + 2);
+    store_block(part, L.N + 2, c, p.last, n0, L.N, false, ga);
+    // the sums of the lanes that took every STEP-th token
 #pragma unroll
-    for (int r = 0; r < RC; ++r) {
-        const int64_t c = p.first + tile + r;
-        if (c >= p.last) continue;
-        if (p.seg == 0 && B.S.ginit != nullptr) store_states<RN>(B.S.ginit + (p.b * L.C + c) * L.N, n0, L.N, wide, dh[r]);
-        store_states<RN>(B.S.part_c + (part_row + c) * (L.N + 2), n0, L.N, false, ga[r]);
+    for (int m = PAIRS; m < 32; m *= 2) {
+        gskip.x += __shfl_xor_sync(0xffffffffu, gskip.x, m);
+        gskip.y += __shfl_xor_sync(0xffffffffu, gskip.y, m);
+        gbias.x += __shfl_xor_sync(0xffffffffu, gbias.x, m);
+        gbias.y += __shfl_xor_sync(0xffffffffu, gbias.y, m);
     }
-    if (owner) {
-        float* const q = B.S.part_c + (part_row + oc) * (L.N + 2) + L.N;
-        q[0] = gskip;
-        q[1] = gbias;
+    if (at0 == 0) {
+        float* const q = part + c2 * (L.N + 2) + L.N;
+        if (c2 < p.last) q[0] = gskip.x, q[1] = gbias.x;
+        if (c2 + 1 < p.last) q[L.N + 2] = gskip.y, q[L.N + 3] = gbias.y;
     }
+    tc::fence_before();
+    __syncthreads();
+    if (warp == 0) tc::dealloc(buf.tmem, kColumns);
 }
 
 // gB and gC: the sums over the CTAs of a group, token by token
@@ -322,10 +380,10 @@ __global__ void __launch_bounds__(256) k_sscan_sum_c(const __grid_constant__ Bwd
     to[e < L.N ? c * L.N + e : c] = s;
 }
 
-template <typename T, int RN, bool VEC>
+template <typename T, int NL>
 cudaError_t go(const BwdArgs& B) {
-    const int bytes = static_cast<int>(sizeof(typename Shape<T, RN>::Buf));
-    auto* kernel = k_sscan_bwd<T, RN, VEC>;
+    const int size = static_cast<int>(sizeof(BwdTile<T, NL>)), bytes = size > kLeastBytes ? size : kLeastBytes;
+    auto* kernel = k_sscan_bwd<T, NL>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     const ScanLaunch& L = B.A.L;
@@ -333,30 +391,30 @@ cudaError_t go(const BwdArgs& B) {
     return cudaGetLastError();
 }
 
-template <typename T, bool VEC>
+template <typename T>
 cudaError_t by_states(const BwdArgs& B) {
     const int N = B.A.L.N;
-    if (N <= 8) return go<T, 2, VEC>(B);
-    if (N <= 16) return go<T, 4, VEC>(B);
-    if (N <= 32) return go<T, 8, VEC>(B);
-    return go<T, 16, VEC>(B);
+    if (N <= 8) return go<T, 2>(B);
+    if (N <= 16) return go<T, 4>(B);
+    if (N <= 32) return go<T, 8>(B);
+    return go<T, 16>(B);
 }
 
 }  // namespace
 
 cudaError_t launch_scan_backward(const ScanBackward& S, int* kernels) {
-    BwdArgs B{scan_args(S.f), S};
+    BwdArgs B{scan_args(S.f, scan_bwd_channels(S.f.N)), S};
     B.A.g = S.g;
     const ScanLaunch& L = S.f;
-    const bool vec = scan_vectors(L, &S.g);
+    B.A.vec = scan_vectors(L, &S.g);
+    B.A.pairs = scan_pairs(L, S.gx) && scan_pairs(L, S.gdelta) && (S.ggate.data == nullptr || scan_pairs(L, S.ggate));
     cudaError_t e;
     *kernels = 0;
     if (L.segs > 1) {
         if ((e = launch_scan_own_grads(S)) != cudaSuccess) return e;
         ++*kernels;
     }
-    if (L.bf16) e = vec ? by_states<__nv_bfloat16, true>(B) : by_states<__nv_bfloat16, false>(B);
-    else e = vec ? by_states<float, true>(B) : by_states<float, false>(B);
+    e = L.bf16 ? by_states<__nv_bfloat16>(B) : by_states<float>(B);
     if (e != cudaSuccess) return e;
     ++*kernels;
     if (L.T > 0) {
