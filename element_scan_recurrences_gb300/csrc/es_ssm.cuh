@@ -78,25 +78,25 @@ __device__ __forceinline__ float softplus(float x) {
 // of e^-z, for results rounded to bf16).
 __device__ __forceinline__ float2 pair_of(float v) { return make_float2(v, v); }
 
+// e^-m for m >= -87 (past 87 it is 0 or next to it)
 template <bool EXACT>
-__device__ __forceinline__ float2 pair_exp(float2 x) {
-    const float2 t = pair_mul(x, pair_of(kLog2e));
+__device__ __forceinline__ float2 pair_exp_minus(float2 m) {
+    const float2 t = pair_mul(m, pair_of(-kLog2e));
     const float2 e = make_float2(exp2_hw(t.x), exp2_hw(t.y));
     if constexpr (!EXACT) return e;
-    const float2 lost = pair_fma(x, pair_of(kLog2eLow), pair_fma(x, pair_of(kLog2e), make_float2(-t.x, -t.y)));
-    return pair_fma(e, pair_mul(lost, pair_of(kLn2)), e);
+    const float2 lost = pair_fma(m, pair_of(kLog2eLow), pair_fma(m, pair_of(kLog2e), t));
+    return pair_fma(e, pair_mul(lost, pair_of(-kLn2)), e);
 }
 
 template <bool EXACT>
 __device__ __forceinline__ float2 pair_logistic(float2 z) {
-    const float2 e = pair_exp<EXACT>(make_float2(-fmaxf(z.x, -87.0f), -fmaxf(z.y, -87.0f)));
-    const float2 d = pair_add(e, pair_of(1.0f));
+    const float2 d = pair_add(pair_exp_minus<EXACT>(make_float2(fmaxf(z.x, -87.0f), fmaxf(z.y, -87.0f))), pair_of(1.0f));
     return make_float2(rcp_hw(d.x), rcp_hw(d.y));
 }
 
 __device__ __forceinline__ float2 pair_softplus(float2 x) {
     const float2 m = make_float2(fabsf(x.x), fabsf(x.y));
-    const float2 e = pair_exp<true>(make_float2(-fminf(m.x, 87.0f), -fminf(m.y, 87.0f)));
+    const float2 e = pair_exp_minus<true>(make_float2(fminf(m.x, 87.0f), fminf(m.y, 87.0f)));
     float2 p = pair_fma(e, pair_of(-0.003244024235755205f), pair_of(0.019851457327604294f));
     p = pair_fma(p, e, pair_of(-0.056959524750709534f));
     p = pair_fma(p, e, pair_of(0.10603653639554977f));
@@ -141,10 +141,40 @@ __device__ __forceinline__ void store_pack(T* p, const float (&r)[V]) {
     for (int i = 0; i < V; ++i) q.v[i] = from_f32<T>(r[i]);
     *reinterpret_cast<Pack<T, V>*>(p) = q;
 }
+// the same as pairs (one half for V = 1), from what a load left in registers
+template <typename T, int V>
+__device__ __forceinline__ void unpack(const Pack<T, V>& q, float2 (&r)[(V + 1) / 2]) {
+    if constexpr (V == 1) {
+        r[0] = make_float2(to_f32(q.v[0]), 0.0f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) r[i] = make_float2(to_f32(q.v[2 * i]), to_f32(q.v[2 * i + 1]));
+    }
+}
+template <typename T, int V>
+__device__ __forceinline__ Pack<T, V> pack(const float2 (&r)[(V + 1) / 2]) {
+    Pack<T, V> q;
+    if constexpr (V == 1) {
+        q.v[0] = from_f32<T>(r[0].x);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) store_two(&q.v[2 * i], r[i]);
+    }
+    return q;
+}
+template <typename T, int V>
+__device__ __forceinline__ Pack<T, V> load_raw(const T* p) {
+    return *reinterpret_cast<const Pack<T, V>*>(p);
+}
 template <int V>
 __device__ __forceinline__ void zero(float (&r)[V]) {
 #pragma unroll
     for (int i = 0; i < V; ++i) r[i] = 0.0f;
+}
+template <int P>
+__device__ __forceinline__ void zero(float2 (&r)[P]) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) r[i] = make_float2(0.0f, 0.0f);
 }
 
 // a weight of either type

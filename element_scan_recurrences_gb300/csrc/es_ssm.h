@@ -19,6 +19,7 @@ constexpr int kMaxNormDim = 8192;
 
 struct ConvLaunch {
     int bf16, w_bf16, taps, act;
+    int run;                    // tokens a thread takes (the launch sets it)
     int64_t B, T, C;
     es_rows x, out;             // backward: out is grad_x
     const void *w, *bias;
@@ -35,8 +36,8 @@ struct ConvLaunch {
 
 // blocks over batch and tokens of a backward call (each keeps a row of `partial`)
 int64_t conv_backward_rows(const ConvLaunch& L);
-cudaError_t launch_conv(const ConvLaunch& L, int* kernels);
-cudaError_t launch_conv_backward(const ConvLaunch& L, int* kernels);
+cudaError_t launch_conv(ConvLaunch L, int* kernels);
+cudaError_t launch_conv_backward(ConvLaunch L, int* kernels);
 cudaError_t launch_conv_step(const ConvLaunch& L);
 
 // ---------------------------------------------------------------------------

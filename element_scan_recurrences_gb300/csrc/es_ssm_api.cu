@@ -133,8 +133,8 @@ es_status plan_conv(const char* fn, const es_causal_conv_args* a, const es_causa
             P->bytes = static_cast<size_t>(conv_backward_rows(L)) * (W + 1) * C * 4;
     }
     P->empty = B == 0 || C == 0;
-    const int64_t threads = B * (T / 32 + 1) * (C / 128 + 1);
-    if (threads > kMostBlocks) return api_fail(ES_E_UNSUPPORTED, "%s: too many elements", fn);
+    const int64_t blocks = B * (T / 8 + 1) * (C / 128 + 1);
+    if (blocks > kMostBlocks) return api_fail(ES_E_UNSUPPORTED, "%s: too many elements", fn);
     return no_overlap(fn, S, a->workspace, P->bytes);
 }
 

@@ -4,13 +4,14 @@
 //     p[t] = bias + sum_j w[j] x[t - W + 1 + j],   out = p / (1 + e^-p)
 //
 // Bounded by HBM: 2 W + 4 operations against 4 bytes an element in bf16.  A thread
-// takes 16 bytes of channels through a run of tokens with the last W - 1 inputs in
-// registers, so each input is read once but for W - 1 tokens a run; a warp's
-// accesses are whole 512-byte rows, and the unrolled loop keeps several in flight.
-// The gradient is one pass over x and the gradient of out the same way: p is formed
-// again, and the gradients of the last W tokens' p in registers give that of the
-// input W - 1 tokens back.  The weights' sums over a run stay in registers and meet
-// in a second launch, always in one order.
+// takes 16 bytes of channels (8 backwards) through a run of tokens with the last
+// W - 1 inputs in registers, so each input is read once but for W - 1 tokens a run;
+// a warp's accesses are whole rows of 256 bytes or more.  Tokens come in blocks whose
+// loads are issued a block ahead; products and sums are made two channels an
+// instruction.  The gradient is one pass over x and the gradient of out the same
+// way: p is formed again, and the gradients of the last W tokens' p in registers give
+// that of the input W - 1 tokens back.  The weights' sums over a run stay in
+// registers and meet in a second launch, always in one order.
 #include "es_attn.h"
 #include "es_ssm.cuh"
 #include "es_ssm.h"
@@ -19,24 +20,56 @@ namespace es {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kRun = 32;            // tokens a thread, forwards
-constexpr int kRunBack = 64;        // and backwards: fewer partial sums of the weights
+
+template <int V>
+constexpr int kPairs = (V + 1) / 2;
+// tokens a block: at least 4, whole rounds of the W places that the last inputs go around
+template <int W>
+constexpr int kBlock = W >= 4 ? W : W == 3 ? 6 : 4;
 
 // The input at token t of a row (the carried one before the first, zeros without).
 template <typename T, int V, int W>
-__device__ __forceinline__ void input_at(const ConvLaunch& L, const T* x, int64_t b, int64_t c, int64_t t, float (&r)[V]) {
-    if (t >= 0) load_pack<T, V>(x + t * L.x.stride_t, r);
-    else if (L.init != nullptr && t >= 1 - W) load_pack<T, V>(static_cast<const T*>(L.init) + (b * (W - 1) + t + W - 1) * L.C + c, r);
+__device__ __forceinline__ void input_at(const ConvLaunch& L, const T* x, int64_t b, int64_t c, int64_t t, float2 (&r)[kPairs<V>]) {
+    if (t >= 0) unpack<T, V>(load_raw<T, V>(x + t * L.x.stride_t), r);
+    else if (L.init != nullptr && t >= 1 - W)
+        unpack<T, V>(load_raw<T, V>(static_cast<const T*>(L.init) + (b * (W - 1) + t + W - 1) * L.C + c), r);
     else zero(r);
 }
 
-template <typename T, int V, int W>
-__device__ __forceinline__ void load_weights(const ConvLaunch& L, int64_t c, float (&w)[W][V], float (&bias)[V]) {
+// The weights of V channels lie side by side.
+template <typename W_, int V, int W>
+__device__ __forceinline__ void weights_of(const W_* p, bool wide, float2 (&w)[W][kPairs<V>]) {
+    constexpr int N = V * W, S = 16 / sizeof(W_);
+    float f[N];
+    if (N % S == 0 && wide) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
+        for (int i = 0; i < N / S; ++i) {
+            const Pack<W_, S> q = load_raw<W_, S>(p + i * S);
 #pragma unroll
-        for (int j = 0; j < W; ++j) w[j][i] = weight_at(L.w, L.w_bf16, (c + i) * W + j);
-        bias[i] = L.bias != nullptr ? weight_at(L.bias, L.w_bf16, c + i) : 0.0f;
+            for (int j = 0; j < S; ++j) f[i * S + j] = to_f32(q.v[j]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) f[i] = to_f32(p[i]);
+    }
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+#pragma unroll
+        for (int i = 0; i < kPairs<V>; ++i)
+            w[j][i] = make_float2(f[2 * i * W + j], 2 * i + 1 < V ? f[(2 * i + 1 < V ? 2 * i + 1 : 0) * W + j] : 0.0f);
+}
+template <int V, int W>
+__device__ __forceinline__ void load_weights(const ConvLaunch& L, int64_t c, float2 (&w)[W][kPairs<V>], float2 (&bias)[kPairs<V>]) {
+    const bool wide = reinterpret_cast<uintptr_t>(L.w) % 16 == 0;
+    if (L.w_bf16) weights_of<__nv_bfloat16, V, W>(static_cast<const __nv_bfloat16*>(L.w) + c * W, wide, w);
+    else weights_of<float, V, W>(static_cast<const float*>(L.w) + c * W, wide, w);
+#pragma unroll
+    for (int i = 0; i < kPairs<V>; ++i) {
+        bias[i] = pair_of(0.f);
+        if (L.bias != nullptr) {
+            bias[i].x = weight_at(L.bias, L.w_bf16, c + 2 * i);
+            if (2 * i + 1 < V) bias[i].y = weight_at(L.bias, L.w_bf16, c + 2 * i + 1);
+        }
     }
 }
 
@@ -44,72 +77,103 @@ struct ConvPlace {
     int64_t b, c, begin;
 };
 // a thread's batch row, channels and first token; false past the last channel
-template <int V, int RUN>
+template <int V>
 __device__ __forceinline__ bool conv_place(const ConvLaunch& L, ConvPlace* p) {
-    const int64_t across = (L.C / V + kThreads - 1) / kThreads, runs = L.T == 0 ? 1 : (L.T + RUN - 1) / RUN;
+    const int64_t across = (L.C / V + kThreads - 1) / kThreads, runs = L.T == 0 ? 1 : (L.T + L.run - 1) / L.run;
     int64_t i = blockIdx.x;
     p->c = (i % across * kThreads + threadIdx.x) * V;
     i /= across;
-    p->begin = i % runs * RUN;
+    p->begin = i % runs * L.run;
     p->b = i / runs;
     return p->c < L.C;
 }
 
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(kThreads) k_conv(const __grid_constant__ ConvLaunch L) {
+    constexpr int P = kPairs<V>, BLK = kBlock<W>;
     ConvPlace p;
-    if (!conv_place<V, kRun>(L, &p)) return;
+    if (!conv_place<V>(L, &p)) return;
     const int64_t len = live_tokens(L.lengths, p.b, L.T);
-    const int64_t stop = p.begin + kRun < L.T ? p.begin + kRun : L.T, end = stop < len ? stop : len;
+    const int64_t stop = p.begin + L.run < L.T ? p.begin + L.run : L.T, end = stop < len ? stop : len;
     const T* const x = static_cast<const T*>(L.x.data) + p.b * L.x.stride_b + p.c;
     T* const out = static_cast<T*>(L.out.data) + p.b * L.out.stride_b + p.c;
-    float w[W][V], bias[V], row[W][V];
+    float2 w[W][P], bias[P], row[W][P];              // token t's input at place (t - begin + W - 1) % W of `row`
+    Pack<T, V> next[BLK];
+    auto fetch = [&](int64_t t) {
+#pragma unroll
+        for (int k = 0; k < BLK; ++k)
+            if (t + k < end) next[k] = load_raw<T, V>(x + (t + k) * L.x.stride_t);
+    };
+    if (p.begin < end) fetch(p.begin);
     if (p.begin < end || p.begin == 0) {
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) input_at<T, V, W>(L, x, p.b, p.c, p.begin - (W - 1) + j, row[j]);
     }
     if (p.begin == 0 && L.fin != nullptr) {
         // the carried inputs may lie where the last ones go: only this thread reads them, and has by now
-        float last[W - 1][V];
+        float2 last[W - 1][P];
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) input_at<T, V, W>(L, x, p.b, p.c, len - (W - 1) + j, last[j]);
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) store_pack<T, V>(static_cast<T*>(L.fin) + (p.b * (W - 1) + j) * L.C + p.c, last[j]);
+        for (int j = 0; j < W - 1; ++j)
+            *reinterpret_cast<Pack<T, V>*>(static_cast<T*>(L.fin) + (p.b * (W - 1) + j) * L.C + p.c) = pack<T, V>(last[j]);
     }
-    load_weights<T, V, W>(L, p.c, w, bias);
-#pragma unroll 4
-    for (int64_t t = p.begin; t < end; ++t) {
-        load_pack<T, V>(x + t * L.x.stride_t, row[W - 1]);
-        float o[V];
+    load_weights<V, W>(L, p.c, w, bias);
+    for (int64_t t = p.begin; t < end; t += BLK) {
+        Pack<T, V> now[BLK];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            float s = bias[i];
+        for (int k = 0; k < BLK; ++k) now[k] = next[k];
+        fetch(t + BLK);
 #pragma unroll
-            for (int j = 0; j < W; ++j) s = fmaf(w[j][i], row[j][i], s);
-            o[i] = L.act ? s * logistic(s) : s;
+        for (int k = 0; k < BLK; ++k) {
+            if (t + k >= end) break;
+            unpack<T, V>(now[k], row[(k + W - 1) % W]);
+            float2 o[P];
 #pragma unroll
-            for (int j = 0; j < W - 1; ++j) row[j][i] = row[j + 1][i];
+            for (int i = 0; i < P; ++i) {
+                o[i] = bias[i];
+#pragma unroll
+                for (int j = 0; j < W; ++j) o[i] = pair_fma(w[j][i], row[(k + j) % W][i], o[i]);
+            }
+            if (L.act) {
+#pragma unroll
+                for (int i = 0; i < P; ++i) o[i] = pair_mul(o[i], pair_logistic<sizeof(T) == 4>(o[i]));
+            }
+            *reinterpret_cast<Pack<T, V>*>(out + (t + k) * L.out.stride_t) = pack<T, V>(o);
         }
-        store_pack<T, V>(out + t * L.out.stride_t, o);
     }
-    float none[V];
+    float2 none[P];
     zero(none);
-    for (int64_t t = end > p.begin ? end : p.begin; t < stop; ++t) store_pack<T, V>(out + t * L.out.stride_t, none);
+    for (int64_t t = end > p.begin ? end : p.begin; t < stop; ++t)
+        *reinterpret_cast<Pack<T, V>*>(out + t * L.out.stride_t) = pack<T, V>(none);
 }
 
 // Token u gives the gradient gp of its p, and with the W - 1 before it that of the
 // input at token u - (W - 1); before the first token those are the carried inputs.
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(kThreads) k_conv_bwd(const __grid_constant__ ConvLaunch L) {
+    constexpr int P = kPairs<V>, BLK = kBlock<W>;
     ConvPlace p;
-    if (!conv_place<V, kRunBack>(L, &p)) return;
+    if (!conv_place<V>(L, &p)) return;
     const int64_t len = live_tokens(L.lengths, p.b, L.T);
-    const int64_t stop = p.begin + kRunBack < L.T ? p.begin + kRunBack : L.T;
+    const int64_t stop = p.begin + L.run < L.T ? p.begin + L.run : L.T;
     const T* const x = static_cast<const T*>(L.x.data) + p.b * L.x.stride_b + p.c;
     const T* const g = static_cast<const T*>(L.g.data) + p.b * L.g.stride_b + p.c;
     T* const out = static_cast<T*>(L.out.data) + p.b * L.out.stride_b + p.c;
-    float w[W][V], bias[V], row[W][V], gp[W][V], gw[W][V], gb[V];
-    load_weights<T, V, W>(L, p.c, w, bias);
+    float2 w[W][P], bias[P], row[W][P], gp[W][P], gw[W][P], gb[P];      // `row` and `gp` go around as in k_conv
+    Pack<T, V> next_x[BLK], next_g[BLK];
+    // the tokens whose p this run needs: W - 1 past its own
+    const int64_t until = stop + W - 1 < len ? stop + W - 1 : len;
+    auto fetch = [&](int64_t u) {
+#pragma unroll
+        for (int k = 0; k < BLK; ++k)
+            if (u + k < until) {
+                next_x[k] = load_raw<T, V>(x + (u + k) * L.x.stride_t);
+                next_g[k] = load_raw<T, V>(g + (u + k) * L.g.stride_t);
+            }
+    };
+    fetch(p.begin);
+    load_weights<V, W>(L, p.c, w, bias);
     zero(gb);
 #pragma unroll
     for (int j = 0; j < W; ++j) {
@@ -121,86 +185,104 @@ __global__ void __launch_bounds__(kThreads) k_conv_bwd(const __grid_constant__ C
         if (p.begin - (W - 1) + j < len) input_at<T, V, W>(L, x, p.b, p.c, p.begin - (W - 1) + j, row[j]);
         else zero(row[j]);
     }
-#pragma unroll 2
-    for (int64_t u = p.begin; u < stop + W - 1; ++u) {
-        const bool live = u < len;
-        float go[V];
-        if (live) {
-            load_pack<T, V>(x + u * L.x.stride_t, row[W - 1]);
-            load_pack<T, V>(g + u * L.g.stride_t, go);
-        } else {
-            zero(row[W - 1]);
-            zero(go);
+    for (int64_t u0 = p.begin; u0 < stop + W - 1; u0 += BLK) {
+        Pack<T, V> now_x[BLK], now_g[BLK];
+#pragma unroll
+        for (int k = 0; k < BLK; ++k) {
+            now_x[k] = next_x[k];
+            now_g[k] = next_g[k];
         }
-        const int64_t t = u - (W - 1), j = t - len + W - 1;      // the input, its place in the state after
-        float gx[V];
-        zero(gx);
-        if (j >= 0 && j < W - 1 && L.gfin != nullptr && (t >= p.begin || p.begin == 0))
-            load_pack<T, V>(static_cast<const T*>(L.gfin) + (p.b * (W - 1) + j) * L.C + p.c, gx);
+        fetch(u0 + BLK);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            float q = go[i];
-            if (L.act) {
-                float s = bias[i];
+        for (int k = 0; k < BLK; ++k) {
+            const int64_t u = u0 + k;
+            if (u >= stop + W - 1) break;
+            auto& q = gp[(k + W - 1) % W];
+            auto& in = row[(k + W - 1) % W];
+            if (u < until) {
+                unpack<T, V>(now_x[k], in);
+                unpack<T, V>(now_g[k], q);
+                if (L.act) {
 #pragma unroll
-                for (int m = 0; m < W; ++m) s = fmaf(w[m][i], row[m][i], s);
-                q *= silu_slope(s, logistic(s));
+                    for (int i = 0; i < P; ++i) {
+                        float2 s = bias[i];
+#pragma unroll
+                        for (int m = 0; m < W; ++m) s = pair_fma(w[m][i], row[(k + m) % W][i], s);
+                        const float2 l = pair_logistic<sizeof(T) == 4>(s);
+                        // l + s l (1 - l)
+                        q[i] = pair_mul(q[i], pair_fma(pair_mul(s, l), pair_fma(l, pair_of(-1.f), pair_of(1.f)), l));
+                    }
+                }
+            } else {
+                zero(in);
+                zero(q);
             }
-            gp[W - 1][i] = q;
             if (u < stop) {
-                gb[i] += q;
 #pragma unroll
-                for (int m = 0; m < W; ++m) gw[m][i] = fmaf(q, row[m][i], gw[m][i]);
+                for (int i = 0; i < P; ++i) {
+                    gb[i] = pair_add(gb[i], q[i]);
+#pragma unroll
+                    for (int m = 0; m < W; ++m) gw[m][i] = pair_fma(q[i], row[(k + m) % W][i], gw[m][i]);
+                }
             }
+            const int64_t t = u - (W - 1), j = t - len + W - 1;      // the input, its place in the state after
+            float2 gx[P];
+            zero(gx);
+            if (j >= 0 && j < W - 1 && L.gfin != nullptr && (t >= p.begin || p.begin == 0))
+                unpack<T, V>(load_raw<T, V>(static_cast<const T*>(L.gfin) + (p.b * (W - 1) + j) * L.C + p.c), gx);
 #pragma unroll
-            for (int m = 0; m < W; ++m) gx[i] = fmaf(w[W - 1 - m][i], gp[m][i], gx[i]);
+            for (int i = 0; i < P; ++i)
 #pragma unroll
-            for (int m = 0; m < W - 1; ++m) {
-                gp[m][i] = gp[m + 1][i];
-                row[m][i] = row[m + 1][i];
-            }
+                for (int m = 0; m < W; ++m) gx[i] = pair_fma(w[W - 1 - m][i], gp[(k + m) % W][i], gx[i]);
+            if (t >= p.begin) *reinterpret_cast<Pack<T, V>*>(out + t * L.out.stride_t) = pack<T, V>(gx);
+            else if (t < 0 && L.fin != nullptr)
+                *reinterpret_cast<Pack<T, V>*>(static_cast<T*>(L.fin) + (p.b * (W - 1) + u) * L.C + p.c) = pack<T, V>(gx);
         }
-        if (t >= p.begin) store_pack<T, V>(out + t * L.out.stride_t, gx);
-        else if (t < 0 && L.fin != nullptr) store_pack<T, V>(static_cast<T*>(L.fin) + (p.b * (W - 1) + u) * L.C + p.c, gx);
     }
     if (L.partial == nullptr) return;
-    const int64_t runs = L.T == 0 ? 1 : (L.T + kRunBack - 1) / kRunBack;
-    float* const q = L.partial + (p.b * runs + p.begin / kRunBack) * (W + 1) * L.C + p.c;
+    const int64_t runs = L.T == 0 ? 1 : (L.T + L.run - 1) / L.run;
+    float* const q = L.partial + (p.b * runs + p.begin / L.run) * (W + 1) * L.C + p.c;
 #pragma unroll
-    for (int j = 0; j < W; ++j) store_pack<float, V>(q + j * L.C, gw[j]);
-    store_pack<float, V>(q + W * L.C, gb);
+    for (int j = 0; j < W; ++j) *reinterpret_cast<Pack<float, V>*>(q + j * L.C) = pack<float, V>(gw[j]);
+    *reinterpret_cast<Pack<float, V>*>(q + W * L.C) = pack<float, V>(gb);
 }
 
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(kThreads) k_conv_step(const __grid_constant__ ConvLaunch L) {
+    constexpr int P = kPairs<V>;
     const int64_t across = (L.C / V + kThreads - 1) / kThreads, b = blockIdx.x / across;
     const int64_t c = (blockIdx.x % across * kThreads + threadIdx.x) * V;
     if (c >= L.C) return;
-    float w[W][V], bias[V], row[W][V], o[V];
+    float2 w[W][P], bias[P], x[P], o[P];
+    Pack<T, V> row[W];
     const T* const from = static_cast<const T*>(L.init) + b * (W - 1) * L.C + c;
     T* const to = static_cast<T*>(L.fin) + b * (W - 1) * L.C + c;
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) load_pack<T, V>(from + j * L.C, row[j]);
-    load_pack<T, V>(static_cast<const T*>(L.x.data) + b * L.x.stride_b + c, row[W - 1]);
-    load_weights<T, V, W>(L, c, w, bias);
+    for (int j = 0; j < W - 1; ++j) row[j] = load_raw<T, V>(from + j * L.C);
+    row[W - 1] = load_raw<T, V>(static_cast<const T*>(L.x.data) + b * L.x.stride_b + c);
+    load_weights<V, W>(L, c, w, bias);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        float s = bias[i];
+    for (int j = 0; j < W - 1; ++j) *reinterpret_cast<Pack<T, V>*>(to + j * L.C) = row[j + 1];
 #pragma unroll
-        for (int j = 0; j < W; ++j) s = fmaf(w[j][i], row[j][i], s);
-        o[i] = L.act ? s * logistic(s) : s;
+    for (int i = 0; i < P; ++i) o[i] = bias[i];
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+        unpack<T, V>(row[j], x);
+#pragma unroll
+        for (int i = 0; i < P; ++i) o[i] = pair_fma(w[j][i], x[i], o[i]);
     }
+    if (L.act) {
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) store_pack<T, V>(to + j * L.C, row[j + 1]);
-    store_pack<T, V>(static_cast<T*>(L.out.data) + b * L.out.stride_b + c, o);
+        for (int i = 0; i < P; ++i) o[i] = pair_mul(o[i], pair_logistic<sizeof(T) == 4>(o[i]));
+    }
+    *reinterpret_cast<Pack<T, V>*>(static_cast<T*>(L.out.data) + b * L.out.stride_b + c) = pack<T, V>(o);
 }
 
 enum Kind { kForward, kBackward, kStep };
 
 template <typename T, int V, int W, Kind KIND>
 cudaError_t go(const ConvLaunch& L) {
-    const int64_t across = (L.C / V + kThreads - 1) / kThreads, run = KIND == kBackward ? kRunBack : kRun;
-    const int64_t runs = KIND == kStep || L.T == 0 ? 1 : (L.T + run - 1) / run;
+    const int64_t across = (L.C / V + kThreads - 1) / kThreads, runs = KIND == kStep || L.T == 0 ? 1 : (L.T + L.run - 1) / L.run;
     const unsigned grid = static_cast<unsigned>(across * runs * L.B);
     if (KIND == kForward) k_conv<T, V, W><<<grid, kThreads, 0, L.stream>>>(L);
     else if (KIND == kBackward) k_conv_bwd<T, V, W><<<grid, kThreads, 0, L.stream>>>(L);
@@ -234,11 +316,29 @@ bool in_units(const ConvLaunch& L, int unit) {
     return true;
 }
 
+// channels a thread
+int width_of(const ConvLaunch& L, bool backward) {
+    if (L.bf16) return backward ? (in_units(L, 8) ? 4 : 1) : in_units(L, 16) ? 8 : 1;
+    return in_units(L, 16) ? 4 : 1;
+}
+
 template <Kind KIND>
 cudaError_t by_type(const ConvLaunch& L) {
-    const bool vec = in_units(L, 16);
-    if (L.bf16) return vec ? by_taps<__nv_bfloat16, 8, KIND>(L) : by_taps<__nv_bfloat16, 1, KIND>(L);
-    return vec ? by_taps<float, 4, KIND>(L) : by_taps<float, 1, KIND>(L);
+    const int V = width_of(L, KIND == kBackward);
+    if (L.bf16) {
+        if (V == 1) return by_taps<__nv_bfloat16, 1, KIND>(L);
+        return by_taps<__nv_bfloat16, KIND == kBackward ? 4 : 8, KIND>(L);
+    }
+    return V == 1 ? by_taps<float, 1, KIND>(L) : by_taps<float, 4, KIND>(L);
+}
+
+// Tokens a run: long ones read fewer inputs twice and leave fewer partial sums,
+// short ones fill the GPU (1024 threads an SM) when there are few rows and channels.
+int run_of(const ConvLaunch& L, bool backward) {
+    int run = backward ? 128 : 64;
+    const int64_t across = L.C / width_of(L, backward);
+    while (run > 8 && L.B * across * ((L.T + run - 1) / run) < static_cast<int64_t>(kSms) * 1024) run /= 2;
+    return run;
 }
 
 // a column of the partial sums: tap (or bias) j of channel c
@@ -255,15 +355,20 @@ struct PutConv {
 
 }  // namespace
 
-int64_t conv_backward_rows(const ConvLaunch& L) { return L.B * (L.T == 0 ? 1 : (L.T + kRunBack - 1) / kRunBack); }
+int64_t conv_backward_rows(const ConvLaunch& L) {
+    const int run = run_of(L, true);
+    return L.B * (L.T == 0 ? 1 : (L.T + run - 1) / run);
+}
 
-cudaError_t launch_conv(const ConvLaunch& L, int* kernels) {
+cudaError_t launch_conv(ConvLaunch L, int* kernels) {
     *kernels = 1;
+    L.run = run_of(L, false);
     return by_type<kForward>(L);
 }
 
-cudaError_t launch_conv_backward(const ConvLaunch& L, int* kernels) {
+cudaError_t launch_conv_backward(ConvLaunch L, int* kernels) {
     *kernels = 1;
+    L.run = run_of(L, true);
     const cudaError_t e = by_type<kBackward>(L);
     if (e != cudaSuccess || L.partial == nullptr) return e;
     ++*kernels;

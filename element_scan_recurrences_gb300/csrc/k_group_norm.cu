@@ -18,6 +18,9 @@ namespace {
 
 template <int TEAM>
 constexpr int kThreadsOf = TEAM <= 32 ? 256 : TEAM;
+// Threads an SM holds, which the registers are fitted to: what hides HBM's latency is
+// the loads in flight, two rows of 32 bytes a thread forwards, of 48 backwards.
+constexpr int kResident = 768, kResidentBack = 512;
 
 // N sums over the threads of a team
 template <int TEAM, int N>
@@ -48,8 +51,11 @@ struct NormArgs {
 };
 
 template <typename T, int V, int NV, int TEAM, bool BWD>
-__global__ void __launch_bounds__(kThreadsOf<TEAM>) k_group_norm(const __grid_constant__ NormArgs A) {
-    constexpr int E = NV * V, TEAMS = kThreadsOf<TEAM> / TEAM;
+__global__ void __launch_bounds__(kThreadsOf<TEAM>, (BWD || NV * V == 16 ? 512 : kResident) / kThreadsOf<TEAM>)
+    k_group_norm(const __grid_constant__ NormArgs A) {
+    constexpr int E = NV * V, P = E / 2, TEAMS = kThreadsOf<TEAM> / TEAM;
+    constexpr bool kWide = sizeof(T) == 4;
+    using Raw = Pack<T, V>;
     __shared__ float part1[32][1];
     __shared__ float part2[32][2];
     const NormLaunch& L = A.L;
@@ -60,117 +66,183 @@ __global__ void __launch_bounds__(kThreadsOf<TEAM>) k_group_norm(const __grid_co
     const int64_t rows = L.B * L.T, step = static_cast<int64_t>(gridDim.x) * A.rows;
     const float inv = 1.0f / static_cast<float>(L.D);
     const bool gated = L.gate.data != nullptr;
-    float w[E], bias[E], gw[BWD ? E : 1], gb[BWD ? E : 1];
-    int col[NV];
+    // values e and e + 1 of a thread, as pairs; those past the group's last are zeros, and so are their weights
+    float2 w[P], bias[P], gw[BWD ? P : 1], gb[BWD ? P : 1];
+    auto col = [&](int e) { return (e / V * TEAM + lane) * V + e % V; };
+    const bool whole = L.D == TEAM * E;
+    auto both = [&](int i, float2 v) {           // v where it is a value of the group
+        if (whole) return v;
+        return make_float2(col(2 * i) < L.D ? v.x : 0.0f, col(2 * i + 1) < L.D ? v.y : 0.0f);
+    };
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        col[k] = (k * TEAM + lane) * V;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const bool in = team_in && col[k] < L.D;
-            w[k * V + i] = in && L.w != nullptr ? weight_at(L.w, L.w_bf16, h * L.D + col[k] + i) : 1.0f;
-            bias[k * V + i] = in && L.bias != nullptr ? weight_at(L.bias, L.w_bf16, h * L.D + col[k] + i) : 0.0f;
-            if constexpr (BWD) gw[k * V + i] = gb[k * V + i] = 0.0f;
-        }
-    }
-    // every team of a warp (of a block) makes every turn: the sums are taken together
-    for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * A.rows; r0 < rows; r0 += step) {
-        const int64_t r = r0 + rs;
-        const bool in = team_in && r < rows;
-        const int64_t b = in ? r / L.T : 0, t = in ? r % L.T : 0;
-        auto place = [&](const es_heads& v) { return b * v.stride_b + t * v.stride_t + h * v.stride_h; };
-        float x[E], z[E], g[BWD ? E : 1];
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const bool here = in && col[k] < L.D;
-            float v[V];
-            zero(v);
-            if (here) load_pack<T, V>(static_cast<const T*>(L.x.data) + place(L.x) + col[k], v);
-#pragma unroll
-            for (int i = 0; i < V; ++i) x[k * V + i] = v[i];
-            zero(v);
-            if (here && gated) load_pack<T, V>(static_cast<const T*>(L.gate.data) + place(L.gate) + col[k], v);
-#pragma unroll
-            for (int i = 0; i < V; ++i) z[k * V + i] = v[i];
-            if constexpr (BWD) {
-                zero(v);
-                if (here) load_pack<T, V>(static_cast<const T*>(L.g.data) + place(L.g) + col[k], v);
-#pragma unroll
-                for (int i = 0; i < V; ++i) g[k * V + i] = v[i];
+    for (int i = 0; i < P; ++i) {
+        w[i] = bias[i] = pair_of(0.f);
+        if (BWD) gw[BWD ? i : 0] = gb[BWD ? i : 0] = pair_of(0.f);
+        if (team_in) {
+            w[i] = both(i, pair_of(1.f));
+            const int64_t at = h * L.D;
+            const bool in0 = col(2 * i) < L.D, in1 = col(2 * i + 1) < L.D;
+            if (L.w != nullptr) {
+                if (in0) w[i].x = weight_at(L.w, L.w_bf16, at + col(2 * i));
+                if (in1) w[i].y = weight_at(L.w, L.w_bf16, at + col(2 * i + 1));
+            }
+            if (L.bias != nullptr) {
+                if (in0) bias[i].x = weight_at(L.bias, L.w_bf16, at + col(2 * i));
+                if (in1) bias[i].y = weight_at(L.bias, L.w_bf16, at + col(2 * i + 1));
             }
         }
-        float u[E];
+    }
+    Raw next_x[NV], next_z[NV], next_g[NV];
+    // Rows come `step` apart: a tensor's place moves by as much from turn to turn, and by
+    // the difference where the tokens of a batch row end.
+    const int64_t step_b = step / L.T, step_t = step % L.T, first = static_cast<int64_t>(blockIdx.x) * A.rows + rs;
+    auto place = [&](const es_heads& v) {
+        return static_cast<const T*>(v.data) + first / L.T * v.stride_b + first % L.T * v.stride_t + h * v.stride_h + lane * V;
+    };
+    auto on = [&](const T*& p, const es_heads& v, bool wrapped) {
+        p += step_b * v.stride_b + step_t * v.stride_t;
+        if (wrapped) p += v.stride_b - L.T * v.stride_t;
+    };
+    const T *px = place(L.x), *pz = gated ? place(L.gate) : nullptr, *pg = BWD ? place(L.g) : nullptr;      // of the row after this
+    const T *po = place(L.out), *pgz = BWD && gated ? place(L.ggate) : nullptr;                             // of this row
+    const int64_t last = rows - 1;
+    auto fetch = [&](int64_t r) {
+        if (!team_in || r > last) return;
 #pragma unroll
-        for (int e = 0; e < E; ++e) u[e] = gated && L.first ? x[e] * (z[e] * logistic(z[e])) : x[e];
+        for (int k = 0; k < NV; ++k) {
+            if (!whole && (k * TEAM + lane) * V >= L.D) continue;
+            next_x[k] = load_raw<T, V>(px + k * TEAM * V);
+            if (gated) next_z[k] = load_raw<T, V>(pz + k * TEAM * V);
+            if (BWD) next_g[k] = load_raw<T, V>(pg + k * TEAM * V);
+        }
+    };
+    auto spread = [&](const Raw (&q)[NV], float2 (&r)[P]) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) r[i] = make_float2(to_f32(q[2 * i / V].v[2 * i % V]), to_f32(q[(2 * i + 1) / V].v[(2 * i + 1) % V]));
+    };
+    auto put = [&](const T* p, const float2 (&q)[P]) {
+        T* const o = const_cast<T*>(p);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            if (!whole && (k * TEAM + lane) * V >= L.D) continue;
+            Raw raw;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int e = k * V + i;
+                if (V == 1) raw.v[i] = from_f32<T>(e % 2 ? q[e / 2].y : q[e / 2].x);
+                else if (i % 2 == 0) store_two(&raw.v[i], q[e / 2]);
+            }
+            *reinterpret_cast<Raw*>(o + k * TEAM * V) = raw;
+        }
+    };
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int i = 0; i < V; ++i) next_x[k].v[i] = next_z[k].v[i] = next_g[k].v[i] = from_f32<T>(0.0f);
+    fetch(first);
+    int64_t t_next = first % L.T;                // the token of the row that px stands at
+    // every team of a warp (of a block) makes every turn: the sums are taken together
+    for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * A.rows; r0 < rows; r0 += step) {
+        const bool in = team_in && r0 + rs <= last;
+        // as loaded until they are needed, which takes half the registers in bf16
+        Raw raw_x[NV], raw_z[NV], raw_g[NV];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            raw_x[k] = next_x[k];
+            raw_z[k] = next_z[k];
+            if (BWD) raw_g[k] = next_g[k];
+        }
+        t_next += step_t;
+        const bool wrapped = t_next >= L.T;
+        if (wrapped) t_next -= L.T;
+        on(px, L.x, wrapped);
+        if (gated) on(pz, L.gate, wrapped);
+        if (BWD) on(pg, L.g, wrapped);
+        fetch(r0 + rs + step);
+        float2 u[P], of_z[P], slope[P];          // of_z: the gate's factor z s(z)
+        auto gate = [&]() {
+            spread(raw_z, of_z);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const float2 s = pair_logistic<kWide>(of_z[i]);
+                of_z[i] = pair_mul(of_z[i], s);
+                if (BWD) slope[i] = pair_fma(of_z[i], pair_fma(s, pair_of(-1.f), pair_of(1.f)), s);      // s + z s (1 - s)
+            }
+        };
+        spread(raw_x, u);
+        if (gated && L.first) {
+            gate();
+#pragma unroll
+            for (int i = 0; i < P; ++i) u[i] = pair_mul(u[i], of_z[i]);
+        }
         if (L.center) {
-            float s[1] = {0.0f};
+            float2 t = pair_of(0.f);
 #pragma unroll
-            for (int e = 0; e < E; ++e) s[0] += u[e];
+            for (int i = 0; i < P; ++i) t = pair_add(t, u[i]);
+            float s[1] = {t.x + t.y};
             team_sum<TEAM>(s, part1);
             const float mean = s[0] * inv;
 #pragma unroll
-            for (int e = 0; e < E; ++e) u[e] = col[e / V] < L.D ? u[e] - mean : 0.0f;
+            for (int i = 0; i < P; ++i) u[i] = both(i, pair_add(u[i], pair_of(-mean)));
         }
-        float s[1] = {0.0f};
+        float2 t = pair_of(0.f);
 #pragma unroll
-        for (int e = 0; e < E; ++e) s[0] = fmaf(u[e], u[e], s[0]);
+        for (int i = 0; i < P; ++i) t = pair_fma(u[i], u[i], t);
+        float s[1] = {t.x + t.y};
         team_sum<TEAM>(s, part1);
-        const float size = rsqrtf(fmaf(s[0], inv, L.eps));
+        const float2 size = pair_of(rsqrtf(fmaf(s[0], inv, L.eps)));
+        if (gated && !L.first) gate();
         if constexpr (!BWD) {
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                float o[V];
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const int e = k * V + i;
-                    o[i] = fmaf(u[e] * size, w[e], bias[e]);
-                    if (gated && !L.first) o[i] *= z[e] * logistic(z[e]);
-                    if (L.act) o[i] *= logistic(o[i]);
-                }
-                if (in && col[k] < L.D) store_pack<T, V>(static_cast<T*>(L.out.data) + place(L.out) + col[k], o);
+            for (int i = 0; i < P; ++i) {
+                u[i] = pair_fma(pair_mul(u[i], size), w[i], bias[i]);
+                if (gated && !L.first) u[i] = pair_mul(u[i], of_z[i]);
+                if (L.act) u[i] = pair_mul(u[i], pair_logistic<kWide>(u[i]));
             }
+            if (in) put(po, u);
         } else {
-            float two[2] = {0.0f, 0.0f};
-            // from here on g is the gradient of n, u is n
+            // g becomes the gradient of n, u is n, `slope` that of the gate
+            float2 g[P];
+            spread(raw_g, g);
+            float2 t0 = pair_of(0.f), t1 = pair_of(0.f);
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                u[e] *= size;
-                const float y = fmaf(u[e], w[e], bias[e]);
+            for (int i = 0; i < P; ++i) {
+                u[i] = pair_mul(u[i], size);
+                if (!in) g[i] = pair_of(0.f);
+                const float2 y = pair_fma(u[i], w[i], bias[i]);
                 if (gated && !L.first) {
-                    const float q = logistic(z[e]), of_gate = g[e] * y * silu_slope(z[e], q);
-                    g[e] *= z[e] * q;
-                    z[e] = of_gate;
+                    slope[i] = pair_mul(pair_mul(g[i], y), slope[i]);
+                    g[i] = pair_mul(g[i], of_z[i]);
                 } else if (L.act) {
-                    g[e] *= silu_slope(y, logistic(y));
+                    const float2 q = pair_logistic<kWide>(y);
+                    g[i] = pair_mul(g[i], pair_fma(pair_mul(y, q), pair_fma(q, pair_of(-1.f), pair_of(1.f)), q));
                 }
-                gw[e] = fmaf(g[e], u[e], gw[e]);
-                gb[e] += g[e];
-                g[e] *= w[e];
-                two[0] += g[e];
-                two[1] = fmaf(g[e], u[e], two[1]);
+                gw[i] = pair_fma(g[i], u[i], gw[i]);
+                gb[i] = pair_add(gb[i], g[i]);
+                g[i] = pair_mul(g[i], w[i]);
+                t0 = pair_add(t0, g[i]);
+                t1 = pair_fma(g[i], u[i], t1);
             }
+            float two[2] = {t0.x + t0.y, t1.x + t1.y};
             team_sum<TEAM>(two, part2);
-            const float of_mean = L.center ? two[0] * inv : 0.0f, of_size = two[1] * inv;
+            float2 x[P];
+            if (gated && L.first) spread(raw_x, x);
+            const float2 of_mean = pair_of(L.center ? -two[0] * inv : 0.0f), of_size = pair_of(-two[1] * inv);
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                float gx[V], gz[V];
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const int e = k * V + i;
-                    gx[i] = (g[e] - of_mean - u[e] * of_size) * size;
-                    gz[i] = z[e];
-                    if (gated && L.first) {
-                        const float q = logistic(z[e]);
-                        gz[i] = gx[i] * x[e] * silu_slope(z[e], q);
-                        gx[i] *= z[e] * q;
-                    }
+            for (int i = 0; i < P; ++i) {
+                g[i] = pair_mul(pair_fma(u[i], of_size, pair_add(g[i], of_mean)), size);
+                if (gated && L.first) {
+                    slope[i] = pair_mul(pair_mul(g[i], x[i]), slope[i]);
+                    g[i] = pair_mul(g[i], of_z[i]);
                 }
-                if (in && col[k] < L.D) {
-                    store_pack<T, V>(static_cast<T*>(L.out.data) + place(L.out) + col[k], gx);
-                    if (gated) store_pack<T, V>(static_cast<T*>(L.ggate.data) + place(L.ggate) + col[k], gz);
-                }
+            }
+            if (in) {
+                put(po, g);
+                if (gated) put(pgz, slope);
             }
         }
+        on(po, L.out, wrapped);
+        if (BWD && gated) on(pgz, L.ggate, wrapped);
     }
     if constexpr (BWD) {
         if (L.partial == nullptr || !team_in) return;
@@ -178,9 +250,9 @@ __global__ void __launch_bounds__(kThreadsOf<TEAM>) k_group_norm(const __grid_co
         float* const q = L.partial + (static_cast<int64_t>(blockIdx.x) * A.rows + rs) * 2 * all + h * L.D;
 #pragma unroll
         for (int e = 0; e < E; ++e)
-            if (col[e / V] < L.D) {
-                q[col[e / V] + e % V] = gw[e];
-                q[all + col[e / V] + e % V] = gb[e];
+            if (col(e) < L.D) {
+                q[col(e)] = e % 2 ? gw[e / 2].y : gw[e / 2].x;
+                q[all + col(e)] = e % 2 ? gb[e / 2].y : gb[e / 2].x;
             }
     }
 }
@@ -206,18 +278,17 @@ bool vectors(const NormLaunch& L) {
     return true;
 }
 
-// The team that a group of D values takes (V values a thread and access).
+// The team that a group of D values takes: 8 values a thread, where 512 threads
+// are enough for that (16 of them hold a backward call's registers to 128 only by
+// spilling), 16 beyond; without 16-byte accesses whole warps.
 struct Team {
-    int threads, accesses;
+    int threads, values;
 };
 Team team_of(const NormLaunch& L, bool vec) {
-    const int D = L.D;
-    if (!vec) return D <= 128 ? Team{32, 4} : D <= 512 ? Team{32, 16} : D <= 2048 ? Team{128, 16} : Team{512, 16};
-    if (L.bf16)
-        return D <= 64 ? Team{8, 1} : D <= 128 ? Team{16, 1} : D <= 256 ? Team{32, 1} : D <= 512 ? Team{32, 2} : D <= 1024 ? Team{128, 1}
-             : D <= 2048 ? Team{128, 2} : D <= 4096 ? Team{512, 1} : Team{512, 2};
-    return D <= 32 ? Team{8, 1} : D <= 64 ? Team{16, 1} : D <= 128 ? Team{32, 1} : D <= 256 ? Team{32, 2} : D <= 512 ? Team{32, 4}
-         : D <= 1024 ? Team{128, 2} : D <= 2048 ? Team{128, 4} : D <= 4096 ? Team{512, 2} : Team{512, 4};
+    if (L.D > 4096) return Team{512, 16};
+    int n = vec ? 8 : 32;
+    while (n * 8 < L.D) n *= vec ? 2 : 4;
+    return Team{n, 8};
 }
 
 // Blocks: as many as stay resident, so that each reads the weights once.
@@ -233,18 +304,18 @@ Grid grid_of(const NormLaunch& L, bool backward) {
     G.y = static_cast<unsigned>((L.H + G.heads - 1) / G.heads);
     const int64_t want = (L.B * L.T + G.rows - 1) / G.rows;
     const int block = threads <= 32 ? 256 : threads;
-    int64_t most = static_cast<int64_t>(kSms) * ((backward ? 768 : 1536) / block) / G.y;
+    int64_t most = static_cast<int64_t>(kSms) * ((backward ? kResidentBack : kResident) / block) / G.y;
     if (most < 1) most = 1;
     G.x = static_cast<unsigned>(want < most ? want : most);
     return G;
 }
 
-template <typename T, int V, int NV, int TEAM>
+template <typename T, int V, int E, int TEAM>
 cudaError_t go(const NormLaunch& L, bool backward) {
     const Grid G = grid_of(L, backward);
     const NormArgs A{L, G.heads, G.rows};
-    if (backward) k_group_norm<T, V, NV, TEAM, true><<<dim3(G.x, G.y), kThreadsOf<TEAM>, 0, L.stream>>>(A);
-    else k_group_norm<T, V, NV, TEAM, false><<<dim3(G.x, G.y), kThreadsOf<TEAM>, 0, L.stream>>>(A);
+    if (backward) k_group_norm<T, V, E / V, TEAM, true><<<dim3(G.x, G.y), kThreadsOf<TEAM>, 0, L.stream>>>(A);
+    else k_group_norm<T, V, E / V, TEAM, false><<<dim3(G.x, G.y), kThreadsOf<TEAM>, 0, L.stream>>>(A);
     return cudaGetLastError();
 }
 
@@ -253,21 +324,17 @@ cudaError_t pick(const NormLaunch& L, bool backward) {
     constexpr int V = 16 / sizeof(T);
     const bool vec = vectors(L);
     const Team t = team_of(L, vec);
-    if (!vec) {
-        if (t.threads == 32) return t.accesses == 4 ? go<T, 1, 4, 32>(L, backward) : go<T, 1, 16, 32>(L, backward);
-        return t.threads == 128 ? go<T, 1, 16, 128>(L, backward) : go<T, 1, 16, 512>(L, backward);
-    }
-    if (t.threads == 8) return go<T, V, 1, 8>(L, backward);
-    if (t.threads == 16) return go<T, V, 1, 16>(L, backward);
-    if constexpr (sizeof(T) == 2) {
-        if (t.threads == 32) return t.accesses == 1 ? go<T, V, 1, 32>(L, backward) : go<T, V, 2, 32>(L, backward);
-        if (t.threads == 128) return t.accesses == 1 ? go<T, V, 1, 128>(L, backward) : go<T, V, 2, 128>(L, backward);
-        return t.accesses == 1 ? go<T, V, 1, 512>(L, backward) : go<T, V, 2, 512>(L, backward);
-    } else {
-        if (t.threads == 32)
-            return t.accesses == 1 ? go<T, V, 1, 32>(L, backward) : t.accesses == 2 ? go<T, V, 2, 32>(L, backward) : go<T, V, 4, 32>(L, backward);
-        if (t.threads == 128) return t.accesses == 2 ? go<T, V, 2, 128>(L, backward) : go<T, V, 4, 128>(L, backward);
-        return t.accesses == 2 ? go<T, V, 2, 512>(L, backward) : go<T, V, 4, 512>(L, backward);
+    if (t.values == 16) return vec ? go<T, V, 16, 512>(L, backward) : go<T, 1, 16, 512>(L, backward);
+    if (!vec)
+        return t.threads == 32 ? go<T, 1, 8, 32>(L, backward) : t.threads == 128 ? go<T, 1, 8, 128>(L, backward) : go<T, 1, 8, 512>(L, backward);
+    switch (t.threads) {
+        case 8: return go<T, V, 8, 8>(L, backward);
+        case 16: return go<T, V, 8, 16>(L, backward);
+        case 32: return go<T, V, 8, 32>(L, backward);
+        case 64: return go<T, V, 8, 64>(L, backward);
+        case 128: return go<T, V, 8, 128>(L, backward);
+        case 256: return go<T, V, 8, 256>(L, backward);
+        default: return go<T, V, 8, 512>(L, backward);
     }
 }
 

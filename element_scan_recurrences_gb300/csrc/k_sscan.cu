@@ -234,7 +234,7 @@ __device__ __forceinline__ void run(const ScanArgs& A, const Run& R, Tile<T, NL>
                 }
             }
             // kBlock tokens at a time: their reads come before the writes of their sums
-            constexpr int kBlock = 4;
+            constexpr int kBlock = 8;
 #pragma unroll 1
             for (int k0 = 0; k0 < live; k0 += kBlock) {
                 float2 y[kBlock];
@@ -282,7 +282,7 @@ __device__ __forceinline__ void run(const ScanArgs& A, const Run& R, Tile<T, NL>
 }
 
 template <typename T, int NL, Mode MODE>
-__global__ void __launch_bounds__(kThreads, 8) k_sscan(const __grid_constant__ ScanArgs A) {
+__global__ void __launch_bounds__(kThreads, 7) k_sscan(const __grid_constant__ ScanArgs A) {
     extern __shared__ __align__(128) unsigned char smem[];
     auto& buf = *reinterpret_cast<Tile<T, NL>*>(smem);
     const ScanLaunch& L = A.L;
