@@ -50,7 +50,10 @@ struct NormArgs {
     int heads, rows;        // heads and rows of a block at a time
 };
 
-template <typename T, int V, int NV, int TEAM, bool BWD>
+// where the gate goes
+enum Gate { kAfter, kFirst, kNone };
+
+template <typename T, int V, int NV, int TEAM, bool BWD, Gate GATE>
 __global__ void __launch_bounds__(kThreadsOf<TEAM>, (BWD || NV * V == 16 ? 512 : kResident) / kThreadsOf<TEAM>)
     k_group_norm(const __grid_constant__ NormArgs A) {
     constexpr int E = NV * V, P = E / 2, TEAMS = kThreadsOf<TEAM> / TEAM;
@@ -65,7 +68,7 @@ __global__ void __launch_bounds__(kThreadsOf<TEAM>, (BWD || NV * V == 16 ? 512 :
     const bool team_in = rs < A.rows && h < L.H;
     const int64_t rows = L.B * L.T, step = static_cast<int64_t>(gridDim.x) * A.rows;
     const float inv = 1.0f / static_cast<float>(L.D);
-    const bool gated = L.gate.data != nullptr;
+    constexpr bool gated = GATE != kNone;
     // values e and e + 1 of a thread, as pairs; those past the group's last are zeros, and so are their weights
     float2 w[P], bias[P], gw[BWD ? P : 1], gb[BWD ? P : 1];
     auto col = [&](int e) { return (e / V * TEAM + lane) * V + e % V; };
@@ -170,7 +173,7 @@ __global__ void __launch_bounds__(kThreadsOf<TEAM>, (BWD || NV * V == 16 ? 512 :
             }
         };
         spread(raw_x, u);
-        if (gated && L.first) {
+        if constexpr (GATE == kFirst) {
             gate();
 #pragma unroll
             for (int i = 0; i < P; ++i) u[i] = pair_mul(u[i], of_z[i]);
@@ -191,13 +194,13 @@ __global__ void __launch_bounds__(kThreadsOf<TEAM>, (BWD || NV * V == 16 ? 512 :
         float s[1] = {t.x + t.y};
         team_sum<TEAM>(s, part1);
         const float2 size = pair_of(rsqrtf(fmaf(s[0], inv, L.eps)));
-        if (gated && !L.first) gate();
+        if constexpr (GATE == kAfter) gate();
         if constexpr (!BWD) {
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 u[i] = pair_fma(pair_mul(u[i], size), w[i], bias[i]);
-                if (gated && !L.first) u[i] = pair_mul(u[i], of_z[i]);
-                if (L.act) u[i] = pair_mul(u[i], pair_logistic<kWide>(u[i]));
+                if constexpr (GATE == kAfter) u[i] = pair_mul(u[i], of_z[i]);
+                if (GATE == kNone && L.act) u[i] = pair_mul(u[i], pair_logistic<kWide>(u[i]));
             }
             if (in) put(po, u);
         } else {
@@ -210,10 +213,10 @@ __global__ void __launch_bounds__(kThreadsOf<TEAM>, (BWD || NV * V == 16 ? 512 :
                 u[i] = pair_mul(u[i], size);
                 if (!in) g[i] = pair_of(0.f);
                 const float2 y = pair_fma(u[i], w[i], bias[i]);
-                if (gated && !L.first) {
+                if constexpr (GATE == kAfter) {
                     slope[i] = pair_mul(pair_mul(g[i], y), slope[i]);
                     g[i] = pair_mul(g[i], of_z[i]);
-                } else if (L.act) {
+                } else if (GATE == kNone && L.act) {
                     const float2 q = pair_logistic<kWide>(y);
                     g[i] = pair_mul(g[i], pair_fma(pair_mul(y, q), pair_fma(q, pair_of(-1.f), pair_of(1.f)), q));
                 }
@@ -226,12 +229,12 @@ __global__ void __launch_bounds__(kThreadsOf<TEAM>, (BWD || NV * V == 16 ? 512 :
             float two[2] = {t0.x + t0.y, t1.x + t1.y};
             team_sum<TEAM>(two, part2);
             float2 x[P];
-            if (gated && L.first) spread(raw_x, x);
+            if constexpr (GATE == kFirst) spread(raw_x, x);
             const float2 of_mean = pair_of(L.center ? -two[0] * inv : 0.0f), of_size = pair_of(-two[1] * inv);
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 g[i] = pair_mul(pair_fma(u[i], of_size, pair_add(g[i], of_mean)), size);
-                if (gated && L.first) {
+                if constexpr (GATE == kFirst) {
                     slope[i] = pair_mul(pair_mul(g[i], x[i]), slope[i]);
                     g[i] = pair_mul(g[i], of_z[i]);
                 }
@@ -314,8 +317,11 @@ template <typename T, int V, int E, int TEAM>
 cudaError_t go(const NormLaunch& L, bool backward) {
     const Grid G = grid_of(L, backward);
     const NormArgs A{L, G.heads, G.rows};
-    if (backward) k_group_norm<T, V, E / V, TEAM, true><<<dim3(G.x, G.y), kThreadsOf<TEAM>, 0, L.stream>>>(A);
-    else k_group_norm<T, V, E / V, TEAM, false><<<dim3(G.x, G.y), kThreadsOf<TEAM>, 0, L.stream>>>(A);
+    const dim3 grid(G.x, G.y);
+    const Gate gate = L.gate.data == nullptr ? kNone : L.first ? kFirst : kAfter;
+    auto* kernel = backward ? (gate == kNone ? k_group_norm<T, V, E / V, TEAM, true, kNone> : gate == kFirst ? k_group_norm<T, V, E / V, TEAM, true, kFirst> : k_group_norm<T, V, E / V, TEAM, true, kAfter>)
+                            : (gate == kNone ? k_group_norm<T, V, E / V, TEAM, false, kNone> : gate == kFirst ? k_group_norm<T, V, E / V, TEAM, false, kFirst> : k_group_norm<T, V, E / V, TEAM, false, kAfter>);
+    kernel<<<grid, kThreadsOf<TEAM>, 0, L.stream>>>(A);
     return cudaGetLastError();
 }
 
