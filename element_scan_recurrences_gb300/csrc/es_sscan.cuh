@@ -195,11 +195,11 @@ inline bool scan_vectors(const ScanLaunch& L, const es_rows* extra) {
     return L.G == 1 || (L.C / L.G) % V == 0;
 }
 
-// stores of two values at an even channel: addresses and strides in pairs
+// accesses of two values: addresses, strides and a group's channels in pairs
 inline bool scan_pairs(const ScanLaunch& L, const es_rows& r) {
     const int size = L.bf16 ? 2 : 4;
     return reinterpret_cast<uintptr_t>(r.data) % (2 * size) == 0 && (L.B == 1 || r.stride_b % 2 == 0) &&
-           (L.T == 1 || r.stride_t % 2 == 0) && (L.G == 1 || (L.C / L.G) % 2 == 0);
+           (L.T == 1 || r.stride_t % 2 == 0) && (L.C / L.G) % 2 == 0;
 }
 
 inline ScanArgs scan_args(const ScanLaunch& L, int channels) {

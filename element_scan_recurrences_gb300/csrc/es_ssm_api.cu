@@ -149,19 +149,40 @@ struct ScanPlan {
     int64_t fwd_seg_chunks;
 };
 
-// Segments a row's tokens are cut into.  A CTA runs one row's block of channels;
-// with fewer CTAs than the GPU takes at once, a row's chunks are shared out among
-// more of them, which costs a pass for the segments' own states.
-int scan_segments(int64_t ctas, int64_t chunks, int per_sm, int64_t* seg_chunks) {
+// Segments a row's tokens are cut into.  A CTA takes a row's block of channels from
+// token to token, and a chunk takes it the longer the more CTAs share its SM: 1 + 0.37
+// us for each of them (7 at most; 2.0 us at 3.4, 3.5 at 6.7).  Segments make more CTAs
+// of fewer chunks, for a pass over all but one of them that finds their own states at
+// 0.6 of that, and a launch.  Backwards (2 CTAs at most, of 4 times the channels) a
+// chunk takes 6 us alone, 8 by two.
+struct Pace {
+    int resident;
+    double alone, more;          // us a chunk of one CTA an SM, what each further one adds
+};
+constexpr Pace kForwards{7, 1.37, 0.37}, kBackwards{2, 6.0, 2.0};
+
+double chunk_us(const Pace& p, int64_t ctas) {
+    const double each = static_cast<double>(ctas) / kSms, here = each < p.resident ? each : p.resident;
+    const double waves = each > p.resident ? each / p.resident : 1.0;
+    return waves * (p.alone + (here > 1.0 ? here - 1.0 : 0.0) * p.more);
+}
+
+// `ctas` of the main pass, `first` of the pass before it, a segment
+int scan_segments(const Pace& p, int64_t ctas, int64_t first, int64_t chunks, int64_t* seg_chunks) {
     *seg_chunks = chunks > 0 ? chunks : 1;
-    const int64_t most = kSms * per_sm / (ctas > 0 ? ctas : 1);
-    if (most < 2 || chunks < 8) return 1;
-    int64_t each = (chunks + most - 1) / most;
-    if (each < 4) each = 4;
-    // a pass over a segment for its state, one for the results, and about four chunks' time of launches
-    if (2 * each + 4 >= chunks) return 1;
-    *seg_chunks = each;
-    return static_cast<int>((chunks + each - 1) / each);
+    const int64_t most = static_cast<int64_t>(kSms) * p.resident / (ctas > 0 ? ctas : 1);
+    double best = static_cast<double>(chunks) * chunk_us(p, ctas);
+    int segs = 1;
+    for (int64_t s = 2; s <= most && s <= chunks; ++s) {
+        const int64_t each = (chunks + s - 1) / s, n = (chunks + each - 1) / each;
+        const double us = static_cast<double>(each) * (chunk_us(p, ctas * n) + 0.6 * chunk_us(kForwards, first * (n - 1))) + 5.0;
+        if (us < best) {
+            best = us;
+            segs = static_cast<int>(n);
+            *seg_chunks = each;
+        }
+    }
+    return segs;
 }
 
 es_status plan_scan(const char* fn, const es_selective_scan_args* a, const es_selective_scan_grads* g, bool step, ScanPlan* P) {
@@ -272,12 +293,12 @@ es_status plan_scan(const char* fn, const es_selective_scan_args* a, const es_se
         const int g = static_cast<int>(G), n = static_cast<int>(N);
         const int64_t ctas = G * scan_blocks(C, g, scan_channels(n)) * B, back = G * scan_blocks(C, g, scan_bwd_channels(n)) * B;
         size_t at = 0;
-        if (!step) P->fwd_segs = scan_segments(ctas, L.chunks, 8, &P->fwd_seg_chunks);
+        if (!step) P->fwd_segs = scan_segments(kForwards, ctas, ctas, L.chunks, &P->fwd_seg_chunks);
         if (!backward) {
             L.segs = P->fwd_segs;
             L.seg_chunks = P->fwd_seg_chunks;
         } else {
-            L.segs = scan_segments(back, L.chunks, 1, &L.seg_chunks);
+            L.segs = scan_segments(kBackwards, back, ctas, L.chunks, &L.seg_chunks);
             P->find = L.kept == nullptr && L.chunks > 0;
         }
         int64_t segs = L.segs;

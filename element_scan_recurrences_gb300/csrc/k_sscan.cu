@@ -146,10 +146,10 @@ __device__ __forceinline__ void help(const ScanArgs& A, const Run& R, Tile<T, NL
                 }
             }
             T* o = out + (t0 + at0) * L.out.stride_t;
-            if (A.pairs && in1) {
+            if (A.pairs) {
 #pragma unroll
                 for (int k = 0; k < K / STEP; ++k) {
-                    if (at0 + k * STEP < live) store_two(o, y[k]);
+                    if (in0 && at0 + k * STEP < live) store_two(o, y[k]);
                     o += STEP * L.out.stride_t;
                 }
             } else {

@@ -127,8 +127,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_sscan_bwd(const __grid_constant
     T* const gdelta = static_cast<T*>(B.S.gdelta.data) + p.b * B.S.gdelta.stride_b + c2;
     T* const ggate = gated ? static_cast<T*>(B.S.ggate.data) + p.b * B.S.ggate.stride_b + c2 : nullptr;
     auto put = [&](T* o, float2 v) {
-        if (B.A.pairs && c2 + 1 < p.last) {
-            store_two(o, v);
+        if (B.A.pairs) {
+            if (c2 < p.last) store_two(o, v);
         } else {
             if (c2 < p.last) o[0] = from_f32<T>(v.x);
             if (c2 + 1 < p.last) o[1] = from_f32<T>(v.y);
@@ -152,18 +152,37 @@ __global__ void __launch_bounds__(kThreads, 2) k_sscan_bwd(const __grid_constant
         // the other stage has been read by all: the next chunk's operands on their way
         if (Buf::STAGES == 2 && i > 0) fetch(i - 1);
         const auto& at = buf.stage[i % Buf::STAGES];
+        // once a token and channel, some tokens at a time
+        constexpr int SOME = K / STEP < 8 ? K / STEP : 8;
+#pragma unroll 1
+        for (int k0 = 0; k0 < K / STEP; k0 += SOME) {
+            float2 d[SOME], gy[SOME];
+            const int first = at0 + k0 * STEP;
 #pragma unroll
-        for (int k = 0; k < K; k += STEP) {
-            const int tt = at0 + k;
-            float2 d = pair_add(load_two(&at.delta[tt][two]), bias), gy = load_two(&at.g[tt][two]);
-            if (L.softplus) d = pair_softplus(d);
-            if (gated) {
-                const float2 z = load_two(&at.gate[tt][two]);
-                gy = pair_mul(gy, pair_mul(z, pair_logistic<kWide>(z)));
+            for (int k = 0; k < SOME; ++k) {
+                d[k] = pair_add(load_two(&at.delta[first + k * STEP][two]), bias);
+                gy[k] = load_two(&at.g[first + k * STEP][two]);
             }
-            store_two(&buf.d[tt][two], d);
-            store_two(&buf.dx[tt][two], pair_mul(d, load_two(&at.x[tt][two])));
-            store_two(&buf.gy[tt][two], gy);
+            if (L.softplus) {
+#pragma unroll
+                for (int k = 0; k < SOME; ++k) d[k] = pair_softplus(d[k]);
+            }
+            if (gated) {
+#pragma unroll
+                for (int k = 0; k < SOME; ++k) {
+                    const float2 z = load_two(&at.gate[first + k * STEP][two]);
+                    gy[k] = pair_mul(gy[k], pair_mul(z, pair_logistic<kWide>(z)));
+                }
+            }
+            // tokens past the last take no step
+#pragma unroll
+            for (int k = 0; k < SOME; ++k) {
+                const int tt = first + k * STEP;
+                if (tt >= live) d[k] = pair_of(0.f);
+                store_two(&buf.d[tt][two], d[k]);
+                store_two(&buf.dx[tt][two], pair_mul(d[k], load_two(&at.x[tt][two])));
+                store_two(&buf.gy[tt][two], gy[k]);
+            }
         }
         __syncwarp();
         Block mend;
@@ -175,14 +194,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_sscan_bwd(const __grid_constant
                 mend[n][1] = decay_mend(pair_mul(make_float2(d.z, d.w), a2[n][1]));
             }
         }
-        // the states before each token
+        // the states before each token; tokens past the last leave them as they are
 #pragma unroll 4
-        for (int tt = 0; tt < live; ++tt) {
-            stash(tmem + 16 * tt, h);
+        for (int tt = 0; tt < K; ++tt) {
             const float4 d4 = *reinterpret_cast<const float4*>(&buf.d[tt][tile]), v4 = *reinterpret_cast<const float4*>(&buf.dx[tt][tile]);
             const float2 d[2] = {make_float2(d4.x, d4.y), make_float2(d4.z, d4.w)};
             const float2 v[2] = {make_float2(v4.x, v4.y), make_float2(v4.z, v4.w)};
             const float4 bv = load_four(&at.b[tt][n0]);
+            stash(tmem + 16 * tt, h);
 #pragma unroll
             for (int n = 0; n < 4; ++n)
 #pragma unroll
@@ -200,36 +219,36 @@ __global__ void __launch_bounds__(kThreads, 2) k_sscan_bwd(const __grid_constant
                 one[4 * n + 2 * r] = __float_as_uint(h[n][r].x);
                 one[4 * n + 2 * r + 1] = __float_as_uint(h[n][r].y);
             }
-        tc::ld(tmem + 16 * (live - 1), other);
+        tc::ld(tmem + 16 * (K - 1), other);
         // token tt: `now` holds the state after it, `before` (on its way) the one before
-        auto step = [&](int tt, uint32_t(&now)[16], uint32_t(&before)[16]) {
+        auto step = [&](int tt, uint32_t(&now)[16], uint32_t(&before)[16], float4& tb, float4& tg, float2(&sums)[3]) {
             const float4 d4 = *reinterpret_cast<const float4*>(&buf.d[tt][tile]), v4 = *reinterpret_cast<const float4*>(&buf.dx[tt][tile]),
                          g4 = *reinterpret_cast<const float4*>(&buf.gy[tt][tile]);
             const float2 d[2] = {make_float2(d4.x, d4.y), make_float2(d4.z, d4.w)};
             const float2 v[2] = {make_float2(v4.x, v4.y), make_float2(v4.z, v4.w)};
             const float2 g[2] = {make_float2(g4.x, g4.y), make_float2(g4.z, g4.w)};
             const float4 bv = load_four(&at.b[tt][n0]), cv = load_four(&at.c[tt][n0]);
-            float2 y[2] = {pair_of(0.f), pair_of(0.f)}, of_b[2] = {pair_of(0.f), pair_of(0.f)}, of_a[2] = {pair_of(0.f), pair_of(0.f)};
-            float tb[4], tcv[4];
+            float2 y[2], of_b[2], of_a[2];
+            float wb[4], wc[4];
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
                 const float2 bn = pair_of(of_four(bv, n)), cn = pair_of(of_four(cv, n));
-                float2 wb, wc;
+                float2 sb, sc;
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const float2 s = stashed(now, n, r), grad = pair_fma(g[r], cn, dh[n][r]);
-                    wc = r == 0 ? pair_mul(g[r], s) : pair_fma(g[r], s, wc);
-                    wb = r == 0 ? pair_mul(grad, v[r]) : pair_fma(grad, v[r], wb);
-                    y[r] = pair_fma(cn, s, y[r]);
-                    of_b[r] = pair_fma(grad, bn, of_b[r]);
+                    sc = r == 0 ? pair_mul(g[r], s) : pair_fma(g[r], s, sc);
+                    sb = r == 0 ? pair_mul(grad, v[r]) : pair_fma(grad, v[r], sb);
+                    y[r] = n == 0 ? pair_mul(cn, s) : pair_fma(cn, s, y[r]);
+                    of_b[r] = n == 0 ? pair_mul(grad, bn) : pair_fma(grad, bn, of_b[r]);
                     const float2 q = pair_fma(d[r], a2[n][r], mend[n][r]);
                     dh[n][r] = pair_mul(grad, make_float2(exp2_hw(q.x), exp2_hw(q.y)));
                 }
-                tb[n] = wb.x + wb.y;
-                tcv[n] = wc.x + wc.y;
+                wb[n] = sb.x + sb.y;
+                wc[n] = sc.x + sc.y;
             }
-            buf.terms[tt % kGroup][0][threadIdx.x] = make_float4(tb[0], tb[1], tb[2], tb[3]);
-            buf.terms[tt % kGroup][1][threadIdx.x] = make_float4(tcv[0], tcv[1], tcv[2], tcv[3]);
+            tb = make_float4(wb[0], wb[1], wb[2], wb[3]);
+            tg = make_float4(wc[0], wc[1], wc[2], wc[3]);
             tc::wait_ld();
             tc::loaded(before);
             if (tt > 0) tc::ld(tmem + 16 * (tt - 1), now);
@@ -238,33 +257,33 @@ __global__ void __launch_bounds__(kThreads, 2) k_sscan_bwd(const __grid_constant
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const float2 u = pair_mul(dh[n][r], stashed(before, n, r));
-                    of_a[r] = pair_fma(u, a2[n][r], of_a[r]);
+                    of_a[r] = n == 0 ? pair_mul(u, a2[n][r]) : pair_fma(u, a2[n][r], of_a[r]);
                     ga[n][r] = pair_fma(u, d[r], ga[n][r]);
                 }
-            put_sum<NL>(&buf.of_b[tt][tile], over_states<NL>(of_b, sub), sub);
-            put_sum<NL>(&buf.of_a[tt][tile], over_states<NL>(of_a, sub), sub);
-            if (gated) {
-                const float2 whole = over_states<NL>(y, sub);
-                __syncwarp();                        // every lane has read its d x of this token
-                put_sum<NL>(&buf.dx[tt][tile], whole, sub);
-            }
+            sums[0] = over_states<NL>(of_b, sub);
+            sums[1] = over_states<NL>(of_a, sub);
+            if (gated) sums[2] = over_states<NL>(y, sub);
         };
-        int tt = live - 1;
-        bool turned = false;
-        for (int k0 = (live - 1) / kGroup * kGroup; k0 >= 0; k0 -= kGroup) {
-            // pairs of tokens, so that the two registers' roles are fixed
+        // the tokens in groups whose sums over channels are taken at once, and in twos whose
+        // reads come before the writes of their sums
 #pragma unroll 1
-            while (tt >= k0) {
-                if (!turned) {
-                    step(tt, one, other);
-                    if (--tt < k0) {
-                        turned = true;
-                        break;
-                    }
+        for (int k0 = K - kGroup; k0 >= 0; k0 -= kGroup) {
+#pragma unroll 1
+            for (int k = kGroup - 2; k >= 0; k -= 2) {
+                float4 tb[2], tg[2];
+                float2 sums[2][3];
+                step(k0 + k + 1, one, other, tb[1], tg[1], sums[1]);
+                step(k0 + k, other, one, tb[0], tg[0], sums[0]);
+                __syncwarp();                        // every lane has read its d x of these tokens, where y goes
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    const int tt = k0 + k + m;
+                    buf.terms[k + m][0][threadIdx.x] = tb[m];
+                    buf.terms[k + m][1][threadIdx.x] = tg[m];
+                    put_sum<NL>(&buf.of_b[tt][tile], sums[m][0], sub);
+                    put_sum<NL>(&buf.of_a[tt][tile], sums[m][1], sub);
+                    if (gated) put_sum<NL>(&buf.dx[tt][tile], sums[m][2], sub);
                 }
-                step(tt, other, one);
-                turned = false;
-                --tt;
             }
             __syncthreads();
             // gB and gC of these tokens: 16 rows (a token's two) of NL float4 each, the sum of 128 / NL terms
@@ -301,21 +320,40 @@ __global__ void __launch_bounds__(kThreads, 2) k_sscan_bwd(const __grid_constant
             }
             __syncthreads();
         }
-#pragma unroll 2
-        for (int k = 0; k < K; k += STEP) {
-            const int t = at0 + k;
-            if (t >= live) break;
-            const float2 x = load_two(&at.x[t][two]), gy = load_two(&buf.gy[t][two]), ob = load_two(&buf.of_b[t][two]);
-            float2 gd = pair_fma(load_two(&buf.of_a[t][two]), pair_of(kLn2), pair_mul(ob, x));
-            if (L.softplus) gd = pair_mul(gd, pair_logistic<true>(pair_add(load_two(&at.delta[t][two]), bias)));
-            gskip = pair_fma(gy, x, gskip);
-            gbias = pair_add(gbias, gd);
-            put(gx + (t0 + t) * B.S.gx.stride_t, pair_fma(ob, load_two(&buf.d[t][two]), pair_mul(gy, skip)));
-            put(gdelta + (t0 + t) * B.S.gdelta.stride_t, gd);
+#pragma unroll 1
+        for (int k0 = 0; k0 < K / STEP; k0 += SOME) {
+            float2 gd[SOME], x[SOME], of_z[SOME];
+            const int first = at0 + k0 * STEP;
+#pragma unroll
+            for (int k = 0; k < SOME; ++k) {
+                const int t = first + k * STEP;
+                x[k] = load_two(&at.x[t][two]);
+                gd[k] = pair_fma(load_two(&buf.of_a[t][two]), pair_of(kLn2), pair_mul(load_two(&buf.of_b[t][two]), x[k]));
+            }
+            if (L.softplus) {
+#pragma unroll
+                for (int k = 0; k < SOME; ++k)
+                    gd[k] = pair_mul(gd[k], pair_logistic<true>(pair_add(load_two(&at.delta[first + k * STEP][two]), bias)));
+            }
             if (gated) {
-                const float2 z = load_two(&at.gate[t][two]), s = pair_logistic<kWide>(z);
-                const float2 of_z = pair_mul(load_two(&at.g[t][two]), pair_fma(skip, x, load_two(&buf.dx[t][two])));
-                put(ggate + (t0 + t) * B.S.ggate.stride_t, pair_mul(of_z, make_float2(silu_slope(z.x, s.x), silu_slope(z.y, s.y))));
+#pragma unroll
+                for (int k = 0; k < SOME; ++k) {
+                    const int t = first + k * STEP;
+                    const float2 z = load_two(&at.gate[t][two]), s = pair_logistic<kWide>(z);
+                    const float2 slope = pair_fma(pair_mul(z, s), pair_fma(s, pair_of(-1.f), pair_of(1.f)), s);
+                    of_z[k] = pair_mul(pair_mul(load_two(&at.g[t][two]), pair_fma(skip, x[k], load_two(&buf.dx[t][two]))), slope);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < SOME; ++k) {
+                const int t = first + k * STEP;
+                if (t >= live) break;
+                const float2 gy = load_two(&buf.gy[t][two]);
+                gskip = pair_fma(gy, x[k], gskip);
+                gbias = pair_add(gbias, gd[k]);
+                put(gx + (t0 + t) * B.S.gx.stride_t, pair_fma(load_two(&buf.of_b[t][two]), load_two(&buf.d[t][two]), pair_mul(gy, skip)));
+                put(gdelta + (t0 + t) * B.S.gdelta.stride_t, gd[k]);
+                if (gated) put(ggate + (t0 + t) * B.S.ggate.stride_t, of_z[k]);
             }
         }
         if (Buf::STAGES == 1) {
