@@ -73,6 +73,11 @@ __device__ __forceinline__ void load_weights(const ConvLaunch& L, int64_t c, flo
     }
 }
 
+template <bool B>
+struct Flag {
+    static constexpr bool value = B;
+};
+
 struct ConvPlace {
     int64_t b, c, begin;
 };
@@ -88,8 +93,10 @@ __device__ __forceinline__ bool conv_place(const ConvLaunch& L, ConvPlace* p) {
     return p->c < L.C;
 }
 
+// (The launch bounds hold the registers to what keeps 3 blocks of the common widths on
+// an SM; 4 spill, 46 -> 52 us for 4 x 2047 x 4096.)
 template <typename T, int V, int W>
-__global__ void __launch_bounds__(kThreads) k_conv(const __grid_constant__ ConvLaunch L) {
+__global__ void __launch_bounds__(kThreads, V * W <= 32 ? 3 : 2) k_conv(const __grid_constant__ ConvLaunch L) {
     constexpr int P = kPairs<V>, BLK = kBlock<W>;
     ConvPlace p;
     if (!conv_place<V>(L, &p)) return;
@@ -99,12 +106,21 @@ __global__ void __launch_bounds__(kThreads) k_conv(const __grid_constant__ ConvL
     T* const out = static_cast<T*>(L.out.data) + p.b * L.out.stride_b + p.c;
     float2 w[W][P], bias[P], row[W][P];              // token t's input at place (t - begin + W - 1) % W of `row`
     Pack<T, V> next[BLK];
-    auto fetch = [&](int64_t t) {
+    const int count = end > p.begin ? static_cast<int>(end - p.begin) : 0;
+    const T* px = x + p.begin * L.x.stride_t;        // of the next block
+    T* po = out + p.begin * L.out.stride_t;
+    auto fetch = [&](int left) {
+        if (left >= BLK) {
 #pragma unroll
-        for (int k = 0; k < BLK; ++k)
-            if (t + k < end) next[k] = load_raw<T, V>(x + (t + k) * L.x.stride_t);
+            for (int k = 0; k < BLK; ++k) next[k] = load_raw<T, V>(px + k * L.x.stride_t);
+        } else {
+#pragma unroll
+            for (int k = 0; k < BLK; ++k)
+                if (k < left) next[k] = load_raw<T, V>(px + k * L.x.stride_t);
+        }
+        px += BLK * L.x.stride_t;
     };
-    if (p.begin < end) fetch(p.begin);
+    fetch(count);
     if (p.begin < end || p.begin == 0) {
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) input_at<T, V, W>(L, x, p.b, p.c, p.begin - (W - 1) + j, row[j]);
@@ -119,14 +135,15 @@ __global__ void __launch_bounds__(kThreads) k_conv(const __grid_constant__ ConvL
             *reinterpret_cast<Pack<T, V>*>(static_cast<T*>(L.fin) + (p.b * (W - 1) + j) * L.C + p.c) = pack<T, V>(last[j]);
     }
     load_weights<V, W>(L, p.c, w, bias);
-    for (int64_t t = p.begin; t < end; t += BLK) {
+    // blocks whole and the last: without tests between their tokens they run into one another
+    auto block = [&](int left, auto whole) {
         Pack<T, V> now[BLK];
 #pragma unroll
         for (int k = 0; k < BLK; ++k) now[k] = next[k];
-        fetch(t + BLK);
+        fetch(left - BLK);
 #pragma unroll
         for (int k = 0; k < BLK; ++k) {
-            if (t + k >= end) break;
+            if (!decltype(whole)::value && k >= left) break;
             unpack<T, V>(now[k], row[(k + W - 1) % W]);
             float2 o[P];
 #pragma unroll
@@ -139,9 +156,13 @@ __global__ void __launch_bounds__(kThreads) k_conv(const __grid_constant__ ConvL
 #pragma unroll
                 for (int i = 0; i < P; ++i) o[i] = pair_mul(o[i], pair_logistic<sizeof(T) == 4>(o[i]));
             }
-            *reinterpret_cast<Pack<T, V>*>(out + (t + k) * L.out.stride_t) = pack<T, V>(o);
+            *reinterpret_cast<Pack<T, V>*>(po + k * L.out.stride_t) = pack<T, V>(o);
         }
-    }
+        po += BLK * L.out.stride_t;
+    };
+    int left = count;
+    for (; left >= BLK; left -= BLK) block(left, Flag<true>{});
+    if (left > 0) block(left, Flag<false>{});
     float2 none[P];
     zero(none);
     for (int64_t t = end > p.begin ? end : p.begin; t < stop; ++t)
@@ -151,7 +172,7 @@ __global__ void __launch_bounds__(kThreads) k_conv(const __grid_constant__ ConvL
 // Token u gives the gradient gp of its p, and with the W - 1 before it that of the
 // input at token u - (W - 1); before the first token those are the carried inputs.
 template <typename T, int V, int W>
-__global__ void __launch_bounds__(kThreads) k_conv_bwd(const __grid_constant__ ConvLaunch L) {
+__global__ void __launch_bounds__(kThreads, V * W <= 16 ? 4 : 2) k_conv_bwd(const __grid_constant__ ConvLaunch L) {
     constexpr int P = kPairs<V>, BLK = kBlock<W>;
     ConvPlace p;
     if (!conv_place<V>(L, &p)) return;
@@ -164,15 +185,28 @@ __global__ void __launch_bounds__(kThreads) k_conv_bwd(const __grid_constant__ C
     Pack<T, V> next_x[BLK], next_g[BLK];
     // the tokens whose p this run needs: W - 1 past its own
     const int64_t until = stop + W - 1 < len ? stop + W - 1 : len;
-    auto fetch = [&](int64_t u) {
+    const T *px = x + p.begin * L.x.stride_t, *pg = g + p.begin * L.g.stride_t;      // of the next block
+    auto fetch = [&](int left) {
+        if (left >= BLK) {
 #pragma unroll
-        for (int k = 0; k < BLK; ++k)
-            if (u + k < until) {
-                next_x[k] = load_raw<T, V>(x + (u + k) * L.x.stride_t);
-                next_g[k] = load_raw<T, V>(g + (u + k) * L.g.stride_t);
+            for (int k = 0; k < BLK; ++k) {
+                next_x[k] = load_raw<T, V>(px + k * L.x.stride_t);
+                next_g[k] = load_raw<T, V>(pg + k * L.g.stride_t);
             }
+        } else {
+#pragma unroll
+            for (int k = 0; k < BLK; ++k)
+                if (k < left) {
+                    next_x[k] = load_raw<T, V>(px + k * L.x.stride_t);
+                    next_g[k] = load_raw<T, V>(pg + k * L.g.stride_t);
+                }
+        }
+        px += BLK * L.x.stride_t;
+        pg += BLK * L.g.stride_t;
     };
-    fetch(p.begin);
+    // tokens from the run's first: those with p, with p of its own, all that the loop makes
+    const int live = until > p.begin ? static_cast<int>(until - p.begin) : 0, own = static_cast<int>(stop - p.begin);
+    fetch(live);
     load_weights<V, W>(L, p.c, w, bias);
     zero(gb);
 #pragma unroll
@@ -185,21 +219,24 @@ __global__ void __launch_bounds__(kThreads) k_conv_bwd(const __grid_constant__ C
         if (p.begin - (W - 1) + j < len) input_at<T, V, W>(L, x, p.b, p.c, p.begin - (W - 1) + j, row[j]);
         else zero(row[j]);
     }
-    for (int64_t u0 = p.begin; u0 < stop + W - 1; u0 += BLK) {
+    // `inside`: every token of the block, and every input whose gradient it completes, is the
+    // run's own and reads no state's gradient
+    auto block = [&](int u0, auto inside) {
+        constexpr bool kInside = decltype(inside)::value;
         Pack<T, V> now_x[BLK], now_g[BLK];
 #pragma unroll
         for (int k = 0; k < BLK; ++k) {
             now_x[k] = next_x[k];
             now_g[k] = next_g[k];
         }
-        fetch(u0 + BLK);
+        fetch(live - u0 - BLK);
 #pragma unroll
         for (int k = 0; k < BLK; ++k) {
-            const int64_t u = u0 + k;
-            if (u >= stop + W - 1) break;
+            const int u = u0 + k;
+            if (!kInside && u >= own + W - 1) break;
             auto& q = gp[(k + W - 1) % W];
             auto& in = row[(k + W - 1) % W];
-            if (u < until) {
+            if (kInside || u < live) {
                 unpack<T, V>(now_x[k], in);
                 unpack<T, V>(now_g[k], q);
                 if (L.act) {
@@ -217,7 +254,7 @@ __global__ void __launch_bounds__(kThreads) k_conv_bwd(const __grid_constant__ C
                 zero(in);
                 zero(q);
             }
-            if (u < stop) {
+            if (kInside || u < own) {
 #pragma unroll
                 for (int i = 0; i < P; ++i) {
                     gb[i] = pair_add(gb[i], q[i]);
@@ -225,19 +262,28 @@ __global__ void __launch_bounds__(kThreads) k_conv_bwd(const __grid_constant__ C
                     for (int m = 0; m < W; ++m) gw[m][i] = pair_fma(q[i], row[(k + m) % W][i], gw[m][i]);
                 }
             }
-            const int64_t t = u - (W - 1), j = t - len + W - 1;      // the input, its place in the state after
             float2 gx[P];
             zero(gx);
-            if (j >= 0 && j < W - 1 && L.gfin != nullptr && (t >= p.begin || p.begin == 0))
-                unpack<T, V>(load_raw<T, V>(static_cast<const T*>(L.gfin) + (p.b * (W - 1) + j) * L.C + p.c), gx);
+            const int64_t t = p.begin + u - (W - 1);
+            if (!kInside) {
+                const int64_t j = t - len + W - 1;       // the input's place in the state after
+                if (j >= 0 && j < W - 1 && L.gfin != nullptr && (u >= W - 1 || p.begin == 0))
+                    unpack<T, V>(load_raw<T, V>(static_cast<const T*>(L.gfin) + (p.b * (W - 1) + j) * L.C + p.c), gx);
+            }
 #pragma unroll
             for (int i = 0; i < P; ++i)
 #pragma unroll
                 for (int m = 0; m < W; ++m) gx[i] = pair_fma(w[W - 1 - m][i], gp[(k + m) % W][i], gx[i]);
-            if (t >= p.begin) *reinterpret_cast<Pack<T, V>*>(out + t * L.out.stride_t) = pack<T, V>(gx);
+            if (kInside || u >= W - 1) *reinterpret_cast<Pack<T, V>*>(out + t * L.out.stride_t) = pack<T, V>(gx);
             else if (t < 0 && L.fin != nullptr)
                 *reinterpret_cast<Pack<T, V>*>(static_cast<T*>(L.fin) + (p.b * (W - 1) + u) * L.C + p.c) = pack<T, V>(gx);
         }
+    };
+    // inputs from len - (W - 1) on take the state's gradient
+    const int whole = static_cast<int>(len - p.begin < own ? (len > p.begin ? len - p.begin : 0) : own);
+    for (int u0 = 0; u0 < own + W - 1; u0 += BLK) {
+        if (u0 >= W - 1 && u0 + BLK <= whole) block(u0, Flag<true>{});
+        else block(u0, Flag<false>{});
     }
     if (L.partial == nullptr) return;
     const int64_t runs = L.T == 0 ? 1 : (L.T + L.run - 1) / L.run;
@@ -284,8 +330,8 @@ template <typename T, int V, int W, Kind KIND>
 cudaError_t go(const ConvLaunch& L) {
     const int64_t across = (L.C / V + kThreads - 1) / kThreads, runs = KIND == kStep || L.T == 0 ? 1 : (L.T + L.run - 1) / L.run;
     const unsigned grid = static_cast<unsigned>(across * runs * L.B);
-    if (KIND == kForward) k_conv<T, V, W><<<grid, kThreads, 0, L.stream>>>(L);
-    else if (KIND == kBackward) k_conv_bwd<T, V, W><<<grid, kThreads, 0, L.stream>>>(L);
+    if constexpr (KIND == kForward) k_conv<T, V, W><<<grid, kThreads, 0, L.stream>>>(L);
+    else if constexpr (KIND == kBackward) k_conv_bwd<T, V, W><<<grid, kThreads, 0, L.stream>>>(L);
     else k_conv_step<T, V, W><<<grid, kThreads, 0, L.stream>>>(L);
     return cudaGetLastError();
 }
@@ -318,8 +364,8 @@ bool in_units(const ConvLaunch& L, int unit) {
 
 // channels a thread
 int width_of(const ConvLaunch& L, bool backward) {
-    if (L.bf16) return backward ? (in_units(L, 8) ? 4 : 1) : in_units(L, 16) ? 8 : 1;
-    return in_units(L, 16) ? 4 : 1;
+    const int unit = backward ? 8 : 16;              // bytes
+    return in_units(L, unit) ? unit / (L.bf16 ? 2 : 4) : 1;
 }
 
 template <Kind KIND>
@@ -329,7 +375,7 @@ cudaError_t by_type(const ConvLaunch& L) {
         if (V == 1) return by_taps<__nv_bfloat16, 1, KIND>(L);
         return by_taps<__nv_bfloat16, KIND == kBackward ? 4 : 8, KIND>(L);
     }
-    return V == 1 ? by_taps<float, 1, KIND>(L) : by_taps<float, 4, KIND>(L);
+    return V == 1 ? by_taps<float, 1, KIND>(L) : by_taps<float, KIND == kBackward ? 2 : 4, KIND>(L);
 }
 
 // Tokens a run: long ones read fewer inputs twice and leave fewer partial sums,

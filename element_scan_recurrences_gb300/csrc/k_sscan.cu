@@ -328,77 +328,132 @@ cudaError_t by_type(const ScanArgs& A, int64_t segs) {
 
 // ---------------------------------------------------------------------------
 // one token: bound by the states' bytes (read and written once).  A lane holds
-// VEC of a channel's states, `lanes` of them a channel, and takes ROWS batch rows
-// with the channel's A in registers, their states' loads all in flight.
+// VEC of a channel's states, 2^log_lanes of them a channel, and takes ROWS batch rows
+// with the channel's A in registers, their states' loads all in flight.  What a row
+// and channel need once (the step, the gate, the result) is made by one of the
+// channel's lanes: SHARE of them take the rows in turn.
 constexpr int kStepThreads = 128, ROWS = 4;
 
-template <typename T, int VEC>
-__global__ void __launch_bounds__(kStepThreads) k_sscan_step(const __grid_constant__ ScanLaunch L, int lanes) {
+template <typename T, int VEC, int SHARE>
+__global__ void __launch_bounds__(kStepThreads) k_sscan_step(const __grid_constant__ ScanLaunch L, int log_lanes, int fours) {
+    constexpr int OWN = ROWS / SHARE;                // rows whose once-a-row work a lane does: those with r % SHARE == sub % SHARE
     const int64_t at = static_cast<int64_t>(blockIdx.x) * kStepThreads + threadIdx.x;
-    const int sub = static_cast<int>(at % lanes), n0 = sub * VEC;
-    const int64_t c = at / lanes;
+    const int sub = static_cast<int>(at) & ((1 << log_lanes) - 1), n0 = sub * VEC, turn = sub & (SHARE - 1);
+    const int64_t c = at >> log_lanes;
     const bool mine = c < L.C && n0 < L.N;
-    const int64_t cc = c < L.C ? c : L.C - 1, group = cc / (L.C / L.G);
+    const int64_t cc = c < L.C ? c : L.C - 1;
+    const int64_t group = L.G == 1 ? 0 : static_cast<uint32_t>(cc) / static_cast<uint32_t>(L.C / L.G);
     const int64_t b0 = static_cast<int64_t>(blockIdx.y) * ROWS;
     const int rows = static_cast<int>(L.B - b0 < ROWS ? L.B - b0 : ROWS);
-    float a[VEC], h[ROWS][VEC], bv[ROWS][VEC], cv[ROWS][VEC], xv[ROWS], dv[ROWS], zv[ROWS];
+    const int64_t pitch = L.C * L.N, offset = b0 * pitch + cc * L.N + n0;
+    const float* const s = L.init + offset;
+    const T* const pb = static_cast<const T*>(L.b.data) + b0 * L.b.stride_b + group * L.b.stride_h + n0;
+    const T* const pc = static_cast<const T*>(L.c.data) + b0 * L.c.stride_b + group * L.c.stride_h + n0;
+    float a[VEC], h[ROWS][VEC], bv[ROWS][VEC], cv[ROWS][VEC];
+    float x[OWN], d[OWN], z[OWN], y[ROWS];
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
-        const int64_t b = b0 + (r < rows ? r : 0);
-        const float* s = L.init + (b * L.C + cc) * L.N + n0;
-        const T* pb = static_cast<const T*>(L.b.data) + b * L.b.stride_b + group * L.b.stride_h + n0;
-        const T* pc = static_cast<const T*>(L.c.data) + b * L.c.stride_b + group * L.c.stride_h + n0;
+        const bool on = mine && r < rows;
         if constexpr (VEC == 4) {
-            const float4 v = mine ? *reinterpret_cast<const float4*>(s) : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float4 v = on ? *reinterpret_cast<const float4*>(s + r * pitch) : make_float4(0.f, 0.f, 0.f, 0.f);
             h[r][0] = v.x, h[r][1] = v.y, h[r][2] = v.z, h[r][3] = v.w;
         } else {
-            h[r][0] = mine ? *s : 0.0f;
+            h[r][0] = on ? s[r * pitch] : 0.0f;
         }
+        if (VEC == 4 && fours) {
+            Pack<T, VEC> qb{}, qc{};
+            if (on) {
+                qb = load_raw<T, VEC>(pb + r * L.b.stride_b);
+                qc = load_raw<T, VEC>(pc + r * L.c.stride_b);
+            }
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            bv[r][j] = mine ? to_f32(pb[j]) : 0.0f;
-            cv[r][j] = mine ? to_f32(pc[j]) : 0.0f;
+            for (int j = 0; j < VEC; ++j) {
+                bv[r][j] = to_f32(qb.v[j]);
+                cv[r][j] = to_f32(qc.v[j]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                bv[r][j] = on ? to_f32(pb[r * L.b.stride_b + j]) : 0.0f;
+                cv[r][j] = on ? to_f32(pc[r * L.c.stride_b + j]) : 0.0f;
+            }
         }
-        xv[r] = to_f32((static_cast<const T*>(L.x.data) + b * L.x.stride_b)[cc]);
-        dv[r] = to_f32((static_cast<const T*>(L.delta.data) + b * L.delta.stride_b)[cc]);
-        zv[r] = L.gate.data != nullptr ? to_f32((static_cast<const T*>(L.gate.data) + b * L.gate.stride_b)[cc]) : 0.0f;
+    }
+    const float skip = L.skip != nullptr ? L.skip[cc] : 0.0f, bias = L.bias != nullptr ? L.bias[cc] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < OWN; ++i) {
+        const int r = i * SHARE + turn;
+        const int64_t b = b0 + (r < rows ? r : 0);
+        x[i] = to_f32((static_cast<const T*>(L.x.data) + b * L.x.stride_b)[cc]);
+        d[i] = to_f32((static_cast<const T*>(L.delta.data) + b * L.delta.stride_b)[cc]) + bias;
+        z[i] = L.gate.data != nullptr ? to_f32((static_cast<const T*>(L.gate.data) + b * L.gate.stride_b)[cc]) : 0.0f;
     }
 #pragma unroll
     for (int j = 0; j < VEC; ++j) a[j] = mine ? L.a[cc * L.N + n0 + j] * kLog2e : 0.0f;
-    const float skip = L.skip != nullptr ? L.skip[cc] : 0.0f, bias = L.bias != nullptr ? L.bias[cc] : 0.0f;
+    if (L.softplus) {
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) d[i] = softplus(d[i]);
+    }
+    float* const to = L.fin + offset;
+    const int lane = threadIdx.x % 32;
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
-        if (r >= rows) break;
-        const int64_t b = b0 + r;
-        float d = dv[r] + bias;
-        if (L.softplus) d = softplus(d);
-        const float dx = d * xv[r];
-        float y = 0.0f;
+        const int from = (lane & ~(SHARE - 1)) + r % SHARE;
+        const float dr = __shfl_sync(0xffffffffu, d[r / SHARE], from), dx = __shfl_sync(0xffffffffu, d[r / SHARE] * x[r / SHARE], from);
+        y[r] = 0.0f;
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-            h[r][j] = fmaf(exp2_hw(d * a[j]), h[r][j], dx * bv[r][j]);
-            y = fmaf(cv[r][j], h[r][j], y);
+            h[r][j] = fmaf(exp2_hw(dr * a[j]), h[r][j], dx * bv[r][j]);
+            y[r] = fmaf(cv[r][j], h[r][j], y[r]);
         }
-        if (mine) {
-            float* s = L.fin + (b * L.C + cc) * L.N + n0;
-            if constexpr (VEC == 4) *reinterpret_cast<float4*>(s) = make_float4(h[r][0], h[r][1], h[r][2], h[r][3]);
-            else *s = h[r][0];
+        if (mine && r < rows) {
+            if constexpr (VEC == 4) *reinterpret_cast<float4*>(to + r * pitch) = make_float4(h[r][0], h[r][1], h[r][2], h[r][3]);
+            else to[r * pitch] = h[r][0];
         }
-        for (int m = 1; m < lanes && m < 32; m *= 2) y += __shfl_xor_sync(0xffffffffu, y, m);
-        if constexpr (VEC == 1) {
-            // 64 states of one value a lane are two warps
-            if (lanes > 32) {
-                __shared__ float half[kStepThreads / 32];
-                __syncthreads();
-                if (threadIdx.x % 32 == 0) half[threadIdx.x / 32] = y;
-                __syncthreads();
-                y = half[threadIdx.x / 64 * 2] + half[threadIdx.x / 64 * 2 + 1];
+    }
+    // the sums over a channel's lanes: first each lane gets its own rows' of SHARE lanes
+    float own[OWN];
+#pragma unroll
+    for (int i = 0; i < OWN; ++i) {
+        float v[SHARE];
+#pragma unroll
+        for (int j = 0; j < SHARE; ++j) v[j] = y[i * SHARE + j];
+#pragma unroll
+        for (int n = SHARE / 2; n >= 1; n /= 2) {
+            const bool hi = turn & n;
+#pragma unroll
+            for (int j = 0; j < n; ++j) {
+                const float keep = hi ? v[j + n] : v[j], send = hi ? v[j] : v[j + n];
+                v[j] = keep + __shfl_xor_sync(0xffffffffu, send, n);
             }
         }
-        y = fmaf(skip, xv[r], y);
-        if (L.gate.data != nullptr) y *= zv[r] * logistic(zv[r]);
-        if (sub == 0 && c < L.C) (static_cast<T*>(L.out.data) + b * L.out.stride_b)[cc] = from_f32<T>(y);
+        own[i] = v[0];
+        for (int m = SHARE; m < 1 << log_lanes && m < 32; m *= 2) own[i] += __shfl_xor_sync(0xffffffffu, own[i], m);
     }
+    if constexpr (VEC == 1 && SHARE == 4) {
+        // 64 states of one value a lane are two warps
+        if (log_lanes > 5) {
+            __shared__ float half[kStepThreads / 32][SHARE];
+            if (lane < SHARE) half[threadIdx.x / 32][lane] = own[0];
+            __syncthreads();
+            own[0] = half[threadIdx.x / 64 * 2][turn] + half[threadIdx.x / 64 * 2 + 1][turn];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < OWN; ++i) {
+        const int r = i * SHARE + turn;
+        float v = fmaf(skip, x[i], own[i]);
+        if (L.gate.data != nullptr) v *= z[i] * logistic(z[i]);
+        if (sub < SHARE && c < L.C && r < rows) (static_cast<T*>(L.out.data) + (b0 + r) * L.out.stride_b)[cc] = from_f32<T>(v);
+    }
+}
+
+template <typename T, int VEC>
+cudaError_t step(const ScanLaunch& L, int log_lanes, int fours) {
+    const dim3 grid(static_cast<unsigned>(((L.C << log_lanes) + kStepThreads - 1) / kStepThreads), static_cast<unsigned>((L.B + ROWS - 1) / ROWS));
+    auto* kernel = log_lanes == 0 ? k_sscan_step<T, VEC, 1> : log_lanes == 1 ? k_sscan_step<T, VEC, 2> : k_sscan_step<T, VEC, 4>;
+    kernel<<<grid, kStepThreads, 0, L.stream>>>(L, log_lanes, fours);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -429,17 +484,16 @@ cudaError_t launch_scan_own_grads(const ScanBackward& S) {
 
 cudaError_t launch_scan_step(const ScanLaunch& L) {
     const bool vec = L.wide;
-    int lanes = 1;
-    while (lanes * (vec ? 4 : 1) < L.N) lanes *= 2;
-    const dim3 grid(static_cast<unsigned>((L.C * lanes + kStepThreads - 1) / kStepThreads), static_cast<unsigned>((L.B + ROWS - 1) / ROWS));
-    if (L.bf16) {
-        if (vec) k_sscan_step<__nv_bfloat16, 4><<<grid, kStepThreads, 0, L.stream>>>(L, lanes);
-        else k_sscan_step<__nv_bfloat16, 1><<<grid, kStepThreads, 0, L.stream>>>(L, lanes);
-    } else {
-        if (vec) k_sscan_step<float, 4><<<grid, kStepThreads, 0, L.stream>>>(L, lanes);
-        else k_sscan_step<float, 1><<<grid, kStepThreads, 0, L.stream>>>(L, lanes);
-    }
-    return cudaGetLastError();
+    int log_lanes = 0;
+    while ((vec ? 4 : 1) << log_lanes < L.N) ++log_lanes;
+    // four neighbouring values of B and C in one access
+    const int size = L.bf16 ? 2 : 4;
+    int fours = vec;
+    for (const es_heads* r : {&L.b, &L.c})
+        if (reinterpret_cast<uintptr_t>(r->data) % (4 * size) != 0 || (L.B > 1 && r->stride_b % 4 != 0) || (L.G > 1 && r->stride_h % 4 != 0))
+            fours = 0;
+    if (L.bf16) return vec ? step<__nv_bfloat16, 4>(L, log_lanes, fours) : step<__nv_bfloat16, 1>(L, log_lanes, fours);
+    return vec ? step<float, 4>(L, log_lanes, fours) : step<float, 1>(L, log_lanes, fours);
 }
 
 }  // namespace es
