@@ -18,9 +18,14 @@ namespace {
 
 template <int TEAM>
 constexpr int kThreadsOf = TEAM <= 32 ? 256 : TEAM;
-// Threads an SM holds, which the registers are fitted to: what hides HBM's latency is
-// the loads in flight, two rows of 32 bytes a thread forwards, of 48 backwards.
+// Threads an SM holds, which the registers are fitted to.
 constexpr int kResident = 768, kResidentBack = 512;
+// What hides HBM's latency is the bytes in flight: a thread's rows come through places
+// of its own in shared memory (cp.async, no barrier), kAhead of them on their way.  In
+// registers there was room for one: 51 us forwards for 16384 x 16 x 128 in bf16, 87
+// backwards.
+template <int NV, int V>
+constexpr int kAhead = V == 1 || NV >= 4 ? 1 : NV == 2 ? 2 : 4;
 
 // N sums over the threads of a team
 template <int TEAM, int N>
@@ -95,7 +100,11 @@ __global__ void __launch_bounds__(kThreadsOf<TEAM>, (BWD || NV * V == 16 ? 512 :
             }
         }
     }
-    Raw next_x[NV], next_z[NV], next_g[NV];
+    constexpr int AHEAD = kAhead<NV, V>, SLOTS = AHEAD + 1, KINDS = BWD ? 3 : 2;
+    extern __shared__ __align__(16) unsigned char smem[];
+    auto slot = [&](int64_t turn, int kind, int k) -> Raw& {
+        return reinterpret_cast<Raw*>(smem)[((turn * KINDS + kind) * NV + k) * kThreadsOf<TEAM> + threadIdx.x];
+    };
     // Rows come `step` apart: a tensor's place moves by as much from turn to turn, and by
     // the difference where the tokens of a batch row end.
     const int64_t step_b = step / L.T, step_t = step % L.T, first = static_cast<int64_t>(blockIdx.x) * A.rows + rs;
@@ -109,15 +118,29 @@ __global__ void __launch_bounds__(kThreadsOf<TEAM>, (BWD || NV * V == 16 ? 512 :
     const T *px = place(L.x), *pz = gated ? place(L.gate) : nullptr, *pg = BWD ? place(L.g) : nullptr;      // of the row after this
     const T *po = place(L.out), *pgz = BWD && gated ? place(L.ggate) : nullptr;                             // of this row
     const int64_t last = rows - 1;
-    auto fetch = [&](int64_t r) {
-        if (!team_in || r > last) return;
+    auto move = [&](Raw& to, const T* from) {
+        if constexpr (V == 1) to = load_raw<T, V>(from);
+        else copy16(&to, from, 16);
+    };
+    // the row at (px, pz, pg) into the places of a turn, and on to the next one
+    int64_t t_next = first % L.T;                // the token of the row that px stands at
+    auto fetch = [&](int64_t r, int turn) {
+        if (team_in && r <= last) {
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            if (!whole && (k * TEAM + lane) * V >= L.D) continue;
-            next_x[k] = load_raw<T, V>(px + k * TEAM * V);
-            if (gated) next_z[k] = load_raw<T, V>(pz + k * TEAM * V);
-            if (BWD) next_g[k] = load_raw<T, V>(pg + k * TEAM * V);
+            for (int k = 0; k < NV; ++k) {
+                if (!whole && (k * TEAM + lane) * V >= L.D) continue;
+                move(slot(turn, 0, k), px + k * TEAM * V);
+                if (gated) move(slot(turn, 1, k), pz + k * TEAM * V);
+                if (BWD) move(slot(turn, KINDS - 1, k), pg + k * TEAM * V);
+            }
         }
+        copies_done();
+        t_next += step_t;
+        const bool wrapped = t_next >= L.T;
+        if (wrapped) t_next -= L.T;
+        on(px, L.x, wrapped);
+        if (gated) on(pz, L.gate, wrapped);
+        if (BWD) on(pg, L.g, wrapped);
     };
     auto spread = [&](const Raw (&q)[NV], float2 (&r)[P]) {
 #pragma unroll
@@ -138,30 +161,27 @@ __global__ void __launch_bounds__(kThreadsOf<TEAM>, (BWD || NV * V == 16 ? 512 :
             *reinterpret_cast<Raw*>(o + k * TEAM * V) = raw;
         }
     };
+    // places past the group's last value and of rows past the last hold zeros
+    for (int i = 0; i < SLOTS * KINDS * NV; ++i) reinterpret_cast<Raw*>(smem)[i * kThreadsOf<TEAM> + threadIdx.x] = Raw{};
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
-#pragma unroll
-        for (int i = 0; i < V; ++i) next_x[k].v[i] = next_z[k].v[i] = next_g[k].v[i] = from_f32<T>(0.0f);
-    fetch(first);
-    int64_t t_next = first % L.T;                // the token of the row that px stands at
+    for (int i = 0; i < AHEAD; ++i) fetch(first + i * step, i);
+    int turn = 0;
+    int64_t t_out = first % L.T;
     // every team of a warp (of a block) makes every turn: the sums are taken together
     for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * A.rows; r0 < rows; r0 += step) {
         const bool in = team_in && r0 + rs <= last;
+        copies_wait<AHEAD - 1>();
         // as loaded until they are needed, which takes half the registers in bf16
         Raw raw_x[NV], raw_z[NV], raw_g[NV];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            raw_x[k] = next_x[k];
-            raw_z[k] = next_z[k];
-            if (BWD) raw_g[k] = next_g[k];
+            raw_x[k] = slot(turn, 0, k);
+            if (gated) raw_z[k] = slot(turn, 1, k);
+            if (BWD) raw_g[k] = slot(turn, KINDS - 1, k);
         }
-        t_next += step_t;
-        const bool wrapped = t_next >= L.T;
-        if (wrapped) t_next -= L.T;
-        on(px, L.x, wrapped);
-        if (gated) on(pz, L.gate, wrapped);
-        if (BWD) on(pg, L.g, wrapped);
-        fetch(r0 + rs + step);
+        // the place read a turn ago takes the row that comes kAhead after this
+        fetch(r0 + rs + AHEAD * step, turn == 0 ? AHEAD : turn - 1);
+        if (++turn == SLOTS) turn = 0;
         float2 u[P], of_z[P], slope[P];          // of_z: the gate's factor z s(z)
         auto gate = [&]() {
             spread(raw_z, of_z);
@@ -244,6 +264,9 @@ __global__ void __launch_bounds__(kThreadsOf<TEAM>, (BWD || NV * V == 16 ? 512 :
                 if (gated) put(pgz, slope);
             }
         }
+        t_out += step_t;
+        const bool wrapped = t_out >= L.T;
+        if (wrapped) t_out -= L.T;
         on(po, L.out, wrapped);
         if (BWD && gated) on(pgz, L.ggate, wrapped);
     }
@@ -321,7 +344,10 @@ cudaError_t go(const NormLaunch& L, bool backward) {
     const Gate gate = L.gate.data == nullptr ? kNone : L.first ? kFirst : kAfter;
     auto* kernel = backward ? (gate == kNone ? k_group_norm<T, V, E / V, TEAM, true, kNone> : gate == kFirst ? k_group_norm<T, V, E / V, TEAM, true, kFirst> : k_group_norm<T, V, E / V, TEAM, true, kAfter>)
                             : (gate == kNone ? k_group_norm<T, V, E / V, TEAM, false, kNone> : gate == kFirst ? k_group_norm<T, V, E / V, TEAM, false, kFirst> : k_group_norm<T, V, E / V, TEAM, false, kAfter>);
-    kernel<<<grid, kThreadsOf<TEAM>, 0, L.stream>>>(A);
+    const int bytes = (kAhead<E / V, V> + 1) * (backward ? 3 : 2) * E * static_cast<int>(sizeof(T)) * kThreadsOf<TEAM>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, kThreadsOf<TEAM>, bytes, L.stream>>>(A);
     return cudaGetLastError();
 }
 
