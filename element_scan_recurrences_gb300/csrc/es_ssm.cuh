@@ -187,6 +187,14 @@ __device__ __forceinline__ void copy16(void* to, const void* from, int n) {
     const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(to));
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(a), "l"(from), "r"(n) : "memory");
 }
+// BYTES (4, 8 or 16) into shared memory, to be waited for; fewer at once
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* to, const void* from) {
+    const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(to));
+    if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(a), "l"(from) : "memory");
+    else if constexpr (BYTES >= 4) asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(a), "l"(from), "n"(BYTES) : "memory");
+    else *static_cast<uint16_t*>(to) = *static_cast<const uint16_t*>(from);
+}
 __device__ __forceinline__ void copies_done() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // all groups but the LEFT last ones are there (0: every copy, in a group or not)
 template <int LEFT>

@@ -154,12 +154,12 @@ struct ScanPlan {
 // us for each of them (7 at most; 2.0 us at 3.4, 3.5 at 6.7).  Segments make more CTAs
 // of fewer chunks, for a pass over all but one of them that finds their own states at
 // 0.6 of that, and a launch.  Backwards (2 CTAs at most, of 4 times the channels) a
-// chunk takes 6 us alone, 8 by two.
+// chunk takes 9.4 us alone, 13 by two.
 struct Pace {
     int resident;
     double alone, more;          // us a chunk of one CTA an SM, what each further one adds
 };
-constexpr Pace kForwards{7, 1.37, 0.37}, kBackwards{2, 6.0, 2.0};
+constexpr Pace kForwards{7, 1.37, 0.37}, kBackwards{2, 9.4, 3.7};
 
 double chunk_us(const Pace& p, int64_t ctas) {
     const double each = static_cast<double>(ctas) / kSms, here = each < p.resident ? each : p.resident;

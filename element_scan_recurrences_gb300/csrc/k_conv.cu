@@ -6,8 +6,11 @@
 // Bounded by HBM: 2 W + 4 operations against 4 bytes an element in bf16.  A thread
 // takes 16 bytes of channels (8 backwards) through a run of tokens with the last
 // W - 1 inputs in registers, so each input is read once but for W - 1 tokens a run;
-// a warp's accesses are whole rows of 256 bytes or more.  Tokens come in blocks whose
-// loads are issued a block ahead; products and sums are made two channels an
+// a warp's accesses are whole rows of 256 bytes or more.  Tokens come in blocks through
+// places of the thread's own in shared memory (cp.async, no barrier), two blocks on
+// their way: that many bytes in flight hide HBM's latency, where in registers there
+// was room for one block (54 us for 8 x 2048 x 4096 ragged prompts in bf16, 77 the
+// gradient of 4 x 2047 x 4096).  Products and sums are made two channels an
 // instruction.  The gradient is one pass over x and the gradient of out the same
 // way: p is formed again, and the gradients of the last W tokens' p in registers give
 // that of the input W - 1 tokens back.  The weights' sums over a run stay in
@@ -73,6 +76,9 @@ __device__ __forceinline__ void load_weights(const ConvLaunch& L, int64_t c, flo
     }
 }
 
+// A thread's blocks of tokens on their way, kAheadBlocks of them
+constexpr int kAheadBlocks = 2, kPlaces = kAheadBlocks + 1;
+
 template <bool B>
 struct Flag {
     static constexpr bool value = B;
@@ -105,22 +111,21 @@ __global__ void __launch_bounds__(kThreads, V * W <= 32 ? 3 : 2) k_conv(const __
     const T* const x = static_cast<const T*>(L.x.data) + p.b * L.x.stride_b + p.c;
     T* const out = static_cast<T*>(L.out.data) + p.b * L.out.stride_b + p.c;
     float2 w[W][P], bias[P], row[W][P];              // token t's input at place (t - begin + W - 1) % W of `row`
-    Pack<T, V> next[BLK];
+    using Raw = Pack<T, V>;
+    __shared__ Raw ring[kPlaces][BLK][kThreads];
     const int count = end > p.begin ? static_cast<int>(end - p.begin) : 0;
     const T* px = x + p.begin * L.x.stride_t;        // of the next block
     T* po = out + p.begin * L.out.stride_t;
-    auto fetch = [&](int left) {
-        if (left >= BLK) {
+    auto fetch = [&](int left, int place) {
 #pragma unroll
-            for (int k = 0; k < BLK; ++k) next[k] = load_raw<T, V>(px + k * L.x.stride_t);
-        } else {
-#pragma unroll
-            for (int k = 0; k < BLK; ++k)
-                if (k < left) next[k] = load_raw<T, V>(px + k * L.x.stride_t);
-        }
+        for (int k = 0; k < BLK; ++k)
+            if (k < left) copy_async<sizeof(Raw)>(&ring[place][k][threadIdx.x], px + k * L.x.stride_t);
+        copies_done();
         px += BLK * L.x.stride_t;
     };
-    fetch(count);
+#pragma unroll
+    for (int i = 0; i < kAheadBlocks; ++i) fetch(count - i * BLK, i);
+    int place = 0;
     if (p.begin < end || p.begin == 0) {
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) input_at<T, V, W>(L, x, p.b, p.c, p.begin - (W - 1) + j, row[j]);
@@ -137,14 +142,15 @@ __global__ void __launch_bounds__(kThreads, V * W <= 32 ? 3 : 2) k_conv(const __
     load_weights<V, W>(L, p.c, w, bias);
     // blocks whole and the last: without tests between their tokens they run into one another
     auto block = [&](int left, auto whole) {
-        Pack<T, V> now[BLK];
-#pragma unroll
-        for (int k = 0; k < BLK; ++k) now[k] = next[k];
-        fetch(left - BLK);
+        copies_wait<kAheadBlocks - 1>();
+        // the place read a block ago takes the block that comes kAheadBlocks after this
+        fetch(left - kAheadBlocks * BLK, place == 0 ? kAheadBlocks : place - 1);
+        const auto& now = ring[place];
+        if (++place == kPlaces) place = 0;
 #pragma unroll
         for (int k = 0; k < BLK; ++k) {
             if (!decltype(whole)::value && k >= left) break;
-            unpack<T, V>(now[k], row[(k + W - 1) % W]);
+            unpack<T, V>(now[k][threadIdx.x], row[(k + W - 1) % W]);
             float2 o[P];
 #pragma unroll
             for (int i = 0; i < P; ++i) {
@@ -182,31 +188,27 @@ __global__ void __launch_bounds__(kThreads, V * W <= 16 ? 4 : 2) k_conv_bwd(cons
     const T* const g = static_cast<const T*>(L.g.data) + p.b * L.g.stride_b + p.c;
     T* const out = static_cast<T*>(L.out.data) + p.b * L.out.stride_b + p.c;
     float2 w[W][P], bias[P], row[W][P], gp[W][P], gw[W][P], gb[P];      // `row` and `gp` go around as in k_conv
-    Pack<T, V> next_x[BLK], next_g[BLK];
+    using Raw = Pack<T, V>;
+    __shared__ Raw ring[kPlaces][2][BLK][kThreads];
     // the tokens whose p this run needs: W - 1 past its own
     const int64_t until = stop + W - 1 < len ? stop + W - 1 : len;
     const T *px = x + p.begin * L.x.stride_t, *pg = g + p.begin * L.g.stride_t;      // of the next block
-    auto fetch = [&](int left) {
-        if (left >= BLK) {
+    auto fetch = [&](int left, int place) {
 #pragma unroll
-            for (int k = 0; k < BLK; ++k) {
-                next_x[k] = load_raw<T, V>(px + k * L.x.stride_t);
-                next_g[k] = load_raw<T, V>(pg + k * L.g.stride_t);
+        for (int k = 0; k < BLK; ++k)
+            if (k < left) {
+                copy_async<sizeof(Raw)>(&ring[place][0][k][threadIdx.x], px + k * L.x.stride_t);
+                copy_async<sizeof(Raw)>(&ring[place][1][k][threadIdx.x], pg + k * L.g.stride_t);
             }
-        } else {
-#pragma unroll
-            for (int k = 0; k < BLK; ++k)
-                if (k < left) {
-                    next_x[k] = load_raw<T, V>(px + k * L.x.stride_t);
-                    next_g[k] = load_raw<T, V>(pg + k * L.g.stride_t);
-                }
-        }
+        copies_done();
         px += BLK * L.x.stride_t;
         pg += BLK * L.g.stride_t;
     };
     // tokens from the run's first: those with p, with p of its own, all that the loop makes
     const int live = until > p.begin ? static_cast<int>(until - p.begin) : 0, own = static_cast<int>(stop - p.begin);
-    fetch(live);
+#pragma unroll
+    for (int i = 0; i < kAheadBlocks; ++i) fetch(live - i * BLK, i);
+    int place = 0;
     load_weights<V, W>(L, p.c, w, bias);
     zero(gb);
 #pragma unroll
@@ -223,13 +225,10 @@ __global__ void __launch_bounds__(kThreads, V * W <= 16 ? 4 : 2) k_conv_bwd(cons
     // run's own and reads no state's gradient
     auto block = [&](int u0, auto inside) {
         constexpr bool kInside = decltype(inside)::value;
-        Pack<T, V> now_x[BLK], now_g[BLK];
-#pragma unroll
-        for (int k = 0; k < BLK; ++k) {
-            now_x[k] = next_x[k];
-            now_g[k] = next_g[k];
-        }
-        fetch(live - u0 - BLK);
+        copies_wait<kAheadBlocks - 1>();
+        fetch(live - u0 - kAheadBlocks * BLK, place == 0 ? kAheadBlocks : place - 1);
+        const auto& now = ring[place];
+        if (++place == kPlaces) place = 0;
 #pragma unroll
         for (int k = 0; k < BLK; ++k) {
             const int u = u0 + k;
@@ -237,8 +236,8 @@ __global__ void __launch_bounds__(kThreads, V * W <= 16 ? 4 : 2) k_conv_bwd(cons
             auto& q = gp[(k + W - 1) % W];
             auto& in = row[(k + W - 1) % W];
             if (kInside || u < live) {
-                unpack<T, V>(now_x[k], in);
-                unpack<T, V>(now_g[k], q);
+                unpack<T, V>(now[0][k][threadIdx.x], in);
+                unpack<T, V>(now[1][k][threadIdx.x], q);
                 if (L.act) {
 #pragma unroll
                     for (int i = 0; i < P; ++i) {
