@@ -15,8 +15,7 @@ namespace {
 bool known(int64_t dtype) { return dtype == ES_F32 || dtype == ES_BF16; }
 int64_t size_of(int64_t dtype) { return dtype == ES_BF16 ? 2 : 4; }
 
-// The spans a call reads and writes.  Of the written ones the first `pairs` may
-// each be a read one itself (a state updated in its place).
+// The spans a call reads and writes.
 struct Spans {
     Span in[16], out[12];
     int n_in = 0, n_out = 0;
@@ -144,17 +143,19 @@ es_status plan_conv(const char* fn, const es_causal_conv_args* a, const es_causa
 struct ScanPlan {
     ScanBackward S;
     bool empty, find;            // find: a backward call without checkpoints
-    size_t kept, seg_state, seg_sum, first, part_bc, part_c, bytes, kept_bytes;
+    size_t kept, seg_state, seg_sum, part_bc, part_c, bytes, kept_bytes;
+    size_t first;                // offset of the copy of init, plus one (0: none)
     int fwd_segs;                // of the pass that finds the kept states
     int64_t fwd_seg_chunks;
 };
 
 // Segments a row's tokens are cut into.  A CTA takes a row's block of channels from
 // token to token, and a chunk takes it the longer the more CTAs share its SM: 1 + 0.37
-// us for each of them (7 at most; 2.0 us at 3.4, 3.5 at 6.7).  Segments make more CTAs
-// of fewer chunks, for a pass over all but one of them that finds their own states at
-// 0.6 of that, and a launch.  Backwards (2 CTAs at most, of 4 times the channels) a
-// chunk takes 9.4 us alone, 13 by two.
+// us for each of them (7 at most; measured 2.0 us at 3.4, 3.5 at 6.7).  Segments make
+// more CTAs of fewer chunks, for a pass over all but one of them that finds their own
+// states at 0.6 of that, and a launch.  Backwards (2 CTAs at most, of 4 times the
+// channels) a chunk takes 9.4 us alone, 13 by two.  4 x 2048 x 4096 whole and in two
+// segments: forwards 260 us, 298; backwards 1289, 908 (an earlier form of the kernel).
 struct Pace {
     int resident;
     double alone, more;          // us a chunk of one CTA an SM, what each further one adds
@@ -173,7 +174,8 @@ int scan_segments(const Pace& p, int64_t ctas, int64_t first, int64_t chunks, in
     const int64_t most = static_cast<int64_t>(kSms) * p.resident / (ctas > 0 ? ctas : 1);
     double best = static_cast<double>(chunks) * chunk_us(p, ctas);
     int segs = 1;
-    for (int64_t s = 2; s <= most && s <= chunks; ++s) {
+    // (some forty numbers of segments: a plan is made at every call)
+    for (int64_t s = 2; s <= most && s <= chunks; s += s < 16 ? 1 : s / 16) {
         const int64_t each = (chunks + s - 1) / s, n = (chunks + each - 1) / each;
         const double us = static_cast<double>(each) * (chunk_us(p, ctas * n) + 0.6 * chunk_us(kForwards, first * (n - 1))) + 5.0;
         if (us < best) {
@@ -339,7 +341,7 @@ es_status plan_norm(const char* fn, const es_group_norm_args* a, const es_group_
     if (H < 0) return api_fail(ES_E_DIM_001, "E-DIM-001 %s: a negative dimension", fn);
     if (D < 1 || D > kMaxNormDim)
         return api_fail(ES_E_UNSUPPORTED, "%s: groups of %lld values; 1..%d are supported", fn, static_cast<long long>(D), kMaxNormDim);
-    if (H > (1 << 18)) return api_fail(ES_E_UNSUPPORTED, "%s: too many groups", fn);
+    if (H > 65535) return api_fail(ES_E_UNSUPPORTED, "%s: %lld groups a token; 65535 are supported", fn, static_cast<long long>(H));
     if ((st = check_sizes(fn, B, T, H * D)) != ES_OK) return st;
     if (!(a->eps >= 0) || !std::isfinite(a->eps)) return api_fail(ES_E_ARG, "%s: eps %g", fn, a->eps);
     const bool backward = g != nullptr, gated = a->gate.data != nullptr;

@@ -981,7 +981,8 @@ es_status es_selective_scan_step(const es_selective_scan_args *args, es_stream_t
  *     no gate (data null):    u = x,         out = s(y) with activation, else y
  *
  *   dtype, weight_dtype   of x, gate, out; of weight and bias.
- *   dim               1..8192 (var is the mean square distance from the mean).
+ *   dim               1..8192 (var is the mean square distance from the mean);
+ *                     heads 0..65535.
  *   out               may not overlap an input.
  * activation goes without a gate only (ES_E_ARG).  Sums are f32.
  */
