@@ -19,7 +19,10 @@
 // (d and d x), and the last tile's results, two channels an instruction: 50 of the
 // 133 instructions a token and channel, and half of the warps that hide each
 // other's latencies (with every warp doing all three in turn 1.7 of them were there a
-// scheduler, and it issued in 38 of 100 clocks).  One barrier a tile.
+// scheduler, and it issued in 38 of 100 clocks).  One barrier a tile.  8 x 1024 x 4096
+// channels x 16 states in bf16: 222 us (57 for the exponentials alone), 57 of 100
+// clocks issue.  Eight tokens a block of the inner loop: with two 229 us, four 234,
+// sixteen 242.
 //
 // A channel's tokens are a chain, so few channels leave the GPU idle: then the
 // tokens are cut into segments, a first pass finds the state each segment makes
