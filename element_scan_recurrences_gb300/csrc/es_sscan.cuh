@@ -25,7 +25,7 @@ struct ScanArgs {
     int64_t per_group;       // channels of a group
     int64_t blocks;          // CTAs over a group's channels
     int keep_only;           // the kept states and no results
-    int vec;                 // loads in 16-byte pieces
+    int vec, vec_bc;         // loads in 16-byte pieces: of rows of channels, of B and C
     int pairs;               // stores of two values
 };
 
@@ -179,20 +179,24 @@ __device__ __forceinline__ void put_sum(float* row, float2 s, int sub) {
     else if (NL == 4 || sub < 4) row[2 * (sub & 1) + (sub >> 1 & 1)] = s.x;
 }
 
-// 16-byte pieces of every operand's rows: addresses and strides in them, and no piece across two groups
+// 16-byte pieces: of the rows of channels (addresses and strides in them, and no piece
+// across two groups), of B and C
 inline bool scan_vectors(const ScanLaunch& L, const es_rows* extra) {
-    const int size = L.bf16 ? 2 : 4, V = 16 / size;
+    const int V = L.bf16 ? 8 : 4;
     const es_rows* rows[4] = {&L.x, &L.delta, &L.gate, extra};
-    const es_heads* heads[2] = {&L.b, &L.c};
-    for (const es_heads* r : heads)
-        if (reinterpret_cast<uintptr_t>(r->data) % 16 != 0 || (L.B > 1 && r->stride_b % V != 0) || (L.T > 1 && r->stride_t % V != 0) ||
-            (L.G > 1 && r->stride_h % V != 0))
-            return false;
     for (const es_rows* r : rows)
         if (r != nullptr && r->data != nullptr &&
             (reinterpret_cast<uintptr_t>(r->data) % 16 != 0 || (L.B > 1 && r->stride_b % V != 0) || (L.T > 1 && r->stride_t % V != 0)))
             return false;
     return L.G == 1 || (L.C / L.G) % V == 0;
+}
+inline bool scan_bc_vectors(const ScanLaunch& L) {
+    const int V = L.bf16 ? 8 : 4;
+    for (const es_heads* r : {&L.b, &L.c})
+        if (reinterpret_cast<uintptr_t>(r->data) % 16 != 0 || (L.B > 1 && r->stride_b % V != 0) || (L.T > 1 && r->stride_t % V != 0) ||
+            (L.G > 1 && r->stride_h % V != 0))
+            return false;
+    return true;
 }
 
 // accesses of two values: addresses, strides and a group's channels in pairs
@@ -207,6 +211,7 @@ inline ScanArgs scan_args(const ScanLaunch& L, int channels) {
     A.L = L;
     A.per_group = L.C / L.G;
     A.blocks = scan_blocks(L.C, L.G, channels);
+    A.vec_bc = scan_bc_vectors(L);
     return A;
 }
 

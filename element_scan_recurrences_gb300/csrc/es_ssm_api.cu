@@ -153,31 +153,35 @@ struct ScanPlan {
 // token to token, and a chunk takes it the longer the more CTAs share its SM: 1 + 0.37
 // us for each of them (7 at most; measured 2.0 us at 3.4, 3.5 at 6.7).  Segments make
 // more CTAs of fewer chunks, for a pass over all but one of them that finds their own
-// states at 0.6 of that, and a launch.  Backwards (2 CTAs at most, of 4 times the
-// channels) a chunk takes 9.4 us alone, 13 by two.  4 x 2048 x 4096 whole and in two
-// segments: forwards 260 us, 298; backwards 1289, 908 (an earlier form of the kernel).
+// states at 0.6 of that, a launch, and at the start of each a read of those before it.
+// More CTAs than the GPU holds even out what its SMs get: 65536 tokens x 2048 channels
+// 1397 us in 16 segments, 1347 in 19, 1301 in 32, 1331 in 64.  Backwards (2 CTAs an SM
+// at most, of 4 times the channels) a chunk takes 9.4 us alone, 13 by two, and a
+// second wave would run alone.  4 x 2048 x 4096 whole and in two segments: forwards 260
+// us, 298; backwards 1289, 908 (an earlier form of the kernel).
 struct Pace {
-    int resident;
+    int resident, waves;
     double alone, more;          // us a chunk of one CTA an SM, what each further one adds
 };
-constexpr Pace kForwards{7, 1.37, 0.37}, kBackwards{2, 9.4, 3.7};
+constexpr Pace kForwards{7, 4, 1.37, 0.37}, kBackwards{2, 1, 9.4, 3.7};
 
 double chunk_us(const Pace& p, int64_t ctas) {
-    const double each = static_cast<double>(ctas) / kSms, here = each < p.resident ? each : p.resident;
-    const double waves = each > p.resident ? each / p.resident : 1.0;
-    return waves * (p.alone + (here > 1.0 ? here - 1.0 : 0.0) * p.more);
+    const double each = static_cast<double>(ctas) / kSms;
+    // (the last wave ends raggedly: a twentieth of one)
+    if (each > p.resident) return (each / p.resident + 0.05) * (p.alone + (p.resident - 1) * p.more);
+    return p.alone + (std::ceil(each) > 1.0 ? std::ceil(each) - 1.0 : 0.0) * p.more;
 }
 
 // `ctas` of the main pass, `first` of the pass before it, a segment
 int scan_segments(const Pace& p, int64_t ctas, int64_t first, int64_t chunks, int64_t* seg_chunks) {
     *seg_chunks = chunks > 0 ? chunks : 1;
-    const int64_t most = static_cast<int64_t>(kSms) * p.resident / (ctas > 0 ? ctas : 1);
+    const int64_t most = static_cast<int64_t>(kSms) * p.resident * p.waves / (ctas > 0 ? ctas : 1);
     double best = static_cast<double>(chunks) * chunk_us(p, ctas);
     int segs = 1;
     // (some forty numbers of segments: a plan is made at every call)
     for (int64_t s = 2; s <= most && s <= chunks; s += s < 16 ? 1 : s / 16) {
         const int64_t each = (chunks + s - 1) / s, n = (chunks + each - 1) / each;
-        const double us = static_cast<double>(each) * (chunk_us(p, ctas * n) + 0.6 * chunk_us(kForwards, first * (n - 1))) + 5.0;
+        const double us = static_cast<double>(each) * (chunk_us(p, ctas * n) + 0.6 * chunk_us(kForwards, first * (n - 1))) + 5.0 + 0.6 * n;
         if (us < best) {
             best = us;
             segs = static_cast<int>(n);

@@ -90,8 +90,8 @@ __device__ __forceinline__ void help(const ScanArgs& A, const Run& R, Tile<T, NL
         load_tile<T, CB, kHalf>(id, to.x, from(kReads ? L.x : A.g, t0), kReads ? L.x.stride_t : A.g.stride_t, width, live, A.vec);
         load_tile<T, CB, kHalf>(id, to.delta, from(L.delta, t0), L.delta.stride_t, width, live, A.vec);
         if (gated) load_tile<T, CB, kHalf>(id, to.gate, from(L.gate, t0), L.gate.stride_t, width, live, A.vec);
-        if (kReads) load_tile<T, NP, kHalf>(id, to.b, of_group(L.b, t0), L.b.stride_t, L.N, live, A.vec);
-        if (MODE != kOwnState) load_tile<T, NP, kHalf>(id, to.c, of_group(L.c, t0), L.c.stride_t, L.N, live, A.vec);
+        if (kReads) load_tile<T, NP, kHalf>(id, to.b, of_group(L.b, t0), L.b.stride_t, L.N, live, A.vec_bc);
+        if (MODE != kOwnState) load_tile<T, NP, kHalf>(id, to.c, of_group(L.c, t0), L.c.stride_t, L.N, live, A.vec_bc);
     };
     T* const out = static_cast<T*>(L.out.data) + p.b * L.out.stride_b + c2;
     if (R.tiles > 0) fetch(0);

@@ -126,8 +126,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_sscan_bwd(const __grid_constant
         load_tile<T, CB, kThreads>(threadIdx.x, to.delta, from(L.delta, t0), L.delta.stride_t, width, live, B.A.vec);
         load_tile<T, CB, kThreads>(threadIdx.x, to.g, from(B.A.g, t0), B.A.g.stride_t, width, live, B.A.vec);
         if (gated) load_tile<T, CB, kThreads>(threadIdx.x, to.gate, from(L.gate, t0), L.gate.stride_t, width, live, B.A.vec);
-        load_tile<T, NP, kThreads>(threadIdx.x, to.b, of_group(L.b, t0), L.b.stride_t, L.N, live, B.A.vec);
-        load_tile<T, NP, kThreads>(threadIdx.x, to.c, of_group(L.c, t0), L.c.stride_t, L.N, live, B.A.vec);
+        load_tile<T, NP, kThreads>(threadIdx.x, to.b, of_group(L.b, t0), L.b.stride_t, L.N, live, B.A.vec_bc);
+        load_tile<T, NP, kThreads>(threadIdx.x, to.c, of_group(L.c, t0), L.c.stride_t, L.N, live, B.A.vec_bc);
     };
     T* const gx = static_cast<T*>(B.S.gx.data) + p.b * B.S.gx.stride_b + c2;
     T* const gdelta = static_cast<T*>(B.S.gdelta.data) + p.b * B.S.gdelta.stride_b + c2;

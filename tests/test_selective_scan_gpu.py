@@ -229,6 +229,12 @@ def test_views(dtype):
             assert torch.equal(x, y)
         for x, y in zip(es.selective_scan_backward(*a, view(c.go), grad_final_state=c.gfin, **c.kw()), gwant):
             assert torch.equal(x, y)
+    # B and C alone at odd addresses, then the rows alone
+    for which in ((3, 4), (0, 1, 6)):
+        a = [odd(t) if i in which else t for i, t in enumerate(c.args)]
+        assert torch.equal(es.selective_scan(*a, **c.kw())[0], want[0])
+        for x, y in zip(es.selective_scan_backward(*a, c.go, grad_final_state=c.gfin, **c.kw()), gwant):
+            assert torch.equal(x, y)
     # states at addresses of 4 bytes
     box = torch.zeros(c.init.numel() + 1, device="cuda")
     init = box[1:].view_as(c.init)

@@ -170,3 +170,57 @@ def test_long_checkpoints():
     assert torch.allclose(out[:, -64:].float(), o2[:, -64:].float(), rtol=2.0 ** -7, atol=2.0 ** -7)
     for i in (0, 1, 3, 4):
         assert torch.allclose(g[i][:, -64:].float(), g2[i][:, -64:].float(), rtol=2.0 ** -7, atol=2.0 ** -7), i
+
+
+def test_autograd_in_a_graph():
+    """Forward and backward of the layer through autograd in one graph, replayed on
+    other inputs.  (No eager graph of the same leaves may live meanwhile: PyTorch's
+    own nodes of the leaves then wait on the stream it was made on.)"""
+    p, G = pieces(torch.float32)
+    leaves = {k: p[k].requires_grad_(True) for k in p if k != "go"}
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            torch.autograd.grad(layer(leaves, G), list(leaves.values()), p["go"])
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = layer(leaves, G)
+        got = torch.autograd.grad(out, list(leaves.values()), p["go"])
+    with torch.no_grad():
+        p["xz"].normal_()
+        p["delta"].normal_()
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got, torch.autograd.grad(layer(leaves, G), list(leaves.values()), p["go"])):
+        assert torch.equal(a, b)
+
+
+def test_calls_on_two_streams():
+    """Two calls at once, each with its own results: those of one after the other."""
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    cases = []
+    for seed in range(2):
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        n = lambda *s: torch.randn(s, generator=gen, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+        x, delta, go, b, c = n(2, 600, 256), n(2, 600, 256), n(2, 600, 256), n(2, 600, 1, 16), n(2, 600, 1, 16)
+        a = -torch.rand(256, 16, generator=gen, device="cuda") - 0.1
+        cases.append(((x, delta, a, b, c, None, None, None), go))
+
+    def run(case):
+        args, go = case
+        out, _, kept = es.selective_scan(*args, checkpoints=True)
+        return (out,) + tuple(t for t in es.selective_scan_backward(*args, go, checkpoints=kept) if t is not None)
+
+    want = [run(c) for c in cases]
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(3):
+        for i, s in enumerate(sides):
+            with torch.cuda.stream(s):
+                got[i] = run(cases[i])
+    torch.cuda.synchronize()
+    for x, y in zip(got, want):
+        for p, q in zip(x, y):
+            assert torch.equal(p, q)
