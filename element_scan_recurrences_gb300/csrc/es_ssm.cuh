@@ -39,46 +39,11 @@ __device__ __forceinline__ float rcp_hw(float x) {
     return r;
 }
 
-// e^x for finite x: what x log2(e) loses in its rounding, |x| 2^-24 of the
-// result, goes back in to first order.
-__device__ __forceinline__ float exp_f32(float x) {
-    const float t = x * kLog2e;
-    const float lost = fmaf(x, kLog2eLow, fmaf(x, kLog2e, -t));
-    const float e = exp2_hw(t);
-    return fmaf(e, lost * kLn2, e);
-}
-
-// 1 / (1 + e^-z).  Below -87 it is 0 (e^87 = 6e37 keeps 1 + e^-z finite).
-__device__ __forceinline__ float logistic(float z) { return rcp_hw(1.0f + exp_f32(-fmaxf(z, -87.0f))); }
-
-// log(1 + e^x) = max(x, 0) + log(1 + e), e = e^-|x| in (0, 1].  log(1 + e) / e
-// is a polynomial of degree 9, fitted for the least relative error on [0, 1]
-// (5e-9; 1.3e-7 as evaluated in f32), so small results keep their bits.
-__device__ __forceinline__ float log1p_poly(float e) {
-    float p = -0.003244024235755205f;
-    p = fmaf(p, e, 0.019851457327604294f);
-    p = fmaf(p, e, -0.056959524750709534f);
-    p = fmaf(p, e, 0.10603653639554977f);
-    p = fmaf(p, e, -0.15305592119693756f);
-    p = fmaf(p, e, 0.1967593878507614f);
-    p = fmaf(p, e, -0.24954134225845337f);
-    p = fmaf(p, e, 0.3332996368408203f);
-    p = fmaf(p, e, -0.4999990165233612f);
-    p = fmaf(p, e, 1.0f);
-    return p * e;
-}
-
-// A NaN stays one through the first term.
-__device__ __forceinline__ float softplus(float x) {
-    const float m = fabsf(x);
-    return fmaf(0.5f, m, 0.5f * x) + log1p_poly(exp_f32(-fminf(m, 87.0f)));
-}
-
-// The same of two values; without EXACT the exponent's rounding is left (|z| 2^-24
-// of e^-z, for results rounded to bf16).
 __device__ __forceinline__ float2 pair_of(float v) { return make_float2(v, v); }
 
-// e^-m for m >= -87 (past 87 it is 0 or next to it)
+// e^-m (0 past 87).  EXACT, for m from -88.5 to 104: what m log2(e) loses in its
+// rounding, |m| 2^-24 of the result, goes back in to first order; results rounded to
+// bf16 go without.
 template <bool EXACT>
 __device__ __forceinline__ float2 pair_exp_minus(float2 m) {
     const float2 t = pair_mul(m, pair_of(-kLog2e));
@@ -88,12 +53,22 @@ __device__ __forceinline__ float2 pair_exp_minus(float2 m) {
     return pair_fma(e, pair_mul(lost, pair_of(-kLn2)), e);
 }
 
+// 1 / (1 + e^-z), for any z: 0 below -88, where it would be subnormal, and 1 far above
+// 0, so that z times it is 0 for the lowest finite values too.  The exponent's
+// correction needs a finite power and product, hence EXACT's bounds (e^88.5 = 2.7e38,
+// whose reciprocal the hardware flushes to 0).
 template <bool EXACT>
 __device__ __forceinline__ float2 pair_logistic(float2 z) {
-    const float2 d = pair_add(pair_exp_minus<EXACT>(make_float2(fmaxf(z.x, -87.0f), fmaxf(z.y, -87.0f))), pair_of(1.0f));
+    if constexpr (EXACT) z = make_float2(fminf(fmaxf(z.x, -88.5f), 104.0f), fminf(fmaxf(z.y, -88.5f), 104.0f));
+    const float2 d = pair_add(pair_exp_minus<EXACT>(z), pair_of(1.0f));
     return make_float2(rcp_hw(d.x), rcp_hw(d.y));
 }
+__device__ __forceinline__ float logistic(float z) { return pair_logistic<true>(pair_of(z)).x; }
 
+// log(1 + e^x) = max(x, 0) + log(1 + e), e = e^-|x| in (0, 1].  log(1 + e) / e
+// is a polynomial of degree 9, fitted for the least relative error on [0, 1]
+// (5e-9; 1.3e-7 as evaluated in f32), so small results keep their bits.  A NaN stays
+// one through the first term, (|x| + x) / 2.
 __device__ __forceinline__ float2 pair_softplus(float2 x) {
     const float2 m = make_float2(fabsf(x.x), fabsf(x.y));
     const float2 e = pair_exp_minus<true>(make_float2(fminf(m.x, 87.0f), fminf(m.y, 87.0f)));
@@ -108,9 +83,7 @@ __device__ __forceinline__ float2 pair_softplus(float2 x) {
     p = pair_fma(p, e, pair_of(1.0f));
     return pair_fma(p, e, pair_fma(m, pair_of(0.5f), pair_mul(x, pair_of(0.5f))));
 }
-
-// d/dz of z s(z), s = logistic(z)
-__device__ __forceinline__ float silu_slope(float z, float s) { return fmaf(z * s, 1.0f - s, s); }
+__device__ __forceinline__ float softplus(float x) { return pair_softplus(pair_of(x)).x; }
 
 // two neighbouring values in shared memory
 __device__ __forceinline__ float2 load_two(const float* p) { return *reinterpret_cast<const float2*>(p); }
@@ -128,20 +101,7 @@ struct alignas(sizeof(T) * V) Pack {
     T v[V];
 };
 
-template <typename T, int V>
-__device__ __forceinline__ void load_pack(const T* p, float (&r)[V]) {
-    const Pack<T, V> q = *reinterpret_cast<const Pack<T, V>*>(p);
-#pragma unroll
-    for (int i = 0; i < V; ++i) r[i] = to_f32(q.v[i]);
-}
-template <typename T, int V>
-__device__ __forceinline__ void store_pack(T* p, const float (&r)[V]) {
-    Pack<T, V> q;
-#pragma unroll
-    for (int i = 0; i < V; ++i) q.v[i] = from_f32<T>(r[i]);
-    *reinterpret_cast<Pack<T, V>*>(p) = q;
-}
-// the same as pairs (one half for V = 1), from what a load left in registers
+// as pairs (one half for V = 1), from what a load left in registers
 template <typename T, int V>
 __device__ __forceinline__ void unpack(const Pack<T, V>& q, float2 (&r)[(V + 1) / 2]) {
     if constexpr (V == 1) {
@@ -165,11 +125,6 @@ __device__ __forceinline__ Pack<T, V> pack(const float2 (&r)[(V + 1) / 2]) {
 template <typename T, int V>
 __device__ __forceinline__ Pack<T, V> load_raw(const T* p) {
     return *reinterpret_cast<const Pack<T, V>*>(p);
-}
-template <int V>
-__device__ __forceinline__ void zero(float (&r)[V]) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) r[i] = 0.0f;
 }
 template <int P>
 __device__ __forceinline__ void zero(float2 (&r)[P]) {
@@ -208,45 +163,6 @@ __device__ __forceinline__ int64_t live_tokens(const int32_t* lengths, int64_t b
     if (lengths == nullptr) return T;
     const int64_t n = lengths[b];
     return n < 0 ? 0 : n < T ? n : T;
-}
-
-// RN of a channel's N states from number n0 on (zeros past the last); `wide`: N is
-// a multiple of 4 and p of 16 bytes
-template <int RN>
-__device__ __forceinline__ void load_states(const float* p, int n0, int N, bool wide, float2 (&h)[RN / 2]) {
-    if constexpr (RN % 4 == 0) {
-        if (wide) {
-#pragma unroll
-            for (int i = 0; i < RN; i += 4) {
-                const float4 v = n0 + i < N ? *reinterpret_cast<const float4*>(p + n0 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-                h[i / 2] = make_float2(v.x, v.y);
-                h[i / 2 + 1] = make_float2(v.z, v.w);
-            }
-            return;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < RN; i += 2) {
-        h[i / 2].x = n0 + i < N ? p[n0 + i] : 0.0f;
-        h[i / 2].y = n0 + i + 1 < N ? p[n0 + i + 1] : 0.0f;
-    }
-}
-
-template <int RN>
-__device__ __forceinline__ void store_states(float* p, int n0, int N, bool wide, const float2 (&h)[RN / 2]) {
-    if constexpr (RN % 4 == 0) {
-        if (wide) {
-#pragma unroll
-            for (int i = 0; i < RN; i += 4)
-                if (n0 + i < N) *reinterpret_cast<float4*>(p + n0 + i) = make_float4(h[i / 2].x, h[i / 2].y, h[i / 2 + 1].x, h[i / 2 + 1].y);
-            return;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < RN; i += 2) {
-        if (n0 + i < N) p[n0 + i] = h[i / 2].x;
-        if (n0 + i + 1 < N) p[n0 + i + 1] = h[i / 2].y;
-    }
 }
 
 // Sums of the rows of a [rows][M] table, put(j, sum) for each column: a block takes

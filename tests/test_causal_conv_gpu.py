@@ -202,6 +202,26 @@ def test_captured():
         assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_values_of_any_size(dtype):
+    """Weights 0 and 1: s(x) for inputs up to the largest finite values, and its slope.  Some
+    16 roundings and one to the result's type, 2^-20 and 2^-8 of it; a subnormal factor
+    may be 0, under 2^-119 at |x| < 89."""
+    rel, tiny = 2.0 ** -8 + 2.0 ** -20 if dtype == BF16 else 2.0 ** -20, 2.0 ** -119
+    big = torch.finfo(dtype).max
+    z = torch.tensor([-big, -1e30, -200.0, -89.0, -88.0, -87.0, -1.0, 0.0, 1.0, 88.0, 105.0, 200.0, 1e30, big], device="cuda").to(dtype)
+    n = z.numel()
+    x = z.view(1, 1, n).clone().requires_grad_()
+    w = torch.tensor([0.0, 1.0], device="cuda").to(dtype).expand(n, 2).contiguous()
+    out = ag.causal_conv(x, w)[0]
+    out.backward(torch.ones_like(out))
+    step = es.causal_conv_step(z.view(1, n), w, None, torch.zeros(1, 1, n, dtype=dtype, device="cuda"))[0]
+    want, slope = S.silu(num(z)), S.slope(num(z))
+    for got in (out.detach(), step):
+        assert (np.abs(num(got).ravel() - want) <= rel * np.abs(want) + tiny).all(), got
+    assert (np.abs(num(x.grad).ravel() - slope) <= rel * 2.0 + tiny).all(), x.grad
+
+
 def test_refusals():
     c = Case(F32, 2, 10, 16, seed=10)
 

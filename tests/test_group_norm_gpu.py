@@ -184,6 +184,24 @@ def test_autograd():
     check(c, out.detach(), [t.grad for t in leaves])
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_gates_of_any_size(dtype):
+    """A row of ones by its mean square, 1 / sqrt(1 + eps), times s(z) for gates up to the
+    largest finite values.  Some 16 roundings and one to the result's type, 2^-20 and
+    2^-8 of it; a subnormal factor may be 0, under 2^-119 at |z| < 89."""
+    rel, tiny = 2.0 ** -8 + 2.0 ** -20 if dtype == BF16 else 2.0 ** -20, 2.0 ** -119
+    big = torch.finfo(dtype).max
+    z = torch.tensor([-big, -1e30, -200.0, -89.0, -88.0, -87.0, -1.0, 0.0, 1.0, 88.0, 105.0, 200.0, 1e30, big, 0.5, -0.5], device="cuda").to(dtype)
+    gate = z.view(1, 1, 1, -1).clone().requires_grad_()
+    one = torch.ones_like(gate)
+    out = ag.group_norm(one, gate=gate, center=False)
+    out.backward(one)
+    size = 1 / np.sqrt(1 + 1e-5)
+    want, slope = size * S.silu(num(z)), size * S.slope(num(z))
+    assert (np.abs(num(out.detach()).ravel() - want) <= rel * np.abs(want) + tiny).all(), out
+    assert (np.abs(num(gate.grad).ravel() - slope) <= rel * 2.0 + tiny).all(), gate.grad
+
+
 def test_refusals():
     c = Case(F32, 2, 10, 4, 16)
 

@@ -329,3 +329,39 @@ def test_refusals():
     refused(es.EsError, lambda: es.selective_scan_backward(*a, c.go[:1]))
     refused(TypeError, lambda: es.selective_scan(*a, lengths=torch.tensor([1, 2], device="cuda")))
     assert torch.equal(es.selective_scan(*a)[0], es.selective_scan(*a)[0])
+
+
+SIZES = [-1e30, -200.0, -89.0, -88.0, -87.0, -1.0, 0.0, 1.0, 88.0, 105.0, 200.0, 1e30]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_gates_and_steps_of_any_size(dtype):
+    """Gates and steps up to the largest finite values, one state and token, y = 0.5: y
+    times s(z), which is 0 far below 0 and z far above.  Some 16 roundings and one to
+    the result's type: 2^-20 and 2^-8 of it; a subnormal factor may be 0, 2^-126 z at
+    |z| < 89, under 2^-119."""
+    rel, tiny = 2.0 ** -8 + 2.0 ** -20 if dtype == BF16 else 2.0 ** -20, 2.0 ** -119
+    big = torch.finfo(dtype).max
+    z = torch.tensor([-big] + SIZES + [big], device="cuda").to(dtype)
+    n = z.numel()
+    one, two = torch.ones(1, 1, n, dtype=dtype, device="cuda"), torch.ones(1, 1, 1, 1, dtype=dtype, device="cuda")
+    a = torch.full((n, 1), -1.0, device="cuda")
+    gate = z.view(1, 1, n)
+    half = one * 0.5
+    prompt = es.selective_scan(half, one, a, two, two, gate=gate, softplus=False)[0]
+    state = torch.zeros(1, n, 1, device="cuda")
+    step = es.selective_scan_step(half[0], one[0], a, two[0], two[0], None, gate[0], None, state, softplus=False)[0]
+    want = 0.5 * S.silu(num(z))
+    for out in (prompt, step):
+        assert (np.abs(num(out).ravel() - want) <= rel * np.abs(want) + tiny).all(), out
+    leaf = gate.clone().requires_grad_()
+    ag.selective_scan(half, one, a, two, two, gate=leaf, softplus=False)[0].backward(one)
+    want = 0.5 * S.slope(num(z))
+    # the slope is a sum of terms no larger than 1 + |z| e^-|z|
+    assert (np.abs(num(leaf.grad).ravel() - want) <= rel * 2.0 + tiny).all(), leaf.grad
+    # steps: A = 0, so that the state is 2 softplus(delta); log 2 is of 3 roundings more
+    d = torch.tensor([-1e30, -100.0, 0.0, 100.0, 1e30], device="cuda").view(1, 1, 5).to(dtype)
+    x = torch.full_like(d, 2.0)
+    out = num(es.selective_scan(x, d, torch.zeros(5, 1, device="cuda"), two, two)[0]).ravel()
+    want = 2.0 * S.softplus(num(d)).ravel()
+    assert (np.abs(out - want) <= rel * np.abs(want) + tiny).all(), out
