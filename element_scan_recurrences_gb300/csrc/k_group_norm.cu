@@ -213,7 +213,10 @@ __global__ void __launch_bounds__(kThreadsOf<TEAM>, (BWD || NV * V == 16 ? 512 :
         for (int i = 0; i < P; ++i) t = pair_fma(u[i], u[i], t);
         float s[1] = {t.x + t.y};
         team_sum<TEAM>(s, part1);
-        const float2 size = pair_of(rsqrtf(fmaf(s[0], inv, L.eps)));
+        // (0 for a team without a row: its places may hold nothing but zeros, whose reciprocal
+        // deviation is infinite where eps is 0, and 0 times that would enter the weights' sums;
+        // a team that has its block to itself has a row in every turn)
+        const float2 size = pair_of(BWD && TEAMS > 1 && !in ? 0.0f : rsqrtf(fmaf(s[0], inv, L.eps)));
         if constexpr (GATE == kAfter) gate();
         if constexpr (!BWD) {
 #pragma unroll
