@@ -87,6 +87,8 @@ cudaError_t launch_scan(const ScanLaunch& L, bool keep_only, int* kernels);
 // gradients that the segments' own tokens leave (seg_state, seg_sum, from the second segment on)
 cudaError_t launch_scan_own_grads(const ScanBackward& L);
 cudaError_t launch_scan_backward(const ScanBackward& L, int* kernels);
+// gB and gC from the channel blocks' parts (without channels zeros); B, T > 0
+cudaError_t launch_scan_sum_bc(const ScanBackward& L);
 cudaError_t launch_scan_step(const ScanLaunch& L);
 
 // ---------------------------------------------------------------------------

@@ -203,6 +203,8 @@ es_status plan_scan(const char* fn, const es_selective_scan_args* a, const es_se
     if (G < 1 || C % G != 0)
         return api_fail(ES_E_DIM_001, "E-DIM-001 %s: %lld groups do not divide the %lld channels", fn, static_cast<long long>(G),
                         static_cast<long long>(C));
+    // (channels bound the groups, but for none)
+    if (C == 0 && (st = check_sizes(fn, B, T, G)) != ES_OK) return st;
     if (step && T != 1) return api_fail(ES_E_DIM_001, "E-DIM-001 %s: a step is one token, not %lld", fn, static_cast<long long>(T));
     if (step && (a->lengths != nullptr || a->checkpoints != nullptr))
         return api_fail(ES_E_ARG, "%s: a step takes no lengths and leaves no checkpoints", fn);
@@ -263,8 +265,8 @@ es_status plan_scan(const char* fn, const es_selective_scan_args* a, const es_se
         if ((st = add_rows(fn, "grad_x", g->grad_x, B, T, C, size, true, &S)) != ES_OK) return st;
         if ((st = add_rows(fn, "grad_delta", g->grad_delta, B, T, C, size, true, &S)) != ES_OK) return st;
         if (gated && (st = add_rows(fn, "grad_gate", g->grad_gate, B, T, C, size, true, &S)) != ES_OK) return st;
-        if ((st = add_heads(fn, "grad_b", g->grad_b, G, B, C > 0 ? T : 0, N, size, true, &S)) != ES_OK) return st;
-        if ((st = add_heads(fn, "grad_c", g->grad_c, G, B, C > 0 ? T : 0, N, size, true, &S)) != ES_OK) return st;
+        if ((st = add_heads(fn, "grad_b", g->grad_b, G, B, T, N, size, true, &S)) != ES_OK) return st;
+        if ((st = add_heads(fn, "grad_c", g->grad_c, G, B, T, N, size, true, &S)) != ES_OK) return st;
         if ((st = add_dense(fn, "grad_a", g->grad_a, C * N, 4, true, &S)) != ES_OK) return st;
         if ((st = add_dense(fn, "grad_skip", g->grad_skip, C, 4, true, &S)) != ES_OK) return st;
         if ((st = add_dense(fn, "grad_delta_bias", g->grad_delta_bias, C, 4, true, &S)) != ES_OK) return st;
@@ -525,6 +527,11 @@ es_status es_selective_scan_backward(const es_selective_scan_args* args, const e
                         (S.gskip != nullptr && (e = cudaMemsetAsync(S.gskip, 0, L.C * 4, L.stream)) != cudaSuccess) ||
                         (S.gbias != nullptr && (e = cudaMemsetAsync(S.gbias, 0, L.C * 4, L.stream)) != cudaSuccess)))
             return es::cuda_fail(fn, e);
+        // no channels: those of b and c too
+        if (L.C == 0 && L.B > 0 && L.T > 0) {
+            if ((e = es::launch_scan_sum_bc(S)) != cudaSuccess) return es::cuda_fail(fn, e);
+            es::count_launch();
+        }
         return ES_OK;
     }
     if ((st = es::check_workspace(fn, args->workspace, args->workspace_bytes, P.bytes)) != ES_OK) return st;

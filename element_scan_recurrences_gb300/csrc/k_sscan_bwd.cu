@@ -446,6 +446,17 @@ cudaError_t by_states(const BwdArgs& B) {
 
 }  // namespace
 
+cudaError_t launch_scan_sum_bc(const ScanBackward& S) {
+    const BwdArgs B{scan_args(S.f, scan_bwd_channels(S.f.N)), S};
+    const ScanLaunch& L = S.f;
+    const int64_t all = L.B * L.T * L.G * 2 * L.N, most = static_cast<int64_t>(kSms) * 16;
+    const int64_t want = (all + 255) / 256;
+    const unsigned blocks = static_cast<unsigned>(want < most ? want : most);
+    if (L.bf16) k_sscan_sum_bc<__nv_bfloat16><<<blocks, 256, 0, L.stream>>>(B);
+    else k_sscan_sum_bc<float><<<blocks, 256, 0, L.stream>>>(B);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_scan_backward(const ScanBackward& S, int* kernels) {
     BwdArgs B{scan_args(S.f, scan_bwd_channels(S.f.N)), S};
     B.A.g = S.g;
@@ -462,12 +473,7 @@ cudaError_t launch_scan_backward(const ScanBackward& S, int* kernels) {
     if (e != cudaSuccess) return e;
     ++*kernels;
     if (L.T > 0) {
-        const int64_t all = L.B * L.T * L.G * 2 * L.N, most = static_cast<int64_t>(kSms) * 16;
-        const int64_t want = (all + 255) / 256;
-        const unsigned blocks = static_cast<unsigned>(want < most ? want : most);
-        if (L.bf16) k_sscan_sum_bc<__nv_bfloat16><<<blocks, 256, 0, L.stream>>>(B);
-        else k_sscan_sum_bc<float><<<blocks, 256, 0, L.stream>>>(B);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if ((e = launch_scan_sum_bc(S)) != cudaSuccess) return e;
         ++*kernels;
     }
     k_sscan_sum_c<<<static_cast<unsigned>((L.C * (L.N + 2) + 255) / 256), 256, 0, L.stream>>>(B);

@@ -936,7 +936,8 @@ es_status es_selective_scan(const es_selective_scan_args *args, es_stream_t stre
  * grad_delta_bias [channels], grad_initial_state (each null: not wanted).
  * args->checkpoints: those the forward call of the same operands wrote, or
  * null (they are then found first, in the workspace).  args->out and
- * args->final_state are not used.  All sums are taken in a fixed order.
+ * args->final_state are not used.  All sums are taken in a fixed order; over
+ * no rows or no channels they are zeros.
  */
 typedef struct es_selective_scan_grads {
     es_rows grad_out, grad_x, grad_delta, grad_gate;
