@@ -8,14 +8,21 @@
 
 namespace es {
 
-// The hardware's 2^q is low in the mean: for -1 < q < 0 by 0.09 parts in 2^24 where
-// q > -2^-8 and by 0.37 below (measured, 2^18 values in each quarter octave; 0.5 to 0.7
-// at random about it).  Over the hundreds of tokens that a weak decay remembers the
-// mean adds up where the rest does not (2.7e-6 of a state after 2048 tokens), so it
-// is put back with the exponent, in the sum that a product with it costs anyway.
+// The hardware's 2^q is low in the mean, in parts of 2^24: for -1 < q < 0 by 0.09 where
+// |q| < 2^-9, rising in a line to 0.42 at 2^-7 (0.11 at 0.0025, 0.21 at 0.0043, 0.33 at
+// 0.006, 0.40 at 0.0076) and by 0.2 to 0.55 beyond (measured, 2^20 values in each
+// twelfth of an octave; 0.5 to 0.7 at random about it).  Over the hundreds of tokens that
+// a weak decay remembers the mean adds up where the rest does not (300 tokens of q =
+// -0.0047: 4.3e-6 of a state), so it is put back with the exponent, in the sum that a
+// product with it costs anyway: under 0.04 is left up to 2^-7, 0.25 up to 2^-6, and from
+// 2^-9 on costs a state under 1.6e-6 (one value of 0.37 past 2^-8: 3.4e-6).  One q speaks
+// for a tile of kScanChunk tokens (its first token's, or where a pass runs backwards its
+// last's).
 __device__ __forceinline__ float2 decay_mend(float2 q) {
-    constexpr float kSmall = 0.09f / 16777216.0f * 1.44269504f, kRest = 0.37f / 16777216.0f * 1.44269504f;
-    return make_float2(q.x > -0.00390625f ? kSmall : kRest, q.y > -0.00390625f ? kSmall : kRest);
+    constexpr float kPart = 1.44269504f / 16777216.0f;           // of the exponent
+    constexpr float kLow = 0.09f, kRise = 0.33f, kSlope = -62.0f / kRise, kFrom = -0.15f / kRise;
+    const float2 s = make_float2(__saturatef(fmaf(q.x, kSlope, kFrom)), __saturatef(fmaf(q.y, kSlope, kFrom)));
+    return pair_fma(s, pair_of(kRise * kPart), pair_of(kLow * kPart));
 }
 
 struct ScanArgs {

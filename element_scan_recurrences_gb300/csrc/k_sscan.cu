@@ -226,7 +226,7 @@ __device__ __forceinline__ void run(const ScanArgs& A, const Run& R, Tile<T, NL>
             constexpr int CB = Tile<T, NL>::CB;
             if (MODE == kMain && L.kept != nullptr)
                 store_block(L.kept + (p.b * L.chunks + t0 / K) * rows, L.N, c, p.last, n0, L.N, wide, h);
-            // what makes up for the exponentials' mean error, by their size in this tile
+            // what makes up for the exponentials' mean error, by their size at the tile's first (last) token
             Block mend;
             {
                 const float4 d = *reinterpret_cast<const float4*>(ds + (MODE == kOwnGrad ? live - 1 : 0) * CB);
