@@ -10,19 +10,20 @@ namespace es {
 
 // The hardware's 2^q is low in the mean, in parts of 2^24: for -1 < q < 0 by 0.09 where
 // |q| < 2^-9, rising in a line to 0.42 at 2^-7 (0.11 at 0.0025, 0.21 at 0.0043, 0.33 at
-// 0.006, 0.40 at 0.0076) and by 0.2 to 0.55 beyond (measured, 2^20 values in each
+// 0.006, 0.40 at 0.0076) and by 0.2 to 0.6 beyond (measured, 2^20 values in each
 // twelfth of an octave; 0.5 to 0.7 at random about it).  Over the hundreds of tokens that
 // a weak decay remembers the mean adds up where the rest does not (300 tokens of q =
 // -0.0047: 4.3e-6 of a state), so it is put back with the exponent, in the sum that a
 // product with it costs anyway: under 0.04 is left up to 2^-7, 0.25 up to 2^-6, and from
-// 2^-9 on costs a state under 1.6e-6 (one value of 0.37 past 2^-8: 3.4e-6).  One q speaks
-// for a tile of kScanChunk tokens (its first token's, or where a pass runs backwards its
-// last's).
+// 2^-9 on costs a state under 1.6e-6 (one value of 0.37 past 2^-8: 3.4e-6).  Over
+// whole rows one q speaks for a tile of kScanChunk tokens (its first token's, or where a
+// pass runs backwards its last's).
+constexpr float kMendLow = 0.09f, kMendRise = 0.33f, kMendSlope = -62.0f / kMendRise, kMendFrom = -0.15f / kMendRise;
+constexpr float kMendPart = 1.44269504f / 16777216.0f;           // of the exponent
+__device__ __forceinline__ float mend_place(float q) { return __saturatef(fmaf(q, kMendSlope, kMendFrom)); }
+__device__ __forceinline__ float decay_mend(float q) { return fmaf(mend_place(q), kMendRise * kMendPart, kMendLow * kMendPart); }
 __device__ __forceinline__ float2 decay_mend(float2 q) {
-    constexpr float kPart = 1.44269504f / 16777216.0f;           // of the exponent
-    constexpr float kLow = 0.09f, kRise = 0.33f, kSlope = -62.0f / kRise, kFrom = -0.15f / kRise;
-    const float2 s = make_float2(__saturatef(fmaf(q.x, kSlope, kFrom)), __saturatef(fmaf(q.y, kSlope, kFrom)));
-    return pair_fma(s, pair_of(kRise * kPart), pair_of(kLow * kPart));
+    return pair_fma(make_float2(mend_place(q.x), mend_place(q.y)), pair_of(kMendRise * kMendPart), pair_of(kMendLow * kMendPart));
 }
 
 struct ScanArgs {

@@ -85,9 +85,32 @@ def test_a_prompt_in_tiles(dtype, N):
     assert far(state, want) <= 42
 
 
+def tokens(args, state):
+    """... and one by one."""
+    x, delta, a, b, c = args[:5]
+    for t in range(x.shape[1]):
+        es.selective_scan_step(x[:, t], delta[:, t], a, b[:, t], c[:, t], None, None, None, state, softplus=False)
+    return state
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("N", [16, 5])
+def test_single_tokens(dtype, N):
+    """Served token by token, a state is as near 64 bits as a prompt's.  Where the steps of
+    each tile are alike they are the same bits (the same sums in the same order)."""
+    args, _ = weak(dtype, 2048, C=40, N=N, B=2, seed=1)
+    state = tokens(args, torch.zeros(2, 40, N, device="cuda"))
+    want = S.selective_scan(*(None if v is None else num(v) for v in args), soft=False)[1]
+    assert far(state, want) <= 42
+    alike = args[1][:, ::16].repeat_interleave(16, 1)
+    args = (args[0], alike) + args[2:]
+    assert torch.equal(tokens(args, torch.zeros(2, 40, N, device="cuda")), in_tiles(args, torch.zeros(2, 40, N, device="cuda")))
+
+
 def test_no_decay_keeps_every_bit():
     """A = 0: states are the sums of their inputs, here whole numbers, exactly, however
-    long the row."""
+    long the row, on the prompt's way and token by token; the tokens that a block past a
+    row's end still takes leave a state as it is."""
     T, C, N = 4099, 8, 4
     one = torch.ones(1, T, C, device="cuda")
     two = torch.ones(1, T, 1, N, device="cuda")
@@ -95,6 +118,17 @@ def test_no_decay_keeps_every_bit():
     out, state, _ = es.selective_scan(one, one, zero, two, two, softplus=False, final_state=True)
     assert torch.equal(state, torch.full((1, C, N), float(T), device="cuda"))
     assert torch.equal(out[0, :, 0], N * torch.arange(1, T + 1, device="cuda").float())
+    step = torch.full((1, C, N), 2.0 ** 22, device="cuda")
+    for t in range(64):
+        es.selective_scan_step(one[:, 0], one[:, 0], zero, two[:, 0], two[:, 0], None, None, None, step, softplus=False)
+    assert torch.equal(step, torch.full_like(step, 2.0 ** 22 + 64))
+    # one live token and seven that take no step
+    weak_a = torch.full((C, N), -2.0 ** -8, device="cuda")
+    first = torch.rand(1, C, N, device="cuda")
+    alone = es.selective_scan(one[:, :1], one[:, :1], weak_a, two[:, :1], two[:, :1], softplus=False, initial_state=first, final_state=True)[1]
+    token = first.clone()
+    es.selective_scan_step(one[:, 0], one[:, 0], weak_a, two[:, 0], two[:, 0], None, None, None, token, softplus=False)
+    assert torch.equal(alone, token)
 
 
 def test_steps_and_gates_pointwise():
