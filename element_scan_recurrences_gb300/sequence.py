@@ -210,12 +210,13 @@ def selective_scan(x, delta, A, B, C, D=None, gate=None, delta_bias=None, softpl
         h[t] = exp(d[t] * A[c]) * h[t-1] + d[t] * x[t] * B[t]
         out[t] = (C[t] . h[t] + D[c] * x[t]) * gate[t] / (1 + exp(-gate[t]))
 
-    (d the sum itself without ``softplus``; no last factor without ``gate``).
-    x, delta, gate [B, T, channels]; A [channels, N] f32, N 1..64, meant to be
-    negative; B, C [B, T, groups, N], the groups dividing the channels; D,
-    ``delta_bias`` f32 [channels]; ``initial_state`` f32 [B, channels, N];
-    ``lengths`` int32 [B]: tokens past a row's length are not read and give
-    zeros.  Returns (out, the last state or None, checkpoints or None).
+    (d the sum itself without ``softplus``, with it 0 for a delta of -inf; no
+    last factor without ``gate``).  x, delta, gate [B, T, channels]; A
+    [channels, N] f32, N 1..64, meant to be negative; B, C [B, T, groups, N],
+    the groups dividing the channels; D, ``delta_bias`` f32 [channels];
+    ``initial_state`` f32 [B, channels, N]; ``lengths`` int32 [B]: tokens past a
+    row's length are not read and give zeros.  Returns (out, the last state or
+    None, checkpoints or None).
     ``final_state`` is True, or the tensor to write it to (which may be
     ``initial_state``); ``checkpoints`` likewise: states on the way, which
     ``selective_scan_backward`` of the same operands takes.

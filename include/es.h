@@ -908,9 +908,11 @@ es_status es_causal_conv_step(const es_causal_conv_args *args, es_stream_t strea
  *   out               may not overlap an input.
  *   workspace         es_selective_scan_workspace bytes, 16-byte aligned (may be
  *                     null where that is 0).
- * States and sums are f32; results are rounded once.  Operands are meant to be
- * finite: an infinity or NaN makes NaNs of its own channel's later tokens (in b
- * or c of its group's), and in a backward call of its row's earlier ones too.
+ * States and sums are f32; results are rounded once.  With softplus a delta of
+ * -infinity is a step of nothing: the token leaves the state as it is, and no
+ * gradient passes by its step.  Else operands are meant to be finite: an
+ * infinity or NaN makes NaNs of its own channel's later tokens (in b or c of
+ * its group's), and in a backward call of its row's earlier ones too.
  */
 typedef struct es_selective_scan_args {
     int64_t dtype, batch, length, channels, states, groups, softplus;
