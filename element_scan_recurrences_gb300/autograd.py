@@ -263,8 +263,9 @@ def selective_scan(x: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, B: tor
     floating operand: (out, the last state or None).  The forward keeps states
     on the way for the backward (4 N bytes a channel every 16 tokens); with
     ``checkpoints`` false it keeps none, and the backward finds them again."""
+    # (within the function gradients are off, and an operand's need of one is there in inference too)
     return _SelectiveScan.apply(x, delta, A, B, C, D, gate, delta_bias, bool(softplus), initial_state, lengths,
-                                bool(final_state), bool(checkpoints))
+                                bool(final_state), bool(checkpoints) and torch.is_grad_enabled())
 
 
 class _GroupNorm(torch.autograd.Function):
