@@ -239,18 +239,18 @@ class _SelectiveScan(torch.autograd.Function):
         out, fin, kept = sequence.selective_scan(x, delta, A, B, C, D, gate, delta_bias, softplus=softplus,
                                                  initial_state=initial_state, lengths=lengths, final_state=final_state,
                                                  checkpoints=keep)
-        ctx.save_for_backward(x, delta, A, B, C, D, gate, delta_bias, initial_state, lengths)
-        ctx.softplus, ctx.kept = softplus, kept
+        ctx.save_for_backward(x, delta, A, B, C, D, gate, delta_bias, initial_state, lengths, kept)
+        ctx.softplus = softplus
         return out, fin
 
     @staticmethod
     @once_differentiable
     def backward(ctx, grad_out, grad_fin):
-        x, delta, A, B, C, D, gate, delta_bias, initial_state, lengths = ctx.saved_tensors
+        x, delta, A, B, C, D, gate, delta_bias, initial_state, lengths, kept = ctx.saved_tensors
         gx, gdelta, gA, gB, gC, gD, ggate, gbias, gi = sequence.selective_scan_backward(
             x, delta, A, B, C, D, gate, delta_bias, grad_out if grad_out.stride(-1) == 1 else grad_out.contiguous(),
             softplus=ctx.softplus, initial_state=initial_state,
-            grad_final_state=None if grad_fin is None else grad_fin.contiguous(), lengths=lengths, checkpoints=ctx.kept)
+            grad_final_state=None if grad_fin is None else grad_fin.contiguous(), lengths=lengths, checkpoints=kept)
         return gx, gdelta, gA, gB, gC, gD, ggate, gbias, None, gi, None, None, None
 
 

@@ -1,6 +1,9 @@
 """What the differentiable selective scan keeps between its forward and its backward
 call, without a GPU: the library's calls are stood in for by functions that record
 their arguments and give tensors of the right shapes."""
+import gc
+import weakref
+
 import pytest
 import torch
 
@@ -51,3 +54,42 @@ def test_no_checkpoints_in_inference(calls, mode):
         ag.selective_scan(*args)
     ag.selective_scan(*operands(leaf=False))
     assert [c[1] for c in calls] == [False, False]
+
+
+def test_checkpoints_are_saved_tensors(calls):
+    """They pass by the hooks for saved tensors, as the operands do."""
+    packed = []
+
+    def pack(t):
+        packed.append(t.dtype)
+        return t
+
+    with torch.autograd.graph.saved_tensors_hooks(pack, lambda t: t):
+        out, _ = ag.selective_scan(*operands())
+    assert torch.uint8 in packed
+    out.sum().backward()
+    assert calls[-1] == ("backward", True)
+
+
+def test_checkpoints_go_with_the_backward(calls):
+    """They are let go of once the backward has run, however long its result lives."""
+    class Held:
+        def __init__(self, t):
+            self.t = t
+
+    held = []
+
+    def pack(t):
+        h = Held(t)
+        if t.dtype == torch.uint8:
+            held.append(weakref.ref(h))
+        return h
+
+    with torch.autograd.graph.saved_tensors_hooks(pack, lambda h: h.t):
+        out, _ = ag.selective_scan(*operands())
+    assert len(held) == 1 and held[0]() is not None
+    out.sum().backward()
+    gc.collect()
+    assert held[0]() is None
+    with pytest.raises(RuntimeError):
+        out.sum().backward()
