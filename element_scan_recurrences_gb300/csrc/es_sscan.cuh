@@ -1,6 +1,6 @@
 // es_sscan.cuh -- what the selective scan's kernels share: a CTA's place, tiles of
-// operands in shared memory.  A CTA takes scan_block_channels() channels of one
-// group, one batch row and one segment of its tokens.
+// operands in shared memory.  A CTA takes scan_channels() (backwards
+// scan_bwd_channels()) channels of one group, one batch row and one segment of its tokens.
 #pragma once
 
 #include "es_ssm.cuh"

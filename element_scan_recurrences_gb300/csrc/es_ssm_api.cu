@@ -157,8 +157,16 @@ struct ScanPlan {
 // More CTAs than the GPU holds even out what its SMs get: 65536 tokens x 2048 channels
 // 1397 us in 16 segments, 1347 in 19, 1301 in 32, 1331 in 64.  Backwards (2 CTAs an SM
 // at most, of 4 times the channels) a chunk takes 9.4 us alone, 13 by two, and a
-// second wave would run alone.  4 x 2048 x 4096 whole and in two segments: forwards 260
-// us, 298; backwards 1289, 908 (an earlier form of the kernel).
+// second wave would run alone.  4 x 2048 x 4096 whole and in two segments: forwards 249
+// us, 290; backwards 1200, 874 (chosen: one, two).
+//
+// The paces and the CTAs an SM holds were measured in bf16 at 16 states.  By their tiles
+// others hold fewer: forwards 4 at up to 8 states (f32 2, and 5 or 6 above), backwards
+// one at up to 8 states.  They go by the same rule; compared were 4 x 1024 x 2048 channels
+// whole, in two segments and as chosen, forwards and backwards: 8 states 131, 105, 78 us
+// and 717, 421, 242 (f32 136, 107, 112 and 726, 435, 266), 16 states 103, 101, 102 and 594,
+// 352, 250 (f32 126, 114, 113 and 593, 357, 258), 32 states 132, 140, 132 and 574, 425, 425,
+// 64 states 181, 241, 181 and 758, 823, 758.
 struct Pace {
     int resident, waves;
     double alone, more;          // us a chunk of one CTA an SM, what each further one adds
@@ -178,7 +186,7 @@ int scan_segments(const Pace& p, int64_t ctas, int64_t first, int64_t chunks, in
     const int64_t most = static_cast<int64_t>(kSms) * p.resident * p.waves / (ctas > 0 ? ctas : 1);
     double best = static_cast<double>(chunks) * chunk_us(p, ctas);
     int segs = 1;
-    // (some forty numbers of segments: a plan is made at every call)
+    // (some forty numbers of segments, a hundred for a CTA or two: a plan is made at every call)
     for (int64_t s = 2; s <= most && s <= chunks; s += s < 16 ? 1 : s / 16) {
         const int64_t each = (chunks + s - 1) / s, n = (chunks + each - 1) / each;
         const double us = static_cast<double>(each) * (chunk_us(p, ctas * n) + 0.6 * chunk_us(kForwards, first * (n - 1))) + 5.0 + 0.6 * n;

@@ -16,13 +16,13 @@
 // Tokens come in tiles of kScanChunk.  Half of a CTA's warps run the states through
 // a tile, where the only chain from token to token is one product and sum; the
 // other half at the same time make what the next tile's tokens and channels need once
-// (d and d x), and the last tile's results, two channels an instruction: 50 of the
-// 133 instructions a token and channel, and half of the warps that hide each
+// (d and d x), and the last tile's results, two channels an instruction: some 50 of
+// the 131 instructions a token and channel, and half of the warps that hide each
 // other's latencies (with every warp doing all three in turn 1.7 of them were there a
 // scheduler, and it issued in 38 of 100 clocks).  One barrier a tile.  8 x 1024 x 4096
-// channels x 16 states in bf16: 222 us (57 for the exponentials alone), 57 of 100
-// clocks issue.  Eight tokens a block of the inner loop: with two 229 us, four 234,
-// sixteen 242.
+// channels x 16 states in bf16: 213 us (57 for the exponentials alone), 57 of 100
+// clocks issue.  Eight tokens a block of the inner loop: with two it took 7 us more,
+// four 12, sixteen 20.
 //
 // A channel's tokens are a chain, so few channels leave the GPU idle: then the
 // tokens are cut into segments, a first pass finds the state each segment makes

@@ -19,10 +19,10 @@
 // 28), those over the CTAs of a group through a second launch, always in one order.
 //
 // 4 x 2048 x 4096 channels x 16 states in bf16: 762 us, 0.43 of the issue slots taken
-// by 364 instructions a token and channel.  What keeps it there is 1.7 warps a
-// scheduler: 255 registers a thread, and tensor memory for two CTAs.  Other warps for
-// what is made once a token and channel, as the forward kernel has them, cost five
-// barriers a chunk and took 1099 us.
+// by 362 instructions a token and channel.  What keeps it there is 1.7 warps a
+// scheduler: 255 registers a thread, and tensor memory for two CTAs (at up to 8 states
+// shared memory for one: 149 KB, in f32 182).  Other warps for what is made once a token
+// and channel, as the forward kernel has them, cost five barriers a chunk and took 1099 us.
 #include "es_attn.h"
 #include "es_sscan.cuh"
 #include "es_tcgen05.cuh"
